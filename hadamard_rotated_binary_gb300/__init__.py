@@ -38,9 +38,24 @@ from ._binding import (  # noqa: F401
     q1g128_words,
 )
 
+_PAGED = ("KVBatch", "PAIRS_ADJACENT", "PAIRS_HALF", "PagedKV", "Rope")
+
+
+def __getattr__(name: str):
+    """The attention side is loaded on first use: it needs torch, the rest of the package does not."""
+    if name in _PAGED:
+        from . import _paged
+
+        return getattr(_paged, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
 __all__ = [
     "BitLinear",
     "BitlinError",
+    "Rope",
+    "PagedKV",
+    "KVBatch",
     "mlp_forward",
     "load_q1g128",
     "q1g128_words",
@@ -51,6 +66,8 @@ __all__ = [
     "PATH_DECODE",
     "PATH_PREFILL",
     "PATH_TC_EXACT",
+    "PAIRS_HALF",
+    "PAIRS_ADJACENT",
     "PERM_NONE",
     "PERM_SSM_TILED_TO_GROUPED",
 ]

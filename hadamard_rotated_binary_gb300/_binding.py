@@ -28,6 +28,20 @@ PATH_TC_EXACT = 3
 _lib = None
 
 
+class Rows(ctypes.Structure):
+    """bitlin_rows: heads of tokens in device memory, strides in elements."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong)]
+
+
+class Batch(ctypes.Structure):
+    """bitlin_kv_batch: the new tokens of a batch of sequences, in device memory."""
+
+    _fields_ = [("seqs", ctypes.c_int), ("q_offsets", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_pages", ctypes.c_int), ("table_stride", ctypes.c_longlong)]
+
+
 def library_path() -> str:
     return os.path.join(PKG, "libbitlin.so")
 
@@ -78,6 +92,19 @@ def lib() -> ctypes.CDLL:
     L.bitlin_cuda_error.argtypes = [P]
     L.bitlin_status_string.argtypes = [i32]
     L.bitlin_status_string.restype = ctypes.c_char_p
+    R, B = ctypes.POINTER(Rows), ctypes.POINTER(Batch)
+    L.bitlin_rope_create.argtypes = [ctypes.POINTER(P), i32, i32, P, P, i32]
+    L.bitlin_rope_apply.argtypes = [P, R, i32, i32, i32, P, R, i32, P]
+    L.bitlin_rope_destroy.argtypes = [P]
+    L.bitlin_kv_create.argtypes = [ctypes.POINTER(P), P, P, i32, i32, i32, i32, i32, i64, i64, i64]
+    L.bitlin_kv_append.argtypes = [P, B, i32, P, P, R, R, R, i32, R, P]
+    L.bitlin_kv_attend.argtypes = [P, B, i32, R, i32, ctypes.c_float, i32, R, P, P]
+    L.bitlin_kv_get_error.argtypes = [P]
+    L.bitlin_kv_cuda_error.argtypes = [P]
+    L.bitlin_kv_destroy.argtypes = [P]
+    for name in ("bitlin_rope_create", "bitlin_rope_apply", "bitlin_rope_destroy", "bitlin_kv_create", "bitlin_kv_append",
+                 "bitlin_kv_attend", "bitlin_kv_get_error", "bitlin_kv_cuda_error", "bitlin_kv_destroy"):
+        getattr(L, name).restype = i32
     for name in ("bitlin_create", "bitlin_create_q1g128", "bitlin_forward", "bitlin_forward_host", "bitlin_embed", "bitlin_mlp_forward",
                  "bitlin_argmax", "bitlin_set_path", "bitlin_plan", "bitlin_set_wait_budget", "bitlin_test_stall", "bitlin_destroy", "bitlin_get_error",
                  "bitlin_cuda_error", "bitlin_version"):

@@ -1,0 +1,205 @@
+"""Binding of the attention side: rotary positions, the paged cache and attention over it
+(argument marshalling only; the calls are declared in include/bitlin.h)."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from ._binding import BITLIN_OK, BitlinError, Rows, Batch, lib
+
+F32, BF16, F16 = 0, 1, 2
+PAIRS_HALF, PAIRS_ADJACENT = 0, 1
+
+_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _rows(x, what: str) -> Rows:
+    """The C-ABI's view of a CUDA tensor [tokens][heads][dim] whose last dimension is contiguous."""
+    code = _CODES.get(x.dtype)
+    if code is None or not x.is_cuda or x.dim() != 3:
+        raise ValueError(f"{what} must be a float32, bfloat16 or float16 CUDA tensor [tokens][heads][dim]")
+    token, head, one = x.stride()
+    if one != 1 and x.shape[2] != 1:
+        raise ValueError(f"{what}'s last dimension must be contiguous")
+    # a dimension of one has no stride that matters
+    if x.shape[1] == 1:
+        head = x.shape[2]
+    if x.shape[0] == 1:
+        token = x.shape[1] * head
+    return Rows(x.data_ptr(), code, token, head)
+
+
+def _stream(stream, device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+
+
+def _positions(pos, axes: int, tokens: int):
+    if pos.dtype != torch.int32 or not pos.is_cuda or not pos.is_contiguous() or pos.numel() != axes * tokens:
+        raise ValueError(f"pos must be a contiguous int32 CUDA tensor [{axes}][{tokens}]")
+    return pos.data_ptr()
+
+
+class Rope:
+    """Rotary positions with one or several axes (a bitlin_rope handle on the current device).
+
+    inv_freq  R/2 numbers: pair i turns by pos[axis[i]] * inv_freq[i]
+    axis      R/2 axis indices, or None: one axis
+    adjacent  pairs (2i, 2i + 1) instead of (i, i + R/2)
+    """
+
+    def __init__(self, inv_freq, axis=None, adjacent: bool = False):
+        freq = [float(f) for f in inv_freq]
+        of = None if axis is None else [int(a) for a in axis]
+        if of is not None and len(of) != len(freq):
+            raise ValueError("axis must name one axis per frequency")
+        self.rotary_dim = 2 * len(freq)
+        self.axes = 1 if not of else max(of) + 1
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        h = ctypes.c_void_p()
+        st = lib().bitlin_rope_create(ctypes.byref(h), self.rotary_dim, self.axes,
+                                      (ctypes.c_float * len(freq))(*freq),
+                                      None if of is None else (ctypes.c_int32 * len(of))(*of),
+                                      PAIRS_ADJACENT if adjacent else PAIRS_HALF)
+        if st != BITLIN_OK:
+            raise BitlinError(st, "bitlin_rope_create")
+        self._h = h
+
+    def apply(self, x, pos, out=None, dtype=None, inverse: bool = False, stream=None):
+        """bitlin_rope_apply: x [tokens][heads][dim] rotated by pos (int32 [axes][tokens]), into `out`
+        (x itself is allowed) or a new tensor of `dtype` (x's where None)."""
+        src = _rows(x, "x")
+        if out is None:
+            out = torch.empty(x.shape, dtype=dtype or x.dtype, device=x.device)
+        elif out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+        dst = _rows(out, "out")
+        tokens, heads, dim = x.shape
+        st = lib().bitlin_rope_apply(self._h, src, tokens, heads, dim, _positions(pos, self.axes, tokens), dst,
+                                     1 if inverse else 0, _stream(stream, x.device))
+        if st != BITLIN_OK:
+            raise BitlinError(st, "bitlin_rope_apply")
+        return out
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().bitlin_rope_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KVBatch:
+    """The new tokens of a batch of sequences (a bitlin_kv_batch; holds the tensors).
+
+    q_offsets  int32 CUDA [seqs + 1]: sequence s owns token rows q_offsets[s] .. q_offsets[s + 1] - 1
+    kv_lens    int32 CUDA [seqs]: tokens in the cache, the new ones with them
+    table      int32 CUDA [seqs][pages per sequence]
+    """
+
+    def __init__(self, q_offsets, kv_lens, table):
+        for t in (q_offsets, kv_lens, table):
+            if t.dtype != torch.int32 or not t.is_cuda:
+                raise ValueError("q_offsets, kv_lens and table must be int32 CUDA tensors")
+        seqs = kv_lens.numel()
+        if not (q_offsets.is_contiguous() and kv_lens.is_contiguous()) or q_offsets.numel() != seqs + 1:
+            raise ValueError("q_offsets [seqs + 1] and kv_lens [seqs] must be contiguous")
+        if table.dim() != 2 or table.shape[0] != seqs or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table must be [seqs][pages] with contiguous rows")
+        if table.stride(0) < table.shape[1] and seqs > 1:
+            raise ValueError("table's rows must not overlap")
+        self.q_offsets, self.kv_lens, self.table = q_offsets, kv_lens, table
+        # the row length bounds what is read; rows of a wider table may be longer apart
+        self.c = Batch(seqs, q_offsets.data_ptr(), kv_lens.data_ptr(), table.data_ptr(), table.shape[1],
+                       table.stride(0))
+
+
+class PagedKV:
+    """One layer's paged cache (a bitlin_kv handle on the caller's pools, which it keeps alive).
+
+    k, v  bfloat16 or float16 CUDA tensors [pages][page_size][kv_heads][head_dim] with the same
+          strides, head_dim contiguous (a permuted view of another page layout is fine)
+    """
+
+    def __init__(self, k, v):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must be [pages][page_size][kv_heads][head_dim] of one type and layout")
+        if not (k.is_cuda and v.is_cuda) or k.stride(3) != 1 or k.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("k and v must be bfloat16 or float16 CUDA tensors with contiguous heads")
+        self.k, self.v = k, v
+        self.device, self.dtype = k.device, k.dtype
+        pages, page_size, self.kv_heads, self.head_dim = k.shape
+        page_stride, slot_stride, head_stride = k.stride()[:3]
+        h = ctypes.c_void_p()
+        with torch.cuda.device(k.device):
+            st = lib().bitlin_kv_create(ctypes.byref(h), k.data_ptr(), v.data_ptr(), pages, page_size, self.kv_heads,
+                                        self.head_dim, _CODES[k.dtype], page_stride, slot_stride, head_stride)
+        if st != BITLIN_OK:
+            raise BitlinError(st, "bitlin_kv_create")
+        self._h = h
+
+    def _check(self, st: int, what: str):
+        if st != BITLIN_OK:
+            raise BitlinError(st, what, lib().bitlin_kv_cuda_error(self._h))
+
+    def append(self, k, v, batch: KVBatch, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None):
+        """bitlin_kv_append: k and v [tokens][kv_heads][head_dim] to their places, k rotated; q
+        [tokens][heads][head_dim], when given, is rotated too and returned in the cache's type."""
+        tokens = k.shape[0]
+        if k.shape != v.shape or k.shape[1] != self.kv_heads or k.shape[2] != self.head_dim:
+            raise ValueError(f"k and v must be [tokens][{self.kv_heads}][{self.head_dim}]")
+        heads, src, dst = 0, None, None
+        if q is not None:
+            heads = q.shape[1]
+            if q.shape[0] != tokens or q.shape[2] != self.head_dim:
+                raise ValueError(f"q must be [{tokens}][heads][{self.head_dim}]")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=self.dtype, device=q.device)
+            elif q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+            src, dst = _rows(q, "q"), _rows(q_out, "q_out")
+        at = None if pos is None or rope is None else _positions(pos, rope.axes, tokens)
+        self._check(lib().bitlin_kv_append(self._h, batch.c, tokens, None if rope is None else rope._h, at,
+                                           _rows(k, "k"), _rows(v, "v"), src, heads, dst,
+                                           _stream(stream, k.device)), "bitlin_kv_append")
+        return q_out if q is not None else None
+
+    def attend(self, q, batch: KVBatch, scale: float | None = None, causal: bool = True, out=None, dtype=None,
+               lse=None, stream=None):
+        """bitlin_kv_attend: attention of q [tokens][heads][head_dim] over the batch's sequences, into
+        `out` or a new tensor of `dtype` (the cache's type, or float32); lse: float32 [tokens][heads]."""
+        src = _rows(q, "q")
+        tokens, heads, dim = q.shape
+        if dim != self.head_dim:
+            raise ValueError(f"q must be [tokens][heads][{self.head_dim}]")
+        if out is None:
+            out = torch.empty(q.shape, dtype=dtype or self.dtype, device=q.device)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous() or
+                                lse.shape != q.shape[:2]):
+            raise ValueError("lse must be a contiguous float32 CUDA tensor [tokens][heads]")
+        self._check(lib().bitlin_kv_attend(self._h, batch.c, tokens, src, heads,
+                                           1.0 / math.sqrt(dim) if scale is None else scale, 1 if causal else 0,
+                                           _rows(out, "out"), None if lse is None else lse.data_ptr(),
+                                           _stream(stream, q.device)), "bitlin_kv_attend")
+        return out
+
+    def get_error(self) -> int:
+        return lib().bitlin_kv_get_error(self._h)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().bitlin_kv_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

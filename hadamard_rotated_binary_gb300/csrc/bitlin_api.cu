@@ -10,8 +10,23 @@
 #include <new>
 
 #include "bitlin_internal.cuh"
+#include "tensormap.cuh"
 
 using namespace bitlin_impl;
+
+PFN_cuTensorMapEncodeTiled_v12000 bitlin_tensormap_encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
 
 namespace {
 
@@ -64,20 +79,6 @@ cudaError_t ensure_partials(bitlin_t h, int M)
     return e;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
-
 // Rotated-activation buffer for the tensor-core paths and its TMA descriptor:
 // bf16 [M][K] (prefill) or [4M][K] (exact: three digits and a zero row per token).
 bitlin_status ensure_xt(bitlin_t h, int M, int exact)
@@ -92,7 +93,7 @@ bitlin_status ensure_xt(bitlin_t h, int M, int exact)
         h->xt_M = rows;
     }
     if (h->tmap_M != M || h->tmap_exact != exact) {
-        PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
+        PFN_cuTensorMapEncodeTiled_v12000 enc = bitlin_tensormap_encode_fn();
         if (!enc) return from_cuda(h, cudaErrorNotSupported);
         // Viewed as [K/64][rows][64]: one box {64, tile width, 2} is a K-group's
         // two 128-byte-swizzled halves, stacked, in a single copy.
@@ -261,7 +262,7 @@ bitlin_status bitlin_create(bitlin_t* out, int N, int K, const uint32_t* packed_
     st = nullptr;
     {
         // Tensor-path bits as a [N][K/32] u32 tensor, read in boxes of 4 words x 128 rows.
-        PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
+        PFN_cuTensorMapEncodeTiled_v12000 enc = bitlin_tensormap_encode_fn();
         if (!enc) {
             e = cudaErrorNotSupported;
             goto fail_cuda;

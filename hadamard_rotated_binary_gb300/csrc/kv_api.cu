@@ -1,0 +1,299 @@
+// C-ABI of the attention side: rotary handles, paged-cache handles, argument checks.
+#include <cuda_runtime.h>
+
+#include <math.h>
+
+#include <memory>
+#include <new>
+
+#include "kv_internal.cuh"
+
+using namespace bitlin_impl;
+
+namespace {
+
+bitlin_status status_of(cudaError_t e)
+{
+    return e == cudaSuccess ? BITLIN_OK : e == cudaErrorMemoryAllocation ? BITLIN_ENOMEM : BITLIN_ECUDA;
+}
+
+bitlin_status from_cuda(bitlin_kv_t h, cudaError_t e)
+{
+    if (e != cudaSuccess) h->last_cuda_error = (int)e;
+    return status_of(e);
+}
+
+// The current device, when it is one this library runs on.
+bitlin_status current_device(int* dev)
+{
+    int major = 0, minor = 0;
+    if (cudaGetDevice(dev) != cudaSuccess) return BITLIN_EDEVICE;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev);
+    return major == 10 && minor == 3 ? BITLIN_OK : BITLIN_EDEVICE;
+}
+
+bool on_device(int device)
+{
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == device;
+}
+
+int type_size(int dtype) { return dtype == BITLIN_F32 ? 4 : 2; }
+
+// A call of no tokens may have no memory.
+bool rows_ok(const bitlin_rows* r, int tokens)
+{
+    return r && (r->data || tokens == 0) && (r->dtype == BITLIN_F32 || r->dtype == BITLIN_BF16 || r->dtype == BITLIN_F16) &&
+           reinterpret_cast<uintptr_t>(r->data) % type_size(r->dtype) == 0;
+}
+
+// Rows that are moved 16 bytes at a time (TMA, vector stores).
+bool rows_wide(const bitlin_rows* r)
+{
+    return reinterpret_cast<uintptr_t>(r->data) % 16 == 0 && r->token_stride > 0 && r->head_stride > 0 &&
+           r->token_stride % 8 == 0 && r->head_stride % 8 == 0 && r->token_stride < (1LL << 38) &&
+           r->head_stride < (1LL << 38);
+}
+
+bool sizes_ok(int tokens, int heads, int dim)
+{
+    return tokens >= 0 && heads >= 1 && heads <= 4096 && (unsigned long long)tokens * (unsigned)dim < (1ULL << 32);
+}
+
+bool batch_ok(const bitlin_kv_batch* b)
+{
+    return b && b->seqs >= 1 && b->q_offsets && b->kv_lens && b->table && b->table_pages >= 1 &&
+           (b->seqs == 1 || b->table_stride >= b->table_pages);
+}
+
+KvBatch batch_of(const bitlin_kv_batch* b) { return {b->q_offsets, b->kv_lens, b->table, b->table_stride, b->table_pages, b->seqs}; }
+
+void set_source(TurnParams& p, int i, const bitlin_rows* r)
+{
+    p.src[i] = r->data;
+    p.src_token[i] = r->token_stride;
+    p.src_head[i] = r->head_stride;
+}
+
+void set_rope(TurnParams& p, bitlin_rope_t r, const int32_t* pos)
+{
+    p.turns = r ? r->turns : nullptr;
+    p.rotary = r ? r->rotary : 0;
+    p.adjacent = r ? r->adjacent : 0;
+    p.pos = pos;
+}
+
+void set_out(TurnParams& p, const bitlin_rows* r)
+{
+    p.out = r->data;
+    p.out_token = r->token_stride;
+    p.out_head = r->head_stride;
+}
+
+}  // namespace
+
+extern "C" {
+
+bitlin_status bitlin_rope_create(bitlin_rope_t* out, int rotary_dim, int axes, const float* inv_freq,
+                                 const int32_t* axis, int pairing)
+{
+    if (!out) return BITLIN_EINVAL;
+    *out = nullptr;
+    if (!inv_freq || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > 65536 || axes < 1 || axes > 8) return BITLIN_EINVAL;
+    if (pairing != BITLIN_PAIRS_HALF && pairing != BITLIN_PAIRS_ADJACENT) return BITLIN_EINVAL;
+    const int pairs = rotary_dim / 2;
+    for (int i = 0; i < pairs; ++i)
+        if (!isfinite(inv_freq[i]) || (axis && (axis[i] < 0 || axis[i] >= axes))) return BITLIN_EINVAL;
+    int dev = 0;
+    bitlin_status st = current_device(&dev);
+    if (st != BITLIN_OK) return st;
+
+    std::unique_ptr<Turn[]> turns(new (std::nothrow) Turn[pairs]);
+    std::unique_ptr<bitlin_rope> r(new (std::nothrow) bitlin_rope());
+    if (!turns || !r) return BITLIN_ENOMEM;
+    for (int i = 0; i < pairs; ++i) {
+        // turns per place, modulo one turn, in 2^-64 (f64: 2^-54 of the frequency's own value)
+        double f = (double)inv_freq[i] / 6.283185307179586476925;
+        f -= floor(f);
+        if (f >= 1.0) f = 0.0;
+        turns[i] = {(uint64_t)ldexp(f, 64), axis ? axis[i] : 0, 0};
+    }
+    r->device = dev;
+    r->rotary = rotary_dim;
+    r->axes = axes;
+    r->adjacent = pairing == BITLIN_PAIRS_ADJACENT;
+    cudaError_t e = cudaMalloc(&r->turns, pairs * sizeof(Turn));
+    if (e == cudaSuccess) e = cudaMemcpy(r->turns, turns.get(), pairs * sizeof(Turn), cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) {
+        cudaFree(r->turns);
+        return status_of(e);
+    }
+    *out = r.release();
+    return BITLIN_OK;
+}
+
+bitlin_status bitlin_rope_apply(bitlin_rope_t r, const bitlin_rows* x, int tokens, int heads, int head_dim,
+                                const int32_t* pos, const bitlin_rows* out, int inverse, bitlin_stream_t stream)
+{
+    if (!r || !rows_ok(x, tokens) || !rows_ok(out, tokens) || (!pos && tokens) || !sizes_ok(tokens, heads, head_dim)) return BITLIN_EINVAL;
+    if (head_dim < r->rotary || (inverse != 0 && inverse != 1) || !on_device(r->device)) return BITLIN_EINVAL;
+    if (tokens == 0) return BITLIN_OK;
+    TurnParams p = {};
+    set_source(p, 0, x);
+    set_out(p, out);
+    set_rope(p, r, pos);
+    p.tokens = tokens;
+    p.heads = heads;
+    p.dim = head_dim;
+    p.inverse = inverse;
+    return status_of(bitlin_launch_turn(p, x->dtype, out->dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bitlin_status bitlin_rope_destroy(bitlin_rope_t r)
+{
+    if (!r) return BITLIN_OK;
+    cudaError_t e = cudaDeviceSynchronize();
+    cudaFree(r->turns);
+    delete r;
+    return e == cudaSuccess ? BITLIN_OK : BITLIN_ECUDA;
+}
+
+bitlin_status bitlin_kv_create(bitlin_kv_t* out, void* k, void* v, int pages, int page_size, int kv_heads,
+                               int head_dim, int dtype, long long page_stride, long long slot_stride,
+                               long long head_stride)
+{
+    if (!out) return BITLIN_EINVAL;
+    *out = nullptr;
+    if (!k || !v || reinterpret_cast<uintptr_t>(k) % 16 || reinterpret_cast<uintptr_t>(v) % 16) return BITLIN_EINVAL;
+    if (pages < 1 || page_size < 8 || page_size % 8 || page_size > 65536 || kv_heads < 1 || kv_heads > 4096)
+        return BITLIN_EINVAL;
+    if (head_dim < 8 || head_dim % 8 || head_dim > 256 || (dtype != BITLIN_BF16 && dtype != BITLIN_F16))
+        return BITLIN_EINVAL;
+    for (long long stride : {page_stride, slot_stride, head_stride})
+        if (stride < 8 || stride % 8 || stride >= (1LL << 39)) return BITLIN_EINVAL;
+    int dev = 0;
+    bitlin_status st = current_device(&dev);
+    if (st != BITLIN_OK) return st;
+    std::unique_ptr<bitlin_kv> h(new (std::nothrow) bitlin_kv());
+    if (!h) return BITLIN_ENOMEM;
+    h->device = dev;
+    h->k = k;
+    h->v = v;
+    h->pages = pages;
+    h->page_size = page_size;
+    h->kv_heads = kv_heads;
+    h->dim = head_dim;
+    h->dtype = dtype;
+    h->page_stride = page_stride;
+    h->slot_stride = slot_stride;
+    h->head_stride = head_stride;
+    cudaError_t e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaMalloc(&h->dev_error, 2 * sizeof(int));
+    if (e == cudaSuccess) e = cudaMemset(h->dev_error, 0, 2 * sizeof(int));
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) {
+        cudaFree(h->dev_error);
+        return status_of(e);
+    }
+    *out = h.release();
+    return BITLIN_OK;
+}
+
+bitlin_status bitlin_kv_append(bitlin_kv_t kv, const bitlin_kv_batch* batch, int tokens, bitlin_rope_t rope,
+                               const int32_t* pos, const bitlin_rows* k, const bitlin_rows* v,
+                               const bitlin_rows* q, int heads, const bitlin_rows* q_out, bitlin_stream_t stream)
+{
+    if (!kv || !batch_ok(batch) || !rows_ok(k, tokens) || !rows_ok(v, tokens) || k->dtype != v->dtype) return BITLIN_EINVAL;
+    if (!sizes_ok(tokens, q ? heads : 1, kv->dim) || (rope && rope->rotary > kv->dim)) return BITLIN_EINVAL;
+    if (q && (!rows_ok(q, tokens) || !rows_ok(q_out, tokens) || q->dtype != k->dtype || q_out->dtype != kv->dtype)) return BITLIN_EINVAL;
+    if (!on_device(kv->device) || (rope && rope->device != kv->device)) return BITLIN_EINVAL;
+    if (kv->sticky != BITLIN_OK) return kv->sticky;
+    if (tokens == 0) return BITLIN_OK;
+    TurnParams p = {};
+    if (q) {
+        set_source(p, 0, q);
+        set_out(p, q_out);
+    }
+    set_source(p, 1, k);
+    set_source(p, 2, v);
+    set_rope(p, rope, pos);
+    p.pool[0] = kv->k;
+    p.pool[1] = kv->v;
+    p.page_stride = kv->page_stride;
+    p.slot_stride = kv->slot_stride;
+    p.head_stride = kv->head_stride;
+    p.batch = batch_of(batch);
+    p.dev_error = kv->dev_error;
+    p.pages = kv->pages;
+    p.page_size = kv->page_size;
+    p.tokens = tokens;
+    p.heads = q ? heads : 0;
+    p.kv_heads = kv->kv_heads;
+    p.dim = kv->dim;
+    p.append = 1;
+    return from_cuda(kv, bitlin_launch_turn(p, k->dtype, kv->dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q,
+                               int heads, float scale, int causal, const bitlin_rows* out, float* lse,
+                               bitlin_stream_t stream)
+{
+    if (!kv || !batch_ok(batch) || !rows_ok(q, tokens) || !rows_ok(out, tokens) || q->dtype != kv->dtype) return BITLIN_EINVAL;
+    if (out->dtype != kv->dtype && out->dtype != BITLIN_F32) return BITLIN_EINVAL;
+    if (!rows_wide(q) || !rows_wide(out) || !isfinite(scale) || (causal != 0 && causal != 1)) return BITLIN_EINVAL;
+    if (!sizes_ok(tokens, heads, kv->dim) || heads % kv->kv_heads || heads / kv->kv_heads > 128) return BITLIN_EINVAL;
+    if (!on_device(kv->device)) return BITLIN_EINVAL;
+    if (kv->sticky != BITLIN_OK) return kv->sticky;
+    if (tokens == 0) return BITLIN_OK;
+    AttendParams p = {};
+    p.q = q->data;
+    p.q_token = q->token_stride;
+    p.q_head = q->head_stride;
+    p.k_pool = kv->k;
+    p.v_pool = kv->v;
+    p.page_stride = kv->page_stride;
+    p.slot_stride = kv->slot_stride;
+    p.head_stride = kv->head_stride;
+    p.batch = batch_of(batch);
+    p.out = out->data;
+    p.out_token = out->token_stride;
+    p.out_head = out->head_stride;
+    p.lse = lse;
+    p.dev_error = kv->dev_error;
+    p.pages = kv->pages;
+    p.page_size = kv->page_size;
+    p.tokens = tokens;
+    p.heads = heads;
+    p.kv_heads = kv->kv_heads;
+    p.dim = kv->dim;
+    p.causal = causal;
+    p.scale = scale;
+    return from_cuda(kv, bitlin_launch_attend(p, kv->dtype, out->dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bitlin_status bitlin_kv_get_error(bitlin_kv_t kv)
+{
+    if (!kv) return BITLIN_EINVAL;
+    cudaError_t e = cudaDeviceSynchronize();
+    int v[2] = {0, 0};
+    if (e == cudaSuccess) e = cudaMemcpy(v, kv->dev_error, sizeof(v), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return from_cuda(kv, e);
+    if (v[kKvErrTimeout]) kv->sticky = BITLIN_ETIMEOUT;
+    if (kv->sticky != BITLIN_OK || !v[kKvErrIndex]) return kv->sticky;
+    e = cudaMemset(kv->dev_error + kKvErrIndex, 0, sizeof(int));
+    return e == cudaSuccess ? BITLIN_EINDEX : from_cuda(kv, e);
+}
+
+int bitlin_kv_cuda_error(bitlin_kv_t kv) { return kv ? kv->last_cuda_error : 0; }
+
+bitlin_status bitlin_kv_destroy(bitlin_kv_t kv)
+{
+    if (!kv) return BITLIN_OK;
+    cudaError_t e = cudaDeviceSynchronize();
+    cudaFree(kv->dev_error);
+    delete kv;
+    return e == cudaSuccess ? BITLIN_OK : BITLIN_ECUDA;
+}
+
+}  // extern "C"

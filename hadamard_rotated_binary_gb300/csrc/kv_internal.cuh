@@ -1,0 +1,127 @@
+// Declarations shared by the rotary, paged-cache and attention sources (not part of the C-ABI).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "bitlin_internal.cuh"
+
+namespace bitlin_impl {
+
+// Device-side error words of a cache handle.
+constexpr int kKvErrTimeout = 0;  // a bounded wait gave up
+constexpr int kKvErrIndex = 1;    // a place outside the table or a page outside the pool
+
+// A frequency as a fixed-point fraction of a turn per position, 2^-64 turns,
+// so that position * frequency modulo one turn is an exact wrapping product.
+struct Turn {
+    uint64_t per_place;
+    int32_t axis;
+    int32_t pad;
+};
+
+struct KvBatch {
+    const int32_t* q_offsets;  // [seqs + 1]
+    const int32_t* kv_lens;    // [seqs]
+    const int32_t* table;      // [seqs] rows of table_pages entries
+    long long table_stride;
+    int table_pages;
+    int seqs;
+};
+
+// One call of the rotation kernel: rows of q to `out`, and for an append the
+// rows of k (rotated) and v (copied) to the pools.
+struct TurnParams {
+    const void* src[3];       // q, k, v
+    long long src_token[3], src_head[3];
+    void* out;                // q's destination
+    long long out_token, out_head;
+    void* pool[2];            // k, v
+    long long page_stride, slot_stride, head_stride;
+    KvBatch batch;
+    const Turn* turns;        // [rotary / 2], nullptr: no rotation
+    const int32_t* pos;       // [axes][tokens], nullptr: the token's place
+    int* dev_error;
+    int pages, page_size;
+    int tokens, heads, kv_heads, dim, rotary;
+    int adjacent, inverse;
+    int append;               // 0: q alone
+    int units;                // threads per row, set by the launcher
+    int q_groups, kv_groups;  // blocks along y: q, k, v, set by the launcher
+};
+
+// Index of the sequence that owns token row `t` (t < q_offsets[seqs]), found
+// by the whole warp: each round every lane probes one boundary of the range,
+// so up to 32 sequences take one round and up to 1024 two.  Returns the
+// largest s with q_offsets[s] <= t, or seqs when t is past the last row.
+__device__ __forceinline__ int warp_sequence_of(const KvBatch& b, int t)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = b.seqs + 1;  // the answer lies in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) >> 5;
+        const int i = lo + lane * step;
+        const bool le = lane * step < n && b.q_offsets[i] <= t;
+        const unsigned votes = __ballot_sync(0xffffffffu, le);
+        const int last = votes ? 31 - __clz(votes) : 0;
+        const int end = lo + n;
+        lo += last * step;
+        n = min(step, end - lo);
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// One call of the attention kernels.
+struct AttendParams {
+    const void* q;
+    long long q_token, q_head;
+    const void* k_pool;
+    const void* v_pool;
+    long long page_stride, slot_stride, head_stride;
+    KvBatch batch;
+    void* out;
+    long long out_token, out_head;
+    float* lse;                // [tokens][heads] or nullptr
+    int* dev_error;
+    int pages, page_size;
+    int tokens, heads, kv_heads, dim, causal;
+    float scale;
+};
+
+}  // namespace bitlin_impl
+
+struct bitlin_rope {
+    int device = 0;
+    int rotary = 0, axes = 0, adjacent = 0;
+    bitlin_impl::Turn* turns = nullptr;
+};
+
+struct bitlin_kv {
+    int device = 0;
+    int num_sms = 0;
+    void* k = nullptr;
+    void* v = nullptr;
+    int pages = 0, page_size = 0, kv_heads = 0, dim = 0, dtype = 0;
+    long long page_stride = 0, slot_stride = 0, head_stride = 0;
+    int last_cuda_error = 0;
+    bitlin_status sticky = BITLIN_OK;
+    int* dev_error = nullptr;  // [2]: kKvErr*
+};
+
+// Launchers (return a cudaError_t).
+cudaError_t bitlin_launch_turn(const bitlin_impl::TurnParams& p, int src_dtype, int dst_dtype, cudaStream_t s);
+cudaError_t bitlin_launch_attend(const bitlin_impl::AttendParams& p, int dtype, int out_dtype, cudaStream_t s);

@@ -313,6 +313,191 @@ bitlin_status bitlin_get_error(bitlin_t h);
 /* The cudaError_t value behind the last BITLIN_ECUDA of this handle (0 if none). */
 int bitlin_cuda_error(bitlin_t h);
 
+/* ------------------------------------------------------------------------
+ * The attention side of the decoder: rotary positions, a paged key/value
+ * cache, and attention of new tokens over it.  These calls sit between the
+ * folded q, k and v projections and the folded output projection
+ * ("Inside the One-Bit Engine", the grouped-query attention and partial
+ * rotary stations; Pulse "ARCHITECTURE-SPEC", attention heads in groups,
+ * query head h = kv * 6 + r).
+ * ------------------------------------------------------------------------ */
+
+/* Element types. */
+#define BITLIN_F32 0
+#define BITLIN_BF16 1
+#define BITLIN_F16 2
+
+/* Which two elements of a head rotate together (R = rotary_dim). */
+#define BITLIN_PAIRS_HALF 0     /* i and i + R/2 */
+#define BITLIN_PAIRS_ADJACENT 1 /* 2i and 2i + 1 */
+
+/* Rows of heads in device memory: element d of head h of token t is
+ * data[t * token_stride + h * head_stride + d] (strides in elements). */
+typedef struct {
+    void* data;
+    int dtype; /* BITLIN_F32, BITLIN_BF16 or BITLIN_F16 */
+    long long token_stride;
+    long long head_stride;
+} bitlin_rows;
+
+/* The new tokens of a batch of sequences, in device memory.  Sequence s owns
+ * the token rows q_offsets[s] .. q_offsets[s+1]-1 of a call and has
+ * kv_lens[s] tokens in the cache WITH its new ones, so its row i stands at
+ * place kv_lens[s] - (q_offsets[s+1] - i) of the sequence.  Place p lives in
+ * slot p % page_size of page table[s * table_stride + p / page_size]; a row of
+ * the table holds table_pages entries.
+ * Rows from q_offsets[seqs] on are padding and are left alone (a captured
+ * graph can replay with fewer tokens than it was captured with).
+ *   q_offsets  int32 [seqs + 1], q_offsets[0] = 0, not decreasing
+ *   kv_lens    int32 [seqs]; 0 is allowed
+ *   table      int32 [seqs] rows of table_pages entries, table_stride apart;
+ *              entries past a sequence's last page are not used */
+typedef struct {
+    int seqs;
+    const int32_t* q_offsets;
+    const int32_t* kv_lens;
+    const int32_t* table;
+    int table_pages;
+    long long table_stride;
+} bitlin_kv_batch;
+
+/* Opaque handle owning the frequencies of one rotary embedding. */
+typedef struct bitlin_rope* bitlin_rope_t;
+/* Opaque handle on one layer's paged cache (the pools stay the caller's). */
+typedef struct bitlin_kv* bitlin_kv_t;
+
+/*
+ * Rotary positions with one or several axes (time, height, width): pair i of
+ * a head turns by the angle pos[axis[i]][token] * inv_freq[i],
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ * and the head's elements past rotary_dim pass through.
+ *
+ *   rotary_dim  R: even, >= 2.
+ *   axes        number of position axes, 1..8.
+ *   inv_freq    HOST pointer, float [R/2], finite.
+ *   axis        HOST pointer, int32 [R/2], each in [0, axes); NULL: all 0.
+ *               Sections of consecutive pairs and interleaved axes are both
+ *               a choice of this array.
+ *   pairing     BITLIN_PAIRS_*.
+ *
+ * The arrays are copied.  Synchronous.  Errors: BITLIN_EINVAL, BITLIN_ENOMEM,
+ * BITLIN_ECUDA, BITLIN_EDEVICE.  On error *out is set to NULL.
+ */
+bitlin_status bitlin_rope_create(bitlin_rope_t* out, int rotary_dim, int axes, const float* inv_freq,
+                                 const int32_t* axis, int pairing);
+
+/*
+ * out = x rotated, for tokens x heads rows of head_dim elements.
+ *
+ *   x, out   any of the three types each; any strides.  out may be x itself
+ *            (same data, type and strides); otherwise they must not overlap.
+ *   pos      device pointer, int32 [axes][tokens].
+ *   inverse  0, or 1 to turn by the negative angle: the transposed map, which
+ *            is the gradient of the rotation.
+ *
+ * Angles are kept as a 64-bit fixed-point fraction of a turn, so the result
+ * is f32-exact (about 2e-7) at every int32 position; each output is rounded
+ * once to its type.  Asynchronous; allocates nothing.  tokens = 0 does nothing.
+ * Errors: BITLIN_EINVAL (NULL, an unknown type, head_dim < rotary_dim,
+ * heads < 1 or > 4096, tokens < 0, tokens * head_dim >= 2^32, a pointer that
+ * is not aligned to its type), BITLIN_ECUDA.
+ */
+bitlin_status bitlin_rope_apply(bitlin_rope_t r, const bitlin_rows* x, int tokens, int heads, int head_dim,
+                                const int32_t* pos, const bitlin_rows* out, int inverse, bitlin_stream_t stream);
+
+/* Release the handle.  NULL is accepted.  Synchronizes the device. */
+bitlin_status bitlin_rope_destroy(bitlin_rope_t r);
+
+/*
+ * A handle on one layer's paged cache in the caller's memory: element d of
+ * head h of slot s of page g is pool[g * page_stride + s * slot_stride +
+ * h * head_stride + d], for the key pool k and the value pool v alike.
+ *
+ *   k, v        device pointers, 16-byte aligned; they must stay valid while
+ *               the handle lives.  The handle never frees them.
+ *   pages       1 .. 2^31-1.
+ *   page_size   slots per page, a multiple of 8 (8 .. 65536).
+ *   kv_heads    1..4096.  head_dim  a multiple of 8, 8..256.
+ *   dtype       BITLIN_BF16 or BITLIN_F16.
+ *   strides     in elements, positive multiples of 8, below 2^39; no two
+ *               elements may share memory.
+ *
+ * Errors: BITLIN_EINVAL, BITLIN_ENOMEM, BITLIN_ECUDA, BITLIN_EDEVICE.  On
+ * error *out is set to NULL.
+ */
+bitlin_status bitlin_kv_create(bitlin_kv_t* out, void* k, void* v, int pages, int page_size, int kv_heads,
+                               int head_dim, int dtype, long long page_stride, long long slot_stride,
+                               long long head_stride);
+
+/*
+ * Append the batch's new keys and values: row i of k and v goes to its place
+ * (see bitlin_kv_batch), k rotated by `rope` on the way, both rounded to the
+ * cache's type.  In the same launch q, when given, is rotated into q_out in
+ * the cache's type, ready for bitlin_kv_attend.
+ *
+ *   tokens  rows of k and v (and q); rows past q_offsets[seqs] are padding.
+ *   rope    NULL: no rotation.
+ *   pos     device pointer, int32 [axes][tokens]; NULL: every axis is the
+ *           token's place in its sequence.
+ *   k, v    [tokens][kv_heads][head_dim], q [tokens][heads][head_dim]: one
+ *           type for all three, any strides.
+ *   q       NULL: none (heads and q_out are then ignored).
+ *   q_out   the cache's type, any strides; must not overlap q unless it is q.
+ *
+ * Two rows must not have the same page and slot.  A row whose place is
+ * negative, past the table's row or in a page outside [0, pages) is not
+ * written and makes the next bitlin_kv_get_error return BITLIN_EINDEX.
+ * Asynchronous; allocates nothing.  Errors: BITLIN_EINVAL (as
+ * bitlin_rope_apply; the current device is not the handle's), BITLIN_ECUDA,
+ * and the handle's sticky error.
+ */
+bitlin_status bitlin_kv_append(bitlin_kv_t kv, const bitlin_kv_batch* batch, int tokens, bitlin_rope_t rope,
+                               const int32_t* pos, const bitlin_rows* k, const bitlin_rows* v,
+                               const bitlin_rows* q, int heads, const bitlin_rows* q_out, bitlin_stream_t stream);
+
+/*
+ * Attention of the batch's new tokens over their sequences in the cache:
+ *     s_j = scale * (q . k_j),  out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),
+ *     lse = log sum_j exp(s_j),
+ * over the kv_lens[s] places j of the row's sequence (causal: those up to the
+ * row's own place).  Query head h reads key head h / (heads / kv_heads).  A
+ * row that sees no key gets zeros and lse = -inf.  Slots that hold no place
+ * of the sequence never count, whatever they hold.
+ *
+ *   q      [tokens][heads][head_dim] in the cache's type, 16-byte aligned,
+ *          strides positive multiples of 8.
+ *   scale  usually 1/sqrt(head_dim); finite.
+ *   out    [tokens][heads][head_dim], 16-byte aligned, strides multiples of
+ *          8; the cache's type, or BITLIN_F32 (what bitlin_forward reads).
+ *          For a 16-bit out the probabilities are rounded to the cache's type
+ *          before they meet the values; for an f32 out each is split into two
+ *          digits of that type, which keeps f32-level results.
+ *   lse    device pointer, float [tokens][heads], or NULL.
+ *
+ * Sums, the softmax's statistics and the output accumulate in f32.  Requires
+ * heads % kv_heads == 0, heads / kv_heads <= 128.  kv_lens past the table's
+ * row are cut to it, and pages outside [0, pages) read as zeros; both make the
+ * next bitlin_kv_get_error return BITLIN_EINDEX.  Asynchronous; the first
+ * call with a new largest size allocates workspace that the handle keeps.
+ * Calls on one handle share it: use one stream at a time.
+ * Errors: BITLIN_EINVAL, BITLIN_ENOMEM, BITLIN_ECUDA, the handle's sticky
+ * error.
+ */
+bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q,
+                               int heads, float scale, int causal, const bitlin_rows* out, float* lse,
+                               bitlin_stream_t stream);
+
+/* As bitlin_get_error, for a cache handle: BITLIN_ETIMEOUT (sticky),
+ * BITLIN_EINDEX (once, then cleared) or BITLIN_ECUDA.  Synchronizes. */
+bitlin_status bitlin_kv_get_error(bitlin_kv_t kv);
+
+/* The cudaError_t value behind the last BITLIN_ECUDA of this handle (0 if none). */
+int bitlin_kv_cuda_error(bitlin_kv_t kv);
+
+/* Release the handle's own memory (not the pools).  NULL is accepted.
+ * Synchronizes the device. */
+bitlin_status bitlin_kv_destroy(bitlin_kv_t kv);
+
 /* A static, human-readable description of a status value. */
 const char* bitlin_status_string(bitlin_status s);
 
