@@ -101,9 +101,12 @@ def lib() -> ctypes.CDLL:
     L.bitlin_kv_attend.argtypes = [P, B, i32, R, i32, ctypes.c_float, i32, R, P, P]
     L.bitlin_kv_get_error.argtypes = [P]
     L.bitlin_kv_cuda_error.argtypes = [P]
+    L.bitlin_kv_set_wait_budget.argtypes = [P, i64]
+    L.bitlin_kv_test_stall.argtypes = [P, i32]
     L.bitlin_kv_destroy.argtypes = [P]
     for name in ("bitlin_rope_create", "bitlin_rope_apply", "bitlin_rope_destroy", "bitlin_kv_create", "bitlin_kv_append",
-                 "bitlin_kv_attend", "bitlin_kv_get_error", "bitlin_kv_cuda_error", "bitlin_kv_destroy"):
+                 "bitlin_kv_attend", "bitlin_kv_get_error", "bitlin_kv_cuda_error", "bitlin_kv_set_wait_budget",
+                 "bitlin_kv_test_stall", "bitlin_kv_destroy"):
         getattr(L, name).restype = i32
     for name in ("bitlin_create", "bitlin_create_q1g128", "bitlin_forward", "bitlin_forward_host", "bitlin_embed", "bitlin_mlp_forward",
                  "bitlin_argmax", "bitlin_set_path", "bitlin_plan", "bitlin_set_wait_budget", "bitlin_test_stall", "bitlin_destroy", "bitlin_get_error",

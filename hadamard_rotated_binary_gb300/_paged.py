@@ -190,6 +190,12 @@ class PagedKV:
                                            _stream(stream, q.device)), "bitlin_kv_attend")
         return out
 
+    def set_wait_budget(self, ns: int):
+        self._check(lib().bitlin_kv_set_wait_budget(self._h, int(ns)), "bitlin_kv_set_wait_budget")
+
+    def test_stall(self, on: bool):
+        self._check(lib().bitlin_kv_test_stall(self._h, 1 if on else 0), "bitlin_kv_test_stall")
+
     def get_error(self) -> int:
         return lib().bitlin_kv_get_error(self._h)
 

@@ -1,9 +1,39 @@
-// Attention of a batch's new tokens over their sequences in the paged cache.
+// Attention of a batch's new tokens over their sequences in the paged cache,
+// on the tensor cores, one pass over the keys.
 //
 // out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m), s_j = scale * q . k_j,
-// in one pass over the keys with the running maximum m and sum.  One warp per
-// (token, query head): lane l holds elements l, l + 32, ... of q and of the
-// output, and a key's score is a sum across the warp.
+// with a running maximum m and sum per row; exp(x) = 2^(x log2 e).
+//
+// Tile: 128 rows of S = Q K^T in tensor memory (one lane per row), 128 keys.
+// A row is one query head of one token; the heads / kv_heads query heads that
+// read a key head share its rows (tokens outermost), so a single token of a
+// grouped model still reads each key once.
+//
+// Work: an item is (sequence, key head, tile of rows) and costs its visible
+// key tiles.  All items lie end to end on one line of tiles, sequences
+// outermost, then key heads (neighbouring CTAs then read the same keys, which
+// L2 serves), and the persistent CTAs cut the line into equal parts, so a long
+// context splits over all SMs and ragged batches balance, with no length known
+// on the host.  A CTA that has only a part of an item leaves its unnormalised
+// output with the row's maximum and sum in the workspace; the last of the
+// item's CTAs to do so joins the parts in their order (results do not depend
+// on which one is last).
+//
+// Roles of the 8 warps:
+//   0-3  softmax: S from tensor memory, running maximum and sum, the weights P
+//        back over S as the A operand of P V; the item's epilogue;
+//   4    TMA: K and V pages through one ring of 16 KB chunks, in the order the
+//        MMAs use them (K0, K1, V0, K2, V1, ...); a chunk is 128 keys x 64
+//        dims of K or 8192 / DP keys x DP dims of V, page by page;
+//   5    MMA issue: S tiles alternate between two buffers, so Q K^T of the
+//        next tile runs while the softmax works on this one;
+//   6-7  Q of the next item (plain copies: rows of any stride).
+// The output stays in tensor memory; it is rescaled only when a row's maximum
+// grows by more than 2^8 (until then the weights are relative to the older
+// maximum, which f32 sums and the 16-bit weights' exponents hold).
+#include <cuda.h>
+#include <math.h>
+
 #include "kv_internal.cuh"
 #include "ptx.cuh"
 
@@ -11,79 +41,920 @@ using namespace bitlin_impl;
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kRows = 128;        // rows of a tile (UMMA M)
+constexpr int kKeys = 128;        // keys of a tile
+constexpr int kThreads = 256;
+constexpr int kTmaWarp = 4, kMmaWarp = 5, kQWarp = 6;
+constexpr int kChunkBytes = 16384;
+constexpr int kTmemCols = 512;
+constexpr float kLazy = 8.f;      // log2 of the growth that a rescale waits for
+constexpr int kMaxLen = 1 << 30;
 
-template <typename T, typename TO>
-__global__ void __launch_bounds__(32 * kWarps) bitlin_attend_rows(const AttendParams p)
+template <int DP>
+struct Cfg {
+    static constexpr int NC = DP / 64;                    // chunks of a K (and of a V) tile
+    static constexpr int KV = 8192 / DP;                  // keys of a V chunk
+    static constexpr int kQBytes = kRows * DP * 2;
+    static constexpr int kStages = (224 * 1024 - kQBytes) / kChunkBytes > 12 ? 12 : (224 * 1024 - kQBytes) / kChunkBytes;
+    static constexpr int kOCol = 0, kSCol = 256;          // tensor memory: output, two S buffers
+};
+
+// The part of the line that a CTA starts with.
+struct Start {
+    long long total;   // tiles of all items
+    int ctas;          // CTAs that have work
+    int seq, head, qt; // item
+    int skip;          // its tiles that belong to earlier CTAs
+};
+
+template <int DP>
+struct __align__(8) Shared {
+    uint64_t full[Cfg<DP>::kStages], empty[Cfg<DP>::kStages];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_ready[2], pv_done[2];
+    uint64_t o_free;
+    uint64_t join;    // the four softmax warps meet (a bounded wait, unlike a named barrier)
+    uint64_t never, drain;
+    Start start;
+    uint32_t tmem_base;
+    int last;         // this CTA joins the item's parts
+    int bad;          // 1 + the part whose values held an infinity or a NaN
+    int abort;
+};
+
+template <int DP>
+constexpr int smem_bytes()
 {
-    ptx::griddep_wait();
+    return Cfg<DP>::kQBytes + Cfg<DP>::kStages * kChunkBytes + (int)sizeof(Shared<DP>) + 1024;
+}
+
+// ---- the line of tiles ------------------------------------------------------
+
+// A sequence's rows and keys, with every index brought into range.
+struct Seq {
+    int row0, rows;   // token rows of the call
+    int place0;       // place of the first
+    int len;          // keys held
+    int tiles;        // row tiles
+};
+
+__device__ __forceinline__ Seq load_seq(const AttendParams& p, int s)
+{
+    Seq q;
+    const int lo = p.batch.q_offsets[s], hi = p.batch.q_offsets[s + 1];
+    const int raw = min(max(p.batch.kv_lens[s], 0), kMaxLen);
+    const long long cap = (long long)p.batch.table_pages * p.page_size;
+    q.row0 = min(max(lo, 0), p.tokens);
+    q.rows = min(max(hi, q.row0), p.tokens) - q.row0;
+    q.place0 = raw - (min(max(hi, 0), kMaxLen) - q.row0);
+    q.len = raw < cap ? raw : (int)cap;
+    q.tiles = (q.rows + p.tile_tokens - 1) / p.tile_tokens;
+    if (q.len < raw) p.dev_error[kKvErrIndex] = 1;
+    return q;
+}
+
+// Keys that the last row of row tile qt sees.
+__device__ __forceinline__ int item_end(const AttendParams& p, int rows, int place0, int len, int qt)
+{
+    if (!p.causal) return len;
+    return min(max(place0 + min(rows, (qt + 1) * p.tile_tokens), 0), len);
+}
+
+// Key tiles of an item; one that sees no key still costs a tile (it writes zeros).
+__device__ __forceinline__ int item_tiles(const AttendParams& p, int rows, int place0, int len, int qt)
+{
+    return max(1, (item_end(p, rows, place0, len, qt) + kKeys - 1) / kKeys);
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v)  // inclusive
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T u = __shfl_up_sync(0xffffffffu, v, o);
+        if ((int)(threadIdx.x & 31) >= o) v += u;
+    }
+    return v;
+}
+
+// Tiles of one key head of sequence base + lane (0 past the last sequence).
+// Sequences of several row tiles are summed by the whole warp, one after the other.
+__device__ __forceinline__ long long seq_tiles(const AttendParams& p, int base, Seq& q)
+{
     const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= (long long)p.tokens * p.heads) return;
-    const int t = (int)(row / p.heads), h = (int)(row - (long long)t * p.heads);
-    const int seq = warp_sequence_of(p.batch, t);
-    if (seq >= p.batch.seqs) return;
-    int len = p.batch.kv_lens[seq];
-    const long long held = (long long)p.batch.table_pages * p.page_size;
-    if (len > held) {
-        p.dev_error[kKvErrIndex] = 1;
-        len = (int)held;
+    q = {};
+    if (base + lane < p.batch.seqs) q = load_seq(p, base + lane);
+    long long sum = q.tiles == 1 ? item_tiles(p, q.rows, q.place0, q.len, 0) : 0;
+    unsigned many = __ballot_sync(0xffffffffu, q.tiles > 1);
+    while (many) {
+        const int l = __ffs(many) - 1;
+        many &= many - 1;
+        const int rows = __shfl_sync(0xffffffffu, q.rows, l), place0 = __shfl_sync(0xffffffffu, q.place0, l);
+        const int len = __shfl_sync(0xffffffffu, q.len, l), tiles = __shfl_sync(0xffffffffu, q.tiles, l);
+        long long part = 0;
+        for (int qt = lane; qt < tiles; qt += 32) part += item_tiles(p, rows, place0, len, qt);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        if (lane == l) sum = part;
     }
-    const int place = p.batch.kv_lens[seq] - (p.batch.q_offsets[seq + 1] - t);
-    const int end = p.causal ? min(len, place + 1) : len;
-    const int kh = h / (p.heads / p.kv_heads);
-
-    const T* q = static_cast<const T*>(p.q) + t * p.q_token + h * p.q_head;
-    float qv[8], acc[8], m = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        qv[i] = lane + 32 * i < p.dim ? to_f32(q[lane + 32 * i]) * p.scale : 0.f;
-        acc[i] = 0.f;
-    }
-    for (int j = 0; j < end; ++j) {
-        const int at = j / p.page_size;
-        const int page = p.batch.table[seq * p.batch.table_stride + at];
-        float kv[8], vv[8], s = 0.f;
-        const bool in = page >= 0 && page < p.pages;
-        if (!in) p.dev_error[kKvErrIndex] = 1;
-        const long long base = page * p.page_stride + (j - at * p.page_size) * p.slot_stride + kh * p.head_stride;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool use = in && lane + 32 * i < p.dim;
-            kv[i] = use ? to_f32(static_cast<const T*>(p.k_pool)[base + lane + 32 * i]) : 0.f;
-            vv[i] = use ? to_f32(static_cast<const T*>(p.v_pool)[base + lane + 32 * i]) : 0.f;
-            s += qv[i] * kv[i];
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float top = fmaxf(m, s), use = top == -INFINITY ? 0.f : top;
-        const float keep = expf(m - use), w = expf(s - use);
-        sum = sum * keep + w;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = acc[i] * keep + w * vv[i];
-        m = top;
-    }
-    TO* out = static_cast<TO*>(p.out) + t * p.out_token + h * p.out_head;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (lane + 32 * i < p.dim) out[lane + 32 * i] = from_f32<TO>(acc[i] * inv);
-    if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
+    return sum;
 }
 
-template <typename T, typename TO>
-cudaError_t launch(const AttendParams& p, cudaStream_t s)
+__device__ __forceinline__ long long cut(long long total, int ctas, int c) { return total * c / ctas; }
+// The CTA whose part holds tile x.
+__device__ __forceinline__ int cta_of(long long total, int ctas, long long x)
 {
-    const long long rows = (long long)p.tokens * p.heads;
-    bitlin_attend_rows<T, TO><<<(unsigned)((rows + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(p);
-    return cudaGetLastError();
+    return (int)(((x + 1) * ctas - 1) / total);
 }
+
+// One warp: where this CTA's part of the line begins.
+__device__ void locate(const AttendParams& p, Start* out)
+{
+    const int lane = threadIdx.x & 31;
+    Seq q;
+    long long total = 0;
+    for (int base = 0; base < p.batch.seqs; base += 32) {
+        long long n = seq_tiles(p, base, q) * p.kv_heads;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        total += n;
+    }
+    Start st = {};
+    st.total = total;
+    st.ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
+    if ((int)blockIdx.x < st.ctas) {
+        const long long x = cut(total, st.ctas, blockIdx.x);
+        long long before = 0;
+        for (int base = 0; base < p.batch.seqs; base += 32) {
+            const long long one = seq_tiles(p, base, q), all = one * p.kv_heads;
+            const long long upto = before + warp_scan(all);
+            const unsigned past = __ballot_sync(0xffffffffu, upto > x);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                const long long per = __shfl_sync(0xffffffffu, one, l);
+                long long off = x - __shfl_sync(0xffffffffu, upto - all, l);
+                st.seq = base + l;
+                st.head = (int)(off / per);
+                off -= st.head * per;
+                const int rows = __shfl_sync(0xffffffffu, q.rows, l), place0 = __shfl_sync(0xffffffffu, q.place0, l);
+                const int len = __shfl_sync(0xffffffffu, q.len, l), tiles = __shfl_sync(0xffffffffu, q.tiles, l);
+                for (int qb = 0; qb < tiles; qb += 32) {
+                    const int n = qb + lane < tiles ? item_tiles(p, rows, place0, len, qb + lane) : 0;
+                    const long long to = warp_scan((long long)n);
+                    const unsigned hit = __ballot_sync(0xffffffffu, to > off);
+                    if (hit) {
+                        const int h = __ffs(hit) - 1;
+                        st.qt = qb + h;
+                        st.skip = (int)(off - __shfl_sync(0xffffffffu, to - n, h));
+                        break;
+                    }
+                    off -= __shfl_sync(0xffffffffu, to, 31);
+                }
+                break;
+            }
+            before = __shfl_sync(0xffffffffu, upto, 31);
+        }
+    }
+    if (lane == 0) *out = st;
+}
+
+// A CTA's parts of items, one after the other; every role walks them alike.
+struct Walk {
+    const AttendParams& p;
+    long long left;       // tiles of this CTA still to come
+    int seq, head, qt;
+    Seq q;
+    int end;              // keys the item's last row sees
+    int tiles, j0, j1;    // the item's key tiles, and this part of them
+
+    __device__ Walk(const AttendParams& params, const Start& s) : p(params), seq(s.seq), head(s.head), qt(s.qt)
+    {
+        left = 0;
+        j0 = j1 = 0;
+        if ((int)blockIdx.x < s.ctas) {
+            left = cut(s.total, s.ctas, blockIdx.x + 1) - cut(s.total, s.ctas, blockIdx.x);
+            q = load_seq(p, seq);
+            set(s.skip);
+        }
+    }
+    __device__ bool valid() const { return left > 0; }
+    __device__ void set(int skip)
+    {
+        end = item_end(p, q.rows, q.place0, q.len, qt);
+        tiles = max(1, (end + kKeys - 1) / kKeys);
+        j0 = skip;
+        j1 = (int)min((long long)tiles, j0 + left);
+    }
+    __device__ void next()
+    {
+        left -= j1 - j0;
+        if (left <= 0) return;
+        if (++qt == q.tiles) {
+            qt = 0;
+            if (++head == p.kv_heads) {
+                head = 0;
+                q.tiles = 0;
+                while (q.tiles == 0 && seq + 1 < p.batch.seqs) q = load_seq(p, ++seq);
+                if (q.tiles == 0) {  // the lengths changed under the call
+                    left = 0;
+                    return;
+                }
+            }
+        }
+        set(0);
+    }
+    // tokens of the row tile
+    __device__ int tokens() const { return min(p.tile_tokens, q.rows - qt * p.tile_tokens); }
+};
+
+// A whole warp waits; true when every lane saw the phase complete.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, long long phase, volatile int* abort, long long budget)
+{
+    return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, (uint32_t)phase & 1u, abort, budget));
+}
+
+// ---- weights ----------------------------------------------------------------
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v)
+{
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t v)
+{
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// Exponent bits of a 16-bit element: all ones is an infinity or a NaN.
+template <typename T>
+constexpr uint32_t kExpBits = 0x7F80u;
+template <>
+constexpr uint32_t kExpBits<__half> = 0x7C00u;
+
+// f16 weights are held 2^6 larger, which keeps 2^-31 of the largest one above
+// their smallest step; with kLazy they stay below 2^14.  bf16 has f32's range.
+template <typename T>
+constexpr float kShift = 0.f;
+template <>
+constexpr float kShift<__half> = 6.f;
+
+// Zero the infinities and NaNs of a word of two elements; whether there were any.
+template <typename T>
+__device__ __forceinline__ bool clean(uint32_t& w)
+{
+    constexpr uint32_t e = kExpBits<T>;
+    const bool lo = (w & e) == e, hi = ((w >> 16) & e) == e;
+    if (lo) w &= 0xFFFF0000u;
+    if (hi) w &= 0x0000FFFFu;
+    return lo || hi;
+}
+
+// ---- the kernel -------------------------------------------------------------
+
+// F32OUT: the output is f32 and each weight is two digits of T, hi = T(w) and
+// lo = T(w - hi), multiplied into the same accumulator one after the other.
+template <int DP, typename T, bool F32OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    bitlin_attend(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                  const __grid_constant__ AttendParams p)
+{
+    using C = Cfg<DP>;
+    constexpr int NC = C::NC, NS = C::kStages, KV = C::KV;
+    constexpr bool kBf16 = sizeof(T) == 2 && kExpBits<T> == 0x7F80u;
+
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char* tile_q = smem;                // [NC][128 rows][64], 128-byte swizzle
+    unsigned char* ring = smem + C::kQBytes;     // [NS][16 KB]
+    auto* sh = reinterpret_cast<Shared<DP>*>(ring + NS * kChunkBytes);
+    volatile int* abort = &sh->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long budget = p.wait_budget_ns;
+
+    if (threadIdx.x == 32 * kTmaWarp) {
+        for (int i = 0; i < NS; ++i) {
+            ptx::mbar_init(&sh->full[i], 1);
+            ptx::mbar_init(&sh->empty[i], 1);
+        }
+        ptx::mbar_init(&sh->q_full, 64);
+        ptx::mbar_init(&sh->q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sh->s_full[i], 1);
+            ptx::mbar_init(&sh->p_ready[i], kRows);
+            ptx::mbar_init(&sh->pv_done[i], 1);
+        }
+        ptx::mbar_init(&sh->o_free, kRows);
+        ptx::mbar_init(&sh->join, kRows);
+        ptx::mbar_init(&sh->never, 1);
+        ptx::mbar_init(&sh->drain, 1);
+        sh->abort = 0;
+        sh->bad = 0;
+        ptx::mbar_fence_init();
+        ptx::fence_proxy_async_smem();
+        ptx::prefetch_tmap(&tmap_k);
+        ptx::prefetch_tmap(&tmap_v);
+    }
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(&sh->tmem_base, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::griddep_wait();
+    if (warp == 0) locate(p, &sh->start);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    ptx::griddep_launch_dependents();
+    const uint32_t tmem = sh->tmem_base;
+    const Start start = sh->start;
+    Walk w(p, start);
+
+    if (warp == kTmaWarp) {
+        int stage = 0;
+        uint32_t phase = 0;
+        long long issued = 0;
+        bool ok = true;
+        // Lane l holds the page of keys 8l .. 8l+7 of a tile.
+        auto page_of = [&](int j) {
+            const int key = j * kKeys + 8 * lane;
+            int page = -1;
+            if (lane < kKeys / 8 && key < w.end) {
+                page = p.batch.table[w.seq * p.batch.table_stride + key / p.page_size];
+                if (page < 0 || page >= p.pages) {  // outside the pool: the copy fills zeros
+                    p.dev_error[kKvErrIndex] = 1;
+                    page = -1;
+                }
+            }
+            return page;
+        };
+        auto next_stage = [&]() {
+            ++issued;
+            if (++stage == NS) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        };
+        for (; w.valid() && ok; w.next()) {
+            int page_k = page_of(w.j0), page_v = -1, page_next = -1;
+            for (int j = w.j0; j <= w.j1 && ok; ++j) {
+                if (j + 1 < w.j1) page_next = page_of(j + 1);
+                if (j < w.j1) {
+                    // K tile j: NC chunks of 128 keys x 64 dims
+                    const int keys = min(kKeys, w.end - j * kKeys);
+                    const int boxes = keys > 0 ? (keys + p.box_k - 1) / p.box_k : 0;
+                    const int at = min(lane * p.box_k, kKeys - 8);
+                    const int page = __shfl_sync(0xffffffffu, page_k, at >> 3);
+                    const int slot = (j * kKeys + at) % p.page_size;
+                    for (int c = 0; c < NC; ++c) {
+                        ok = warp_wait(&sh->empty[stage], phase ^ 1u, abort, budget);
+                        if (!ok) break;
+                        unsigned char* dst = ring + stage * kChunkBytes;
+                        if (lane == 0) {
+                            if (boxes) ptx::mbar_arrive_expect_tx(&sh->full[stage], boxes * p.box_k * 128);
+                            else ptx::mbar_arrive(&sh->full[stage]);
+                        }
+                        __syncwarp();
+                        if (lane < boxes)
+                            ptx::tma_load_4d(dst + lane * p.box_k * 128, &tmap_k, 64 * c, slot, w.head, page,
+                                             &sh->full[stage]);
+                        next_stage();
+                    }
+                }
+                if (j > w.j0 && ok) {
+                    // V tile j - 1: NC chunks of KV keys x DP dims, as [dims / 64][KV][64]
+                    const int box = lane / NC, dims = lane % NC;
+                    for (int c = 0; c < NC; ++c) {
+                        const int key = (j - 1) * kKeys + c * KV;
+                        const int keys = min(KV, w.end - key);
+                        const int boxes = keys > 0 ? (keys + p.box_v - 1) / p.box_v : 0;
+                        const int at = min(c * KV + box * p.box_v, kKeys - 8);
+                        const int page = __shfl_sync(0xffffffffu, page_v, at >> 3);
+                        const int slot = ((j - 1) * kKeys + at) % p.page_size;
+                        ok = warp_wait(&sh->empty[stage], phase ^ 1u, abort, budget);
+                        if (!ok) break;
+                        unsigned char* dst = ring + stage * kChunkBytes;
+                        if (lane == 0) {
+                            if (boxes) ptx::mbar_arrive_expect_tx(&sh->full[stage], boxes * p.box_v * 128 * NC);
+                            else ptx::mbar_arrive(&sh->full[stage]);
+                        }
+                        __syncwarp();
+                        if (box < boxes)
+                            ptx::tma_load_4d(dst + dims * (KV * 128) + box * p.box_v * 128, &tmap_v, 64 * dims, slot,
+                                             w.head, page, &sh->full[stage]);
+                        next_stage();
+                    }
+                }
+                page_v = page_k;
+                page_k = page_next;
+            }
+        }
+        // Every copy issued here must land before the CTA may exit.
+        for (long long i = issued > NS ? issued - NS : 0; i < issued; ++i) {
+            volatile int no_abort = 0;
+            ptx::mbar_wait_bounded(&sh->full[i % NS], (uint32_t)(i / NS) & 1u, &no_abort, budget);
+        }
+    } else if (warp == kMmaWarp) {
+        constexpr uint32_t idesc_s = ptx::idesc_f32(kRows, kKeys, kBf16, false);
+        constexpr uint32_t idesc_o = ptx::idesc_f32(kRows, DP, kBf16, true);
+        const uint64_t desc_q = ptx::smem_desc_sw128(ptx::smem_u32(tile_q));
+        const uint64_t desc_k = ptx::smem_desc_sw128(ptx::smem_u32(ring));
+        const uint64_t desc_v = ptx::smem_desc_sw128_mn(ptx::smem_u32(ring), KV * 128);
+        int stage = 0;
+        uint32_t phase = 0;
+        long long gt = 0;  // tiles so far, over all parts: S buffer gt & 1
+        int part = 0;
+        bool ok = true, any = false;
+        auto next_stage = [&]() {
+            if (++stage == NS) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        };
+        for (; w.valid() && ok; w.next(), ++part) {
+            const int n = w.j1 - w.j0;
+            ok = warp_wait(&sh->q_full, part, abort, budget);
+            // step i: S(i) = Q K(i)^T, then O += P(i-1) V(i-1)
+            for (int i = 0; i <= n && ok; ++i) {
+                if (i < n) {
+                    const int b = (int)((gt + i) & 1);
+                    // the buffer's previous weights have been multiplied
+                    if (gt + i >= 2)
+                        ok = warp_wait(&sh->pv_done[b], (gt + i - 2) >> 1, abort, budget);
+                    for (int c = 0; c < NC && ok; ++c) {
+                        ok = warp_wait(&sh->full[stage], phase, abort, budget);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        if (ptx::elect_one()) {
+                            const uint32_t d = tmem + C::kSCol + b * kKeys;
+                            const uint64_t a = desc_q + (uint64_t)((c * kChunkBytes) >> 4);
+                            const uint64_t k = desc_k + (uint64_t)((stage * kChunkBytes) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                ptx::mma_bf16(d, a + 2 * kk, k + 2 * kk, idesc_s, c > 0 || kk > 0 ? 1u : 0u);
+                            ptx::mma_commit(&sh->empty[stage]);
+                            if (c == NC - 1) {
+                                ptx::mma_commit(&sh->s_full[b]);
+                                if (i == n - 1) ptx::mma_commit(&sh->q_empty);
+                            }
+                        }
+                        __syncwarp();
+                        any = true;
+                        next_stage();
+                    }
+                }
+                if (i > 0 && ok) {
+                    const long long t = gt + i - 1;
+                    const int b = (int)(t & 1);
+                    if (i == 1 && part > 0)
+                        ok = warp_wait(&sh->o_free, part - 1, abort, budget);
+                    ok = ok && warp_wait(&sh->p_ready[b], t >> 1, abort, budget);
+                    for (int c = 0; c < NC && ok; ++c) {
+                        ok = warp_wait(&sh->full[stage], phase, abort, budget);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        if (ptx::elect_one()) {
+                            const uint32_t pcol = tmem + C::kSCol + b * kKeys + c * (KV / 2);
+                            const uint64_t v = desc_v + (uint64_t)((stage * kChunkBytes) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < KV / 16; ++kk) {
+                                ptx::mma_bf16_ts(tmem + C::kOCol, pcol + 8 * kk, v + (uint64_t)(kk * 2048 >> 4), idesc_o,
+                                                 i > 1 || c > 0 || kk > 0 ? 1u : 0u);
+                                if (F32OUT)
+                                    ptx::mma_bf16_ts(tmem + C::kOCol, pcol + 64 + 8 * kk, v + (uint64_t)(kk * 2048 >> 4),
+                                                     idesc_o, 1u);
+                            }
+                            ptx::mma_commit(&sh->empty[stage]);
+                            if (c == NC - 1) ptx::mma_commit(&sh->pv_done[b]);
+                        }
+                        __syncwarp();
+                        next_stage();
+                    }
+                }
+            }
+            gt += n;
+        }
+        // Wait for every MMA issued here before tensor memory is released.
+        if (any) {
+            if (ptx::elect_one()) ptx::mma_commit(&sh->drain);
+            __syncwarp();
+            volatile int no_abort = 0;
+            ptx::mbar_wait_bounded(&sh->drain, 0u, &no_abort, budget);
+        }
+    } else if (warp >= kQWarp) {
+        // Q rows of each part, 16 bytes a lane; dims past the head's are zeros
+        // (K's are, and a zero times what lies there must stay zero).
+        constexpr int U = DP / 8, kPerPass = 64 / U;
+        const int me = threadIdx.x - 32 * kQWarp, u = me % U;
+        int part = 0;
+        bool ok = true;
+        for (; w.valid() && ok; w.next(), ++part) {
+            if (part > 0) ok = ptx::mbar_wait_bounded(&sh->q_empty, (uint32_t)(part - 1) & 1u, abort, budget);
+            if (!ok) break;
+            const int rows = w.tokens() * p.group;
+            const T* base = static_cast<const T*>(p.q) + (long long)(w.q.row0 + w.qt * p.tile_tokens) * p.q_token +
+                            (long long)w.head * p.group * p.q_head + 8 * u;
+            for (int r = me / U; r < rows; r += kPerPass) {
+                const int t = r / p.group, g = r - t * p.group;
+                unsigned char* dst = tile_q + (u >> 3) * kChunkBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+                if (8 * u < p.dim) ptx::cp_async16(dst, base + t * p.q_token + g * p.q_head);
+                else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+            }
+            ptx::cp_async_wait_all();
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(&sh->q_full);
+        }
+    } else {
+        // ---- softmax and epilogue: thread = row
+        const int r = threadIdx.x;
+        const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+        const float sl2 = fabsf(p.scale) * 1.4426950408889634f;
+        const bool negative = p.scale < 0.f;
+        const int my_token = r / p.group, my_head = r - my_token * p.group;
+        long long gt = 0, consumed = 0;  // tiles and ring chunks before this part
+        int part = 0, joined = 0;        // parts before this one, meetings of the four warps
+        long long item_start = start.ctas > (int)blockIdx.x ? cut(start.total, start.ctas, blockIdx.x) - start.skip : 0;
+        bool ok = true;
+        for (; w.valid() && ok; w.next(), ++part) {
+            const int n = w.j1 - w.j0;
+            const int tokens = w.tokens();
+            const bool valid = my_token < tokens;
+            const bool active = 32 * warp < tokens * p.group;  // the warp has a valid row
+            const int first = w.q.place0 + w.qt * p.tile_tokens;  // place of the first token
+            const int lim_first = p.causal ? min(max(first + 1, 0), w.q.len) : w.q.len;
+            const int lim = !valid ? w.end : p.causal ? min(max(first + my_token + 1, 0), w.q.len) : w.q.len;
+            float m = -INFINITY, base = -kShift<T>, sum = 0.f;
+            bool bad = false;
+            for (int i = 0; i < n && ok; ++i) {
+                const long long t = gt + i;
+                const int b = (int)(t & 1);
+                uint64_t* wbar = p.stall_test && t == 0 ? &sh->never : &sh->s_full[b];
+                ok = warp_wait(wbar, t >> 1, abort, budget);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const int key0 = (w.j0 + i) * kKeys;
+                const bool edge = key0 + kKeys > lim_first;  // some row does not see the whole tile
+                const uint32_t taddr = tmem + lane_base + C::kSCol + b * kKeys;
+                if (active) {
+                    float s[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) ptx::tmem_ld32(taddr + 32 * c, s[c]);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) ptx::tmem_landed(s[c]);
+                    if (negative) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) s[c][k] = -s[c][k];
+                    }
+                    const int see = lim - key0;  // keys of the tile that the row sees
+                    if (edge) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (32 * c + k >= see) s[c][k] = -INFINITY;
+                    }
+                    float top[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        top[c] = fmaxf(s[c][0], s[c][1]);
+#pragma unroll
+                        for (int k = 2; k < 32; k += 2) top[c] = fmaxf(top[c], fmaxf(s[c][k], s[c][k + 1]));
+                    }
+                    const float now = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                    const bool grow = now > m && (m == -INFINITY || (now - m) * sl2 > kLazy);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        float keep = 1.f;
+                        if (grow) {
+                            const float to = now * sl2 - kShift<T>;
+                            keep = m == -INFINITY ? 0.f : ptx::ex2(base - to);
+                            m = now;
+                            base = to;
+                            sum *= keep;
+                        }
+                        if (i > 0) {
+                            ok = warp_wait(&sh->pv_done[b ^ 1], (t - 1) >> 1, abort, budget);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            const float2 keep2 = make_float2(keep, keep);
+#pragma unroll 1
+                            for (int c = 0; c < DP; c += 32) {
+                                float o[32];
+                                uint32_t u[32];
+                                ptx::tmem_ld32(tmem + lane_base + C::kOCol + c, o);
+                                ptx::tmem_wait_ld();
+                                ptx::tmem_landed(o);
+#pragma unroll
+                                for (int k = 0; k < 32; k += 2) {
+                                    const float2 x = __fmul2_rn(make_float2(o[k], o[k + 1]), keep2);
+                                    u[k] = __float_as_uint(x.x);
+                                    u[k + 1] = __float_as_uint(x.y);
+                                }
+                                ptx::tmem_st32(tmem + lane_base + C::kOCol + c, u);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    const float2 mul = make_float2(sl2, sl2), sub = make_float2(-base, -base);
+                    float2 add0 = make_float2(0.f, 0.f), add1 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t hi[32], lo[32];
+#pragma unroll
+                        for (int k = 0; k < 64; k += 2) {
+                            const int c = 2 * h + (k >> 5), at = k & 31;
+                            const float2 x = __ffma2_rn(make_float2(s[c][at], s[c][at + 1]), mul, sub);
+                            float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+                            if (edge) {
+                                if (64 * h + k >= see) e.x = 0.f;
+                                if (64 * h + k + 1 >= see) e.y = 0.f;
+                            }
+                            if (k & 2) add1 = __fadd2_rn(add1, e);
+                            else add0 = __fadd2_rn(add0, e);
+                            hi[k / 2] = pack2<T>(e.x, e.y);
+                            if (F32OUT) {
+                                const float2 f = unpack2<T>(hi[k / 2]);
+                                lo[k / 2] = pack2<T>(e.x - f.x, e.y - f.y);
+                            }
+                        }
+                        ptx::tmem_st32(taddr + 32 * h, hi);
+                        if (F32OUT) ptx::tmem_st32(taddr + 64 + 32 * h, lo);
+                    }
+                    add0 = __fadd2_rn(add0, add1);
+                    sum += add0.x + add0.y;
+                }
+                if (edge) {
+                    // Values that some row does not see: those past the item's last
+                    // key become zeros (a weight of zero times what a free slot
+                    // holds must be zero), infinities and NaNs between the first
+                    // row's and the last row's last key too; the epilogue gives
+                    // them back to the rows that see them.
+                    const int lo = max(lim_first - key0, 0), hi = w.end - key0;
+                    const long long v0 = consumed + (long long)NC * (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
+#pragma unroll 1
+                    for (int c = lo / KV; c < NC && ok; ++c) {
+                        const int st = (int)((v0 + c) % NS);
+                        ok = warp_wait(&sh->full[st], (v0 + c) / NS, abort, budget);
+                        if (!ok) break;
+                        for (int row = max(lo - c * KV, 0) + (r >> 3); row < KV; row += 16) {
+                            uint4* at = reinterpret_cast<uint4*>(ring + st * kChunkBytes + row * 128 + (r & 7) * 16);
+#pragma unroll
+                            for (int d = 0; d < NC; ++d, at += KV * 8) {
+                                if (c * KV + row >= hi) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                } else {
+                                    uint4 x = *at;
+                                    bool any = clean<T>(x.x);
+                                    any |= clean<T>(x.y);
+                                    any |= clean<T>(x.z);
+                                    any |= clean<T>(x.w);
+                                    if (any) {
+                                        *at = x;
+                                        bad = true;
+                                    }
+                                }
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&sh->p_ready[b]);
+            }
+            if (!ok) break;
+            gt += n;
+            consumed += 2LL * NC * n;
+            // All four warps: was there an infinity or a NaN among the values of this part?
+            const bool edges = p.causal && w.j1 * kKeys > lim_first && lim_first < w.end;
+            if (edges) {
+                if (bad) sh->bad = part + 1;
+                ptx::mbar_arrive(&sh->join);
+                ok = warp_wait(&sh->join, joined++, abort, budget);
+                if (!ok) break;
+                bad = *(volatile int*)&sh->bad >= part + 1;  // (a later part's mark only costs a look)
+            }
+
+            // ---- epilogue
+            const bool whole = w.j0 == 0 && w.j1 == w.tiles;
+            const long long slot = 2LL * blockIdx.x + (w.j0 == 0 ? 1 : 0);
+            float* ws_o = p.ws_o + (slot * kRows + r) * DP;
+            ok = warp_wait(&sh->pv_done[(gt - 1) & 1], (gt - 1) >> 1, abort, budget);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const long long token = w.q.row0 + w.qt * p.tile_tokens + my_token;
+            const int head = w.head * p.group + my_head;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            if (active) {
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 32) {
+                    float o[32];
+                    ptx::tmem_ld32(tmem + lane_base + C::kOCol + c, o);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_landed(o);
+                    if (bad && edges && valid) {
+#pragma unroll 1
+                        for (int key = max(lim_first, w.j0 * kKeys); key < min(lim, w.j1 * kKeys); ++key) {
+                            const int at = key / p.page_size;
+                            const int page = p.batch.table[w.seq * p.batch.table_stride + at];
+                            if (page < 0 || page >= p.pages) continue;
+                            const T* v = static_cast<const T*>(p.v_pool) + page * p.page_stride +
+                                         (key - at * p.page_size) * p.slot_stride + w.head * p.head_stride;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const float x = c + k < p.dim ? to_f32(v[c + k]) : 0.f;
+                                if (!isfinite(x)) o[k] += x;
+                            }
+                        }
+                    }
+                    if (!valid) {
+                    } else if (!whole) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            __stcg(reinterpret_cast<float4*>(ws_o + c + k),
+                                   make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
+                    } else if (F32OUT) {
+                        float* out = static_cast<float*>(p.out) + token * p.out_token + head * p.out_head + c;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            if (c + k < p.dim)
+                                *reinterpret_cast<float4*>(out + k) =
+                                    make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
+                    } else {
+                        T* out = static_cast<T*>(p.out) + token * p.out_token + head * p.out_head + c;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8)
+                            if (c + k < p.dim)
+                                *reinterpret_cast<uint4*>(out + k) =
+                                    make_uint4(pack2<T>(o[k] * inv, o[k + 1] * inv), pack2<T>(o[k + 2] * inv, o[k + 3] * inv),
+                                               pack2<T>(o[k + 4] * inv, o[k + 5] * inv), pack2<T>(o[k + 6] * inv, o[k + 7] * inv));
+                    }
+                    __syncwarp();
+                }
+            }
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&sh->o_free);
+            if (whole) {
+                if (valid && p.lse)
+                    p.lse[token * p.heads + head] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (base + log2f(sum));
+                item_start += w.tiles;
+                continue;
+            }
+
+            // ---- a part of an item: the last one to arrive joins them
+            if (valid) __stcg(reinterpret_cast<float2*>(p.ws_ml) + slot * kRows + r, make_float2(sum == 0.f ? -INFINITY : base, sum));
+            const int from = cta_of(start.total, start.ctas, item_start);
+            const int to = cta_of(start.total, start.ctas, item_start + w.tiles - 1);
+            __threadfence();
+            ptx::mbar_arrive(&sh->join);
+            ok = warp_wait(&sh->join, joined++, abort, budget);
+            if (!ok) break;
+            if (r == 0) {
+                const int before = atomicAdd(&p.tickets[from], 1);
+                sh->last = before == to - from;
+                if (sh->last) p.tickets[from] = 0;
+            }
+            ptx::mbar_arrive(&sh->join);
+            ok = warp_wait(&sh->join, joined++, abort, budget);
+            if (!ok) break;
+            if (*(volatile int*)&sh->last) {
+                __threadfence();
+                const int rows = tokens * p.group;
+                for (int row = warp; row < rows; row += 4) {
+                    // the first part lies in its CTA's second slot, the others in their first
+                    auto slot_of = [&](int c) { return ((2LL * c + (c == from ? 1 : 0)) * kRows + row); };
+                    float top = -INFINITY;
+                    for (int c = from + lane; c <= to; c += 32)
+                        top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot_of(c)).x);
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    float total = 0.f, acc[DP / 32] = {};
+                    for (int c0 = from; c0 <= to; c0 += 32) {
+                        float wgt = 0.f, part = 0.f;
+                        if (c0 + lane <= to) {
+                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot_of(c0 + lane));
+                            wgt = ml.y == 0.f ? 0.f : ptx::ex2(ml.x - ref);
+                            part = wgt * ml.y;
+                        }
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+                        total += part;
+                        const int parts = min(32, to - c0 + 1);
+#pragma unroll 8
+                        for (int k = 0; k < parts; ++k) {
+                            const float x = __shfl_sync(0xffffffffu, wgt, k);
+                            const float* o = p.ws_o + slot_of(c0 + k) * DP + lane;
+                            // a part without a key (weight 0) adds nothing, whatever it holds
+                            if (x != 0.f) {
+#pragma unroll
+                                for (int d = 0; d < DP / 32; ++d) acc[d] += x * __ldcg(o + 32 * d);
+                            }
+                        }
+                    }
+                    const int t = row / p.group, g = row - t * p.group;
+                    const long long tok = w.q.row0 + w.qt * p.tile_tokens + t;
+                    const int hd = w.head * p.group + g;
+                    const float scale = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+                    for (int d = 0; d < DP / 32; ++d) {
+                        if (lane + 32 * d >= p.dim) continue;
+                        const long long at = tok * p.out_token + hd * p.out_head + lane + 32 * d;
+                        if (F32OUT) static_cast<float*>(p.out)[at] = acc[d] * scale;
+                        else static_cast<T*>(p.out)[at] = from_f32<T>(acc[d] * scale);
+                    }
+                    if (p.lse && lane == 0)
+                        p.lse[tok * p.heads + hd] = total == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(total));
+                }
+            }
+            item_start += w.tiles;
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (threadIdx.x == 0 && sh->abort) p.dev_error[kKvErrTimeout] = 1;
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int DP, typename T, bool F32OUT>
+cudaError_t launch(const AttendParams& p, const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s)
+{
+    static PerDeviceOnce once;
+    int dev = 0;
+    cudaError_t e = once.run(&dev, [](int) {
+        return cudaFuncSetAttribute(bitlin_attend<DP, T, F32OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<DP>();
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, bitlin_attend<DP, T, F32OUT>, *static_cast<const CUtensorMap*>(tmap_k),
+                              *static_cast<const CUtensorMap*>(tmap_v), p);
+}
+
+template <typename T, bool F32OUT>
+cudaError_t pick_dim(const AttendParams& p, const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s)
+{
+    if (p.dim <= 64) return launch<64, T, F32OUT>(p, tmap_k, tmap_v, num_sms, s);
+    if (p.dim <= 128) return launch<128, T, F32OUT>(p, tmap_k, tmap_v, num_sms, s);
+    return launch<256, T, F32OUT>(p, tmap_k, tmap_v, num_sms, s);
+}
+
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 }  // namespace
 
-cudaError_t bitlin_launch_attend(const AttendParams& p, int dtype, int out_dtype, cudaStream_t s)
+void bitlin_attend_boxes(int dim, int page_size, int* box_k, int* box_v)
 {
+    const int padded = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
+    *box_k = gcd(page_size, kKeys);
+    *box_v = gcd(page_size, 8192 / padded);
+}
+
+size_t bitlin_attend_workspace(int dim, int num_sms, size_t* ml_offset, size_t* ticket_offset)
+{
+    const size_t padded = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
+    const size_t rows = (size_t)2 * num_sms * kRows;
+    *ml_offset = rows * padded * sizeof(float);
+    *ticket_offset = *ml_offset + rows * 2 * sizeof(float);
+    return *ticket_offset + num_sms * sizeof(int);
+}
+
+cudaError_t bitlin_launch_attend(const AttendParams& p, int dtype, int out_dtype, const void* tmap_k,
+                                 const void* tmap_v, int num_sms, cudaStream_t s)
+{
+    const bool f32 = out_dtype == BITLIN_F32;
     if (dtype == BITLIN_BF16)
-        return out_dtype == BITLIN_F32 ? launch<__nv_bfloat16, float>(p, s) : launch<__nv_bfloat16, __nv_bfloat16>(p, s);
-    return out_dtype == BITLIN_F32 ? launch<__half, float>(p, s) : launch<__half, __half>(p, s);
+        return f32 ? pick_dim<__nv_bfloat16, true>(p, tmap_k, tmap_v, num_sms, s)
+                   : pick_dim<__nv_bfloat16, false>(p, tmap_k, tmap_v, num_sms, s);
+    return f32 ? pick_dim<__half, true>(p, tmap_k, tmap_v, num_sms, s)
+               : pick_dim<__half, false>(p, tmap_k, tmap_v, num_sms, s);
 }

@@ -2,15 +2,19 @@
 #include <cuda_runtime.h>
 
 #include <math.h>
+#include <stdlib.h>
 
 #include <memory>
 #include <new>
 
 #include "kv_internal.cuh"
+#include "tensormap.cuh"
 
 using namespace bitlin_impl;
 
 namespace {
+
+constexpr long long kDefaultWaitBudgetNs = 2000000000LL;  // 2 s per bounded wait
 
 bitlin_status status_of(cudaError_t e)
 {
@@ -89,6 +93,23 @@ void set_out(TurnParams& p, const bitlin_rows* r)
     p.out = r->data;
     p.out_token = r->token_stride;
     p.out_head = r->head_stride;
+}
+
+// A pool seen as [page][head][slot][dim], copied `box` slots x 64 dims of one
+// head at a time (128-byte swizzle; dims past the head's read as zeros).
+cudaError_t encode_pool(const bitlin_kv& h, void* pool, int box, unsigned char* tmap)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = bitlin_tensormap_encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    cuuint64_t dims[4] = {(cuuint64_t)h.dim, (cuuint64_t)h.page_size, (cuuint64_t)h.kv_heads, (cuuint64_t)h.pages};
+    cuuint64_t strides[3] = {(cuuint64_t)h.slot_stride * 2, (cuuint64_t)h.head_stride * 2, (cuuint64_t)h.page_stride * 2};
+    cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(reinterpret_cast<CUtensorMap*>(tmap),
+                     h.dtype == BITLIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, pool,
+                     dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -188,7 +209,16 @@ bitlin_status bitlin_kv_create(bitlin_kv_t* out, void* k, void* v, int pages, in
     h->page_stride = page_stride;
     h->slot_stride = slot_stride;
     h->head_stride = head_stride;
+    h->wait_budget_ns = kDefaultWaitBudgetNs;
+    if (const char* env = getenv("BITLIN_WAIT_BUDGET_NS")) {
+        const long long ns = atoll(env);
+        if (ns > 0) h->wait_budget_ns = ns;
+    }
+    int box_k = 0, box_v = 0;
+    bitlin_attend_boxes(head_dim, page_size, &box_k, &box_v);
     cudaError_t e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = encode_pool(*h, k, box_k, h->tmap_k);
+    if (e == cudaSuccess) e = encode_pool(*h, v, box_v, h->tmap_v);
     if (e == cudaSuccess) e = cudaMalloc(&h->dev_error, 2 * sizeof(int));
     if (e == cudaSuccess) e = cudaMemset(h->dev_error, 0, 2 * sizeof(int));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
@@ -246,11 +276,23 @@ bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
     if (!on_device(kv->device)) return BITLIN_EINVAL;
     if (kv->sticky != BITLIN_OK) return kv->sticky;
     if (tokens == 0) return BITLIN_OK;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    size_t ml = 0, tickets = 0;
+    const size_t bytes = bitlin_attend_workspace(kv->dim, kv->num_sms, &ml, &tickets);
+    if (!kv->workspace) {
+        cudaError_t e = cudaMalloc(&kv->workspace, bytes);
+        // zeroed in stream order: the kernel sees zero tickets
+        if (e == cudaSuccess) e = cudaMemsetAsync(kv->workspace + tickets, 0, bytes - tickets, st);
+        if (e != cudaSuccess) {
+            cudaFree(kv->workspace);
+            kv->workspace = nullptr;
+            return from_cuda(kv, e);
+        }
+    }
     AttendParams p = {};
     p.q = q->data;
     p.q_token = q->token_stride;
     p.q_head = q->head_stride;
-    p.k_pool = kv->k;
     p.v_pool = kv->v;
     p.page_stride = kv->page_stride;
     p.slot_stride = kv->slot_stride;
@@ -260,16 +302,38 @@ bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
     p.out_token = out->token_stride;
     p.out_head = out->head_stride;
     p.lse = lse;
+    p.ws_o = reinterpret_cast<float*>(kv->workspace);
+    p.ws_ml = reinterpret_cast<float*>(kv->workspace + ml);
+    p.tickets = reinterpret_cast<int*>(kv->workspace + tickets);
     p.dev_error = kv->dev_error;
+    p.wait_budget_ns = kv->wait_budget_ns;
     p.pages = kv->pages;
     p.page_size = kv->page_size;
     p.tokens = tokens;
     p.heads = heads;
     p.kv_heads = kv->kv_heads;
+    p.group = heads / kv->kv_heads;
     p.dim = kv->dim;
     p.causal = causal;
+    p.tile_tokens = 128 / p.group;
+    bitlin_attend_boxes(kv->dim, kv->page_size, &p.box_k, &p.box_v);
+    p.stall_test = kv->stall_test;
     p.scale = scale;
-    return from_cuda(kv, bitlin_launch_attend(p, kv->dtype, out->dtype, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(kv, bitlin_launch_attend(p, kv->dtype, out->dtype, kv->tmap_k, kv->tmap_v, kv->num_sms, st));
+}
+
+bitlin_status bitlin_kv_set_wait_budget(bitlin_kv_t kv, long long ns)
+{
+    if (!kv || ns <= 0) return BITLIN_EINVAL;
+    kv->wait_budget_ns = ns;
+    return BITLIN_OK;
+}
+
+bitlin_status bitlin_kv_test_stall(bitlin_kv_t kv, int on)
+{
+    if (!kv) return BITLIN_EINVAL;
+    kv->stall_test = on ? 1 : 0;
+    return BITLIN_OK;
 }
 
 bitlin_status bitlin_kv_get_error(bitlin_kv_t kv)
@@ -292,6 +356,7 @@ bitlin_status bitlin_kv_destroy(bitlin_kv_t kv)
     if (!kv) return BITLIN_OK;
     cudaError_t e = cudaDeviceSynchronize();
     cudaFree(kv->dev_error);
+    cudaFree(kv->workspace);
     delete kv;
     return e == cudaSuccess ? BITLIN_OK : BITLIN_ECUDA;
 }

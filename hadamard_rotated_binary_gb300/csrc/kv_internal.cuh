@@ -85,20 +85,26 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// One call of the attention kernels.
+// One call of the attention kernel.
 struct AttendParams {
     const void* q;
     long long q_token, q_head;
-    const void* k_pool;
-    const void* v_pool;
+    const void* v_pool;        // for the rare values that are put back (see attend.cu)
     long long page_stride, slot_stride, head_stride;
     KvBatch batch;
     void* out;
     long long out_token, out_head;
     float* lse;                // [tokens][heads] or nullptr
+    float* ws_o;               // [2 * CTAs][128][padded dim]: unnormalised parts of outputs
+    float* ws_ml;              // [2 * CTAs][128][2]: their rows' log2 maxima and sums
+    int* tickets;              // [CTAs], zero between calls
     int* dev_error;
+    long long wait_budget_ns;
     int pages, page_size;
-    int tokens, heads, kv_heads, dim, causal;
+    int tokens, heads, kv_heads, group, dim, causal;
+    int tile_tokens;           // tokens of a 128-row tile: 128 / group
+    int box_k, box_v;          // slots of a page per TMA copy
+    int stall_test;
     float scale;
 };
 
@@ -120,8 +126,19 @@ struct bitlin_kv {
     int last_cuda_error = 0;
     bitlin_status sticky = BITLIN_OK;
     int* dev_error = nullptr;  // [2]: kKvErr*
+    long long wait_budget_ns = 0;
+    int stall_test = 0;
+    alignas(64) unsigned char tmap_k[128];  // TMA descriptors of the pools (CUtensorMaps)
+    alignas(64) unsigned char tmap_v[128];
+    // attention's workspace, allocated by the first call
+    unsigned char* workspace = nullptr;
 };
 
 // Launchers (return a cudaError_t).
 cudaError_t bitlin_launch_turn(const bitlin_impl::TurnParams& p, int src_dtype, int dst_dtype, cudaStream_t s);
-cudaError_t bitlin_launch_attend(const bitlin_impl::AttendParams& p, int dtype, int out_dtype, cudaStream_t s);
+cudaError_t bitlin_launch_attend(const bitlin_impl::AttendParams& p, int dtype, int out_dtype, const void* tmap_k,
+                                 const void* tmap_v, int num_sms, cudaStream_t s);
+// Slots per TMA copy of the key and value pools.
+void bitlin_attend_boxes(int dim, int page_size, int* box_k, int* box_v);
+// Bytes of the attention workspace, and where its parts begin (the outputs at 0).
+size_t bitlin_attend_workspace(int dim, int num_sms, size_t* ml_offset, size_t* ticket_offset);

@@ -471,14 +471,16 @@ bitlin_status bitlin_kv_append(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
  *          8; the cache's type, or BITLIN_F32 (what bitlin_forward reads).
  *          For a 16-bit out the probabilities are rounded to the cache's type
  *          before they meet the values; for an f32 out each is split into two
- *          digits of that type, which keeps f32-level results.
+ *          digits of that type, which keeps f32-level results (an infinite
+ *          value may come out of them as NaN).
  *   lse    device pointer, float [tokens][heads], or NULL.
  *
  * Sums, the softmax's statistics and the output accumulate in f32.  Requires
  * heads % kv_heads == 0, heads / kv_heads <= 128.  kv_lens past the table's
  * row are cut to it, and pages outside [0, pages) read as zeros; both make the
  * next bitlin_kv_get_error return BITLIN_EINDEX.  Asynchronous; the first
- * call with a new largest size allocates workspace that the handle keeps.
+ * call allocates workspace that the handle keeps (40 MB at head_dim 256), so
+ * make it before a stream capture.
  * Calls on one handle share it: use one stream at a time.
  * Errors: BITLIN_EINVAL, BITLIN_ENOMEM, BITLIN_ECUDA, the handle's sticky
  * error.
@@ -486,6 +488,11 @@ bitlin_status bitlin_kv_append(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
 bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q,
                                int heads, float scale, int causal, const bitlin_rows* out, float* lse,
                                bitlin_stream_t stream);
+
+/* As bitlin_set_wait_budget and bitlin_test_stall, for the attention kernel's
+ * waits (default 2e9 ns, or BITLIN_WAIT_BUDGET_NS at create). */
+bitlin_status bitlin_kv_set_wait_budget(bitlin_kv_t kv, long long ns);
+bitlin_status bitlin_kv_test_stall(bitlin_kv_t kv, int on);
 
 /* As bitlin_get_error, for a cache handle: BITLIN_ETIMEOUT (sticky),
  * BITLIN_EINDEX (once, then cleared) or BITLIN_ECUDA.  Synchronizes. */

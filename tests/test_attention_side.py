@@ -512,6 +512,50 @@ def test_attend_infinite_scores_and_values(hrb):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_attend_later_tokens_do_not_reach_earlier_rows(hrb, dtype):
+    """An infinity or a NaN in a token's key or value reaches that token's rows and the later ones alone."""
+    lens, new = [300], [90]
+    batch, offsets, kp, vp, q = attend_case(hrb, 128, 16, 1, 2, new, lens, dtype, 21)
+    cache = hrb.PagedKV(kp, vp)
+    place = 240  # token row 30
+    where = int(batch.table[0, place // 16]), place % 16
+    value, key = vp[where[0], where[1], 0].clone(), kp[where[0], where[1], 0].clone()
+    for out_dtype in (dtype, torch.float32):
+        vp[where[0], where[1], 0], kp[where[0], where[1], 0] = value, key
+        clean = cache.attend(q, batch, dtype=out_dtype)
+        vp[where[0], where[1], 0, 3] = math.inf
+        vp[where[0], where[1], 0, 77] = math.nan
+        got = cache.attend(q, batch, dtype=out_dtype)
+        assert torch.equal(got[:30], clean[:30])
+        assert bool(torch.isnan(got[30:, :, 77]).all())
+        # two digits of a weight may multiply an infinity with opposite signs: not a number then
+        assert not bool(torch.isfinite(got[30:, :, 3]).any())
+        assert out_dtype == torch.float32 or bool((got[30:, :, 3] == math.inf).all())
+        rest = [d for d in range(128) if d not in (3, 77)]
+        assert torch.equal(got[30:][..., rest], clean[30:][..., rest])
+        kp[where[0], where[1], 0, 9] = math.nan
+        got = cache.attend(q, batch, dtype=out_dtype)
+        assert torch.equal(got[:30], clean[:30]) and bool(torch.isnan(got[30:]).all())
+
+
+@gpu
+def test_attend_wait_that_runs_out(hrb):
+    """A barrier that nothing arrives at: the kernel gives up, the status is sticky, the context stays usable."""
+    batch, offsets, kp, vp, q = attend_case(hrb, 128, 16, 2, 4, [40, 1], [300, 20], torch.bfloat16, 22)
+    cache = hrb.PagedKV(kp, vp)
+    want = cache.attend(q, batch)
+    assert cache.get_error() == 0
+    cache.set_wait_budget(2_000_000)
+    cache.test_stall(True)
+    cache.attend(q, batch)
+    assert cache.get_error() == hrb.BITLIN_ETIMEOUT
+    with pytest.raises(hrb.BitlinError):
+        cache.attend(q, batch)
+    assert torch.equal(hrb.PagedKV(kp, vp).attend(q, batch), want)
+
+
+@gpu
 def test_attend_long_ragged_batch_matches_its_parts(hrb):
     """Work split over the keys and joined: a long sequence beside short ones, against each alone."""
     lens, new = [9000, 3, 2500, 129, 1], [1, 3, 130, 2, 1]
@@ -657,6 +701,7 @@ def test_refusals_without_device(hrb):
     assert L.bitlin_kv_append(None, b, 1, None, None, r, r, None, 0, None, None) == E
     assert L.bitlin_kv_attend(None, b, 1, r, 1, 1.0, 1, r, None, None) == E
     assert L.bitlin_kv_get_error(None) == E
+    assert L.bitlin_kv_set_wait_budget(None, 1) == E and L.bitlin_kv_test_stall(None, 1) == E
     assert L.bitlin_kv_cuda_error(None) == 0
     assert L.bitlin_kv_destroy(None) == 0 and L.bitlin_rope_destroy(None) == 0
 
