@@ -19,18 +19,26 @@
 // item's CTAs to do so joins the parts in their order (results do not depend
 // on which one is last).
 //
-// Roles of the 8 warps:
-//   0-3  softmax: S from tensor memory, running maximum and sum, the weights P
-//        back over S as the A operand of P V; the item's epilogue;
-//   4    TMA: K and V pages through one ring of 16 KB chunks, in the order the
-//        MMAs use them (K0, K1, V0, K2, V1, ...); a chunk is 128 keys x 64
-//        dims of K or 8192 / DP keys x DP dims of V, page by page;
-//   5    MMA issue: S tiles alternate between two buffers, so Q K^T of the
-//        next tile runs while the softmax works on this one;
-//   6-7  Q of the next item (plain copies: rows of any stride).
+// Roles of the 16 warps:
+//   0-7   softmax, two warps to 32 rows (each takes half of the columns): S from
+//         tensor memory, running maximum and sum, the weights P back over S as
+//         the A operand of P V; the item's epilogue;
+//   8-11  TMA: K and V pages through one ring of 16 KB chunks, in the order the
+//         MMAs use them (K0, K1, V0, K2, V1, ...); a chunk is 128 keys x 64 dims
+//         of K or 8192 / DP keys x DP dims of V, page by page.  One warp's copies
+//         run one after the other at about 40 B a clock, whatever their boxes
+//         (measured: 31 B with 64-slot boxes, 62 from two warps, 91 from four,
+//         where L2 is the limit), and the tensor cores eat 64 B a clock at DP =
+//         256: four warps take the chunks in turn;
+//   12    MMA issue: S tiles alternate between two buffers, so Q K^T of the next
+//         tile runs while the softmax works on this one;
+//   13-15 Q of the next item (plain copies: rows of any stride).
 // The output stays in tensor memory; it is rescaled only when a row's maximum
 // grows by more than 2^8 (until then the weights are relative to the older
-// maximum, which f32 sums and the 16-bit weights' exponents hold).
+// maximum, which f32 sums and the 16-bit weights' exponents hold).  The tensor
+// cores' f32 additions truncate (measured: 2.1e-8 of the output lost per
+// addition), so every kDrain tiles it is added, rounded to nearest, to an f32
+// copy in the workspace and starts again from zero.
 #include <cuda.h>
 #include <math.h>
 
@@ -43,12 +51,22 @@ namespace {
 
 constexpr int kRows = 128;        // rows of a tile (UMMA M)
 constexpr int kKeys = 128;        // keys of a tile
-constexpr int kThreads = 256;
-constexpr int kTmaWarp = 4, kMmaWarp = 5, kQWarp = 6;
+constexpr int kThreads = 512;
+constexpr int kSoftmax = 256;     // threads of the softmax warps
+constexpr int kTmaWarp = 8, kTmaWarps = 4, kMmaWarp = 12, kQWarp = 13;
+constexpr int kQThreads = 96;
+// Registers a thread: launched with 128, the two softmax warpgroups take what
+// the other two give (2 * 168 + 2 * 88 = 4 * 128).
+constexpr int kManyRegs = 168, kFewRegs = 88;
 constexpr int kChunkBytes = 16384;
 constexpr int kTmemCols = 512;
 constexpr float kLazy = 8.f;      // log2 of the growth that a rescale waits for
 constexpr int kMaxLen = 1 << 30;
+// Tiles that accumulate in tensor memory before the output is drained: 16
+// additions a tile for an f32 output (2.7e-6 lost at 8 tiles), 8 for a 16-bit
+// one (4e-5, a hundredth of bf16's rounding).
+template <bool F32OUT>
+constexpr int kDrain = F32OUT ? 8 : 256;
 
 template <int DP>
 struct Cfg {
@@ -59,12 +77,22 @@ struct Cfg {
     static constexpr int kOCol = 0, kSCol = 256;          // tensor memory: output, two S buffers
 };
 
+// A sequence's rows and keys, with every index brought into range.
+struct Seq {
+    int row0, rows;   // token rows of the call
+    int place0;       // place of the first
+    int len;          // keys held
+    int tiles;        // row tiles
+};
+
 // The part of the line that a CTA starts with.
 struct Start {
-    long long total;   // tiles of all items
+    long long per;     // tiles of each CTA's part; the first `extra` have one more
+    int extra;
     int ctas;          // CTAs that have work
     int seq, head, qt; // item
     int skip;          // its tiles that belong to earlier CTAs
+    Seq q;             // its sequence
 };
 
 template <int DP>
@@ -73,30 +101,26 @@ struct __align__(8) Shared {
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_ready[2], pv_done[2];
     uint64_t o_free;
-    uint64_t join;    // the four softmax warps meet (a bounded wait, unlike a named barrier)
+    uint64_t pair[4];  // the two softmax warps of 32 rows meet (a bounded wait, unlike a named barrier)
+    uint64_t join;     // all softmax warps meet
     uint64_t never, drain;
     Start start;
     uint32_t tmem_base;
     int last;         // this CTA joins the item's parts
     int bad;          // 1 + the part whose values held an infinity or a NaN
+    float row[2][2][kRows];  // what the two warps of a row tell each other
     int abort;
 };
 
 template <int DP>
 constexpr int smem_bytes()
 {
-    return Cfg<DP>::kQBytes + Cfg<DP>::kStages * kChunkBytes + (int)sizeof(Shared<DP>) + 1024;
+    constexpr int bytes = Cfg<DP>::kQBytes + Cfg<DP>::kStages * kChunkBytes + (int)sizeof(Shared<DP>);
+    static_assert(bytes <= 227 * 1024, "shared memory of an SM");
+    return bytes;
 }
 
 // ---- the line of tiles ------------------------------------------------------
-
-// A sequence's rows and keys, with every index brought into range.
-struct Seq {
-    int row0, rows;   // token rows of the call
-    int place0;       // place of the first
-    int len;          // keys held
-    int tiles;        // row tiles
-};
 
 __device__ __forceinline__ Seq load_seq(const AttendParams& p, int s)
 {
@@ -160,11 +184,17 @@ __device__ __forceinline__ long long seq_tiles(const AttendParams& p, int base, 
     return sum;
 }
 
-__device__ __forceinline__ long long cut(long long total, int ctas, int c) { return total * c / ctas; }
-// The CTA whose part holds tile x.
-__device__ __forceinline__ int cta_of(long long total, int ctas, long long x)
+// x / n for n > 0; the sizes at hand nearly always fit 32 bits.
+__device__ __forceinline__ long long divide(long long x, long long n)
 {
-    return (int)(((x + 1) * ctas - 1) / total);
+    return ((x | n) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)n) : x / n;
+}
+// First tile of CTA c's part of the line, and the CTA whose part holds tile x.
+__device__ __forceinline__ long long cut(const Start& s, int c) { return s.per * c + min(c, s.extra); }
+__device__ __forceinline__ int cta_of(const Start& s, long long x)
+{
+    const long long longer = s.extra * (s.per + 1);
+    return x < longer ? (int)divide(x, s.per + 1) : s.extra + (int)divide(x - longer, s.per);
 }
 
 // One warp: where this CTA's part of the line begins.
@@ -172,21 +202,24 @@ __device__ void locate(const AttendParams& p, Start* out)
 {
     const int lane = threadIdx.x & 31;
     Seq q;
-    long long total = 0;
+    long long total = 0, one = 0;
     for (int base = 0; base < p.batch.seqs; base += 32) {
-        long long n = seq_tiles(p, base, q) * p.kv_heads;
+        one = seq_tiles(p, base, q);
+        long long n = one * p.kv_heads;
 #pragma unroll
         for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
         total += n;
     }
     Start st = {};
-    st.total = total;
     st.ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
     if ((int)blockIdx.x < st.ctas) {
-        const long long x = cut(total, st.ctas, blockIdx.x);
+        st.per = divide(total, st.ctas);
+        st.extra = (int)(total - st.per * st.ctas);
+        const long long x = cut(st, blockIdx.x);
         long long before = 0;
         for (int base = 0; base < p.batch.seqs; base += 32) {
-            const long long one = seq_tiles(p, base, q), all = one * p.kv_heads;
+            if (p.batch.seqs > 32) one = seq_tiles(p, base, q);
+            const long long all = one * p.kv_heads;
             const long long upto = before + warp_scan(all);
             const unsigned past = __ballot_sync(0xffffffffu, upto > x);
             if (past) {
@@ -194,12 +227,16 @@ __device__ void locate(const AttendParams& p, Start* out)
                 const long long per = __shfl_sync(0xffffffffu, one, l);
                 long long off = x - __shfl_sync(0xffffffffu, upto - all, l);
                 st.seq = base + l;
-                st.head = (int)(off / per);
+                st.head = (int)divide(off, per);
                 off -= st.head * per;
-                const int rows = __shfl_sync(0xffffffffu, q.rows, l), place0 = __shfl_sync(0xffffffffu, q.place0, l);
-                const int len = __shfl_sync(0xffffffffu, q.len, l), tiles = __shfl_sync(0xffffffffu, q.tiles, l);
-                for (int qb = 0; qb < tiles; qb += 32) {
-                    const int n = qb + lane < tiles ? item_tiles(p, rows, place0, len, qb + lane) : 0;
+                st.q.row0 = __shfl_sync(0xffffffffu, q.row0, l);
+                st.q.rows = __shfl_sync(0xffffffffu, q.rows, l);
+                st.q.place0 = __shfl_sync(0xffffffffu, q.place0, l);
+                st.q.len = __shfl_sync(0xffffffffu, q.len, l);
+                st.q.tiles = __shfl_sync(0xffffffffu, q.tiles, l);
+                for (int qb = 0; qb < st.q.tiles; qb += 32) {
+                    const int n = qb + lane < st.q.tiles
+                                      ? item_tiles(p, st.q.rows, st.q.place0, st.q.len, qb + lane) : 0;
                     const long long to = warp_scan((long long)n);
                     const unsigned hit = __ballot_sync(0xffffffffu, to > off);
                     if (hit) {
@@ -232,8 +269,8 @@ struct Walk {
         left = 0;
         j0 = j1 = 0;
         if ((int)blockIdx.x < s.ctas) {
-            left = cut(s.total, s.ctas, blockIdx.x + 1) - cut(s.total, s.ctas, blockIdx.x);
-            q = load_seq(p, seq);
+            left = s.per + ((int)blockIdx.x < s.extra ? 1 : 0);
+            q = s.q;
             set(s.skip);
         }
     }
@@ -268,9 +305,19 @@ struct Walk {
 };
 
 // A whole warp waits; true when every lane saw the phase complete.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, long long phase, volatile int* abort, long long budget)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, volatile int* abort, long long budget)
 {
     return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, (uint32_t)phase & 1u, abort, budget));
+}
+
+// Page of a sequence and slot in it that hold key `key`.
+__device__ __forceinline__ int page_at(const AttendParams& p, int key)
+{
+    return p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+}
+__device__ __forceinline__ int slot_at(const AttendParams& p, int key)
+{
+    return p.page_shift >= 0 ? key & (p.page_size - 1) : key % p.page_size;
 }
 
 // ---- weights ----------------------------------------------------------------
@@ -339,9 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int NC = C::NC, NS = C::kStages, KV = C::KV;
     constexpr bool kBf16 = sizeof(T) == 2 && kExpBits<T> == 0x7F80u;
 
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem = reinterpret_cast<unsigned char*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) unsigned char smem[];  // (the swizzle's atoms are 1024 bytes)
     unsigned char* tile_q = smem;                // [NC][128 rows][64], 128-byte swizzle
     unsigned char* ring = smem + C::kQBytes;     // [NS][16 KB]
     auto* sh = reinterpret_cast<Shared<DP>*>(ring + NS * kChunkBytes);
@@ -354,15 +399,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&sh->full[i], 1);
             ptx::mbar_init(&sh->empty[i], 1);
         }
-        ptx::mbar_init(&sh->q_full, 64);
+        ptx::mbar_init(&sh->q_full, kQThreads);
         ptx::mbar_init(&sh->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sh->s_full[i], 1);
-            ptx::mbar_init(&sh->p_ready[i], kRows);
+            ptx::mbar_init(&sh->p_ready[i], kSoftmax);
             ptx::mbar_init(&sh->pv_done[i], 1);
         }
-        ptx::mbar_init(&sh->o_free, kRows);
-        ptx::mbar_init(&sh->join, kRows);
+        ptx::mbar_init(&sh->o_free, kSoftmax);
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(&sh->pair[i], 64);
+        ptx::mbar_init(&sh->join, kSoftmax);
         ptx::mbar_init(&sh->never, 1);
         ptx::mbar_init(&sh->drain, 1);
         sh->abort = 0;
@@ -383,20 +429,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     ptx::griddep_launch_dependents();
     const uint32_t tmem = sh->tmem_base;
-    const Start start = sh->start;
-    Walk w(p, start);
+    const Start& start = sh->start;
 
-    if (warp == kTmaWarp) {
+    if (warp >= kTmaWarp && warp < kTmaWarp + kTmaWarps) {
+        ptx::give_registers<kFewRegs>();
+        Walk w(p, start);
+        const int mine = warp - kTmaWarp;
         int stage = 0;
         uint32_t phase = 0;
-        long long issued = 0;
+        int issued = 0;
         bool ok = true;
         // Lane l holds the page of keys 8l .. 8l+7 of a tile.
         auto page_of = [&](int j) {
             const int key = j * kKeys + 8 * lane;
             int page = -1;
             if (lane < kKeys / 8 && key < w.end) {
-                page = p.batch.table[w.seq * p.batch.table_stride + key / p.page_size];
+                page = p.batch.table[w.seq * p.batch.table_stride + page_at(p, key)];
                 if (page < 0 || page >= p.pages) {  // outside the pool: the copy fills zeros
                     p.dev_error[kKvErrIndex] = 1;
                     page = -1;
@@ -421,8 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int boxes = keys > 0 ? (keys + p.box_k - 1) / p.box_k : 0;
                     const int at = min(lane * p.box_k, kKeys - 8);
                     const int page = __shfl_sync(0xffffffffu, page_k, at >> 3);
-                    const int slot = (j * kKeys + at) % p.page_size;
-                    for (int c = 0; c < NC; ++c) {
+                    const int slot = slot_at(p, j * kKeys + at);
+                    for (int c = 0; c < NC; ++c, next_stage()) {
+                        if ((issued & (kTmaWarps - 1)) != mine) continue;
                         ok = warp_wait(&sh->empty[stage], phase ^ 1u, abort, budget);
                         if (!ok) break;
                         unsigned char* dst = ring + stage * kChunkBytes;
@@ -434,19 +483,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane < boxes)
                             ptx::tma_load_4d(dst + lane * p.box_k * 128, &tmap_k, 64 * c, slot, w.head, page,
                                              &sh->full[stage]);
-                        next_stage();
                     }
                 }
                 if (j > w.j0 && ok) {
                     // V tile j - 1: NC chunks of KV keys x DP dims, as [dims / 64][KV][64]
                     const int box = lane / NC, dims = lane % NC;
-                    for (int c = 0; c < NC; ++c) {
+                    for (int c = 0; c < NC; ++c, next_stage()) {
+                        if ((issued & (kTmaWarps - 1)) != mine) continue;
                         const int key = (j - 1) * kKeys + c * KV;
                         const int keys = min(KV, w.end - key);
                         const int boxes = keys > 0 ? (keys + p.box_v - 1) / p.box_v : 0;
                         const int at = min(c * KV + box * p.box_v, kKeys - 8);
                         const int page = __shfl_sync(0xffffffffu, page_v, at >> 3);
-                        const int slot = ((j - 1) * kKeys + at) % p.page_size;
+                        const int slot = slot_at(p, (j - 1) * kKeys + at);
                         ok = warp_wait(&sh->empty[stage], phase ^ 1u, abort, budget);
                         if (!ok) break;
                         unsigned char* dst = ring + stage * kChunkBytes;
@@ -458,7 +507,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (box < boxes)
                             ptx::tma_load_4d(dst + dims * (KV * 128) + box * p.box_v * 128, &tmap_v, 64 * dims, slot,
                                              w.head, page, &sh->full[stage]);
-                        next_stage();
                     }
                 }
                 page_v = page_k;
@@ -466,11 +514,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // Every copy issued here must land before the CTA may exit.
-        for (long long i = issued > NS ? issued - NS : 0; i < issued; ++i) {
+        for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) {
+            if ((i & (kTmaWarps - 1)) != mine) continue;
             volatile int no_abort = 0;
             ptx::mbar_wait_bounded(&sh->full[i % NS], (uint32_t)(i / NS) & 1u, &no_abort, budget);
         }
     } else if (warp == kMmaWarp) {
+        ptx::give_registers<kFewRegs>();
+        Walk w(p, start);
         constexpr uint32_t idesc_s = ptx::idesc_f32(kRows, kKeys, kBf16, false);
         constexpr uint32_t idesc_o = ptx::idesc_f32(kRows, DP, kBf16, true);
         const uint64_t desc_q = ptx::smem_desc_sw128(ptx::smem_u32(tile_q));
@@ -478,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t desc_v = ptx::smem_desc_sw128_mn(ptx::smem_u32(ring), KV * 128);
         int stage = 0;
         uint32_t phase = 0;
-        long long gt = 0;  // tiles so far, over all parts: S buffer gt & 1
+        int gt = 0;  // tiles so far, over all parts: S buffer gt & 1
         int part = 0;
         bool ok = true, any = false;
         auto next_stage = [&]() {
@@ -493,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // step i: S(i) = Q K(i)^T, then O += P(i-1) V(i-1)
             for (int i = 0; i <= n && ok; ++i) {
                 if (i < n) {
-                    const int b = (int)((gt + i) & 1);
+                    const int b = (gt + i) & 1;
                     // the buffer's previous weights have been multiplied
                     if (gt + i >= 2)
                         ok = warp_wait(&sh->pv_done[b], (gt + i - 2) >> 1, abort, budget);
@@ -520,8 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (i > 0 && ok) {
-                    const long long t = gt + i - 1;
-                    const int b = (int)(t & 1);
+                    const int t = gt + i - 1, b = t & 1;
                     if (i == 1 && part > 0)
                         ok = warp_wait(&sh->o_free, part - 1, abort, budget);
                     ok = ok && warp_wait(&sh->p_ready[b], t >> 1, abort, budget);
@@ -530,15 +580,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         ptx::tc_fence_after();
                         if (ptx::elect_one()) {
-                            const uint32_t pcol = tmem + C::kSCol + b * kKeys + c * (KV / 2);
+                            const uint32_t pcol = tmem + C::kSCol + b * kKeys;
                             const uint64_t v = desc_v + (uint64_t)((stage * kChunkBytes) >> 4);
 #pragma unroll
                             for (int kk = 0; kk < KV / 16; ++kk) {
-                                ptx::mma_bf16_ts(tmem + C::kOCol, pcol + 8 * kk, v + (uint64_t)(kk * 2048 >> 4), idesc_o,
-                                                 i > 1 || c > 0 || kk > 0 ? 1u : 0u);
+                                // 16 keys: 8 columns of each 64-column half's weights
+                                const int key = c * KV + 16 * kk;
+                                const uint32_t col = pcol + (key >> 6) * 64 + ((key & 63) >> 1);
+                                ptx::mma_bf16_ts(tmem + C::kOCol, col, v + (uint64_t)(kk * 2048 >> 4), idesc_o,
+                                                 (i - 1) % kDrain<F32OUT> != 0 || c > 0 || kk > 0 ? 1u : 0u);
                                 if (F32OUT)
-                                    ptx::mma_bf16_ts(tmem + C::kOCol, pcol + 64 + 8 * kk, v + (uint64_t)(kk * 2048 >> 4),
-                                                     idesc_o, 1u);
+                                    ptx::mma_bf16_ts(tmem + C::kOCol, col + 32, v + (uint64_t)(kk * 2048 >> 4), idesc_o, 1u);
                             }
                             ptx::mma_commit(&sh->empty[stage]);
                             if (c == NC - 1) ptx::mma_commit(&sh->pv_done[b]);
@@ -560,7 +612,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kQWarp) {
         // Q rows of each part, 16 bytes a lane; dims past the head's are zeros
         // (K's are, and a zero times what lies there must stay zero).
-        constexpr int U = DP / 8, kPerPass = 64 / U;
+        ptx::give_registers<kFewRegs>();
+        Walk w(p, start);
+        constexpr int U = DP / 8, kPerPass = kQThreads / U;
         const int me = threadIdx.x - 32 * kQWarp, u = me % U;
         int part = 0;
         bool ok = true;
@@ -581,73 +635,115 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_arrive(&sh->q_full);
         }
     } else {
-        // ---- softmax and epilogue: thread = row
-        const int r = threadIdx.x;
-        const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+        // ---- softmax and epilogue: thread = row and half of the columns
+        ptx::take_registers<kManyRegs>();
+        Walk w(p, start);
+        constexpr int HALF = DP / 2;             // output columns of a thread
+        constexpr int G = kDrain<F32OUT>;
+        const int side = warp >> 2;              // which half
+        const int r = threadIdx.x & (kRows - 1);
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const float sl2 = fabsf(p.scale) * 1.4426950408889634f;
         const bool negative = p.scale < 0.f;
         const int my_token = r / p.group, my_head = r - my_token * p.group;
-        long long gt = 0, consumed = 0;  // tiles and ring chunks before this part
-        int part = 0, joined = 0;        // parts before this one, meetings of the four warps
-        long long item_start = start.ctas > (int)blockIdx.x ? cut(start.total, start.ctas, blockIdx.x) - start.skip : 0;
+        uint64_t* pair = &sh->pair[warp & 3];
+        int gt = 0, consumed = 0;                // tiles and ring chunks before this part
+        int part = 0, joined = 0, paired = 0;    // parts before this one, meetings so far
+        long long item_start = start.ctas > (int)blockIdx.x ? cut(start, blockIdx.x) - start.skip : 0;
         bool ok = true;
         for (; w.valid() && ok; w.next(), ++part) {
             const int n = w.j1 - w.j0;
             const int tokens = w.tokens();
             const bool valid = my_token < tokens;
-            const bool active = 32 * warp < tokens * p.group;  // the warp has a valid row
-            const int first = w.q.place0 + w.qt * p.tile_tokens;  // place of the first token
+            const bool active = 32 * (warp & 3) < tokens * p.group;  // the warp has a valid row
+            const int first = w.q.place0 + w.qt * p.tile_tokens;     // place of the first token
             const int lim_first = p.causal ? min(max(first + 1, 0), w.q.len) : w.q.len;
             const int lim = !valid ? w.end : p.causal ? min(max(first + my_token + 1, 0), w.q.len) : w.q.len;
             float m = -INFINITY, base = -kShift<T>, sum = 0.f;
             bool bad = false;
+            // this thread's part of the workspace: f32 output drained so far, at maximum ws_base
+            const long long slot = 2LL * blockIdx.x + (w.j0 == 0 ? 1 : 0);
+            float* ws_o = p.ws_o + (slot * kRows + r) * DP + side * HALF;
+            float ws_base = 0.f;
+            // o = tensor memory's columns c.. + drained * 2^(ws_base - base)
+            auto read_out = [&](int c, bool drained, float f, float (&o)[32]) {
+                float4 x[8];
+                if (drained && valid) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = __ldcg(reinterpret_cast<const float4*>(ws_o + c) + k);
+                }
+                ptx::tmem_ld32(tmem + lane_base + C::kOCol + side * HALF + c, o);
+                ptx::tmem_wait_ld();
+                ptx::tmem_landed(o);
+                if (drained && valid) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        o[4 * k] = fmaf(x[k].x, f, o[4 * k]);
+                        o[4 * k + 1] = fmaf(x[k].y, f, o[4 * k + 1]);
+                        o[4 * k + 2] = fmaf(x[k].z, f, o[4 * k + 2]);
+                        o[4 * k + 3] = fmaf(x[k].w, f, o[4 * k + 3]);
+                    }
+                }
+                __syncwarp();
+            };
+            auto write_ws = [&](int c, const float (&o)[32]) {
+                if (valid) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        __stcg(reinterpret_cast<float4*>(ws_o + c + k), make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
+                }
+                __syncwarp();
+            };
             for (int i = 0; i < n && ok; ++i) {
-                const long long t = gt + i;
-                const int b = (int)(t & 1);
+                const int t = gt + i, b = t & 1;
                 uint64_t* wbar = p.stall_test && t == 0 ? &sh->never : &sh->s_full[b];
                 ok = warp_wait(wbar, t >> 1, abort, budget);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const int key0 = (w.j0 + i) * kKeys;
                 const bool edge = key0 + kKeys > lim_first;  // some row does not see the whole tile
-                const uint32_t taddr = tmem + lane_base + C::kSCol + b * kKeys;
+                const uint32_t taddr = tmem + lane_base + C::kSCol + b * kKeys + 64 * side;
                 if (active) {
-                    float s[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) ptx::tmem_ld32(taddr + 32 * c, s[c]);
+                    float s[2][32];
+                    ptx::tmem_ld32(taddr, s[0]);
+                    ptx::tmem_ld32(taddr + 32, s[1]);
                     ptx::tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) ptx::tmem_landed(s[c]);
+                    ptx::tmem_landed(s[0]);
+                    ptx::tmem_landed(s[1]);
                     if (negative) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) s[c][k] = -s[c][k];
+                        for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = -s[k >> 5][k & 31];
                     }
-                    const int see = lim - key0;  // keys of the tile that the row sees
+                    const int see = lim - key0 - 64 * side;  // of these 64 keys, those that the row sees
                     if (edge) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (32 * c + k >= see) s[c][k] = -INFINITY;
+                        for (int k = 0; k < 64; ++k)
+                            if (k >= see) s[k >> 5][k & 31] = -INFINITY;
                     }
                     float top[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        top[c] = fmaxf(s[c][0], s[c][1]);
+                        top[c] = fmaxf(s[c >> 1][16 * (c & 1)], s[c >> 1][16 * (c & 1) + 1]);
 #pragma unroll
-                        for (int k = 2; k < 32; k += 2) top[c] = fmaxf(top[c], fmaxf(s[c][k], s[c][k + 1]));
+                        for (int k = 2; k < 16; k += 2)
+                            top[c] = fmaxf(top[c], fmaxf(s[c >> 1][16 * (c & 1) + k], s[c >> 1][16 * (c & 1) + k + 1]));
                     }
-                    const float now = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                    // both halves of a row take the same reference, so their weights meet in one output
+                    const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    sh->row[b][side][r] = mine;
+                    ptx::mbar_arrive(pair);
+                    ok = warp_wait(pair, paired++, abort, budget);
+                    if (!ok) break;
+                    const float now = fmaxf(m, fmaxf(mine, *(volatile float*)&sh->row[b][side ^ 1][r]));
                     const bool grow = now > m && (m == -INFINITY || (now - m) * sl2 > kLazy);
-                    if (__any_sync(0xffffffffu, grow)) {
+                    const bool drain = i > 0 && i % G == 0;
+                    if (__any_sync(0xffffffffu, grow) || drain) {
+                        const float old = base;
                         float keep = 1.f;
                         if (grow) {
-                            const float to = now * sl2 - kShift<T>;
-                            keep = m == -INFINITY ? 0.f : ptx::ex2(base - to);
+                            base = now * sl2 - kShift<T>;
+                            keep = m == -INFINITY ? 0.f : ptx::ex2(old - base);
                             m = now;
-                            base = to;
                             sum *= keep;
                         }
                         if (i > 0) {
@@ -655,49 +751,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!ok) break;
                             ptx::tc_fence_after();
                             const float2 keep2 = make_float2(keep, keep);
+                            const float f = ptx::ex2(ws_base - old);
 #pragma unroll 1
-                            for (int c = 0; c < DP; c += 32) {
+                            for (int c = 0; c < HALF; c += 32) {
                                 float o[32];
-                                uint32_t u[32];
-                                ptx::tmem_ld32(tmem + lane_base + C::kOCol + c, o);
-                                ptx::tmem_wait_ld();
-                                ptx::tmem_landed(o);
+                                if (drain) {
+                                    read_out(c, i > G, f, o);
+                                    write_ws(c, o);
+                                } else {
+                                    uint32_t u[32];
+                                    read_out(c, false, f, o);
 #pragma unroll
-                                for (int k = 0; k < 32; k += 2) {
-                                    const float2 x = __fmul2_rn(make_float2(o[k], o[k + 1]), keep2);
-                                    u[k] = __float_as_uint(x.x);
-                                    u[k + 1] = __float_as_uint(x.y);
+                                    for (int k = 0; k < 32; k += 2) {
+                                        const float2 x = __fmul2_rn(make_float2(o[k], o[k + 1]), keep2);
+                                        u[k] = __float_as_uint(x.x);
+                                        u[k + 1] = __float_as_uint(x.y);
+                                    }
+                                    ptx::tmem_st32(tmem + lane_base + C::kOCol + side * HALF + c, u);
                                 }
-                                ptx::tmem_st32(tmem + lane_base + C::kOCol + c, u);
                             }
+                            if (drain) ws_base = old;
                         }
                     }
                     __syncwarp();
                     const float2 mul = make_float2(sl2, sl2), sub = make_float2(-base, -base);
                     float2 add0 = make_float2(0.f, 0.f), add1 = make_float2(0.f, 0.f);
+                    uint32_t hi[32], lo[32];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t hi[32], lo[32];
-#pragma unroll
-                        for (int k = 0; k < 64; k += 2) {
-                            const int c = 2 * h + (k >> 5), at = k & 31;
-                            const float2 x = __ffma2_rn(make_float2(s[c][at], s[c][at + 1]), mul, sub);
-                            float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-                            if (edge) {
-                                if (64 * h + k >= see) e.x = 0.f;
-                                if (64 * h + k + 1 >= see) e.y = 0.f;
-                            }
-                            if (k & 2) add1 = __fadd2_rn(add1, e);
-                            else add0 = __fadd2_rn(add0, e);
-                            hi[k / 2] = pack2<T>(e.x, e.y);
-                            if (F32OUT) {
-                                const float2 f = unpack2<T>(hi[k / 2]);
-                                lo[k / 2] = pack2<T>(e.x - f.x, e.y - f.y);
-                            }
+                    for (int k = 0; k < 64; k += 2) {
+                        const float2 x = __ffma2_rn(make_float2(s[k >> 5][k & 31], s[k >> 5][(k & 31) + 1]), mul, sub);
+                        float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+                        if (edge) {
+                            if (k >= see) e.x = 0.f;
+                            if (k + 1 >= see) e.y = 0.f;
                         }
-                        ptx::tmem_st32(taddr + 32 * h, hi);
-                        if (F32OUT) ptx::tmem_st32(taddr + 64 + 32 * h, lo);
+                        if (k & 2) add1 = __fadd2_rn(add1, e);
+                        else add0 = __fadd2_rn(add0, e);
+                        hi[k / 2] = pack2<T>(e.x, e.y);
+                        if (F32OUT) {
+                            const float2 f = unpack2<T>(hi[k / 2]);
+                            lo[k / 2] = pack2<T>(e.x - f.x, e.y - f.y);
+                        }
                     }
+                    ptx::tmem_st32(taddr, hi);
+                    if (F32OUT) ptx::tmem_st32(taddr + 32, lo);
                     add0 = __fadd2_rn(add0, add1);
                     sum += add0.x + add0.y;
                 }
@@ -708,14 +805,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // row's and the last row's last key too; the epilogue gives
                     // them back to the rows that see them.
                     const int lo = max(lim_first - key0, 0), hi = w.end - key0;
-                    const long long v0 = consumed + (long long)NC * (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
+                    const int v0 = consumed + NC * (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
 #pragma unroll 1
                     for (int c = lo / KV; c < NC && ok; ++c) {
-                        const int st = (int)((v0 + c) % NS);
+                        const int st = (v0 + c) % NS;
                         ok = warp_wait(&sh->full[st], (v0 + c) / NS, abort, budget);
                         if (!ok) break;
-                        for (int row = max(lo - c * KV, 0) + (r >> 3); row < KV; row += 16) {
-                            uint4* at = reinterpret_cast<uint4*>(ring + st * kChunkBytes + row * 128 + (r & 7) * 16);
+                        const int u = threadIdx.x;  // 0..255: row u / 8, 16 bytes u % 8
+                        for (int row = max(lo - c * KV, 0) + (u >> 3); row < KV; row += kSoftmax / 8) {
+                            uint4* at = reinterpret_cast<uint4*>(ring + st * kChunkBytes + row * 128 + (u & 7) * 16);
 #pragma unroll
                             for (int d = 0; d < NC; ++d, at += KV * 8) {
                                 if (c * KV + row >= hi) {
@@ -744,8 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             gt += n;
-            consumed += 2LL * NC * n;
-            // All four warps: was there an infinity or a NaN among the values of this part?
+            consumed += 2 * NC * n;
+            // All warps meet: was there an infinity or a NaN among the values of this part?
             const bool edges = p.causal && w.j1 * kKeys > lim_first && lim_first < w.end;
             if (edges) {
                 if (bad) sh->bad = part + 1;
@@ -754,11 +852,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 bad = *(volatile int*)&sh->bad >= part + 1;  // (a later part's mark only costs a look)
             }
+            if (active) {
+                // the row's sum: this half and the other
+                sh->row[gt & 1][side][r] = sum;
+                ptx::mbar_arrive(pair);
+                ok = warp_wait(pair, paired++, abort, budget);
+                if (!ok) break;
+                const float other = *(volatile float*)&sh->row[gt & 1][side ^ 1][r];
+                sum = side ? other + sum : sum + other;
+            }
 
             // ---- epilogue
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;
-            const long long slot = 2LL * blockIdx.x + (w.j0 == 0 ? 1 : 0);
-            float* ws_o = p.ws_o + (slot * kRows + r) * DP;
             ok = warp_wait(&sh->pv_done[(gt - 1) & 1], (gt - 1) >> 1, abort, budget);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -766,48 +871,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int head = w.head * p.group + my_head;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             if (active) {
+                const float f = ptx::ex2(ws_base - base);
 #pragma unroll 1
-                for (int c = 0; c < DP; c += 32) {
+                for (int c = 0; c < HALF; c += 32) {
                     float o[32];
-                    ptx::tmem_ld32(tmem + lane_base + C::kOCol + c, o);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_landed(o);
+                    const int dim0 = side * HALF + c;
+                    read_out(c, n > G, f, o);
                     if (bad && edges && valid) {
 #pragma unroll 1
                         for (int key = max(lim_first, w.j0 * kKeys); key < min(lim, w.j1 * kKeys); ++key) {
-                            const int at = key / p.page_size;
-                            const int page = p.batch.table[w.seq * p.batch.table_stride + at];
+                            const int page = p.batch.table[w.seq * p.batch.table_stride + page_at(p, key)];
                             if (page < 0 || page >= p.pages) continue;
                             const T* v = static_cast<const T*>(p.v_pool) + page * p.page_stride +
-                                         (key - at * p.page_size) * p.slot_stride + w.head * p.head_stride;
+                                         slot_at(p, key) * p.slot_stride + w.head * p.head_stride;
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
-                                const float x = c + k < p.dim ? to_f32(v[c + k]) : 0.f;
+                                const float x = dim0 + k < p.dim ? to_f32(v[dim0 + k]) : 0.f;
                                 if (!isfinite(x)) o[k] += x;
                             }
                         }
                     }
-                    if (!valid) {
-                    } else if (!whole) {
+                    __syncwarp();
+                    if (!whole) {
+                        write_ws(c, o);
+                    } else if (valid) {
+                        if (F32OUT) {
+                            float* out = static_cast<float*>(p.out) + token * p.out_token + head * p.out_head + dim0;
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            __stcg(reinterpret_cast<float4*>(ws_o + c + k),
-                                   make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
-                    } else if (F32OUT) {
-                        float* out = static_cast<float*>(p.out) + token * p.out_token + head * p.out_head + c;
+                            for (int k = 0; k < 32; k += 4)
+                                if (dim0 + k < p.dim)
+                                    *reinterpret_cast<float4*>(out + k) =
+                                        make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
+                        } else {
+                            T* out = static_cast<T*>(p.out) + token * p.out_token + head * p.out_head + dim0;
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            if (c + k < p.dim)
-                                *reinterpret_cast<float4*>(out + k) =
-                                    make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
-                    } else {
-                        T* out = static_cast<T*>(p.out) + token * p.out_token + head * p.out_head + c;
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8)
-                            if (c + k < p.dim)
-                                *reinterpret_cast<uint4*>(out + k) =
-                                    make_uint4(pack2<T>(o[k] * inv, o[k + 1] * inv), pack2<T>(o[k + 2] * inv, o[k + 3] * inv),
-                                               pack2<T>(o[k + 4] * inv, o[k + 5] * inv), pack2<T>(o[k + 6] * inv, o[k + 7] * inv));
+                            for (int k = 0; k < 32; k += 8)
+                                if (dim0 + k < p.dim)
+                                    *reinterpret_cast<uint4*>(out + k) = make_uint4(
+                                        pack2<T>(o[k] * inv, o[k + 1] * inv), pack2<T>(o[k + 2] * inv, o[k + 3] * inv),
+                                        pack2<T>(o[k + 4] * inv, o[k + 5] * inv), pack2<T>(o[k + 6] * inv, o[k + 7] * inv));
+                        }
                     }
                     __syncwarp();
                 }
@@ -815,21 +918,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_before();
             ptx::mbar_arrive(&sh->o_free);
             if (whole) {
-                if (valid && p.lse)
+                if (valid && side == 0 && p.lse)
                     p.lse[token * p.heads + head] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (base + log2f(sum));
                 item_start += w.tiles;
                 continue;
             }
 
             // ---- a part of an item: the last one to arrive joins them
-            if (valid) __stcg(reinterpret_cast<float2*>(p.ws_ml) + slot * kRows + r, make_float2(sum == 0.f ? -INFINITY : base, sum));
-            const int from = cta_of(start.total, start.ctas, item_start);
-            const int to = cta_of(start.total, start.ctas, item_start + w.tiles - 1);
+            if (valid && side == 0)
+                __stcg(reinterpret_cast<float2*>(p.ws_ml) + slot * kRows + r, make_float2(sum == 0.f ? -INFINITY : base, sum));
+            const int from = cta_of(start, item_start);
+            const int to = cta_of(start, item_start + w.tiles - 1);
             __threadfence();
             ptx::mbar_arrive(&sh->join);
             ok = warp_wait(&sh->join, joined++, abort, budget);
             if (!ok) break;
-            if (r == 0) {
+            if (threadIdx.x == 0) {
                 const int before = atomicAdd(&p.tickets[from], 1);
                 sh->last = before == to - from;
                 if (sh->last) p.tickets[from] = 0;
@@ -840,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (*(volatile int*)&sh->last) {
                 __threadfence();
                 const int rows = tokens * p.group;
-                for (int row = warp; row < rows; row += 4) {
+                for (int row = warp; row < rows; row += kSoftmax / 32) {
                     // the first part lies in its CTA's second slot, the others in their first
                     auto slot_of = [&](int c) { return ((2LL * c + (c == from ? 1 : 0)) * kRows + row); };
                     float top = -INFINITY;
@@ -851,17 +955,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float ref = top == -INFINITY ? 0.f : top;
                     float total = 0.f, acc[DP / 32] = {};
                     for (int c0 = from; c0 <= to; c0 += 32) {
-                        float wgt = 0.f, part = 0.f;
+                        float wgt = 0.f, part_sum = 0.f;
                         if (c0 + lane <= to) {
                             const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot_of(c0 + lane));
                             wgt = ml.y == 0.f ? 0.f : ptx::ex2(ml.x - ref);
-                            part = wgt * ml.y;
+                            part_sum = wgt * ml.y;
                         }
 #pragma unroll
-                        for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-                        total += part;
+                        for (int o = 16; o; o >>= 1) part_sum += __shfl_xor_sync(0xffffffffu, part_sum, o);
+                        total += part_sum;
                         const int parts = min(32, to - c0 + 1);
-#pragma unroll 8
+#pragma unroll 4
                         for (int k = 0; k < parts; ++k) {
                             const float x = __shfl_sync(0xffffffffu, wgt, k);
                             const float* o = p.ws_o + slot_of(c0 + k) * DP + lane;
@@ -872,8 +976,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    const int t = row / p.group, g = row - t * p.group;
-                    const long long tok = w.q.row0 + w.qt * p.tile_tokens + t;
+                    const int tk = row / p.group, g = row - tk * p.group;
+                    const long long tok = w.q.row0 + w.qt * p.tile_tokens + tk;
                     const int hd = w.head * p.group + g;
                     const float scale = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll

@@ -309,6 +309,7 @@ bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
     p.wait_budget_ns = kv->wait_budget_ns;
     p.pages = kv->pages;
     p.page_size = kv->page_size;
+    p.page_shift = kv->page_size & (kv->page_size - 1) ? -1 : __builtin_ctz((unsigned)kv->page_size);
     p.tokens = tokens;
     p.heads = heads;
     p.kv_heads = kv->kv_heads;

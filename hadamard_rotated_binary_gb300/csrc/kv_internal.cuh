@@ -100,7 +100,7 @@ struct AttendParams {
     int* tickets;              // [CTAs], zero between calls
     int* dev_error;
     long long wait_budget_ns;
-    int pages, page_size;
+    int pages, page_size, page_shift;  // page_shift: log2 of a power of two, else -1
     int tokens, heads, kv_heads, group, dim, causal;
     int tile_tokens;           // tokens of a 128-row tile: 128 / group
     int box_k, box_v;          // slots of a page per TMA copy
