@@ -32,7 +32,8 @@ def _rows(x, what: str) -> Rows:
 
 
 def _stream(stream, device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+    # the raw handle: building a Stream object costs more than the launch
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _positions(pos, axes: int, tokens: int):

@@ -56,8 +56,8 @@ constexpr int kSoftmax = 256;     // threads of the softmax warps
 constexpr int kTmaWarp = 8, kTmaWarps = 4, kMmaWarp = 12, kQWarp = 13;
 constexpr int kQThreads = 96;
 // Registers a thread: launched with 128, the two softmax warpgroups take what
-// the other two give (2 * 168 + 2 * 88 = 4 * 128).
-constexpr int kManyRegs = 168, kFewRegs = 88;
+// the other two give (2 * 184 + 2 * 72 = 4 * 128).
+constexpr int kManyRegs = 184, kFewRegs = 72;
 constexpr int kChunkBytes = 16384;
 constexpr int kTmemCols = 512;
 constexpr float kLazy = 8.f;      // log2 of the growth that a rescale waits for
@@ -304,10 +304,25 @@ struct Walk {
     __device__ int tokens() const { return min(p.tile_tokens, q.rows - qt * p.tile_tokens); }
 };
 
+// Waits for a barrier's phase like ptx::mbar_wait_bounded, in fewer
+// instructions: this kernel's loops are bound by instruction fetch where they
+// grow (see the softmax).
+__device__ __forceinline__ bool wait(uint64_t* bar, int phase, volatile int* abort, long long budget)
+{
+    if (ptx::mbar_try_wait(bar, (uint32_t)phase & 1u)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    do {
+        if (ptx::mbar_try_wait(bar, (uint32_t)phase & 1u)) return true;
+        if (*abort) return false;
+    } while ((long long)(ptx::globaltimer() - t0) <= budget);
+    *abort = 1;
+    return false;
+}
+
 // A whole warp waits; true when every lane saw the phase complete.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, volatile int* abort, long long budget)
 {
-    return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, (uint32_t)phase & 1u, abort, budget));
+    return __all_sync(0xffffffffu, wait(bar, phase, abort, budget));
 }
 
 // Page of a sequence and slot in it that hold key `key`.
@@ -619,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int part = 0;
         bool ok = true;
         for (; w.valid() && ok; w.next(), ++part) {
-            if (part > 0) ok = ptx::mbar_wait_bounded(&sh->q_empty, (uint32_t)(part - 1) & 1u, abort, budget);
+            if (part > 0) ok = wait(&sh->q_empty, part - 1, abort, budget);
             if (!ok) break;
             const int rows = w.tokens() * p.group;
             const T* base = static_cast<const T*>(p.q) + (long long)(w.q.row0 + w.qt * p.tile_tokens) * p.q_token +
@@ -643,7 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int side = warp >> 2;              // which half
         const int r = threadIdx.x & (kRows - 1);
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-        const float sl2 = fabsf(p.scale) * 1.4426950408889634f;
+        // log2 units; a scale of 0 becomes one that no score can make count, so
+        // that a masked score (-inf) times it still is -inf
+        const float sl2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);
         const bool negative = p.scale < 0.f;
         const int my_token = r / p.group, my_head = r - my_token * p.group;
         uint64_t* pair = &sh->pair[warp & 3];
@@ -666,18 +683,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* ws_o = p.ws_o + (slot * kRows + r) * DP + side * HALF;
             float ws_base = 0.f;
             // o = tensor memory's columns c.. + drained * 2^(ws_base - base)
-            auto read_out = [&](int c, bool drained, float f, float (&o)[32]) {
-                float4 x[8];
+            auto read_out = [&](int c, bool drained, float f, float (&o)[16]) {
+                float4 x[4];
                 if (drained && valid) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = __ldcg(reinterpret_cast<const float4*>(ws_o + c) + k);
+                    for (int k = 0; k < 4; ++k) x[k] = __ldcg(reinterpret_cast<const float4*>(ws_o + c) + k);
                 }
-                ptx::tmem_ld32(tmem + lane_base + C::kOCol + side * HALF + c, o);
+                ptx::tmem_ld16(tmem + lane_base + C::kOCol + side * HALF + c, o);
                 ptx::tmem_wait_ld();
                 ptx::tmem_landed(o);
                 if (drained && valid) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         o[4 * k] = fmaf(x[k].x, f, o[4 * k]);
                         o[4 * k + 1] = fmaf(x[k].y, f, o[4 * k + 1]);
                         o[4 * k + 2] = fmaf(x[k].z, f, o[4 * k + 2]);
@@ -686,10 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            auto write_ws = [&](int c, const float (&o)[32]) {
+            auto write_ws = [&](int c, const float (&o)[16]) {
                 if (valid) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4)
+                    for (int k = 0; k < 16; k += 4)
                         __stcg(reinterpret_cast<float4*>(ws_o + c + k), make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
                 }
                 __syncwarp();
@@ -710,23 +727,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_wait_ld();
                     ptx::tmem_landed(s[0]);
                     ptx::tmem_landed(s[1]);
-                    if (negative) {
-#pragma unroll
-                        for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = -s[k >> 5][k & 31];
-                    }
-                    const int see = lim - key0 - 64 * side;  // of these 64 keys, those that the row sees
+                    // The straight line from here to the weights is what every tile
+                    // runs; masks and the sign of the scale stay out of it.
                     if (edge) {
+                        const int see = lim - key0 - 64 * side;  // of these 64 keys, those that the row sees
+                        const float masked = negative ? INFINITY : -INFINITY;
 #pragma unroll
                         for (int k = 0; k < 64; ++k)
-                            if (k >= see) s[k >> 5][k & 31] = -INFINITY;
+                            if (k >= see) s[k >> 5][k & 31] = masked;
                     }
                     float top[4];
+                    if (negative) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        top[c] = fmaxf(s[c >> 1][16 * (c & 1)], s[c >> 1][16 * (c & 1) + 1]);
+                        for (int k = 0; k < 64; ++k)
+                            top[k & 3] = k < 4 ? -s[0][k] : fmaxf(top[k & 3], -s[k >> 5][k & 31]);
+                    } else {
 #pragma unroll
-                        for (int k = 2; k < 16; k += 2)
-                            top[c] = fmaxf(top[c], fmaxf(s[c >> 1][16 * (c & 1) + k], s[c >> 1][16 * (c & 1) + k + 1]));
+                        for (int k = 0; k < 64; k += 2) {
+                            const float x = fmaxf(s[k >> 5][k & 31], s[k >> 5][(k & 31) + 1]);
+                            top[(k >> 1) & 3] = k < 8 ? x : fmaxf(top[(k >> 1) & 3], x);
+                        }
                     }
                     // both halves of a row take the same reference, so their weights meet in one output
                     const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
@@ -735,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = warp_wait(pair, paired++, abort, budget);
                     if (!ok) break;
                     const float now = fmaxf(m, fmaxf(mine, *(volatile float*)&sh->row[b][side ^ 1][r]));
-                    const bool grow = now > m && (m == -INFINITY || (now - m) * sl2 > kLazy);
+                    const bool grow = valid && now > m && (m == -INFINITY || (now - m) * sl2 > kLazy);
                     const bool drain = i > 0 && i % G == 0;
                     if (__any_sync(0xffffffffu, grow) || drain) {
                         const float old = base;
@@ -753,38 +773,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float2 keep2 = make_float2(keep, keep);
                             const float f = ptx::ex2(ws_base - old);
 #pragma unroll 1
-                            for (int c = 0; c < HALF; c += 32) {
-                                float o[32];
+                            for (int c = 0; c < HALF; c += 16) {
+                                float o[16];
                                 if (drain) {
                                     read_out(c, i > G, f, o);
                                     write_ws(c, o);
                                 } else {
-                                    uint32_t u[32];
+                                    uint32_t u[16];
                                     read_out(c, false, f, o);
 #pragma unroll
-                                    for (int k = 0; k < 32; k += 2) {
+                                    for (int k = 0; k < 16; k += 2) {
                                         const float2 x = __fmul2_rn(make_float2(o[k], o[k + 1]), keep2);
                                         u[k] = __float_as_uint(x.x);
                                         u[k + 1] = __float_as_uint(x.y);
                                     }
-                                    ptx::tmem_st32(tmem + lane_base + C::kOCol + side * HALF + c, u);
+                                    ptx::tmem_st16(tmem + lane_base + C::kOCol + side * HALF + c, u);
                                 }
                             }
                             if (drain) ws_base = old;
                         }
                     }
                     __syncwarp();
-                    const float2 mul = make_float2(sl2, sl2), sub = make_float2(-base, -base);
+                    const float2 mul = make_float2(negative ? -sl2 : sl2, negative ? -sl2 : sl2), sub = make_float2(-base, -base);
                     float2 add0 = make_float2(0.f, 0.f), add1 = make_float2(0.f, 0.f);
                     uint32_t hi[32], lo[32];
 #pragma unroll
                     for (int k = 0; k < 64; k += 2) {
                         const float2 x = __ffma2_rn(make_float2(s[k >> 5][k & 31], s[k >> 5][(k & 31) + 1]), mul, sub);
-                        float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-                        if (edge) {
-                            if (k >= see) e.x = 0.f;
-                            if (k + 1 >= see) e.y = 0.f;
-                        }
+                        const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
                         if (k & 2) add1 = __fadd2_rn(add1, e);
                         else add0 = __fadd2_rn(add0, e);
                         hi[k / 2] = pack2<T>(e.x, e.y);
@@ -873,8 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (active) {
                 const float f = ptx::ex2(ws_base - base);
 #pragma unroll 1
-                for (int c = 0; c < HALF; c += 32) {
-                    float o[32];
+                for (int c = 0; c < HALF; c += 16) {
+                    float o[16];
                     const int dim0 = side * HALF + c;
                     read_out(c, n > G, f, o);
                     if (bad && edges && valid) {
@@ -885,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const T* v = static_cast<const T*>(p.v_pool) + page * p.page_stride +
                                          slot_at(p, key) * p.slot_stride + w.head * p.head_stride;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
+                            for (int k = 0; k < 16; ++k) {
                                 const float x = dim0 + k < p.dim ? to_f32(v[dim0 + k]) : 0.f;
                                 if (!isfinite(x)) o[k] += x;
                             }
@@ -898,14 +914,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (F32OUT) {
                             float* out = static_cast<float*>(p.out) + token * p.out_token + head * p.out_head + dim0;
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4)
+                            for (int k = 0; k < 16; k += 4)
                                 if (dim0 + k < p.dim)
                                     *reinterpret_cast<float4*>(out + k) =
                                         make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
                         } else {
                             T* out = static_cast<T*>(p.out) + token * p.out_token + head * p.out_head + dim0;
 #pragma unroll
-                            for (int k = 0; k < 32; k += 8)
+                            for (int k = 0; k < 16; k += 8)
                                 if (dim0 + k < p.dim)
                                     *reinterpret_cast<uint4*>(out + k) = make_uint4(
                                         pack2<T>(o[k] * inv, o[k + 1] * inv), pack2<T>(o[k + 2] * inv, o[k + 3] * inv),
