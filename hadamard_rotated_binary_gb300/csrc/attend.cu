@@ -74,7 +74,12 @@ struct Cfg {
     static constexpr int KV = 8192 / DP;                  // keys of a V chunk
     static constexpr int kQBytes = kRows * DP * 2;
     static constexpr int kStages = (224 * 1024 - kQBytes) / kChunkBytes > 12 ? 12 : (224 * 1024 - kQBytes) / kChunkBytes;
-    static constexpr int kOCol = 0, kSCol = 256;          // tensor memory: output, two S buffers
+    // Tensor memory: the output, then NB buffers of S, which run AHEAD tiles in
+    // front of the output's products.  Three buffers where they fit keep a tile
+    // of scores waiting for either softmax group.
+    static constexpr int NB = DP == 256 ? 2 : 3, AHEAD = NB - 1;
+    static constexpr int kOCol = 0, kSCol = kTmemCols - NB * kKeys;
+    static_assert(kSCol >= DP, "tensor memory");
 };
 
 // A sequence's rows and keys, with every index brought into range.
@@ -99,7 +104,7 @@ template <int DP>
 struct __align__(8) Shared {
     uint64_t full[Cfg<DP>::kStages], empty[Cfg<DP>::kStages];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_ready[2], pv_done[2];
+    uint64_t s_full[Cfg<DP>::NB], p_ready[Cfg<DP>::NB], pv_done[Cfg<DP>::NB];
     uint64_t o_free;
     uint64_t pair[4];  // the two softmax warps of 32 rows meet (a bounded wait, unlike a named barrier)
     uint64_t join;     // all softmax warps meet
@@ -108,7 +113,9 @@ struct __align__(8) Shared {
     uint32_t tmem_base;
     int last;         // this CTA joins the item's parts
     int bad;          // 1 + the part whose values held an infinity or a NaN
-    float row[2][2][kRows];  // what the two warps of a row tell each other
+    int grown[4];            // 1 + the last tile that asked for another reference
+    float top[2][kRows];     // maxima of the two halves of a tile's columns
+    float sum[2][kRows];     // their sums of weights over a part
     int abort;
 };
 
@@ -416,13 +423,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::mbar_init(&sh->q_full, kQThreads);
         ptx::mbar_init(&sh->q_empty, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::NB; ++i) {
             ptx::mbar_init(&sh->s_full[i], 1);
             ptx::mbar_init(&sh->p_ready[i], kSoftmax);
             ptx::mbar_init(&sh->pv_done[i], 1);
         }
         ptx::mbar_init(&sh->o_free, kSoftmax);
-        for (int i = 0; i < 4; ++i) ptx::mbar_init(&sh->pair[i], 64);
+        for (int i = 0; i < 4; ++i) {
+            ptx::mbar_init(&sh->pair[i], 2);
+            sh->grown[i] = 0;
+        }
         ptx::mbar_init(&sh->join, kSoftmax);
         ptx::mbar_init(&sh->never, 1);
         ptx::mbar_init(&sh->drain, 1);
@@ -475,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         for (; w.valid() && ok; w.next()) {
-            int page_k = page_of(w.j0), page_v = -1, page_next = -1;
-            for (int j = w.j0; j <= w.j1 && ok; ++j) {
+            int page_k = page_of(w.j0), page_next = -1, page_v[C::AHEAD];
+            for (int j = w.j0; j < w.j1 + C::AHEAD && ok; ++j) {
                 if (j + 1 < w.j1) page_next = page_of(j + 1);
                 if (j < w.j1) {
                     // K tile j: NC chunks of 128 keys x 64 dims
@@ -485,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int at = min(lane * p.box_k, kKeys - 8);
                     const int page = __shfl_sync(0xffffffffu, page_k, at >> 3);
                     const int slot = slot_at(p, j * kKeys + at);
+#pragma unroll 1
                     for (int c = 0; c < NC; ++c, next_stage()) {
                         if ((issued & (kTmaWarps - 1)) != mine) continue;
                         ok = warp_wait(&sh->empty[stage], phase ^ 1u, abort, budget);
@@ -500,17 +511,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              &sh->full[stage]);
                     }
                 }
-                if (j > w.j0 && ok) {
-                    // V tile j - 1: NC chunks of KV keys x DP dims, as [dims / 64][KV][64]
+                if (j >= w.j0 + C::AHEAD && ok) {
+                    // V tile j - AHEAD: NC chunks of KV keys x DP dims, as [dims / 64][KV][64]
                     const int box = lane / NC, dims = lane % NC;
+#pragma unroll 1
                     for (int c = 0; c < NC; ++c, next_stage()) {
                         if ((issued & (kTmaWarps - 1)) != mine) continue;
-                        const int key = (j - 1) * kKeys + c * KV;
+                        const int key = (j - C::AHEAD) * kKeys + c * KV;
                         const int keys = min(KV, w.end - key);
                         const int boxes = keys > 0 ? (keys + p.box_v - 1) / p.box_v : 0;
                         const int at = min(c * KV + box * p.box_v, kKeys - 8);
-                        const int page = __shfl_sync(0xffffffffu, page_v, at >> 3);
-                        const int slot = slot_at(p, (j - 1) * kKeys + at);
+                        const int page = __shfl_sync(0xffffffffu, page_v[C::AHEAD - 1], at >> 3);
+                        const int slot = slot_at(p, (j - C::AHEAD) * kKeys + at);
                         ok = warp_wait(&sh->empty[stage], phase ^ 1u, abort, budget);
                         if (!ok) break;
                         unsigned char* dst = ring + stage * kChunkBytes;
@@ -524,7 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              w.head, page, &sh->full[stage]);
                     }
                 }
-                page_v = page_k;
+#pragma unroll
+                for (int a = C::AHEAD - 1; a > 0; --a) page_v[a] = page_v[a - 1];
+                page_v[0] = page_k;
                 page_k = page_next;
             }
         }
@@ -544,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t desc_v = ptx::smem_desc_sw128_mn(ptx::smem_u32(ring), KV * 128);
         int stage = 0;
         uint32_t phase = 0;
-        int gt = 0;  // tiles so far, over all parts: S buffer gt & 1
+        int gt = 0;       // tiles so far, over all parts: S buffer t % NB of tile t
         int part = 0;
         bool ok = true, any = false;
         auto next_stage = [&]() {
@@ -556,13 +570,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; w.valid() && ok; w.next(), ++part) {
             const int n = w.j1 - w.j0;
             ok = warp_wait(&sh->q_full, part, abort, budget);
-            // step i: S(i) = Q K(i)^T, then O += P(i-1) V(i-1)
-            for (int i = 0; i <= n && ok; ++i) {
+            // step i: S(i) = Q K(i)^T, then O += P(i - AHEAD) V(i - AHEAD)
+            for (int i = 0; i < n + C::AHEAD && ok; ++i) {
                 if (i < n) {
-                    const int b = (gt + i) & 1;
+                    const int t = gt + i, b = t % C::NB;
                     // the buffer's previous weights have been multiplied
-                    if (gt + i >= 2)
-                        ok = warp_wait(&sh->pv_done[b], (gt + i - 2) >> 1, abort, budget);
+                    if (t >= C::NB) ok = warp_wait(&sh->pv_done[b], t / C::NB - 1, abort, budget);
                     for (int c = 0; c < NC && ok; ++c) {
                         ok = warp_wait(&sh->full[stage], phase, abort, budget);
                         if (!ok) break;
@@ -585,11 +598,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         next_stage();
                     }
                 }
-                if (i > 0 && ok) {
-                    const int t = gt + i - 1, b = t & 1;
-                    if (i == 1 && part > 0)
-                        ok = warp_wait(&sh->o_free, part - 1, abort, budget);
-                    ok = ok && warp_wait(&sh->p_ready[b], t >> 1, abort, budget);
+                if (i >= C::AHEAD && ok) {
+                    const int iv = i - C::AHEAD, t = gt + iv, b = t % C::NB;
+                    const bool fresh = iv % kDrain<F32OUT> == 0;  // the output starts from zero
+                    if (iv == 0 && part > 0) ok = warp_wait(&sh->o_free, part - 1, abort, budget);
+                    ok = ok && warp_wait(&sh->p_ready[b], t / C::NB, abort, budget);
                     for (int c = 0; c < NC && ok; ++c) {
                         ok = warp_wait(&sh->full[stage], phase, abort, budget);
                         if (!ok) break;
@@ -599,13 +612,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint64_t v = desc_v + (uint64_t)((stage * kChunkBytes) >> 4);
 #pragma unroll
                             for (int kk = 0; kk < KV / 16; ++kk) {
-                                // 16 keys: 8 columns of each 64-column half's weights
+                                // 16 keys are 8 columns; the weights of 32 keys lie in their scores' columns
                                 const int key = c * KV + 16 * kk;
-                                const uint32_t col = pcol + (key >> 6) * 64 + ((key & 63) >> 1);
+                                const uint32_t col = pcol + (key & ~31) + ((key & 31) >> 1);
                                 ptx::mma_bf16_ts(tmem + C::kOCol, col, v + (uint64_t)(kk * 2048 >> 4), idesc_o,
-                                                 (i - 1) % kDrain<F32OUT> != 0 || c > 0 || kk > 0 ? 1u : 0u);
+                                                 !fresh || c > 0 || kk > 0 ? 1u : 0u);
                                 if (F32OUT)
-                                    ptx::mma_bf16_ts(tmem + C::kOCol, col + 32, v + (uint64_t)(kk * 2048 >> 4), idesc_o, 1u);
+                                    ptx::mma_bf16_ts(tmem + C::kOCol, col + 16, v + (uint64_t)(kk * 2048 >> 4), idesc_o, 1u);
                             }
                             ptx::mma_commit(&sh->empty[stage]);
                             if (c == NC - 1) ptx::mma_commit(&sh->pv_done[b]);
@@ -650,169 +663,190 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_arrive(&sh->q_full);
         }
     } else {
-        // ---- softmax and epilogue: thread = row and half of the columns
+        // ---- softmax and epilogue: thread = row and half of the columns.
+        // A tile's weights are taken relative to the row's reference of the tile
+        // before.  No maximum is looked for as long as their sum stays below
+        // 2^kLazy, which bounds each of them: a pass over the scores less than a
+        // running maximum needs.  Where a sum passes it (and in the first tile)
+        // the two warps of the row find the maximum, rescale and start over.
         ptx::take_registers<kManyRegs>();
         Walk w(p, start);
         constexpr int HALF = DP / 2;             // output columns of a thread
-        constexpr int G = kDrain<F32OUT>;
-        const int side = warp >> 2;              // which half
+        constexpr int G = kDrain<F32OUT>, NB = C::NB;
+        const int side = warp >> 2, quad = warp & 3;
         const int r = threadIdx.x & (kRows - 1);
-        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
         // log2 units; a scale of 0 becomes one that no score can make count, so
         // that a masked score (-inf) times it still is -inf
         const float sl2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);
         const bool negative = p.scale < 0.f;
+        const float mul = negative ? -sl2 : sl2;
+        const float limit = exp2f(kLazy + kShift<T>);
         const int my_token = r / p.group, my_head = r - my_token * p.group;
-        uint64_t* pair = &sh->pair[warp & 3];
         int gt = 0, consumed = 0;                // tiles and ring chunks before this part
         int part = 0, joined = 0, paired = 0;    // parts before this one, meetings so far
         long long item_start = start.ctas > (int)blockIdx.x ? cut(start, blockIdx.x) - start.skip : 0;
         bool ok = true;
+        // the two warps of these rows meet
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh->pair[quad]);
+            ok = warp_wait(&sh->pair[quad], paired++, abort, budget);
+        };
         for (; w.valid() && ok; w.next(), ++part) {
             const int n = w.j1 - w.j0;
             const int tokens = w.tokens();
             const bool valid = my_token < tokens;
-            const bool active = 32 * (warp & 3) < tokens * p.group;  // the warp has a valid row
-            const int first = w.q.place0 + w.qt * p.tile_tokens;     // place of the first token
+            const bool active = 32 * quad < tokens * p.group;     // the warp has a valid row
+            const int first = w.q.place0 + w.qt * p.tile_tokens;  // place of the first token
             const int lim_first = p.causal ? min(max(first + 1, 0), w.q.len) : w.q.len;
             const int lim = !valid ? w.end : p.causal ? min(max(first + my_token + 1, 0), w.q.len) : w.q.len;
-            float m = -INFINITY, base = -kShift<T>, sum = 0.f;
+            float m = -INFINITY, base = -kShift<T>;  // reference, and what is subtracted from scaled scores
+            float sum = 0.f;                         // weights of this half
             bool bad = false;
-            // this thread's part of the workspace: f32 output drained so far, at maximum ws_base
+            // this thread's part of the workspace: f32 output drained so far, at reference ws_base
             const long long slot = 2LL * blockIdx.x + (w.j0 == 0 ? 1 : 0);
             float* ws_o = p.ws_o + (slot * kRows + r) * DP + side * HALF;
             float ws_base = 0.f;
-            // o = tensor memory's columns c.. + drained * 2^(ws_base - base)
-            auto read_out = [&](int c, bool drained, float f, float (&o)[16]) {
-                float4 x[4];
-                if (drained && valid) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] = __ldcg(reinterpret_cast<const float4*>(ws_o + c) + k);
-                }
-                ptx::tmem_ld16(tmem + lane_base + C::kOCol + side * HALF + c, o);
-                ptx::tmem_wait_ld();
-                ptx::tmem_landed(o);
-                if (drained && valid) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        o[4 * k] = fmaf(x[k].x, f, o[4 * k]);
-                        o[4 * k + 1] = fmaf(x[k].y, f, o[4 * k + 1]);
-                        o[4 * k + 2] = fmaf(x[k].z, f, o[4 * k + 2]);
-                        o[4 * k + 3] = fmaf(x[k].w, f, o[4 * k + 3]);
-                    }
-                }
-                __syncwarp();
-            };
-            auto write_ws = [&](int c, const float (&o)[16]) {
-                if (valid) {
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4)
-                        __stcg(reinterpret_cast<float4*>(ws_o + c + k), make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
-                }
-                __syncwarp();
-            };
+            const uint32_t out_col = tmem + lane_base + C::kOCol + side * HALF;
             for (int i = 0; i < n && ok; ++i) {
-                const int t = gt + i, b = t & 1;
+                const int t = gt + i, b = t % NB;
                 uint64_t* wbar = p.stall_test && t == 0 ? &sh->never : &sh->s_full[b];
-                ok = warp_wait(wbar, t >> 1, abort, budget);
+                ok = warp_wait(wbar, t / NB, abort, budget);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const int key0 = (w.j0 + i) * kKeys;
                 const bool edge = key0 + kKeys > lim_first;  // some row does not see the whole tile
-                const uint32_t taddr = tmem + lane_base + C::kSCol + b * kKeys + 64 * side;
-                if (active) {
-                    float s[2][32];
-                    ptx::tmem_ld32(taddr, s[0]);
-                    ptx::tmem_ld32(taddr + 32, s[1]);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_landed(s[0]);
-                    ptx::tmem_landed(s[1]);
-                    // The straight line from here to the weights is what every tile
-                    // runs; masks and the sign of the scale stay out of it.
-                    if (edge) {
-                        const int see = lim - key0 - 64 * side;  // of these 64 keys, those that the row sees
-                        const float masked = negative ? INFINITY : -INFINITY;
-#pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (k >= see) s[k >> 5][k & 31] = masked;
-                    }
-                    float top[4];
-                    if (negative) {
-#pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            top[k & 3] = k < 4 ? -s[0][k] : fmaxf(top[k & 3], -s[k >> 5][k & 31]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 64; k += 2) {
-                            const float x = fmaxf(s[k >> 5][k & 31], s[k >> 5][(k & 31) + 1]);
-                            top[(k >> 1) & 3] = k < 8 ? x : fmaxf(top[(k >> 1) & 3], x);
-                        }
-                    }
-                    // both halves of a row take the same reference, so their weights meet in one output
-                    const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    sh->row[b][side][r] = mine;
-                    ptx::mbar_arrive(pair);
-                    ok = warp_wait(pair, paired++, abort, budget);
+                const bool fresh = i > 0 && i % G == 0;      // the output goes to the workspace first
+                if (fresh) {
+                    ok = warp_wait(&sh->pv_done[(t - 1) % NB], (t - 1) / NB, abort, budget);
                     if (!ok) break;
-                    const float now = fmaxf(m, fmaxf(mine, *(volatile float*)&sh->row[b][side ^ 1][r]));
-                    const bool grow = valid && now > m && (m == -INFINITY || (now - m) * sl2 > kLazy);
-                    const bool drain = i > 0 && i % G == 0;
-                    if (__any_sync(0xffffffffu, grow) || drain) {
-                        const float old = base;
-                        float keep = 1.f;
-                        if (grow) {
-                            base = now * sl2 - kShift<T>;
-                            keep = m == -INFINITY ? 0.f : ptx::ex2(old - base);
-                            m = now;
-                            sum *= keep;
+                    ptx::tc_fence_after();
+                    if (active) {
+                        const float f = ptx::ex2(ws_base - base);
+#pragma unroll 1
+                        for (int c = 0; c < HALF; c += 16) {
+                            float o[16];
+                            ptx::tmem_ld16(out_col + c, o);
+                            ptx::tmem_wait_ld();
+                            ptx::tmem_landed(o);
+                            if (valid) {
+                                float* to = ws_o + c;
+                                if (i > G && f == 1.f) {
+#pragma unroll
+                                    for (int k = 0; k < 16; k += 4) ptx::red_add4(to + k, o[k], o[k + 1], o[k + 2], o[k + 3]);
+                                } else {
+#pragma unroll
+                                    for (int k = 0; k < 16; k += 4) {
+                                        float4 x = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                                        if (i > G) {
+                                            const float4 y = __ldcg(reinterpret_cast<const float4*>(to + k));
+                                            x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+                                        }
+                                        __stcg(reinterpret_cast<float4*>(to + k), x);
+                                    }
+                                }
+                            }
+                            __syncwarp();
                         }
-                        if (i > 0) {
-                            ok = warp_wait(&sh->pv_done[b ^ 1], (t - 1) >> 1, abort, budget);
+                        ws_base = base;
+                    }
+                }
+                if (active) {
+                    const uint32_t taddr = tmem + lane_base + C::kSCol + b * kKeys + 64 * side;
+                    float s[2][32];
+                    auto scores = [&]() {
+                        ptx::tmem_ld32(taddr, s[0]);
+                        ptx::tmem_ld32(taddr + 32, s[1]);
+                        ptx::tmem_wait_ld();
+                        ptx::tmem_landed(s[0]);
+                        ptx::tmem_landed(s[1]);
+                        if (edge) {
+                            const int see = lim - key0 - 64 * side;  // of these 64 keys, those that the row sees
+                            const float masked = negative ? INFINITY : -INFINITY;
+#pragma unroll
+                            for (int k = 0; k < 64; ++k)
+                                if (k >= see) s[k >> 5][k & 31] = masked;
+                        }
+                    };
+                    bool search = i == 0;
+                    float add = 0.f;
+                    uint32_t hi[32], lo[32];
+#pragma unroll 1
+                    for (bool settled = false;; settled = true) {
+                        if (!search) {
+                            scores();
+                            float2 add0 = make_float2(0.f, 0.f), add1 = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int k = 0; k < 64; k += 2) {
+                                const float2 x = __ffma2_rn(make_float2(s[k >> 5][k & 31], s[k >> 5][(k & 31) + 1]),
+                                                            make_float2(mul, mul), make_float2(-base, -base));
+                                const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+                                if (k & 2) add1 = __fadd2_rn(add1, e);
+                                else add0 = __fadd2_rn(add0, e);
+                                hi[k / 2] = pack2<T>(e.x, e.y);
+                                if (F32OUT) {
+                                    const float2 f = unpack2<T>(hi[k / 2]);
+                                    lo[k / 2] = pack2<T>(e.x - f.x, e.y - f.y);
+                                }
+                            }
+                            add0 = __fadd2_rn(add0, add1);
+                            add = add0.x + add0.y;
+                            if (settled) break;
+                            if (__any_sync(0xffffffffu, valid && add > limit) && lane == 0) sh->grown[quad] = t + 1;
+                            meet();
+                            if (!ok || *(volatile int*)&sh->grown[quad] != t + 1) break;
+                        }
+                        scores();
+                        float top[4];
+#pragma unroll
+                        for (int k = 0; k < 64; ++k) {
+                            const float x = negative ? -s[k >> 5][k & 31] : s[k >> 5][k & 31];
+                            top[k & 3] = k < 4 ? x : fmaxf(top[k & 3], x);
+                        }
+                        const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        sh->top[side][r] = mine;
+                        meet();
+                        if (!ok) break;
+                        const float now = fmaxf(m, fmaxf(mine, *(volatile float*)&sh->top[side ^ 1][r]));
+                        const float to = now > m ? now * sl2 - kShift<T> : base;
+                        const float keep = m == -INFINITY ? 0.f : ptx::ex2(base - to);
+                        if (now > m) sum *= keep;
+                        m = now;
+                        if (i > 0 && !fresh) {
+                            ok = warp_wait(&sh->pv_done[(t - 1) % NB], (t - 1) / NB, abort, budget);
                             if (!ok) break;
                             ptx::tc_fence_after();
-                            const float2 keep2 = make_float2(keep, keep);
-                            const float f = ptx::ex2(ws_base - old);
 #pragma unroll 1
                             for (int c = 0; c < HALF; c += 16) {
                                 float o[16];
-                                if (drain) {
-                                    read_out(c, i > G, f, o);
-                                    write_ws(c, o);
-                                } else {
-                                    uint32_t u[16];
-                                    read_out(c, false, f, o);
+                                uint32_t u[16];
+                                ptx::tmem_ld16(out_col + c, o);
+                                ptx::tmem_wait_ld();
+                                ptx::tmem_landed(o);
 #pragma unroll
-                                    for (int k = 0; k < 16; k += 2) {
-                                        const float2 x = __fmul2_rn(make_float2(o[k], o[k + 1]), keep2);
-                                        u[k] = __float_as_uint(x.x);
-                                        u[k + 1] = __float_as_uint(x.y);
-                                    }
-                                    ptx::tmem_st16(tmem + lane_base + C::kOCol + side * HALF + c, u);
-                                }
+                                for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * keep);
+                                ptx::tmem_st16(out_col + c, u);
                             }
-                            if (drain) ws_base = old;
                         }
+                        base = to;
+                        search = false;
                     }
-                    __syncwarp();
-                    const float2 mul = make_float2(negative ? -sl2 : sl2, negative ? -sl2 : sl2), sub = make_float2(-base, -base);
-                    float2 add0 = make_float2(0.f, 0.f), add1 = make_float2(0.f, 0.f);
-                    uint32_t hi[32], lo[32];
+                    if (!ok) break;
+                    sum += add;
+                    // the weights of 32 keys over their scores: hi in the first 16 columns, lo in the others
 #pragma unroll
-                    for (int k = 0; k < 64; k += 2) {
-                        const float2 x = __ffma2_rn(make_float2(s[k >> 5][k & 31], s[k >> 5][(k & 31) + 1]), mul, sub);
-                        const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-                        if (k & 2) add1 = __fadd2_rn(add1, e);
-                        else add0 = __fadd2_rn(add0, e);
-                        hi[k / 2] = pack2<T>(e.x, e.y);
+                    for (int c = 0; c < 32; c += 16) {
+                        uint32_t x[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) x[k] = hi[c + k];
+                        ptx::tmem_st16(taddr + 2 * c, x);
                         if (F32OUT) {
-                            const float2 f = unpack2<T>(hi[k / 2]);
-                            lo[k / 2] = pack2<T>(e.x - f.x, e.y - f.y);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) x[k] = lo[c + k];
+                            ptx::tmem_st16(taddr + 2 * c + 16, x);
                         }
                     }
-                    ptx::tmem_st32(taddr, hi);
-                    if (F32OUT) ptx::tmem_st32(taddr + 32, lo);
-                    add0 = __fadd2_rn(add0, add1);
-                    sum += add0.x + add0.y;
                 }
                 if (edge) {
                     // Values that some row does not see: those past the item's last
@@ -821,13 +855,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // row's and the last row's last key too; the epilogue gives
                     // them back to the rows that see them.
                     const int lo = max(lim_first - key0, 0), hi = w.end - key0;
-                    const int v0 = consumed + NC * (i < n - 1 ? 2 * i + 2 : 2 * n - 1);
+                    const int v0 = consumed + NC * min(2 * i + C::AHEAD + 1, n + i);
 #pragma unroll 1
                     for (int c = lo / KV; c < NC && ok; ++c) {
                         const int st = (v0 + c) % NS;
                         ok = warp_wait(&sh->full[st], (v0 + c) / NS, abort, budget);
                         if (!ok) break;
-                        const int u = threadIdx.x;  // 0..255: row u / 8, 16 bytes u % 8
+                        const int u = threadIdx.x;  // row u / 8, its 16 bytes u % 8
                         for (int row = max(lo - c * KV, 0) + (u >> 3); row < KV; row += kSoftmax / 8) {
                             uint4* at = reinterpret_cast<uint4*>(ring + st * kChunkBytes + row * 128 + (u & 7) * 16);
 #pragma unroll
@@ -859,41 +893,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             gt += n;
             consumed += 2 * NC * n;
-            // All warps meet: was there an infinity or a NaN among the values of this part?
+            // The row's sum: all softmax warps meet once a part.
+            // (A warp writes here again only after it met its partner in the
+            // first tile of a later part, so the partner has read this.)
+            if (active) sh->sum[side][r] = sum;
+            if (bad) sh->bad = part + 1;
+            ptx::mbar_arrive(&sh->join);
+            ok = warp_wait(&sh->join, joined++, abort, budget);
+            if (!ok) break;
+            sum = *(volatile float*)&sh->sum[0][r] + *(volatile float*)&sh->sum[1][r];
+            // was there an infinity or a NaN among the values of this part?  (a later part's mark only costs a look)
             const bool edges = p.causal && w.j1 * kKeys > lim_first && lim_first < w.end;
-            if (edges) {
-                if (bad) sh->bad = part + 1;
-                ptx::mbar_arrive(&sh->join);
-                ok = warp_wait(&sh->join, joined++, abort, budget);
-                if (!ok) break;
-                bad = *(volatile int*)&sh->bad >= part + 1;  // (a later part's mark only costs a look)
-            }
-            if (active) {
-                // the row's sum: this half and the other
-                sh->row[gt & 1][side][r] = sum;
-                ptx::mbar_arrive(pair);
-                ok = warp_wait(pair, paired++, abort, budget);
-                if (!ok) break;
-                const float other = *(volatile float*)&sh->row[gt & 1][side ^ 1][r];
-                sum = side ? other + sum : sum + other;
-            }
+            bad = edges && *(volatile int*)&sh->bad >= part + 1;
 
             // ---- epilogue
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;
-            ok = warp_wait(&sh->pv_done[(gt - 1) & 1], (gt - 1) >> 1, abort, budget);
+            ok = warp_wait(&sh->pv_done[(gt - 1) % C::NB], (gt - 1) / C::NB, abort, budget);
             if (!ok) break;
             ptx::tc_fence_after();
             const long long token = w.q.row0 + w.qt * p.tile_tokens + my_token;
             const int head = w.head * p.group + my_head;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             if (active) {
+                const bool drained = n > G;
                 const float f = ptx::ex2(ws_base - base);
 #pragma unroll 1
                 for (int c = 0; c < HALF; c += 16) {
                     float o[16];
                     const int dim0 = side * HALF + c;
-                    read_out(c, n > G, f, o);
-                    if (bad && edges && valid) {
+                    ptx::tmem_ld16(out_col + c, o);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_landed(o);
+                    if (drained && valid) {
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4*>(ws_o + c + k));
+                            o[k] = fmaf(x.x, f, o[k]);
+                            o[k + 1] = fmaf(x.y, f, o[k + 1]);
+                            o[k + 2] = fmaf(x.z, f, o[k + 2]);
+                            o[k + 3] = fmaf(x.w, f, o[k + 3]);
+                        }
+                    }
+                    if (bad && valid) {
 #pragma unroll 1
                         for (int key = max(lim_first, w.j0 * kKeys); key < min(lim, w.j1 * kKeys); ++key) {
                             const int page = p.batch.table[w.seq * p.batch.table_stride + page_at(p, key)];
@@ -907,11 +948,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    __syncwarp();
-                    if (!whole) {
-                        write_ws(c, o);
-                    } else if (valid) {
-                        if (F32OUT) {
+                    if (valid) {
+                        if (!whole) {
+#pragma unroll
+                            for (int k = 0; k < 16; k += 4)
+                                __stcg(reinterpret_cast<float4*>(ws_o + c + k), make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
+                        } else if (F32OUT) {
                             float* out = static_cast<float*>(p.out) + token * p.out_token + head * p.out_head + dim0;
 #pragma unroll
                             for (int k = 0; k < 16; k += 4)
