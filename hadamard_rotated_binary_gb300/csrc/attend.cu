@@ -10,14 +10,17 @@
 // grouped model still reads each key once.
 //
 // Work: an item is (sequence, key head, tile of rows) and costs its visible
-// key tiles.  All items lie end to end on one line of tiles, sequences
-// outermost, then key heads (neighbouring CTAs then read the same keys, which
-// L2 serves), and the persistent CTAs cut the line into equal parts, so a long
-// context splits over all SMs and ragged batches balance, with no length known
-// on the host.  A CTA that has only a part of an item leaves its unnormalised
-// output with the row's maximum and sum in the workspace; the last of the
-// item's CTAs to do so joins the parts in their order (results do not depend
-// on which one is last).
+// key tiles and a few more for its begin and end.  All items lie end to end on one line of tiles, sequences
+// outermost, then key heads.  Where the items cost about the same, the CTAs
+// first take whole items in rounds, neighbours side by side: the CTAs on one
+// key head then read the same keys at the same time and L2 serves all but the
+// first.  (2,048 tokens over 32,768 keys, 134 MB of K and V: equal parts of the
+// line alone read 4.8 GB from HBM.)  What is left of the line, or all of it, is
+// cut into equal parts, so a long context splits over all SMs and ragged
+// batches balance, with no length known on the host.  A CTA that has only a
+// part of an item leaves its unnormalised output with the row's maximum and
+// sum in the workspace; the last of the item's CTAs to do so joins the parts in
+// their order (results do not depend on which one is last).
 //
 // Roles of the 16 warps:
 //   0-7   softmax, two warps to 32 rows (each takes half of the columns): S from
@@ -90,14 +93,23 @@ struct Seq {
     int tiles;        // row tiles
 };
 
-// The part of the line that a CTA starts with.
+constexpr int kRounds = 64;       // rounds of whole items at most
+
+struct Item {
+    int seq, head, qt;
+};
+
+// What a CTA has to do: `rounds` whole items, then a part of the line's rest.
 struct Start {
-    long long per;     // tiles of each CTA's part; the first `extra` have one more
+    int rounds;
+    int ctas;          // CTAs that have a part of the rest
+    long long per;     // its length; the first `extra` CTAs have one more
     int extra;
-    int ctas;          // CTAs that have work
-    int seq, head, qt; // item
-    int skip;          // its tiles that belong to earlier CTAs
+    Item item;         // where the part begins
+    int skip;          // its cost that belongs to earlier CTAs
+    long long line;    // where it begins on the rest of the line
     Seq q;             // its sequence
+    Item round[kRounds];
 };
 
 template <int DP>
@@ -114,8 +126,7 @@ struct __align__(8) Shared {
     int last;         // this CTA joins the item's parts
     int bad;          // 1 + the part whose values held an infinity or a NaN
     int grown[4];            // 1 + the last tile that asked for another reference
-    float top[2][kRows];     // maxima of the two halves of a tile's columns
-    float sum[2][kRows];     // their sums of weights over a part
+    float half[2][kRows];    // what a row's two halves tell each other: maxima, sums
     int abort;
 };
 
@@ -151,10 +162,15 @@ __device__ __forceinline__ int item_end(const AttendParams& p, int rows, int pla
     return min(max(place0 + min(rows, (qt + 1) * p.tile_tokens), 0), len);
 }
 
-// Key tiles of an item; one that sees no key still costs a tile (it writes zeros).
-__device__ __forceinline__ int item_tiles(const AttendParams& p, int rows, int place0, int len, int qt)
+// Key tiles of an item; one that sees no key still takes a tile (it writes zeros).
+__device__ __forceinline__ int item_tiles(int end) { return max(1, (end + kKeys - 1) / kKeys); }
+
+// What an item costs, in key tiles: those and its begin and end (queries, the
+// search for the first reference, the output).  On the line the begin and end
+// come first: a cut there leaves the item whole.
+__device__ __forceinline__ int item_cost(const AttendParams& p, int rows, int place0, int len, int qt)
 {
-    return max(1, (item_end(p, rows, place0, len, qt) + kKeys - 1) / kKeys);
+    return item_tiles(item_end(p, rows, place0, len, qt)) + p.item_extra;
 }
 
 template <typename T>
@@ -168,14 +184,14 @@ __device__ __forceinline__ T warp_scan(T v)  // inclusive
     return v;
 }
 
-// Tiles of one key head of sequence base + lane (0 past the last sequence).
+// Cost of one key head of sequence base + lane (0 past the last sequence).
 // Sequences of several row tiles are summed by the whole warp, one after the other.
-__device__ __forceinline__ long long seq_tiles(const AttendParams& p, int base, Seq& q)
+__device__ __forceinline__ long long seq_cost(const AttendParams& p, int base, Seq& q)
 {
     const int lane = threadIdx.x & 31;
     q = {};
     if (base + lane < p.batch.seqs) q = load_seq(p, base + lane);
-    long long sum = q.tiles == 1 ? item_tiles(p, q.rows, q.place0, q.len, 0) : 0;
+    long long sum = q.tiles == 1 ? item_cost(p, q.rows, q.place0, q.len, 0) : 0;
     unsigned many = __ballot_sync(0xffffffffu, q.tiles > 1);
     while (many) {
         const int l = __ffs(many) - 1;
@@ -183,7 +199,7 @@ __device__ __forceinline__ long long seq_tiles(const AttendParams& p, int base, 
         const int rows = __shfl_sync(0xffffffffu, q.rows, l), place0 = __shfl_sync(0xffffffffu, q.place0, l);
         const int len = __shfl_sync(0xffffffffu, q.len, l), tiles = __shfl_sync(0xffffffffu, q.tiles, l);
         long long part = 0;
-        for (int qt = lane; qt < tiles; qt += 32) part += item_tiles(p, rows, place0, len, qt);
+        for (int qt = lane; qt < tiles; qt += 32) part += item_cost(p, rows, place0, len, qt);
 #pragma unroll
         for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
         if (lane == l) sum = part;
@@ -196,36 +212,102 @@ __device__ __forceinline__ long long divide(long long x, long long n)
 {
     return ((x | n) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)n) : x / n;
 }
-// First tile of CTA c's part of the line, and the CTA whose part holds tile x.
-__device__ __forceinline__ long long cut(const Start& s, int c) { return s.per * c + min(c, s.extra); }
+// The CTA whose part of the line holds x.
 __device__ __forceinline__ int cta_of(const Start& s, long long x)
 {
     const long long longer = s.extra * (s.per + 1);
     return x < longer ? (int)divide(x, s.per + 1) : s.extra + (int)divide(x - longer, s.per);
 }
 
-// One warp: where this CTA's part of the line begins.
+// One warp: what this CTA has to do.
 __device__ void locate(const AttendParams& p, Start* out)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, grid = (int)gridDim.x, me = (int)blockIdx.x;
     Seq q;
-    long long total = 0, one = 0;
+    long long total = 0, items = 0, one = 0;
+    int least = 0x7fffffff, most = 0;
     for (int base = 0; base < p.batch.seqs; base += 32) {
-        one = seq_tiles(p, base, q);
+        one = seq_cost(p, base, q);
         long long n = one * p.kv_heads;
+        int count = q.tiles;
+        if (count) {
+            least = min(least, item_cost(p, q.rows, q.place0, q.len, 0));
+            most = max(most, item_cost(p, q.rows, q.place0, q.len, q.tiles - 1));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            n += __shfl_xor_sync(0xffffffffu, n, o);
+            count += __shfl_xor_sync(0xffffffffu, count, o);
+        }
+        total += n;
+        items += (long long)count * p.kv_heads;
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    // Rounds of whole items when they cost about the same (within an eighth).
+    const int rounds = items >= grid && most - least <= least / 8 ? (int)min(divide(items, grid), (long long)kRounds) : 0;
+
+    // Cost of row tiles 0 .. qt-1 of a sequence.
+    auto cost_before = [&](const Seq& u, int qt) {
+        long long n = 0;
+        for (int i = lane; i < qt; i += 32) n += item_cost(p, u.rows, u.place0, u.len, i);
 #pragma unroll
         for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-        total += n;
+        return n;
+    };
+    auto lane_seq = [&](int l) {
+        Seq u;
+        u.row0 = __shfl_sync(0xffffffffu, q.row0, l);
+        u.rows = __shfl_sync(0xffffffffu, q.rows, l);
+        u.place0 = __shfl_sync(0xffffffffu, q.place0, l);
+        u.len = __shfl_sync(0xffffffffu, q.len, l);
+        u.tiles = __shfl_sync(0xffffffffu, q.tiles, l);
+        return u;
+    };
+    // The rounds' items, and the tiles on the line before the first item after them.
+    long long line0 = 0;
+    if (rounds) {
+        long long items_before = 0, tiles_upto = 0;
+        line0 = total;
+        int k = 0;
+        for (int base = 0; base < p.batch.seqs && k <= rounds; base += 32) {
+            if (p.batch.seqs > 32) one = seq_cost(p, base, q);
+            const long long upto = items_before + warp_scan((long long)q.tiles * p.kv_heads);
+            const long long tiles = tiles_upto + warp_scan(one * p.kv_heads);
+            for (; k <= rounds; ++k) {
+                const long long x = k < rounds ? me + (long long)k * grid : (long long)rounds * grid;
+                const unsigned past = __ballot_sync(0xffffffffu, upto > x);
+                if (!past) break;
+                const int l = __ffs(past) - 1;
+                const Seq u = lane_seq(l);
+                const int off = (int)(x - __shfl_sync(0xffffffffu, upto - (long long)q.tiles * p.kv_heads, l));
+                const int head = off / u.tiles, qt = off - head * u.tiles;
+                if (k < rounds) {
+                    if (lane == 0) out->round[k] = {base + l, head, qt};
+                } else {
+                    const long long per = __shfl_sync(0xffffffffu, one, l);
+                    line0 = __shfl_sync(0xffffffffu, tiles, l) - per * (p.kv_heads - head) + cost_before(u, qt);
+                }
+            }
+            items_before = __shfl_sync(0xffffffffu, upto, 31);
+            tiles_upto = __shfl_sync(0xffffffffu, tiles, 31);
+        }
     }
-    Start st = {};
-    st.ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
-    if ((int)blockIdx.x < st.ctas) {
-        st.per = divide(total, st.ctas);
-        st.extra = (int)(total - st.per * st.ctas);
-        const long long x = cut(st, blockIdx.x);
+
+    // The rest of the line, in equal parts.
+    const long long rest = total - line0;
+    const int ctas = rest < (long long)grid ? (int)rest : grid;
+    Item item = {};
+    int skip = 0, extra = 0;
+    long long per_cta = 0, line = 0;
+    Seq mine = {};
+    if (me < ctas) {
+        per_cta = divide(rest, ctas);
+        extra = (int)(rest - per_cta * ctas);
+        const long long x = line0 + per_cta * me + min(me, extra);
         long long before = 0;
         for (int base = 0; base < p.batch.seqs; base += 32) {
-            if (p.batch.seqs > 32) one = seq_tiles(p, base, q);
+            if (p.batch.seqs > 32) one = seq_cost(p, base, q);
             const long long all = one * p.kv_heads;
             const long long upto = before + warp_scan(all);
             const unsigned past = __ballot_sync(0xffffffffu, upto > x);
@@ -233,23 +315,19 @@ __device__ void locate(const AttendParams& p, Start* out)
                 const int l = __ffs(past) - 1;
                 const long long per = __shfl_sync(0xffffffffu, one, l);
                 long long off = x - __shfl_sync(0xffffffffu, upto - all, l);
-                st.seq = base + l;
-                st.head = (int)divide(off, per);
-                off -= st.head * per;
-                st.q.row0 = __shfl_sync(0xffffffffu, q.row0, l);
-                st.q.rows = __shfl_sync(0xffffffffu, q.rows, l);
-                st.q.place0 = __shfl_sync(0xffffffffu, q.place0, l);
-                st.q.len = __shfl_sync(0xffffffffu, q.len, l);
-                st.q.tiles = __shfl_sync(0xffffffffu, q.tiles, l);
-                for (int qb = 0; qb < st.q.tiles; qb += 32) {
-                    const int n = qb + lane < st.q.tiles
-                                      ? item_tiles(p, st.q.rows, st.q.place0, st.q.len, qb + lane) : 0;
+                mine = lane_seq(l);
+                item.seq = base + l;
+                item.head = (int)divide(off, per);
+                off -= item.head * per;
+                for (int qb = 0; qb < mine.tiles; qb += 32) {
+                    const int n = qb + lane < mine.tiles ? item_cost(p, mine.rows, mine.place0, mine.len, qb + lane) : 0;
                     const long long to = warp_scan((long long)n);
                     const unsigned hit = __ballot_sync(0xffffffffu, to > off);
                     if (hit) {
                         const int h = __ffs(hit) - 1;
-                        st.qt = qb + h;
-                        st.skip = (int)(off - __shfl_sync(0xffffffffu, to - n, h));
+                        item.qt = qb + h;
+                        skip = (int)(off - __shfl_sync(0xffffffffu, to - n, h));
+                        line = x - line0 - skip;
                         break;
                     }
                     off -= __shfl_sync(0xffffffffu, to, 31);
@@ -259,53 +337,104 @@ __device__ void locate(const AttendParams& p, Start* out)
             before = __shfl_sync(0xffffffffu, upto, 31);
         }
     }
-    if (lane == 0) *out = st;
+    if (lane == 0) {
+        out->rounds = rounds;
+        out->ctas = ctas;
+        out->per = per_cta;
+        out->extra = extra;
+        out->item = item;
+        out->skip = skip;
+        out->line = line;
+        out->q = mine;
+    }
 }
 
-// A CTA's parts of items, one after the other; every role walks them alike.
+// A CTA's items and parts of items, one after the other; every role walks them alike.
 struct Walk {
     const AttendParams& p;
-    long long left;       // tiles of this CTA still to come
+    const Start& start;
+    int round;            // whole items taken
+    long long left;       // length of the part of the line still to come
+    long long line;       // where the item begins on the line's rest
+    int from;             // its cost that belongs to earlier CTAs
     int seq, head, qt;
     Seq q;
     int end;              // keys the item's last row sees
     int tiles, j0, j1;    // the item's key tiles, and this part of them
 
-    __device__ Walk(const AttendParams& params, const Start& s) : p(params), seq(s.seq), head(s.head), qt(s.qt)
+    __device__ Walk(const AttendParams& params, const Start& s) : p(params), start(s), round(0), left(0), line(0), from(0), seq(-1)
     {
-        left = 0;
-        j0 = j1 = 0;
-        if ((int)blockIdx.x < s.ctas) {
-            left = s.per + ((int)blockIdx.x < s.extra ? 1 : 0);
-            q = s.q;
-            set(s.skip);
-        }
+        if (start.rounds) take_round();
+        else take_rest();
     }
-    __device__ bool valid() const { return left > 0; }
-    __device__ void set(int skip)
+    __device__ bool valid() const { return round < start.rounds || left > 0; }
+    __device__ bool in_rest() const { return round >= start.rounds; }
+    __device__ void set()
     {
         end = item_end(p, q.rows, q.place0, q.len, qt);
-        tiles = max(1, (end + kKeys - 1) / kKeys);
-        j0 = skip;
-        j1 = (int)min((long long)tiles, j0 + left);
+        tiles = item_tiles(end);
+        j0 = 0;
+        j1 = tiles;
+        if (in_rest()) {
+            j0 = max(0, from - p.item_extra);
+            j1 = (int)max(0LL, min((long long)tiles, from + left - p.item_extra));
+        }
+    }
+    __device__ void take_round()
+    {
+        const Item it = start.round[round];
+        if (it.seq != seq) q = load_seq(p, it.seq);
+        seq = it.seq;
+        head = it.head;
+        qt = it.qt;
+        set();
+    }
+    __device__ void take_rest()
+    {
+        if ((int)blockIdx.x >= start.ctas) return;
+        left = start.per + ((int)blockIdx.x < start.extra ? 1 : 0);
+        line = start.line;
+        from = start.skip;
+        seq = start.item.seq;
+        head = start.item.head;
+        qt = start.item.qt;
+        q = start.q;
+        set();
+        if (j0 >= j1) step();  // a part of an item's begin alone
     }
     __device__ void next()
     {
-        left -= j1 - j0;
-        if (left <= 0) return;
-        if (++qt == q.tiles) {
-            qt = 0;
-            if (++head == p.kv_heads) {
-                head = 0;
-                q.tiles = 0;
-                while (q.tiles == 0 && seq + 1 < p.batch.seqs) q = load_seq(p, ++seq);
-                if (q.tiles == 0) {  // the lengths changed under the call
-                    left = 0;
-                    return;
+        if (round < start.rounds) {
+            if (++round < start.rounds) take_round();
+            else take_rest();
+        } else {
+            step();
+        }
+    }
+    // The next item of the part of the line that has a tile in it.
+    __device__ void step()
+    {
+        do {
+            const int cost = tiles + p.item_extra;
+            left -= cost - from;
+            line += cost;
+            from = 0;
+            if (left <= 0) return;
+            if (++qt == q.tiles) {
+                qt = 0;
+                if (++head == p.kv_heads) {
+                    head = 0;
+                    q.tiles = 0;
+                    while (q.tiles == 0 && seq + 1 < p.batch.seqs) q = load_seq(p, ++seq);
+                    if (q.tiles == 0) {  // the lengths changed under the call
+                        left = 0;
+                        return;
+                    }
                 }
             }
-        }
-        set(0);
+            set();
+            if (j1 == 0) left = 0;  // the part ends in this item's begin
+        } while (left > 0 && j0 >= j1);
     }
     // tokens of the row tile
     __device__ int tokens() const { return min(p.tile_tokens, q.rows - qt * p.tile_tokens); }
@@ -416,30 +545,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long budget = p.wait_budget_ns;
 
-    if (threadIdx.x == 32 * kTmaWarp) {
-        for (int i = 0; i < NS; ++i) {
-            ptx::mbar_init(&sh->full[i], 1);
-            ptx::mbar_init(&sh->empty[i], 1);
-        }
-        ptx::mbar_init(&sh->q_full, kQThreads);
-        ptx::mbar_init(&sh->q_empty, 1);
-        for (int i = 0; i < C::NB; ++i) {
-            ptx::mbar_init(&sh->s_full[i], 1);
-            ptx::mbar_init(&sh->p_ready[i], kSoftmax);
-            ptx::mbar_init(&sh->pv_done[i], 1);
-        }
-        ptx::mbar_init(&sh->o_free, kSoftmax);
-        for (int i = 0; i < 4; ++i) {
-            ptx::mbar_init(&sh->pair[i], 2);
-            sh->grown[i] = 0;
-        }
-        ptx::mbar_init(&sh->join, kSoftmax);
-        ptx::mbar_init(&sh->never, 1);
-        ptx::mbar_init(&sh->drain, 1);
-        sh->abort = 0;
-        sh->bad = 0;
+    if (warp == kTmaWarp && lane < NS) {
+        ptx::mbar_init(&sh->full[lane], 1);
+        ptx::mbar_init(&sh->empty[lane], 1);
         ptx::mbar_fence_init();
         ptx::fence_proxy_async_smem();
+    }
+    if (warp == kTmaWarp + 1) {
+        if (lane < C::NB) {
+            ptx::mbar_init(&sh->s_full[lane], 1);
+            ptx::mbar_init(&sh->p_ready[lane], kSoftmax);
+            ptx::mbar_init(&sh->pv_done[lane], 1);
+        } else if (lane >= 4 && lane < 8) {
+            ptx::mbar_init(&sh->pair[lane - 4], 2);
+            if (lane == 4) sh->abort = sh->bad = 0;
+        } else if (lane == 8) {
+            ptx::mbar_init(&sh->q_full, kQThreads);
+            ptx::mbar_init(&sh->q_empty, 1);
+            ptx::mbar_init(&sh->o_free, kSoftmax);
+        } else if (lane == 9) {
+            ptx::mbar_init(&sh->join, kSoftmax);
+            ptx::mbar_init(&sh->never, 1);
+            ptx::mbar_init(&sh->drain, 1);
+        } else if (lane >= 10 && lane < 14) {
+            sh->grown[lane - 10] = 0;
+        }
+        ptx::mbar_fence_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == kTmaWarp + 2 && lane == 0) {
         ptx::prefetch_tmap(&tmap_k);
         ptx::prefetch_tmap(&tmap_v);
     }
@@ -685,7 +819,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int my_token = r / p.group, my_head = r - my_token * p.group;
         int gt = 0, consumed = 0;                // tiles and ring chunks before this part
         int part = 0, joined = 0, paired = 0;    // parts before this one, meetings so far
-        long long item_start = start.ctas > (int)blockIdx.x ? cut(start, blockIdx.x) - start.skip : 0;
         bool ok = true;
         // the two warps of these rows meet
         auto meet = [&]() {
@@ -706,8 +839,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool bad = false;
             // this thread's part of the workspace: f32 output drained so far, at reference ws_base
             const long long slot = 2LL * blockIdx.x + (w.j0 == 0 ? 1 : 0);
-            float* ws_o = p.ws_o + (slot * kRows + r) * DP + side * HALF;
+            // Up to 32 rows lie one after the other; more lie four columns of all rows
+            // after the other, so that a warp's accesses are consecutive.
+            const bool by_row = tokens * p.group <= 32;
+            const int ws_col = by_row ? 1 : kRows, ws_row = by_row ? DP / 4 : 1;
+            float4* ws_o = reinterpret_cast<float4*>(p.ws_o) + slot * (DP / 4) * kRows + side * (HALF / 4) * ws_col + r * ws_row;
             float ws_base = 0.f;
+            // before it writes what its partner may still read of the part before
+            if (active && part > 0) meet();
+            if (!ok) break;
             const uint32_t out_col = tmem + lane_base + C::kOCol + side * HALF;
             for (int i = 0; i < n && ok; ++i) {
                 const int t = gt + i, b = t % NB;
@@ -731,20 +871,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ptx::tmem_wait_ld();
                             ptx::tmem_landed(o);
                             if (valid) {
-                                float* to = ws_o + c;
-                                if (i > G && f == 1.f) {
 #pragma unroll
-                                    for (int k = 0; k < 16; k += 4) ptx::red_add4(to + k, o[k], o[k + 1], o[k + 2], o[k + 3]);
-                                } else {
-#pragma unroll
-                                    for (int k = 0; k < 16; k += 4) {
-                                        float4 x = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                                        if (i > G) {
-                                            const float4 y = __ldcg(reinterpret_cast<const float4*>(to + k));
-                                            x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
-                                        }
-                                        __stcg(reinterpret_cast<float4*>(to + k), x);
+                                for (int k = 0; k < 16; k += 4) {
+                                    float4* to = ws_o + (c + k) / 4 * ws_col;
+                                    float4 x = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                                    if (i > G && f == 1.f) {
+                                        ptx::red_add4(to, x);
+                                        continue;
                                     }
+                                    if (i > G) {
+                                        const float4 y = __ldcg(to);
+                                        x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+                                    }
+                                    __stcg(to, x);
                                 }
                             }
                             __syncwarp();
@@ -805,10 +944,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             top[k & 3] = k < 4 ? x : fmaxf(top[k & 3], x);
                         }
                         const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                        sh->top[side][r] = mine;
+                        sh->half[side][r] = mine;
                         meet();
                         if (!ok) break;
-                        const float now = fmaxf(m, fmaxf(mine, *(volatile float*)&sh->top[side ^ 1][r]));
+                        const float now = fmaxf(m, fmaxf(mine, *(volatile float*)&sh->half[side ^ 1][r]));
                         const float to = now > m ? now * sl2 - kShift<T> : base;
                         const float keep = m == -INFINITY ? 0.f : ptx::ex2(base - to);
                         if (now > m) sum *= keep;
@@ -894,14 +1033,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             gt += n;
             consumed += 2 * NC * n;
             // The row's sum: all softmax warps meet once a part.
-            // (A warp writes here again only after it met its partner in the
-            // first tile of a later part, so the partner has read this.)
-            if (active) sh->sum[side][r] = sum;
+            if (active) {
+                meet();  // (the partner has read the maxima)
+                if (!ok) break;
+                sh->half[side][r] = sum;
+            }
             if (bad) sh->bad = part + 1;
             ptx::mbar_arrive(&sh->join);
             ok = warp_wait(&sh->join, joined++, abort, budget);
             if (!ok) break;
-            sum = *(volatile float*)&sh->sum[0][r] + *(volatile float*)&sh->sum[1][r];
+            sum = *(volatile float*)&sh->half[0][r] + *(volatile float*)&sh->half[1][r];
             // was there an infinity or a NaN among the values of this part?  (a later part's mark only costs a look)
             const bool edges = p.causal && w.j1 * kKeys > lim_first && lim_first < w.end;
             bad = edges && *(volatile int*)&sh->bad >= part + 1;
@@ -915,8 +1056,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int head = w.head * p.group + my_head;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             if (active) {
-                const bool drained = n > G;
+                const bool drained = n > G && valid;
                 const float f = ptx::ex2(ws_base - base);
+                float4 x[4] = {};
+                if (drained) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = __ldcg(ws_o + k * ws_col);
+                }
 #pragma unroll 1
                 for (int c = 0; c < HALF; c += 16) {
                     float o[16];
@@ -924,14 +1070,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_ld16(out_col + c, o);
                     ptx::tmem_wait_ld();
                     ptx::tmem_landed(o);
-                    if (drained && valid) {
+                    if (drained) {
 #pragma unroll
-                        for (int k = 0; k < 16; k += 4) {
-                            const float4 x = __ldcg(reinterpret_cast<const float4*>(ws_o + c + k));
-                            o[k] = fmaf(x.x, f, o[k]);
-                            o[k + 1] = fmaf(x.y, f, o[k + 1]);
-                            o[k + 2] = fmaf(x.z, f, o[k + 2]);
-                            o[k + 3] = fmaf(x.w, f, o[k + 3]);
+                        for (int k = 0; k < 4; ++k) {
+                            o[4 * k] = fmaf(x[k].x, f, o[4 * k]);
+                            o[4 * k + 1] = fmaf(x[k].y, f, o[4 * k + 1]);
+                            o[4 * k + 2] = fmaf(x[k].z, f, o[4 * k + 2]);
+                            o[4 * k + 3] = fmaf(x[k].w, f, o[4 * k + 3]);
+                            if (c + 16 < HALF) x[k] = __ldcg(ws_o + ((c + 16) / 4 + k) * ws_col);
                         }
                     }
                     if (bad && valid) {
@@ -952,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!whole) {
 #pragma unroll
                             for (int k = 0; k < 16; k += 4)
-                                __stcg(reinterpret_cast<float4*>(ws_o + c + k), make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
+                                __stcg(ws_o + (c + k) / 4 * ws_col, make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
                         } else if (F32OUT) {
                             float* out = static_cast<float*>(p.out) + token * p.out_token + head * p.out_head + dim0;
 #pragma unroll
@@ -978,78 +1124,125 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (whole) {
                 if (valid && side == 0 && p.lse)
                     p.lse[token * p.heads + head] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (base + log2f(sum));
-                item_start += w.tiles;
                 continue;
             }
 
             // ---- a part of an item: the last one to arrive joins them
             if (valid && side == 0)
                 __stcg(reinterpret_cast<float2*>(p.ws_ml) + slot * kRows + r, make_float2(sum == 0.f ? -INFINITY : base, sum));
-            const int from = cta_of(start, item_start);
-            const int to = cta_of(start, item_start + w.tiles - 1);
-            __threadfence();
+            const int from = cta_of(start, w.line + p.item_extra);
+            const int to = cta_of(start, w.line + p.item_extra + w.tiles - 1);
+            const int parts = to - from + 1;
             ptx::mbar_arrive(&sh->join);
             ok = warp_wait(&sh->join, joined++, abort, budget);
             if (!ok) break;
             if (threadIdx.x == 0) {
-                const int before = atomicAdd(&p.tickets[from], 1);
-                sh->last = before == to - from;
+                // (carries what the other threads wrote before they met, and brings
+                // what the other CTAs' threads wrote before theirs)
+                sh->last = ptx::atom_add_acq_rel(&p.tickets[from], 1) == parts - 1;
                 if (sh->last) p.tickets[from] = 0;
             }
             ptx::mbar_arrive(&sh->join);
             ok = warp_wait(&sh->join, joined++, abort, budget);
             if (!ok) break;
             if (*(volatile int*)&sh->last) {
-                __threadfence();
                 const int rows = tokens * p.group;
-                for (int row = warp; row < rows; row += kSoftmax / 32) {
-                    // the first part lies in its CTA's second slot, the others in their first
-                    auto slot_of = [&](int c) { return ((2LL * c + (c == from ? 1 : 0)) * kRows + row); };
-                    float top = -INFINITY;
-                    for (int c = from + lane; c <= to; c += 32)
-                        top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot_of(c)).x);
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    float total = 0.f, acc[DP / 32] = {};
-                    for (int c0 = from; c0 <= to; c0 += 32) {
-                        float wgt = 0.f, part_sum = 0.f;
-                        if (c0 + lane <= to) {
-                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot_of(c0 + lane));
-                            wgt = ml.y == 0.f ? 0.f : ptx::ex2(ml.x - ref);
-                            part_sum = wgt * ml.y;
-                        }
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) part_sum += __shfl_xor_sync(0xffffffffu, part_sum, o);
-                        total += part_sum;
-                        const int parts = min(32, to - c0 + 1);
+                const long long tok0 = w.q.row0 + w.qt * p.tile_tokens;
+                // the first part lies in its CTA's second slot, the others in their first
+                auto slot_of = [&](int k) { return 2LL * (from + k) + (k == 0 ? 1 : 0); };
+                float2* ml = reinterpret_cast<float2*>(p.ws_ml);
+                const float4* parts_o = reinterpret_cast<const float4*>(p.ws_o);
+                auto weight = [&](float2 x, float ref) { return x.y == 0.f ? 0.f : ptx::ex2(x.x - ref); };
+                auto write_lse = [&](int row, float ref, float total) {
+                    const int tk = row / p.group;
+                    p.lse[(tok0 + tk) * p.heads + w.head * p.group + row - tk * p.group] =
+                        total == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(total));
+                };
+                auto add = [&](float4& acc, float x, float4 o) {
+                    // a part without a key (weight 0) adds nothing, whatever it holds
+                    if (x != 0.f) acc = make_float4(fmaf(x, o.x, acc.x), fmaf(x, o.y, acc.y), fmaf(x, o.z, acc.z), fmaf(x, o.w, acc.w));
+                };
+                auto write_out = [&](int row, int c, float4 v) {
+                    if (4 * c >= p.dim) return;
+                    const int tk = row / p.group;
+                    const long long at = (tok0 + tk) * p.out_token + (w.head * p.group + row - tk * p.group) * p.out_head + 4 * c;
+                    if (F32OUT) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
+                    else *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+                };
+                const float2 none = make_float2(-INFINITY, 0.f);
+                if (!by_row) {
+                    // Many rows: a lane takes a row and an eighth of its columns.
+                    constexpr int kCols = DP / 32;
+                    for (int u = threadIdx.x; u < 8 * kRows; u += kSoftmax) {
+                        const int row = u & (kRows - 1), c0 = (u / kRows) * kCols;
+                        if (row >= rows) continue;
+                        float top = -INFINITY, total = 0.f;
 #pragma unroll 4
+                        for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(ml + slot_of(k) * kRows + row).x);
+                        const float ref = top == -INFINITY ? 0.f : top;
+                        float4 acc[kCols] = {};
                         for (int k = 0; k < parts; ++k) {
-                            const float x = __shfl_sync(0xffffffffu, wgt, k);
-                            const float* o = p.ws_o + slot_of(c0 + k) * DP + lane;
-                            // a part without a key (weight 0) adds nothing, whatever it holds
-                            if (x != 0.f) {
+                            const float2 x = __ldcg(ml + slot_of(k) * kRows + row);
+                            float4 o[kCols];
 #pragma unroll
-                                for (int d = 0; d < DP / 32; ++d) acc[d] += x * __ldcg(o + 32 * d);
+                            for (int c = 0; c < kCols; ++c) o[c] = __ldcg(parts_o + (slot_of(k) * (DP / 4) + c0 + c) * kRows + row);
+                            const float f = weight(x, ref);
+                            total += f * x.y;
+#pragma unroll
+                            for (int c = 0; c < kCols; ++c) add(acc[c], f, o[c]);
+                        }
+                        const float scale = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c)
+                            write_out(row, c0 + c, make_float4(acc[c].x * scale, acc[c].y * scale, acc[c].z * scale, acc[c].w * scale));
+                        if (p.lse && c0 == 0) write_lse(row, ref, total);
+                    }
+                } else {
+                    // A few rows of many parts (single tokens over a long context): a
+                    // warp takes a row, its lanes first the parts, then the columns.
+                    for (int row = warp; row < rows; row += kSoftmax / 32) {
+                        const float2 x0 = lane < parts ? __ldcg(ml + slot_of(lane) * kRows + row) : none;
+                        float top = x0.x;
+                        for (int k = lane + 32; k < parts; k += 32) top = fmaxf(top, __ldcg(ml + slot_of(k) * kRows + row).x);
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const float ref = top == -INFINITY ? 0.f : top;
+                        constexpr int V = DP <= 128 ? 1 : DP / 128;  // float4 columns of a lane
+                        constexpr int kBatch = 8 / V;                // parts in flight
+                        float total = 0.f;
+                        float4 acc[V] = {};
+                        for (int k0 = 0; k0 < parts; k0 += 32) {
+                            const float2 x = k0 == 0 ? x0 : k0 + lane < parts ? __ldcg(ml + slot_of(k0 + lane) * kRows + row) : none;
+                            const float mine = weight(x, ref);
+                            total += mine * x.y;
+                            for (int k = 0; k < min(32, parts - k0); k += kBatch) {
+                                float4 o[kBatch][V];
+#pragma unroll
+                                for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                                    for (int v = 0; v < V; ++v)
+                                        if (k0 + k + j < parts && lane + 32 * v < DP / 4)
+                                            o[j][v] = __ldcg(parts_o + (slot_of(k0 + k + j) * kRows + row) * (DP / 4) + lane + 32 * v);
+#pragma unroll
+                                for (int j = 0; j < kBatch; ++j) {
+                                    const float f = __shfl_sync(0xffffffffu, mine, k + j);
+#pragma unroll
+                                    for (int v = 0; v < V; ++v)
+                                        if (k0 + k + j < parts && lane + 32 * v < DP / 4) add(acc[v], f, o[j][v]);
+                                }
                             }
                         }
-                    }
-                    const int tk = row / p.group, g = row - tk * p.group;
-                    const long long tok = w.q.row0 + w.qt * p.tile_tokens + tk;
-                    const int hd = w.head * p.group + g;
-                    const float scale = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
-                    for (int d = 0; d < DP / 32; ++d) {
-                        if (lane + 32 * d >= p.dim) continue;
-                        const long long at = tok * p.out_token + hd * p.out_head + lane + 32 * d;
-                        if (F32OUT) static_cast<float*>(p.out)[at] = acc[d] * scale;
-                        else static_cast<T*>(p.out)[at] = from_f32<T>(acc[d] * scale);
+                        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+                        const float scale = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            if (lane + 32 * v < DP / 4)
+                                write_out(row, lane + 32 * v, make_float4(acc[v].x * scale, acc[v].y * scale, acc[v].z * scale, acc[v].w * scale));
+                        if (p.lse && lane == 0) write_lse(row, ref, total);
                     }
-                    if (p.lse && lane == 0)
-                        p.lse[tok * p.heads + hd] = total == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(total));
                 }
             }
-            item_start += w.tiles;
         }
     }
     ptx::tc_fence_before();
@@ -1100,6 +1293,11 @@ void bitlin_attend_boxes(int dim, int page_size, int* box_k, int* box_v)
     *box_k = gcd(page_size, kKeys);
     *box_v = gcd(page_size, 8192 / padded);
 }
+
+// Measured, in us, on 4 prompts of 700-4,096 tokens (128 dims): 463 without,
+// 411 at 2, 377 at 4, 390 at 6; 2,048 tokens over 32,768 keys (256 dims, items
+// of about 250 tiles): 1,161 without, 1,152 at 2, 1,167 at 4.
+int bitlin_attend_item_extra(int dim) { return dim > 128 ? 2 : 4; }
 
 size_t bitlin_attend_workspace(int dim, int num_sms, size_t* ml_offset, size_t* ticket_offset)
 {

@@ -317,6 +317,7 @@ bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
     p.dim = kv->dim;
     p.causal = causal;
     p.tile_tokens = 128 / p.group;
+    p.item_extra = bitlin_attend_item_extra(kv->dim);
     bitlin_attend_boxes(kv->dim, kv->page_size, &p.box_k, &p.box_v);
     p.stall_test = kv->stall_test;
     p.scale = scale;

@@ -103,6 +103,7 @@ struct AttendParams {
     int pages, page_size, page_shift;  // page_shift: log2 of a power of two, else -1
     int tokens, heads, kv_heads, group, dim, causal;
     int tile_tokens;           // tokens of a 128-row tile: 128 / group
+    int item_extra;            // key tiles that an item's begin and end cost
     int box_k, box_v;          // slots of a page per TMA copy
     int stall_test;
     float scale;
@@ -138,6 +139,8 @@ struct bitlin_kv {
 cudaError_t bitlin_launch_turn(const bitlin_impl::TurnParams& p, int src_dtype, int dst_dtype, cudaStream_t s);
 cudaError_t bitlin_launch_attend(const bitlin_impl::AttendParams& p, int dtype, int out_dtype, const void* tmap_k,
                                  const void* tmap_v, int num_sms, cudaStream_t s);
+// What an item of attention's work costs beside its key tiles, in key tiles.
+int bitlin_attend_item_extra(int dim);
 // Slots per TMA copy of the key and value pools.
 void bitlin_attend_boxes(int dim, int page_size, int* box_k, int* box_v);
 // Bytes of the attention workspace, and where its parts begin (the outputs at 0).

@@ -245,10 +245,17 @@ __device__ __forceinline__ void give_registers()
 }
 
 // Four consecutive floats added to global memory (16-byte aligned), no answer.
-__device__ __forceinline__ void red_add4(float* p, float a, float b, float c, float d)
+__device__ __forceinline__ void red_add4(float4* p, float4 v)
 {
-    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d)
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
+}
+
+__device__ __forceinline__ int atom_add_acq_rel(int* p, int v)
+{
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
 }
 
 __device__ __forceinline__ float ex2(float x)
