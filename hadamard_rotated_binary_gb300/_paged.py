@@ -1,45 +1,23 @@
-"""Binding of the attention side: rotary positions, the paged cache and attention over it
-(argument marshalling only; the calls are declared in include/bitlin.h)."""
+"""Binding of the attention side: rotary positions, the paged cache and attention over it.
+
+Handles live here (ctypes, as in ``_binding``); the calls on tensors are marshalled by the compiled
+``_paged_native`` (csrc/paged_native.cpp)."""
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
-from ._binding import BITLIN_OK, BitlinError, Rows, Batch, lib
+from ._binding import BITLIN_OK, Batch, BitlinError, lib
+
+lib()  # libbitlin.so first: the compiled binding is linked against it
+
+from . import _paged_native as native  # noqa: E402
 
 F32, BF16, F16 = 0, 1, 2
 PAIRS_HALF, PAIRS_ADJACENT = 0, 1
 
 _CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
-
-
-def _rows(x, what: str) -> Rows:
-    """The C-ABI's view of a CUDA tensor [tokens][heads][dim] whose last dimension is contiguous."""
-    code = _CODES.get(x.dtype)
-    if code is None or not x.is_cuda or x.dim() != 3:
-        raise ValueError(f"{what} must be a float32, bfloat16 or float16 CUDA tensor [tokens][heads][dim]")
-    token, head, one = x.stride()
-    if one != 1 and x.shape[2] != 1:
-        raise ValueError(f"{what}'s last dimension must be contiguous")
-    # a dimension of one has no stride that matters
-    if x.shape[1] == 1:
-        head = x.shape[2]
-    if x.shape[0] == 1:
-        token = x.shape[1] * head
-    return Rows(x.data_ptr(), code, token, head)
-
-
-def _stream(stream, device) -> int:
-    # the raw handle: building a Stream object costs more than the launch
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-
-
-def _positions(pos, axes: int, tokens: int):
-    if pos.dtype != torch.int32 or not pos.is_cuda or not pos.is_contiguous() or pos.numel() != axes * tokens:
-        raise ValueError(f"pos must be a contiguous int32 CUDA tensor [{axes}][{tokens}]")
-    return pos.data_ptr()
 
 
 class Rope:
@@ -65,23 +43,12 @@ class Rope:
                                       PAIRS_ADJACENT if adjacent else PAIRS_HALF)
         if st != BITLIN_OK:
             raise BitlinError(st, "bitlin_rope_create")
-        self._h = h
+        self._h = h.value
 
     def apply(self, x, pos, out=None, dtype=None, inverse: bool = False, stream=None):
         """bitlin_rope_apply: x [tokens][heads][dim] rotated by pos (int32 [axes][tokens]), into `out`
         (x itself is allowed) or a new tensor of `dtype` (x's where None)."""
-        src = _rows(x, "x")
-        if out is None:
-            out = torch.empty(x.shape, dtype=dtype or x.dtype, device=x.device)
-        elif out.shape != x.shape:
-            raise ValueError("out must have x's shape")
-        dst = _rows(out, "out")
-        tokens, heads, dim = x.shape
-        st = lib().bitlin_rope_apply(self._h, src, tokens, heads, dim, _positions(pos, self.axes, tokens), dst,
-                                     1 if inverse else 0, _stream(stream, x.device))
-        if st != BITLIN_OK:
-            raise BitlinError(st, "bitlin_rope_apply")
-        return out
+        return native.rope_apply(self._h, self.axes, x, pos, out, dtype, inverse, stream)
 
     def close(self):
         if getattr(self, "_h", None):
@@ -116,8 +83,9 @@ class KVBatch:
             raise ValueError("table's rows must not overlap")
         self.q_offsets, self.kv_lens, self.table = q_offsets, kv_lens, table
         # the row length bounds what is read; rows of a wider table may be longer apart
-        self.c = Batch(seqs, q_offsets.data_ptr(), kv_lens.data_ptr(), table.data_ptr(), table.shape[1],
-                       table.stride(0))
+        self._c = Batch(seqs, q_offsets.data_ptr(), kv_lens.data_ptr(), table.data_ptr(), table.shape[1],
+                        table.stride(0))
+        self.address = ctypes.addressof(self._c)
 
 
 class PagedKV:
@@ -142,7 +110,7 @@ class PagedKV:
                                         self.head_dim, _CODES[k.dtype], page_stride, slot_stride, head_stride)
         if st != BITLIN_OK:
             raise BitlinError(st, "bitlin_kv_create")
-        self._h = h
+        self._h = h.value
 
     def _check(self, st: int, what: str):
         if st != BITLIN_OK:
@@ -151,45 +119,16 @@ class PagedKV:
     def append(self, k, v, batch: KVBatch, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None):
         """bitlin_kv_append: k and v [tokens][kv_heads][head_dim] to their places, k rotated; q
         [tokens][heads][head_dim], when given, is rotated too and returned in the cache's type."""
-        tokens = k.shape[0]
-        if k.shape != v.shape or k.shape[1] != self.kv_heads or k.shape[2] != self.head_dim:
-            raise ValueError(f"k and v must be [tokens][{self.kv_heads}][{self.head_dim}]")
-        heads, src, dst = 0, None, None
-        if q is not None:
-            heads = q.shape[1]
-            if q.shape[0] != tokens or q.shape[2] != self.head_dim:
-                raise ValueError(f"q must be [{tokens}][heads][{self.head_dim}]")
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=self.dtype, device=q.device)
-            elif q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape")
-            src, dst = _rows(q, "q"), _rows(q_out, "q_out")
-        at = None if pos is None or rope is None else _positions(pos, rope.axes, tokens)
-        self._check(lib().bitlin_kv_append(self._h, batch.c, tokens, None if rope is None else rope._h, at,
-                                           _rows(k, "k"), _rows(v, "v"), src, heads, dst,
-                                           _stream(stream, k.device)), "bitlin_kv_append")
-        return q_out if q is not None else None
+        r, axes = (None, 0) if rope is None else (rope._h, rope.axes)
+        return native.kv_append(self._h, self.kv_heads, self.head_dim, self.dtype, batch.address, k, v, r, axes, pos, q,
+                                q_out, stream)
 
     def attend(self, q, batch: KVBatch, scale: float | None = None, causal: bool = True, out=None, dtype=None,
                lse=None, stream=None):
         """bitlin_kv_attend: attention of q [tokens][heads][head_dim] over the batch's sequences, into
         `out` or a new tensor of `dtype` (the cache's type, or float32); lse: float32 [tokens][heads]."""
-        src = _rows(q, "q")
-        tokens, heads, dim = q.shape
-        if dim != self.head_dim:
-            raise ValueError(f"q must be [tokens][heads][{self.head_dim}]")
-        if out is None:
-            out = torch.empty(q.shape, dtype=dtype or self.dtype, device=q.device)
-        elif out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous() or
-                                lse.shape != q.shape[:2]):
-            raise ValueError("lse must be a contiguous float32 CUDA tensor [tokens][heads]")
-        self._check(lib().bitlin_kv_attend(self._h, batch.c, tokens, src, heads,
-                                           1.0 / math.sqrt(dim) if scale is None else scale, 1 if causal else 0,
-                                           _rows(out, "out"), None if lse is None else lse.data_ptr(),
-                                           _stream(stream, q.device)), "bitlin_kv_attend")
-        return out
+        return native.kv_attend(self._h, self.head_dim, self.dtype, batch.address, q, scale, causal, out, dtype, lse,
+                                stream)
 
     def set_wait_budget(self, ns: int):
         self._check(lib().bitlin_kv_set_wait_budget(self._h, int(ns)), "bitlin_kv_set_wait_budget")

@@ -1,24 +1,31 @@
-"""Compile libbitlin.so (the C-ABI library) in-tree for sm_103a.
+"""Compile libbitlin.so (the C-ABI library) in-tree for sm_103a, and the compiled binding.
 
 Each CUDA source is compiled in parallel with nvcc, then linked into
-``hadamard_rotated_binary_gb300/libbitlin.so``.  Usage: ``python -m
+``hadamard_rotated_binary_gb300/libbitlin.so``; csrc/paged_native.cpp, which takes torch tensors,
+is compiled with g++ against the installed torch and linked into ``_paged_native.so`` beside it.
+Usage: ``python -m
 hadamard_rotated_binary_gb300.build``.
 """
 from __future__ import annotations
 
 import glob
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbitlin.so")
+NATIVE = os.path.join(PKG, "_paged_native.so")
+NATIVE_SRC = os.path.join(CSRC, "paged_native.cpp")
 BUILD_DIR = os.path.join(PKG, "_build")
+NATIVE_OBJ = os.path.join(BUILD_DIR, "paged_native.o")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -48,8 +55,62 @@ def _fingerprint() -> str:
     return h.hexdigest()
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: the compiled binding is built against it")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _start_native(force: bool):
+    """Start compiling paged_native.cpp if it is out of date: (process, fingerprint), or None."""
+    torch = _torch_dir()
+    h = hashlib.sha256()
+    for f in (NATIVE_SRC, os.path.join(INCLUDE, "bitlin.h"), os.path.join(torch, "version.py")):
+        with open(f, "rb") as fh:
+            h.update(fh.read())
+    h.update((sys.version + os.uname().machine).encode())
+    fp, stamp = h.hexdigest(), NATIVE + ".stamp"
+    if not force and os.path.exists(NATIVE) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == fp:
+                return None
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}",
+           "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), f"-I{cuda}", "-c", NATIVE_SRC,
+           "-o", NATIVE_OBJ]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), fp
+
+
+def _finish_native(started) -> None:
+    """Link it against libbitlin.so, which it finds beside itself."""
+    if started is None:
+        return
+    proc, fp = started
+    out, _ = proc.communicate()
+    if proc.returncode != 0:
+        sys.stderr.write(out.decode(errors="replace"))
+        raise RuntimeError("g++ failed on paged_native.cpp")
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    subprocess.run(["g++", "-shared", "-o", tmp, NATIVE_OBJ, f"-L{PKG}", "-l:libbitlin.so", "-Wl,-rpath,$ORIGIN",
+                    f"-L{os.path.join(_torch_dir(), 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"],
+                   check=True)
+    os.replace(tmp, NATIVE)
+    with open(NATIVE + ".stamp", "w") as f:
+        f.write(fp)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build libbitlin.so if its sources changed (or force); returns its path."""
+    """Build libbitlin.so and the compiled binding if their sources changed (or force); returns the library's path."""
+    started = _start_native(force)
+    path = _build_library(force, verbose)
+    _finish_native(started)
+    return path
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     stamp = LIB + ".stamp"
     fp = _fingerprint()
     if not force and os.path.exists(LIB) and os.path.exists(stamp):

@@ -1,0 +1,263 @@
+// CPython binding of the attention side: bitlin_rope_apply, bitlin_kv_append and
+// bitlin_kv_attend on torch tensors.  Argument checks and marshalling only; the
+// calls are declared in include/bitlin.h and run in libbitlin.so.  It is compiled
+// because these calls are small: marshalled through ctypes, one rotated token
+// takes the host 9.7 us where the launch itself takes 2.
+#include <Python.h>
+
+#include <ATen/EmptyTensor.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <math.h>
+
+#include "bitlin.h"
+
+namespace {
+
+// A Python error is set.
+struct Refused {};
+
+[[noreturn]] void refuse(const char* format, const char* what)
+{
+    PyErr_Format(PyExc_ValueError, format, what);
+    throw Refused();
+}
+
+[[noreturn]] void refuse(const char* text)
+{
+    PyErr_SetString(PyExc_ValueError, text);
+    throw Refused();
+}
+
+// Raises BitlinError for a call's status.
+void check(bitlin_status status, const char* call, int cuda_error)
+{
+    if (status == BITLIN_OK) return;
+    PyObject* module = PyImport_ImportModule("hadamard_rotated_binary_gb300._binding");
+    PyObject* type = module ? PyObject_GetAttrString(module, "BitlinError") : nullptr;
+    PyObject* error = type ? PyObject_CallFunction(type, "isi", (int)status, call, cuda_error) : nullptr;
+    if (error) PyErr_SetObject(type, error);
+    Py_XDECREF(error);
+    Py_XDECREF(type);
+    Py_XDECREF(module);
+    throw Refused();
+}
+
+void* handle_of(PyObject* o)
+{
+    void* h = PyLong_AsVoidPtr(o);
+    if (!h) {
+        if (PyErr_Occurred()) throw Refused();
+        refuse("the handle is closed");
+    }
+    return h;
+}
+
+long integer(PyObject* o)
+{
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Refused();
+    return v;
+}
+
+const at::Tensor& tensor(PyObject* o, const char* what)
+{
+    if (!THPVariable_Check(o)) refuse("%s must be a torch tensor", what);
+    return THPVariable_Unpack(o);
+}
+
+int type_of(at::ScalarType t)
+{
+    return t == at::kFloat ? BITLIN_F32 : t == at::kBFloat16 ? BITLIN_BF16 : t == at::kHalf ? BITLIN_F16 : -1;
+}
+
+// The C-ABI's view of a CUDA tensor [tokens][heads][dim] whose last dimension is contiguous.
+bitlin_rows rows_of(const at::Tensor& x, const char* what)
+{
+    const int type = type_of(x.scalar_type());
+    if (type < 0 || !x.is_cuda() || x.dim() != 3)
+        refuse("%s must be a float32, bfloat16 or float16 CUDA tensor [tokens][heads][dim]", what);
+    if (x.stride(2) != 1 && x.size(2) != 1) refuse("%s's last dimension must be contiguous", what);
+    // a dimension of one has no stride that matters
+    const int64_t head = x.size(1) == 1 ? x.size(2) : x.stride(1);
+    const int64_t token = x.size(0) == 1 ? x.size(1) * head : x.stride(0);
+    return {x.data_ptr(), type, token, head};
+}
+
+// `out`, or a new tensor of x's shape and the given type.
+at::Tensor output(PyObject* out, const at::Tensor& x, at::ScalarType type, const char* what)
+{
+    if (out == Py_None) return at::empty(x.sizes(), x.options().dtype(type));
+    const at::Tensor& t = tensor(out, what);
+    if (t.sizes() != x.sizes()) refuse("%s must have the input's shape", what);
+    return t;
+}
+
+at::ScalarType dtype_of(PyObject* o, at::ScalarType otherwise)
+{
+    if (o == Py_None) return otherwise;
+    if (!THPDtype_Check(o)) refuse("dtype must be a torch dtype");
+    return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+
+bitlin_stream_t stream_of(PyObject* stream, const at::Tensor& x)
+{
+    if (stream == Py_None) return c10::cuda::getCurrentCUDAStream(x.device().index()).stream();
+    PyObject* raw = PyObject_GetAttrString(stream, "cuda_stream");
+    void* s = raw ? PyLong_AsVoidPtr(raw) : nullptr;
+    Py_XDECREF(raw);
+    if (PyErr_Occurred()) throw Refused();
+    return static_cast<bitlin_stream_t>(s);
+}
+
+const int32_t* positions(PyObject* pos, long axes, int64_t tokens)
+{
+    const at::Tensor& t = tensor(pos, "pos");
+    if (t.scalar_type() != at::kInt || !t.is_cuda() || !t.is_contiguous() || t.numel() != axes * tokens)
+        refuse("pos must be a contiguous int32 CUDA tensor [axes][tokens]");
+    return static_cast<const int32_t*>(t.data_ptr());
+}
+
+// Sizes reach the C-ABI as int.
+int size_of(int64_t n)
+{
+    if (n > 0x7fffffff) refuse("too many tokens");
+    return (int)n;
+}
+
+PyObject* wrap(const at::Tensor& t, PyObject* given)
+{
+    if (given == Py_None) return THPVariable_Wrap(t);
+    Py_INCREF(given);
+    return given;
+}
+
+bool arguments(Py_ssize_t n, Py_ssize_t want)
+{
+    if (n != want) PyErr_Format(PyExc_TypeError, "%zd arguments, %zd wanted", n, want);
+    return n == want;
+}
+
+// (handle, axes, x, pos, out, dtype, inverse, stream)
+PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    if (!arguments(n, 8)) return nullptr;
+    HANDLE_TH_ERRORS
+    try {
+        auto h = static_cast<bitlin_rope_t>(handle_of(a[0]));
+        const at::Tensor& x = tensor(a[2], "x");
+        const bitlin_rows src = rows_of(x, "x");
+        const int32_t* pos = positions(a[3], integer(a[1]), x.size(0));
+        const at::Tensor out = output(a[4], x, dtype_of(a[5], x.scalar_type()), "out");
+        const bitlin_rows dst = rows_of(out, "out");
+        check(bitlin_rope_apply(h, &src, size_of(x.size(0)), size_of(x.size(1)), size_of(x.size(2)), pos, &dst,
+                                PyObject_IsTrue(a[6]), stream_of(a[7], x)),
+              "bitlin_rope_apply", 0);
+        return wrap(out, a[4]);
+    } catch (const Refused&) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// (handle, kv_heads, head_dim, cache dtype, batch, k, v, rope, axes, pos, q, q_out, stream)
+PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    if (!arguments(n, 13)) return nullptr;
+    HANDLE_TH_ERRORS
+    try {
+        auto h = static_cast<bitlin_kv_t>(handle_of(a[0]));
+        const long kv_heads = integer(a[1]), dim = integer(a[2]);
+        const at::ScalarType type = dtype_of(a[3], at::kFloat);
+        const auto* batch = static_cast<const bitlin_kv_batch*>(handle_of(a[4]));
+        const at::Tensor &k = tensor(a[5], "k"), &v = tensor(a[6], "v");
+        const bitlin_rows kr = rows_of(k, "k"), vr = rows_of(v, "v");
+        if (k.sizes() != v.sizes() || k.size(1) != kv_heads || k.size(2) != dim)
+            refuse("k and v must be [tokens][kv_heads][head_dim]");
+        const int64_t tokens = k.size(0);
+        bitlin_rope_t rope = nullptr;
+        const int32_t* pos = nullptr;
+        if (a[7] != Py_None) {
+            rope = static_cast<bitlin_rope_t>(handle_of(a[7]));
+            if (a[9] != Py_None) pos = positions(a[9], integer(a[8]), tokens);
+        }
+        bitlin_rows qr = {}, or_ = {};
+        at::Tensor out;
+        int heads = 0;
+        if (a[10] != Py_None) {
+            const at::Tensor& q = tensor(a[10], "q");
+            qr = rows_of(q, "q");
+            if (q.size(0) != tokens || q.size(2) != dim) refuse("q must be [tokens][heads][head_dim]");
+            heads = size_of(q.size(1));
+            out = output(a[11], q, type, "q_out");
+            or_ = rows_of(out, "q_out");
+        }
+        const bool has_q = a[10] != Py_None;
+        check(bitlin_kv_append(h, batch, size_of(tokens), rope, pos, &kr, &vr, has_q ? &qr : nullptr, heads,
+                               has_q ? &or_ : nullptr, stream_of(a[12], k)),
+              "bitlin_kv_append", bitlin_kv_cuda_error(h));
+        if (has_q) return wrap(out, a[11]);
+        Py_RETURN_NONE;
+    } catch (const Refused&) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// (handle, head_dim, cache dtype, batch, q, scale, causal, out, dtype, lse, stream)
+PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    if (!arguments(n, 11)) return nullptr;
+    HANDLE_TH_ERRORS
+    try {
+        auto h = static_cast<bitlin_kv_t>(handle_of(a[0]));
+        const long dim = integer(a[1]);
+        const at::ScalarType type = dtype_of(a[2], at::kFloat);
+        const auto* batch = static_cast<const bitlin_kv_batch*>(handle_of(a[3]));
+        const at::Tensor& q = tensor(a[4], "q");
+        const bitlin_rows qr = rows_of(q, "q");
+        if (q.size(2) != dim) refuse("q must be [tokens][heads][head_dim]");
+        double scale = 1.0 / sqrt((double)dim);
+        if (a[5] != Py_None) {
+            scale = PyFloat_AsDouble(a[5]);
+            if (scale == -1.0 && PyErr_Occurred()) throw Refused();
+        }
+        const at::Tensor out = output(a[7], q, dtype_of(a[8], type), "out");
+        const bitlin_rows dst = rows_of(out, "out");
+        float* lse = nullptr;
+        if (a[9] != Py_None) {
+            const at::Tensor& t = tensor(a[9], "lse");
+            if (t.scalar_type() != at::kFloat || !t.is_cuda() || !t.is_contiguous() || t.dim() != 2 ||
+                t.size(0) != q.size(0) || t.size(1) != q.size(1))
+                refuse("lse must be a contiguous float32 CUDA tensor [tokens][heads]");
+            lse = static_cast<float*>(t.data_ptr());
+        }
+        check(bitlin_kv_attend(h, batch, size_of(q.size(0)), &qr, size_of(q.size(1)), (float)scale,
+                               PyObject_IsTrue(a[6]), &dst, lse, stream_of(a[10], q)),
+              "bitlin_kv_attend", bitlin_kv_cuda_error(h));
+        return wrap(out, a[7]);
+    } catch (const Refused&) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL
+
+PyMethodDef methods[] = {
+    {"rope_apply", FAST(rope_apply), nullptr},
+    {"kv_append", FAST(kv_append), nullptr},
+    {"kv_attend", FAST(kv_attend), nullptr},
+    {nullptr, nullptr, 0, nullptr},
+};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__paged_native(void) { return PyModule_Create(&module); }
