@@ -84,6 +84,7 @@ void set_rope(TurnParams& p, bitlin_rope_t r, const int32_t* pos)
 {
     p.turns = r ? r->turns : nullptr;
     p.rotary = r ? r->rotary : 0;
+    p.axes = r ? r->axes : 0;
     p.adjacent = r ? r->adjacent : 0;
     p.pos = pos;
 }
@@ -138,7 +139,7 @@ bitlin_status bitlin_rope_create(bitlin_rope_t* out, int rotary_dim, int axes, c
         double f = (double)inv_freq[i] / 6.283185307179586476925;
         f -= floor(f);
         if (f >= 1.0) f = 0.0;
-        turns[i] = {(uint64_t)ldexp(f, 64), axis ? axis[i] : 0, 0};
+        turns[i] = ((uint64_t)ldexp(f, 64) & ~kAxisMask) | (Turn)(axis ? axis[i] : 0);
     }
     r->device = dev;
     r->rotary = rotary_dim;

@@ -16,11 +16,11 @@ constexpr int kKvErrIndex = 1;    // a place outside the table or a page outside
 
 // A frequency as a fixed-point fraction of a turn per position, 2^-64 turns,
 // so that position * frequency modulo one turn is an exact wrapping product.
-struct Turn {
-    uint64_t per_place;
-    int32_t axis;
-    int32_t pad;
-};
+// The pair's axis lies in the low bits (2^-61 turns a position is below what
+// the frequency's own f32 says).
+using Turn = uint64_t;
+constexpr int kAxisBits = 3;
+constexpr Turn kAxisMask = (1u << kAxisBits) - 1;
 
 struct KvBatch {
     const int32_t* q_offsets;  // [seqs + 1]
@@ -42,6 +42,7 @@ struct TurnParams {
     long long page_stride, slot_stride, head_stride;
     KvBatch batch;
     const Turn* turns;        // [rotary / 2], nullptr: no rotation
+    int axes;
     const int32_t* pos;       // [axes][tokens], nullptr: the token's place
     int* dev_error;
     int pages, page_size;

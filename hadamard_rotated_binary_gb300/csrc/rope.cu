@@ -5,7 +5,9 @@
 // (a, b) -> (a cos t - b sin t, b cos t + a sin t).  A frequency is held as a
 // 64-bit fixed-point fraction of a turn, so pos * frequency modulo one turn is
 // one wrapping integer product, exact at every int32 position; its top 32 bits
-// are the angle to 2^-33 of a turn, and sincospi takes it from there.
+// are the angle to 2^-33 of a turn, already within half a turn of zero.  There
+// the hardware's sine and cosine are good to 2^-21, enough for a 16-bit output
+// (2^-9 and 2^-12); an f32 output takes sincospi.
 //
 // Bound: HBM (each element is read once and written once).  A thread owns one
 // "unit" of a head: two chunks of VEC consecutive elements, half the rotated
@@ -15,6 +17,13 @@
 // once for them and all their loads are in flight together; a warp's chunks
 // are consecutive, so loads and stores coalesce.  Where sizes, strides or
 // alignment do not allow chunks, VEC = 1 takes one pair per thread.
+//
+// Measured (GB300, graph replays): a video clip's 16,128 x 16 x 80 bf16 12.9 us
+// (6.4 TB/s), the gradient of 4,097 x 24 x 256 f32 32.0 us (6.3 TB/s), prompts of
+// 8,191 tokens appended with their queries (48 heads of 128) 40.3 us (5.5 TB/s),
+// one token's queries 1.8 us.  Two heads a thread take the video 15.0 us (the
+// angles are computed twice as often), blocks of 256 13.5, chunks of 8 16-bit
+// elements 13.5, sincospi for a 16-bit output and a 16-byte table entry 15.6.
 #include "kv_internal.cuh"
 #include "ptx.cuh"
 
@@ -22,7 +31,7 @@ using namespace bitlin_impl;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kHeadsPerThread = 4;
 
 template <typename T, int VEC>
@@ -103,15 +112,27 @@ __global__ void __launch_bounds__(kThreads) bitlin_turn(const TurnParams p)
 
     float cs[VEC], sn[VEC];
     if (turning) {
+        // the token's positions on up to four axes (a fifth to eighth is read where it is used)
+        int at4[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) at4[x] = p.pos && x < p.axes ? p.pos[(long long)x * p.tokens + t] : place;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             // adjacent pairs: chunk lo holds pairs lo/2.., chunk hi pairs hi/2..
             int f = lo + j;
             if (p.adjacent) f = VEC == 1 ? u : j < VEC / 2 ? lo / 2 + j : hi / 2 + j - VEC / 2;
             const Turn w = p.turns[f];
-            const long long at = p.pos ? p.pos[(long long)w.axis * p.tokens + t] : place;
-            const int32_t frac = (int32_t)(((uint64_t)at * w.per_place) >> 32);
-            sincospif((float)frac * 4.656612873077393e-10f /* 2^-31: half turns */, &sn[j], &cs[j]);
+            const int axis = (int)(w & kAxisMask);
+            int at = axis & 2 ? (axis & 1 ? at4[3] : at4[2]) : (axis & 1 ? at4[1] : at4[0]);
+            if (axis >= 4 && p.pos) at = p.pos[(long long)axis * p.tokens + t];
+            const int32_t frac = (int32_t)(((uint64_t)(long long)at * (w & ~kAxisMask)) >> 32);
+            if (sizeof(TO) == 2) {
+                const float angle = (float)frac * 1.4629180792671596e-9f;  // 2^-32 of a turn, in radians
+                sn[j] = __sinf(angle);
+                cs[j] = __cosf(angle);
+            } else {
+                sincospif((float)frac * 4.656612873077393e-10f /* 2^-31: half turns */, &sn[j], &cs[j]);
+            }
             if (p.inverse) sn[j] = -sn[j];
         }
     }
@@ -192,19 +213,27 @@ bool chunked(const void* data, long long token, long long head, int size, int ve
     return reinterpret_cast<uintptr_t>(data) % (uintptr_t)(size * vec) == 0 && token % vec == 0 && head % vec == 0;
 }
 
-constexpr int kVec = 4;
-
+// Whether all rows of a call divide into chunks of `vec` elements.
 template <typename TI, typename TO>
-cudaError_t pick_turn(TurnParams p, cudaStream_t s)
+bool divides(const TurnParams& p, int vec)
 {
-    bool ok = p.rotary % (2 * kVec) == 0 && (p.dim - p.rotary) % (2 * kVec) == 0;
+    bool ok = p.rotary % (2 * vec) == 0 && (p.dim - p.rotary) % (2 * vec) == 0;
     if (p.heads) {
-        ok = ok && chunked(p.src[0], p.src_token[0], p.src_head[0], sizeof(TI), kVec);
-        ok = ok && chunked(p.out, p.out_token, p.out_head, sizeof(TO), kVec);
+        ok = ok && chunked(p.src[0], p.src_token[0], p.src_head[0], sizeof(TI), vec);
+        ok = ok && chunked(p.out, p.out_token, p.out_head, sizeof(TO), vec);
     }
     if (p.append)
-        for (int i = 1; i < 3; ++i) ok = ok && chunked(p.src[i], p.src_token[i], p.src_head[i], sizeof(TI), kVec);
-    return ok ? launch_turn<TI, TO, kVec>(p, s) : launch_turn<TI, TO, 1>(p, s);
+        for (int i = 1; i < 3; ++i) ok = ok && chunked(p.src[i], p.src_token[i], p.src_head[i], sizeof(TI), vec);
+    return ok;
+}
+
+template <typename TI, typename TO>
+cudaError_t pick_turn(const TurnParams& p, cudaStream_t s)
+{
+    TurnParams q = p;
+    if (divides<TI, TO>(p, 4)) return launch_turn<TI, TO, 4>(q, s);
+    if (divides<TI, TO>(p, 2)) return launch_turn<TI, TO, 2>(q, s);
+    return launch_turn<TI, TO, 1>(q, s);
 }
 
 template <typename TI>

@@ -396,7 +396,8 @@ bitlin_status bitlin_rope_create(bitlin_rope_t* out, int rotary_dim, int axes, c
  *            is the gradient of the rotation.
  *
  * Angles are kept as a 64-bit fixed-point fraction of a turn, so the result
- * is f32-exact (about 2e-7) at every int32 position; each output is rounded
+ * is good to 2e-7 (an f32 out) or 5e-7 (a 16-bit one, before its own
+ * rounding) at every int32 position; each output is rounded
  * once to its type.  Asynchronous; allocates nothing.  tokens = 0 does nothing.
  * Errors: BITLIN_EINVAL (NULL, an unknown type, head_dim < rotary_dim,
  * heads < 1 or > 4096, tokens < 0, tokens * head_dim >= 2^32, a pointer that

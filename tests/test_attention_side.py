@@ -191,13 +191,16 @@ def fill_past(batch, k, v, lens, value):
     (9, 2, 7, 6, 1, True),       # an odd head
     (130, 9, 128, 32, 1, True),
     (3, 17, 64, 2, 1, False),
+    (11, 3, 80, 20, 3, False),   # chunks of two
+    (11, 3, 80, 20, 3, True),
+    (6, 2, 48, 24, 8, False),    # more axes than registers hold
 ])
 def test_rope_against_the_definition(hrb, tokens, heads, dim, rotary, axes, adjacent):
     gen = generator(tokens * 1000 + dim)
     inv_freq = freqs(rotary // 2)
     axis = [i % axes for i in range(rotary // 2)]
     rope = hrb.Rope(inv_freq, axis, adjacent=adjacent)
-    pos = torch.randint(0, 200000, (axes, tokens), generator=gen, device="cuda", dtype=torch.int32)
+    pos = torch.randint(-5, 200000, (axes, tokens), generator=gen, device="cuda", dtype=torch.int32)
     for src in DTYPES:
         x = torch.randn((tokens, heads, dim), generator=gen, device="cuda").to(src)
         for dst in DTYPES:
