@@ -35,7 +35,7 @@
 //         256: four warps take the chunks in turn;
 //   12    MMA issue: S tiles alternate between two buffers, so Q K^T of the next
 //         tile runs while the softmax works on this one;
-//   13-15 Q of the next item (plain copies: rows of any stride).
+//   13    Q of the next item (TMA: the group's heads of its tokens, row by row).
 // The output stays in tensor memory; it is rescaled only when a row's maximum
 // grows by more than 2^8 (until then the weights are relative to the older
 // maximum, which f32 sums and the 16-bit weights' exponents hold).  The tensor
@@ -57,7 +57,6 @@ constexpr int kKeys = 128;        // keys of a tile
 constexpr int kThreads = 512;
 constexpr int kSoftmax = 256;     // threads of the softmax warps
 constexpr int kTmaWarp = 8, kTmaWarps = 4, kMmaWarp = 12, kQWarp = 13;
-constexpr int kQThreads = 96;
 // Registers a thread: launched with 128, the two softmax warpgroups take what
 // the other two give (2 * 184 + 2 * 72 = 4 * 128).
 constexpr int kManyRegs = 184, kFewRegs = 72;
@@ -530,7 +529,7 @@ __device__ __forceinline__ bool clean(uint32_t& w)
 // lo = T(w - hi), multiplied into the same accumulator one after the other.
 template <int DP, typename T, bool F32OUT>
 __global__ void __launch_bounds__(kThreads, 1)
-    bitlin_attend(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+    bitlin_attend(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const __grid_constant__ AttendParams p)
 {
     using C = Cfg<DP>;
@@ -560,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&sh->pair[lane - 4], 2);
             if (lane == 4) sh->abort = sh->bad = 0;
         } else if (lane == 8) {
-            ptx::mbar_init(&sh->q_full, kQThreads);
+            ptx::mbar_init(&sh->q_full, 1);
             ptx::mbar_init(&sh->q_empty, 1);
             ptx::mbar_init(&sh->o_free, kSoftmax);
         } else if (lane == 9) {
@@ -574,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_proxy_async_smem();
     }
     if (warp == kTmaWarp + 2 && lane == 0) {
+        ptx::prefetch_tmap(&tmap_q);
         ptx::prefetch_tmap(&tmap_k);
         ptx::prefetch_tmap(&tmap_v);
     }
@@ -772,29 +772,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_wait_bounded(&sh->drain, 0u, &no_abort, budget);
         }
     } else if (warp >= kQWarp) {
-        // Q rows of each part, 16 bytes a lane; dims past the head's are zeros
-        // (K's are, and a zero times what lies there must stay zero).
         ptx::give_registers<kFewRegs>();
-        Walk w(p, start);
-        constexpr int U = DP / 8, kPerPass = kQThreads / U;
-        const int me = threadIdx.x - 32 * kQWarp, u = me % U;
-        int part = 0;
-        bool ok = true;
-        for (; w.valid() && ok; w.next(), ++part) {
-            if (part > 0) ok = wait(&sh->q_empty, part - 1, abort, budget);
-            if (!ok) break;
-            const int rows = w.tokens() * p.group;
-            const T* base = static_cast<const T*>(p.q) + (long long)(w.q.row0 + w.qt * p.tile_tokens) * p.q_token +
-                            (long long)w.head * p.group * p.q_head + 8 * u;
-            for (int r = me / U; r < rows; r += kPerPass) {
-                const int t = r / p.group, g = r - t * p.group;
-                unsigned char* dst = tile_q + (u >> 3) * kChunkBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4);
-                if (8 * u < p.dim) ptx::cp_async16(dst, base + t * p.q_token + g * p.q_head);
-                else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+        if (warp == kQWarp) {
+            Walk w(p, start);
+            int part = 0;
+            bool ok = true;
+            for (; w.valid() && ok; w.next(), ++part) {
+                if (part > 0) ok = warp_wait(&sh->q_empty, part - 1, abort, budget);
+                if (!ok) break;
+                // Boxes of q_box tokens x the group's heads x 64 dims; dims past the
+                // head's are zeros (K's are, and a zero times what lies there must stay zero).
+                const int boxes = (w.tokens() + p.q_box - 1) / p.q_box, bytes = p.q_box * p.group * 128;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&sh->q_full, boxes * bytes * NC);
+                __syncwarp();
+                for (int k = lane; k < boxes * NC; k += 32) {
+                    const int c = k % NC, box = k / NC;
+                    ptx::tma_load_3d(tile_q + c * kChunkBytes + box * bytes, &tmap_q, 64 * c, w.head * p.group,
+                                     w.q.row0 + w.qt * p.tile_tokens + box * p.q_box, &sh->q_full);
+                }
             }
-            ptx::cp_async_wait_all();
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(&sh->q_full);
+            // The last copies must land before the CTA may exit.
+            if (part > 0) {
+                volatile int no_abort = 0;
+                ptx::mbar_wait_bounded(&sh->q_full, (uint32_t)(part - 1) & 1u, &no_abort, budget);
+            }
         }
     } else {
         // ---- softmax and epilogue: thread = row and half of the columns.
@@ -814,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // that a masked score (-inf) times it still is -inf
         const float sl2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);
         const bool negative = p.scale < 0.f;
-        const float mul = negative ? -sl2 : sl2;
+        const float sign = negative ? -1.f : 1.f, mul = sign * sl2;
         const float limit = exp2f(kLazy + kShift<T>);
         const int my_token = r / p.group, my_head = r - my_token * p.group;
         int gt = 0, consumed = 0;                // tiles and ring chunks before this part
@@ -893,28 +894,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (active) {
                     const uint32_t taddr = tmem + lane_base + C::kSCol + b * kKeys + 64 * side;
-                    float s[2][32];
-                    auto scores = [&]() {
+                    if (edge) {
+                        // Scores that the row does not see, in place: what every tile
+                        // runs below stays free of masks (and small: this kernel's code
+                        // is larger than the instruction caches, and each way that is
+                        // not the usual one costs a fetch).
+                        const int see = lim - key0 - 64 * side;  // of these 64 keys, those that the row sees
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 16) {
+                            float x[16];
+                            uint32_t u[16];
+                            ptx::tmem_ld16(taddr + c, x);
+                            ptx::tmem_wait_ld();
+                            ptx::tmem_landed(x);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(c + k < see ? x[k] : -INFINITY * sign);
+                            ptx::tmem_st16(taddr + c, u);
+                        }
+                        ptx::tmem_wait_st();
+                    }
+                    bool search = i == 0, settled = false;
+                    float add = 0.f;
+                    uint32_t hi[32], lo[32];
+#pragma unroll 1
+                    for (;;) {
+                        float s[2][32];
                         ptx::tmem_ld32(taddr, s[0]);
                         ptx::tmem_ld32(taddr + 32, s[1]);
                         ptx::tmem_wait_ld();
                         ptx::tmem_landed(s[0]);
                         ptx::tmem_landed(s[1]);
-                        if (edge) {
-                            const int see = lim - key0 - 64 * side;  // of these 64 keys, those that the row sees
-                            const float masked = negative ? INFINITY : -INFINITY;
-#pragma unroll
-                            for (int k = 0; k < 64; ++k)
-                                if (k >= see) s[k >> 5][k & 31] = masked;
-                        }
-                    };
-                    bool search = i == 0;
-                    float add = 0.f;
-                    uint32_t hi[32], lo[32];
-#pragma unroll 1
-                    for (bool settled = false;; settled = true) {
                         if (!search) {
-                            scores();
                             float2 add0 = make_float2(0.f, 0.f), add1 = make_float2(0.f, 0.f);
 #pragma unroll
                             for (int k = 0; k < 64; k += 2) {
@@ -932,17 +942,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             add0 = __fadd2_rn(add0, add1);
                             add = add0.x + add0.y;
                             if (settled) break;
-                            if (__any_sync(0xffffffffu, valid && add > limit) && lane == 0) sh->grown[quad] = t + 1;
+                            // (a row without a reference so far needs one whatever its sum)
+                            const bool ask = __any_sync(0xffffffffu, valid && (m == -INFINITY || add > limit));
+                            if (ask && lane == 0) sh->grown[quad] = t + 1;
                             meet();
                             if (!ok || *(volatile int*)&sh->grown[quad] != t + 1) break;
+                            search = true;
+                            continue;
                         }
-                        scores();
-                        float top[4];
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int k = 0; k < 64; ++k) {
-                            const float x = negative ? -s[k >> 5][k & 31] : s[k >> 5][k & 31];
-                            top[k & 3] = k < 4 ? x : fmaxf(top[k & 3], x);
-                        }
+                        for (int k = 0; k < 64; ++k) top[k & 3] = fmaxf(top[k & 3], s[k >> 5][k & 31] * sign);
                         const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                         sh->half[side][r] = mine;
                         meet();
@@ -970,6 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         base = to;
                         search = false;
+                        settled = true;
                     }
                     if (!ok) break;
                     sum += add;
@@ -1099,21 +1110,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 16; k += 4)
                                 __stcg(ws_o + (c + k) / 4 * ws_col, make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
-                        } else if (F32OUT) {
-                            float* out = static_cast<float*>(p.out) + token * p.out_token + head * p.out_head + dim0;
-#pragma unroll
-                            for (int k = 0; k < 16; k += 4)
-                                if (dim0 + k < p.dim)
-                                    *reinterpret_cast<float4*>(out + k) =
-                                        make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
                         } else {
-                            T* out = static_cast<T*>(p.out) + token * p.out_token + head * p.out_head + dim0;
+                            // eight elements at a time: 32 bytes of an f32 row, 16 of a 16-bit one
+                            const long long at = token * p.out_token + head * p.out_head + dim0;
 #pragma unroll
-                            for (int k = 0; k < 16; k += 8)
-                                if (dim0 + k < p.dim)
-                                    *reinterpret_cast<uint4*>(out + k) = make_uint4(
-                                        pack2<T>(o[k] * inv, o[k + 1] * inv), pack2<T>(o[k + 2] * inv, o[k + 3] * inv),
-                                        pack2<T>(o[k + 4] * inv, o[k + 5] * inv), pack2<T>(o[k + 6] * inv, o[k + 7] * inv));
+                            for (int k = 0; k < 16; k += 8) {
+                                if (dim0 + k >= p.dim) break;
+                                if (F32OUT) {
+                                    float* out = static_cast<float*>(p.out) + at + k;
+#pragma unroll
+                                    for (int j = 0; j < 8; j += 4)
+                                        *reinterpret_cast<float4*>(out + j) = make_float4(o[k + j] * inv, o[k + j + 1] * inv,
+                                                                                          o[k + j + 2] * inv, o[k + j + 3] * inv);
+                                } else {
+                                    *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at + k) =
+                                        make_uint4(pack2<T>(o[k] * inv, o[k + 1] * inv), pack2<T>(o[k + 2] * inv, o[k + 3] * inv),
+                                                   pack2<T>(o[k + 4] * inv, o[k + 5] * inv), pack2<T>(o[k + 6] * inv, o[k + 7] * inv));
+                                }
+                            }
                         }
                     }
                     __syncwarp();
@@ -1253,7 +1267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int DP, typename T, bool F32OUT>
-cudaError_t launch(const AttendParams& p, const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s)
+cudaError_t launch(const AttendParams& p, const void* tmap_q, const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s)
 {
     static PerDeviceOnce once;
     int dev = 0;
@@ -1271,16 +1285,17 @@ cudaError_t launch(const AttendParams& p, const void* tmap_k, const void* tmap_v
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, bitlin_attend<DP, T, F32OUT>, *static_cast<const CUtensorMap*>(tmap_k),
-                              *static_cast<const CUtensorMap*>(tmap_v), p);
+    return cudaLaunchKernelEx(&cfg, bitlin_attend<DP, T, F32OUT>, *static_cast<const CUtensorMap*>(tmap_q),
+                              *static_cast<const CUtensorMap*>(tmap_k), *static_cast<const CUtensorMap*>(tmap_v), p);
 }
 
 template <typename T, bool F32OUT>
-cudaError_t pick_dim(const AttendParams& p, const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s)
+cudaError_t pick_dim(const AttendParams& p, const void* tmap_q, const void* tmap_k, const void* tmap_v, int num_sms,
+                     cudaStream_t s)
 {
-    if (p.dim <= 64) return launch<64, T, F32OUT>(p, tmap_k, tmap_v, num_sms, s);
-    if (p.dim <= 128) return launch<128, T, F32OUT>(p, tmap_k, tmap_v, num_sms, s);
-    return launch<256, T, F32OUT>(p, tmap_k, tmap_v, num_sms, s);
+    if (p.dim <= 64) return launch<64, T, F32OUT>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
+    if (p.dim <= 128) return launch<128, T, F32OUT>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
+    return launch<256, T, F32OUT>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -1308,13 +1323,27 @@ size_t bitlin_attend_workspace(int dim, int num_sms, size_t* ml_offset, size_t* 
     return *ticket_offset + num_sms * sizeof(int);
 }
 
-cudaError_t bitlin_launch_attend(const AttendParams& p, int dtype, int out_dtype, const void* tmap_k,
-                                 const void* tmap_v, int num_sms, cudaStream_t s)
+void bitlin_attend_rows(int tokens, int seqs, int group, int* tile_tokens, int* q_box)
+{
+    // A tile's rows in one box where sequences bring many tokens; where they
+    // bring few, boxes of the fewest tokens whose rows keep the swizzle's atoms
+    // of eight, so that single tokens do not fetch their neighbours' rows.
+    *tile_tokens = kRows / group;
+    *q_box = *tile_tokens;
+    const int few = 8 / gcd(group, 8);
+    if (few < *tile_tokens && tokens / seqs < *tile_tokens) {
+        *q_box = few;
+        *tile_tokens -= *tile_tokens % few;
+    }
+}
+
+cudaError_t bitlin_launch_attend(const AttendParams& p, int dtype, int out_dtype, const void* tmap_q,
+                                 const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s)
 {
     const bool f32 = out_dtype == BITLIN_F32;
     if (dtype == BITLIN_BF16)
-        return f32 ? pick_dim<__nv_bfloat16, true>(p, tmap_k, tmap_v, num_sms, s)
-                   : pick_dim<__nv_bfloat16, false>(p, tmap_k, tmap_v, num_sms, s);
-    return f32 ? pick_dim<__half, true>(p, tmap_k, tmap_v, num_sms, s)
-               : pick_dim<__half, false>(p, tmap_k, tmap_v, num_sms, s);
+        return f32 ? pick_dim<__nv_bfloat16, true>(p, tmap_q, tmap_k, tmap_v, num_sms, s)
+                   : pick_dim<__nv_bfloat16, false>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
+    return f32 ? pick_dim<__half, true>(p, tmap_q, tmap_k, tmap_v, num_sms, s)
+               : pick_dim<__half, false>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
 }

@@ -96,21 +96,38 @@ void set_out(TurnParams& p, const bitlin_rows* r)
     p.out_head = r->head_stride;
 }
 
-// A pool seen as [page][head][slot][dim], copied `box` slots x 64 dims of one
-// head at a time (128-byte swizzle; dims past the head's read as zeros).
-cudaError_t encode_pool(const bitlin_kv& h, void* pool, int box, unsigned char* tmap)
+// A tensor of 16-bit elements copied in boxes of 64 elements x `rows` (two of
+// its dimensions), 128-byte swizzle, zeros outside.  dims and strides (bytes)
+// from the innermost, whose stride is one element.
+cudaError_t encode(unsigned char* tmap, int dtype, int rank, const void* data, const cuuint64_t* dims,
+                   const cuuint64_t* strides, const cuuint32_t* box)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = bitlin_tensormap_encode_fn();
     if (!enc) return cudaErrorNotSupported;
-    cuuint64_t dims[4] = {(cuuint64_t)h.dim, (cuuint64_t)h.page_size, (cuuint64_t)h.kv_heads, (cuuint64_t)h.pages};
-    cuuint64_t strides[3] = {(cuuint64_t)h.slot_stride * 2, (cuuint64_t)h.head_stride * 2, (cuuint64_t)h.page_stride * 2};
-    cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = enc(reinterpret_cast<CUtensorMap*>(tmap),
-                     h.dtype == BITLIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, pool,
-                     dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const CUresult r = enc(reinterpret_cast<CUtensorMap*>(tmap),
+                           dtype == BITLIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                           const_cast<void*>(data), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// A pool seen as [page][head][slot][dim], copied `box` slots of one head at a time.
+cudaError_t encode_pool(const bitlin_kv& h, void* pool, int box, unsigned char* tmap)
+{
+    const cuuint64_t dims[4] = {(cuuint64_t)h.dim, (cuuint64_t)h.page_size, (cuuint64_t)h.kv_heads, (cuuint64_t)h.pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)h.slot_stride * 2, (cuuint64_t)h.head_stride * 2, (cuuint64_t)h.page_stride * 2};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1};
+    return encode(tmap, h.dtype, 4, pool, dims, strides, boxes);
+}
+
+// Queries seen as [token][head][dim], copied a group's heads of `box` tokens at a time.
+cudaError_t encode_queries(const bitlin_kv& h, const bitlin_rows& q, int tokens, int heads, int box, unsigned char* tmap)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)h.dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)q.head_stride * 2, (cuuint64_t)q.token_stride * 2};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)(heads / h.kv_heads), (cuuint32_t)box};
+    return encode(tmap, h.dtype, 3, q.data, dims, strides, boxes);
 }
 
 }  // namespace
@@ -291,9 +308,6 @@ bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
         }
     }
     AttendParams p = {};
-    p.q = q->data;
-    p.q_token = q->token_stride;
-    p.q_head = q->head_stride;
     p.v_pool = kv->v;
     p.page_stride = kv->page_stride;
     p.slot_stride = kv->slot_stride;
@@ -317,12 +331,15 @@ bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
     p.group = heads / kv->kv_heads;
     p.dim = kv->dim;
     p.causal = causal;
-    p.tile_tokens = 128 / p.group;
+    bitlin_attend_rows(tokens, batch->seqs, p.group, &p.tile_tokens, &p.q_box);
     p.item_extra = bitlin_attend_item_extra(kv->dim);
     bitlin_attend_boxes(kv->dim, kv->page_size, &p.box_k, &p.box_v);
     p.stall_test = kv->stall_test;
     p.scale = scale;
-    return from_cuda(kv, bitlin_launch_attend(p, kv->dtype, out->dtype, kv->tmap_k, kv->tmap_v, kv->num_sms, st));
+    alignas(64) unsigned char tmap_q[128];
+    const cudaError_t e = encode_queries(*kv, *q, tokens, heads, p.q_box, tmap_q);
+    if (e != cudaSuccess) return from_cuda(kv, e);
+    return from_cuda(kv, bitlin_launch_attend(p, kv->dtype, out->dtype, tmap_q, kv->tmap_k, kv->tmap_v, kv->num_sms, st));
 }
 
 bitlin_status bitlin_kv_set_wait_budget(bitlin_kv_t kv, long long ns)
