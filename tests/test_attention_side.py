@@ -586,6 +586,123 @@ def test_attend_long_ragged_batch_matches_its_parts(hrb):
         assert float(d.max()) <= err
 
 
+def attend64_long(q, kp, vp, offsets, lens, table, scale):
+    """attend64 for many keys, causal, a sequence at a time on the device.
+
+    The relative error has three terms more.  A weight sum of n f32 additions, rounded to nearest: a
+    random walk, 4 sqrt(n) 2^-24.  The tensor cores' additions, which lose 2.1e-8 of the sum each: 16 of
+    them for each of 8 tiles (f32 output; 2.7e-6 < 2^-18), or 8 for each of 256 (16-bit; 4.3e-5 <
+    2^-14).  One f32 addition for each drain and each part: at most 256 of 2^-24 together.
+    Returns the reference of a 16-bit output and that of an f32 one."""
+    T, H, D = q.shape
+    page, kvh = kp.shape[1], kp.shape[2]
+    out, size = (torch.zeros((T, H, D), dtype=torch.float64, device="cuda") for _ in range(2))
+    lse, rel = (torch.zeros((T, H), dtype=torch.float64, device="cuda") for _ in range(2))
+    for s, n in enumerate(lens):
+        at = torch.arange(n, device="cuda")
+        where = table[s, at // page].long(), at % page
+        k, v = kp[where].double(), vp[where].double()
+        k_size = torch.where(torch.isfinite(k), k, 0.0).abs()
+        new = offsets[s + 1] - offsets[s]
+        for i0 in range(0, new, 64):
+            i1 = min(new, i0 + 64)
+            rows = slice(offsets[s] + i0, offsets[s] + i1)
+            qs = q[rows].double().view(i1 - i0, kvh, H // kvh, D)
+            seen = at[None, :] <= (n - new + torch.arange(i0, i1, device="cuda"))[:, None]
+            logits = scale * torch.einsum("nhgd,khd->nhgk", qs, k)
+            logits = logits.masked_fill(~seen[:, None, None], -math.inf)
+            w = torch.softmax(logits, -1)
+            out[rows] = torch.einsum("nhgk,khd->nhgd", w, v).reshape(i1 - i0, H, D)
+            size[rows] = torch.einsum("nhgk,khd->nhgd", w, v.abs()).reshape(i1 - i0, H, D)
+            lse[rows] = torch.logsumexp(logits, -1).reshape(i1 - i0, H)
+            mag = abs(scale) * torch.einsum("nhgd,khd->nhgk", qs.abs(), k_size).amax(-1).reshape(i1 - i0, H)
+            rel[rows] = 2 * (24 * 2.0**-23 * mag + 2.0**-21 * (1 + mag)) + 2.0**-20
+    walk = 4 * math.sqrt(max(lens)) * 2.0**-24 + 256 * 2.0**-24
+    out, lse, rel, size = out.cpu(), lse.cpu(), rel.cpu()[..., None].expand(T, H, D), size.cpu()
+    return (out, lse, rel + walk + 2.0**-14, size), (out, lse, rel + walk + 2.0**-18, size)
+
+
+def shared_pages(hrb, gen, seqs, new, lens, page, kvh, heads, dim, dtype):
+    """A batch whose sequences all read the same pages, each a length of its own."""
+    batch, _, pages = make_batch(hrb, gen, [1], [max(lens)], page)
+    kp, vp = make_pools(gen, pages, page, kvh, dim, dtype)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    offsets = [i * new for i in range(seqs + 1)]
+    table = batch.table.expand(seqs, -1).contiguous()
+    q = torch.randn((seqs * new, heads, dim), generator=gen, device="cuda").to(dtype)
+    return hrb.KVBatch(i32(offsets), i32(lens), table), offsets, kp, vp, q
+
+
+def check_long(hrb, batch, offsets, kp, vp, q, lens, scale, dtype):
+    cache = hrb.PagedKV(kp, vp)
+    refs = attend64_long(q, kp, vp, offsets, lens, batch.table, scale)
+    for out_dtype, ref in zip((dtype, torch.float32), refs):
+        lse = torch.full(q.shape[:2], 7.0, device="cuda")
+        out = cache.attend(q, batch, scale=scale, dtype=out_dtype, lse=lse)
+        assert cache.get_error() == 0
+        check_attended(out, lse, ref, dtype)
+
+
+@gpu
+@pytest.mark.parametrize("per_sm,extra,kvh,heads,dim,new,length", [
+    (1, 0, 1, 2, 64, 1, 200),     # as many items as SMs
+    (1, 8, 4, 8, 128, 1, 260),    # a round, and a rest that is cut
+    (2, 26, 3, 3, 64, 2, 130),    # two rounds
+    (1, 1, 1, 6, 256, 3, 400),    # a rest of one item
+    (70, 40, 8, 8, 64, 1, 5),     # more than the rounds that are listed
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_attend_rounds_of_like_items(hrb, per_sm, extra, kvh, heads, dim, new, length, dtype):
+    """Items of about the same cost, at least one per SM: taken whole, and the rest cut."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    seqs = -(-(sms * per_sm + extra) // kvh)
+    lens = [length - i % 2 for i in range(seqs)]
+    case = shared_pages(hrb, generator(21), seqs, new, lens, 16, kvh, heads, dim, dtype)
+    check_long(hrb, *case, lens, 1 / math.sqrt(dim), dtype)
+
+
+@gpu
+def test_attend_rounds_of_row_tiles(hrb):
+    """One long sequence whose row tiles (8 tokens of 16 heads) cost about the same."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    new, lens = 8 * (sms + 23) - 3, [16000]
+    batch, offsets, kp, vp, q = attend_case(hrb, 64, 64, 1, 16, [new], lens, torch.bfloat16, 22)
+    check_long(hrb, batch, offsets, kp, vp, q, lens, 0.125, torch.bfloat16)
+
+
+@gpu
+@pytest.mark.parametrize("rise", [0.0, 60.0, -60.0])
+@pytest.mark.parametrize("lens_of", ["alike", "ragged"])
+@pytest.mark.parametrize("dtype,length,dim", [(torch.bfloat16, 3000, 128), (torch.float16, 3000, 256),
+                                              (torch.bfloat16, 36000, 64)])
+def test_attend_drains(hrb, dtype, length, dim, lens_of, rise):
+    """Parts long enough that their output goes to the workspace in between (past 8 tiles for an f32
+    output, past 256 for a 16-bit one), with scores that are flat or rise or fall by 60 along the keys,
+    so that the reference differs from one drain to the next."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    seqs = sms + 48 if length < 10000 else sms + 4
+    lens = [length - i % 3 if lens_of == "alike" else length + (i % 5) * (length // 16) for i in range(seqs)]
+    batch, offsets, kp, vp, q = shared_pages(hrb, generator(23), seqs, 1, lens, 64, 1, 2, dim, dtype)
+    q[..., 0] = 1.0
+    most = max(lens)
+    at = torch.arange(most, device="cuda")
+    kp[batch.table[0, at // 64].long(), at % 64, 0, 0] = (rise * math.sqrt(dim) * at / most).to(dtype)
+    check_long(hrb, batch, offsets, kp, vp, q, lens, 1 / math.sqrt(dim), dtype)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("gone", [[(0, 128)], [(0, 256)], [(0, 300), (384, 512)], [(0, 639)]])
+def test_attend_first_tiles_of_minus_infinity(hrb, dtype, gone):
+    """Keys that score -inf through the whole first tile or more weigh nothing."""
+    batch, offsets, kp, vp, q = attend_case(hrb, 64, 32, 1, 4, [1, 1], [640, 640], dtype, 24)
+    q[..., 0] = 1.0
+    for s in range(2):
+        at = torch.cat([torch.arange(a, b, device="cuda") for a, b in gone])
+        kp[batch.table[s, at // 32].long(), at % 32, 0, 0] = -math.inf
+    check_long(hrb, batch, offsets, kp, vp, q, [640, 640], 0.125, dtype)
+
+
 @gpu
 def test_attend_and_append_past_32_bits(hrb):
     """Pools whose element offsets pass 2^32."""
