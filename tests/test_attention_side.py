@@ -785,6 +785,45 @@ def test_step_in_a_graph_and_on_another_stream(hrb):
     assert cache.get_error() == 0
 
 
+@gpu
+def test_layer_example(hrb):
+    """Prompts and captured single-token steps of a layer, part by part against the definition.
+
+    The projections' results are taken as given (their tests are elsewhere): projecting the same rows
+    again gives the same bits.  The cache and the attention are compared with the definition, and the
+    layer's output with the output projection of that attention, bit by bit.
+    """
+    import os
+    import sys
+
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "examples"))
+    import attention_layer as example
+
+    lens, steps = [70, 1, 133], 5
+    layer, table, inputs, outputs = example.serve(lens, steps)
+    pairs = example.ROTARY // 2
+    freq, axis = [1e7 ** (-i / pairs) for i in range(pairs)], [i % 3 for i in range(pairs)]
+    past = [0] * len(lens)
+    for part, x in enumerate(inputs):
+        new = lens if part == 0 else [1] * len(lens)
+        past = [a + b for a, b in zip(past, new)]
+        batch, pos = example.make_batch(new, past, table)
+        q, gate, k, v = layer.project(x)
+        at = [(s, past[s] - new[s] + i) for s in range(len(lens)) for i in range(new[s])]
+        where = (torch.stack([table[s, i // example.PAGE] for s, i in at]).long(),
+                 torch.tensor([i % example.PAGE for _, i in at], device="cuda"))
+        check_rotated(layer.cache.k[where], k, pos, freq, axis, False)
+        assert torch.equal(layer.cache.v[where], v.bfloat16())
+        # the attention over the cache as it was then
+        q = layer.rope.apply(q, pos, dtype=torch.bfloat16)
+        a = layer.cache.attend(q, batch, dtype=torch.float32)
+        offsets = [sum(new[:i]) for i in range(len(new) + 1)]
+        ref = attend64(q, layer.cache.k, layer.cache.v, offsets, past, table, 1 / math.sqrt(example.DIM), True)
+        check_attended(a, None, ref, torch.bfloat16)
+        again = layer.out((a * torch.sigmoid(gate)).view(-1, example.HEADS * example.DIM))
+        assert torch.equal(again, outputs[part])
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_refusals_without_device(hrb):
