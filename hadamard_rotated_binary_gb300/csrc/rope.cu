@@ -18,12 +18,14 @@
 // are consecutive, so loads and stores coalesce.  Where sizes, strides or
 // alignment do not allow chunks, VEC = 1 takes one pair per thread.
 //
-// Measured (GB300, graph replays): a video clip's 16,128 x 16 x 80 bf16 12.9 us
-// (6.4 TB/s), the gradient of 4,097 x 24 x 256 f32 32.0 us (6.3 TB/s), prompts of
-// 8,191 tokens appended with their queries (48 heads of 128) 40.3 us (5.5 TB/s),
-// one token's queries 1.8 us.  Two heads a thread take the video 15.0 us (the
-// angles are computed twice as often), blocks of 256 13.5, chunks of 8 16-bit
-// elements 13.5, sincospi for a 16-bit output and a 16-byte table entry 15.6.
+// Measured (GB300, inputs changing from call to call): a video clip's 16,128 x
+// 16 x 80 bf16 16.2 us (5.1 TB/s), the gradient of 4,097 x 24 x 256 f32 32.3 us
+// (6.2 TB/s), prompts of 8,191 tokens appended with their queries (48 heads of
+// 128) 40.3 us (5.5 TB/s); one token's queries 1.9 us in a graph.  The variants
+// were compared on graph replays of one clip, whose 83 MB L2 partly holds: 12.9
+// us as it is, two heads a thread 15.0 (the angles are computed twice as often),
+// blocks of 256 13.5, chunks of 8 16-bit elements 13.5, sincospi for a 16-bit
+// output and a 16-byte table entry 15.6.
 #include "kv_internal.cuh"
 #include "ptx.cuh"
 
