@@ -10,8 +10,8 @@
 // grouped model still reads each key once.
 //
 // Work: an item is (sequence, key head, tile of rows) and costs its visible
-// key tiles and a few more for its begin and end.  All items lie end to end on one line of tiles, sequences
-// outermost, then key heads.  Where the items cost about the same, the CTAs
+// key tiles and a few more for its begin and end.  All items lie end to end on
+// one line of tiles, sequences outermost, then key heads.  Where the items cost about the same, the CTAs
 // first take whole items in rounds, neighbours side by side: the CTAs on one
 // key head then read the same keys at the same time and L2 serves all but the
 // first.  (2,048 tokens over 32,768 keys, 134 MB of K and V: equal parts of the
@@ -48,7 +48,10 @@
 // at 131,072 (f32 arithmetic: 0.5e-6 and 1.1e-6).  A third digit, in shared
 // memory for want of tensor memory, with drains every 4 tiles, gives 1.0e-6 and
 // 2.4e-6 and takes 14.7 and 109.4 us instead of 14.0 and 100.1 (the ring is two
-// chunks shorter); not kept.
+// chunks shorter).  Three digits in the lanes that up to 32 rows leave idle (Q
+// loaded once per digit) give 0.7e-6 and 2.0e-6 and take 15.8 and 107.2 us, and
+// f32 prompts 807 us instead of 514.  Neither was kept: keys and values in bf16
+// are themselves rounded to 2e-3.
 //
 // Bound: single tokens by HBM (one over 131,072 keys, 537 MB, 106 us with
 // inputs changing from call to call: 5.1 TB/s; 64 over 100-8,000 keys each, 1.06
