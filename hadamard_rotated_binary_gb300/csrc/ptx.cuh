@@ -224,14 +224,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0,
         : "memory");
 }
 
-// 16 bytes from global to shared memory, asynchronously, in the generic proxy.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // Move registers between the warpgroups of a CTA (all four warps of one execute it).
 template <int N>
 __device__ __forceinline__ void take_registers()
