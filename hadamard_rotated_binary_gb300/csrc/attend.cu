@@ -1025,6 +1025,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // them back to the rows that see them.
                     const int lo = max(lim_first - key0, 0), hi = w.end - key0;
                     const int v0 = consumed + NC * min(2 * i + C::AHEAD + 1, n + i);
+                    // A stage's parity answers for its last two chunks alone.  This tile's
+                    // scores say that its K has landed; where the ring is shorter than from
+                    // there to its V (256 dims: 12 chunks in 10 stages), the chunk before in
+                    // the stage is one of the V before, which the MMAs have then to be
+                    // through with.  (In a part's last tile no K lies between.)
+                    if ((2 * C::AHEAD + 1) * NC > NS && i > 0 && i + 1 < n) {
+                        ok = warp_wait(&sh->pv_done[(t - 1) % NB], (t - 1) / NB, abort, budget);
+                        if (!ok) break;
+                    }
 #pragma unroll 1
                     for (int c = lo / KV; c < NC && ok; ++c) {
                         const int st = (v0 + c) % NS;
