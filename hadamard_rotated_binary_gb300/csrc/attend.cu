@@ -864,7 +864,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool by_row = tokens * p.group <= 32;
             const int ws_col = by_row ? 1 : kRows, ws_row = by_row ? DP / 4 : 1;
             float4* ws_o = reinterpret_cast<float4*>(p.ws_o) + slot * (DP / 4) * kRows + side * (HALF / 4) * ws_col + r * ws_row;
-            float ws_base = 0.f;
+            float ws_base = -INFINITY;
+            // What drained output counts at the present reference: 0 where there was none
+            // yet, since the first one may lie far below what stands for none.
+            auto drained_by = [&]() { return ptx::ex2(ws_base - base); };
             // before it writes what its partner may still read of the part before
             if (active && part > 0) meet();
             if (!ok) break;
@@ -883,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     ptx::tc_fence_after();
                     if (active) {
-                        const float f = ptx::ex2(ws_base - base);
+                        const float f = drained_by();
 #pragma unroll 1
                         for (int c = 0; c < HALF; c += 16) {
                             float o[16];
@@ -908,7 +911,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             __syncwarp();
                         }
-                        ws_base = base;
+                        // (a row without a reference so far has drained nothing but zeros or NaNs)
+                        ws_base = m == -INFINITY ? -INFINITY : base;
                     }
                 }
                 if (active) {
@@ -1096,7 +1100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             if (active) {
                 const bool drained = n > G && valid;
-                const float f = ptx::ex2(ws_base - base);
+                const float f = drained_by();
                 float4 x[4] = {};
                 if (drained) {
 #pragma unroll
