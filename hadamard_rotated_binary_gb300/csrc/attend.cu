@@ -1204,9 +1204,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p.lse[(tok0 + tk) * p.heads + w.head * p.group + row - tk * p.group] =
                         total == 0.f ? -INFINITY : 0.6931471805599453f * (ref + log2f(total));
                 };
+                // A part without a key holds zeros; one whose weight underflows against
+                // another's is added all the same, so that a NaN or an infinity in it
+                // reaches the output wherever the item was cut.
                 auto add = [&](float4& acc, float x, float4 o) {
-                    // a part without a key (weight 0) adds nothing, whatever it holds
-                    if (x != 0.f) acc = make_float4(fmaf(x, o.x, acc.x), fmaf(x, o.y, acc.y), fmaf(x, o.z, acc.z), fmaf(x, o.w, acc.w));
+                    acc = make_float4(fmaf(x, o.x, acc.x), fmaf(x, o.y, acc.y), fmaf(x, o.z, acc.z), fmaf(x, o.w, acc.w));
                 };
                 auto write_out = [&](int row, int c, float4 v) {
                     if (4 * c >= p.dim) return;

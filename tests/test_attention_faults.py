@@ -56,3 +56,37 @@ def test_low_scores_after_drains_of_minus_infinity(hrb, dtype, low, cut, gone, l
     kp[where[0], where[1], 0, 0] = torch.where(at < gone, -math.inf, 0.0).to(dtype)
     kp[where[0], where[1], 0, 1] = 8.0 * low
     check_long(hrb, batch, offsets, kp, vp, q, lens, 0.125, dtype)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("first,last", [(0.0, 300.0), (300.0, 0.0)])
+def test_what_is_not_finite_does_not_depend_on_the_cut(hrb, dtype, new, first, last):
+    """A NaN or an infinity among values whose weights underflow against another part's: one sequence,
+    cut over all SMs, and as many as there are SMs, each in one part."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    length = 20000
+    for seqs in (1, sms):
+        batch, offsets, kp, vp, q = shared_pages(hrb, generator(33), seqs, new, [length] * seqs, 64, 1, 2, 64, dtype)
+        q[..., 0] = 1.0
+        at = torch.arange(length, device="cuda")
+        where = batch.table[0, at // 64].long(), at % 64
+        kp[where[0], where[1], 0, 0] = torch.where(at < length // 2, 8 * first, 8 * last).to(dtype)
+        light = 1000 if first < last else length - 1000  # a key that weighs nothing
+        vp[where[0][light], where[1][light], 0, 5] = math.nan
+        vp[where[0][light], where[1][light], 0, 6] = math.inf
+        cache = hrb.PagedKV(kp, vp)
+        for out_dtype in (dtype, torch.float32):
+            got = cache.attend(q, batch, dtype=out_dtype)
+            assert bool(torch.isnan(got[..., 5:7]).all())
+            assert bool(torch.isfinite(got[..., :5]).all()) and bool(torch.isfinite(got[..., 7:]).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_parts_without_a_key_for_some_rows(hrb, dtype):
+    """Prompts cut inside their last row tiles: a later part holds keys that earlier rows do not see."""
+    for dim, heads, new, length in ((64, 1, 128, 200), (128, 4, 96, 170), (256, 2, 64, 4000), (256, 1, 128, 300)):
+        batch, offsets, kp, vp, q = attend_case(hrb, dim, 16, 1, heads, [new, 1, new], [length, 7, length + 5], dtype, 34)
+        check_long(hrb, batch, offsets, kp, vp, q, [length, 7, length + 5], 1 / math.sqrt(dim), dtype)
