@@ -164,6 +164,9 @@ bitlin_status bitlin_rope_create(bitlin_rope_t* out, int rotary_dim, int axes, c
     r->adjacent = pairing == BITLIN_PAIRS_ADJACENT;
     cudaError_t e = cudaMalloc(&r->turns, pairs * sizeof(Turn));
     if (e == cudaSuccess) e = cudaMemcpy(r->turns, turns.get(), pairs * sizeof(Turn), cudaMemcpyHostToDevice);
+    // A copy from pageable memory may return before it has landed, and streams that
+    // do not block with the default one would not wait for it.
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {
         cudaFree(r->turns);
         return status_of(e);

@@ -90,3 +90,25 @@ def test_parts_without_a_key_for_some_rows(hrb, dtype):
     for dim, heads, new, length in ((64, 1, 128, 200), (128, 4, 96, 170), (256, 2, 64, 4000), (256, 1, 128, 300)):
         batch, offsets, kp, vp, q = attend_case(hrb, dim, 16, 1, heads, [new, 1, new], [length, 7, length + 5], dtype, 34)
         check_long(hrb, batch, offsets, kp, vp, q, [length, 7, length + 5], 1 / math.sqrt(dim), dtype)
+
+
+@gpu
+def test_rope_is_ready_when_it_is_created(hrb):
+    """A handle's frequencies are in place for a stream that does not wait for the default one."""
+    from test_attention_side import check_rotated
+
+    gen = generator(35)
+    side = torch.cuda.Stream()
+    x = torch.randn((2, 1, 4096), generator=gen, device="cuda")
+    pos = torch.tensor([[3, 70000]], dtype=torch.int32, device="cuda")
+    outs = [torch.empty_like(x) for _ in range(40)]
+    torch.cuda.synchronize()
+    made = []
+    for i, out in enumerate(outs):
+        inv_freq = freqs(2048, 1e4 + 100 * i)
+        made.append((hrb.Rope(inv_freq), inv_freq))
+        with torch.cuda.stream(side):
+            made[-1][0].apply(x, pos, out=out)
+    torch.cuda.synchronize()
+    for (_, inv_freq), out in list(zip(made, outs))[::13]:
+        check_rotated(out, x, pos, inv_freq, [0] * 2048, False)
