@@ -369,6 +369,8 @@ bitlin_status bitlin_kv_get_error(bitlin_kv_t kv)
     if (v[kKvErrTimeout]) kv->sticky = BITLIN_ETIMEOUT;
     if (kv->sticky != BITLIN_OK || !v[kKvErrIndex]) return kv->sticky;
     e = cudaMemset(kv->dev_error + kKvErrIndex, 0, sizeof(int));
+    // before a later call, on whatever stream, can set it again
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     return e == cudaSuccess ? BITLIN_EINDEX : from_cuda(kv, e);
 }
 

@@ -112,3 +112,21 @@ def test_rope_is_ready_when_it_is_created(hrb):
     torch.cuda.synchronize()
     for (_, inv_freq), out in list(zip(made, outs))[::13]:
         check_rotated(out, x, pos, inv_freq, [0] * 2048, False)
+
+
+@gpu
+def test_an_index_error_after_a_cleared_one_is_kept(hrb):
+    """Clearing the flag does not race with the next call on a stream of its own."""
+    gen = generator(36)
+    kp, vp = make_pools(gen, 4, 8, 1, 64, torch.bfloat16)
+    cache = hrb.PagedKV(kp, vp)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    k = torch.randn((1, 1, 64), generator=gen, device="cuda")
+    bad = hrb.KVBatch(i32([0, 1]), i32([1]), i32([[4]]))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(100):
+        with torch.cuda.stream(side):
+            cache.append(k, k, bad)
+        assert cache.get_error() == hrb.BITLIN_EINDEX
+    assert cache.get_error() == 0
