@@ -119,6 +119,8 @@ class PagedKV:
     def append(self, k, v, batch: KVBatch, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None):
         """bitlin_kv_append: k and v [tokens][kv_heads][head_dim] to their places, k rotated; q
         [tokens][heads][head_dim], when given, is rotated too and returned in the cache's type."""
+        if rope is not None and not rope._h:
+            raise ValueError("the rope's handle is closed")  # (None would mean no rotation)
         r, axes = (None, 0) if rope is None else (rope._h, rope.axes)
         return native.kv_append(self._h, self.kv_heads, self.head_dim, self.dtype, batch.address, k, v, r, axes, pos, q,
                                 q_out, stream)

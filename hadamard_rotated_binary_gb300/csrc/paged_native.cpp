@@ -50,7 +50,7 @@ void check(bitlin_status status, const char* call, int cuda_error)
 
 void* handle_of(PyObject* o)
 {
-    void* h = PyLong_AsVoidPtr(o);
+    void* h = o == Py_None ? nullptr : PyLong_AsVoidPtr(o);
     if (!h) {
         if (PyErr_Occurred()) throw Refused();
         refuse("the handle is closed");

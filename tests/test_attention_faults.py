@@ -130,3 +130,28 @@ def test_an_index_error_after_a_cleared_one_is_kept(hrb):
             cache.append(k, k, bad)
         assert cache.get_error() == hrb.BITLIN_EINDEX
     assert cache.get_error() == 0
+
+
+@gpu
+def test_closed_handles_are_refused(hrb):
+    """A closed Rope is not the same as none: nothing is written."""
+    gen = generator(37)
+    kp, vp = make_pools(gen, 4, 8, 1, 64, torch.bfloat16)
+    cache = hrb.PagedKV(kp, vp)
+    rope = hrb.Rope(freqs(32))
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    batch, pos = hrb.KVBatch(i32([0, 1]), i32([1]), i32([[2]])), i32([3])
+    k = torch.randn((1, 1, 64), generator=gen, device="cuda")
+    q = k.bfloat16()
+    before = kp.clone(), vp.clone()
+    rope.close()
+    with pytest.raises(ValueError, match="closed"):
+        cache.append(k, k, batch, rope=rope, pos=pos, q=k)
+    with pytest.raises(ValueError, match="closed"):
+        rope.apply(k, pos)
+    cache.close()
+    with pytest.raises(ValueError, match="closed"):
+        cache.append(k, k, batch)
+    with pytest.raises(ValueError, match="closed"):
+        cache.attend(q, batch)
+    assert torch.equal(kp, before[0]) and torch.equal(vp, before[1])
