@@ -8,6 +8,8 @@
 #include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -89,10 +91,25 @@ bitlin_rows rows_of(const at::Tensor& x, const char* what)
     return {x.data_ptr(), type, token, head};
 }
 
-// `out`, or a new tensor of x's shape and the given type.
-at::Tensor output(PyObject* out, const at::Tensor& x, at::ScalarType type, const char* what)
+// `out`, or a new tensor of x's shape and the given type.  A call on a stream of
+// its own takes the new tensor's memory on that stream: the current one may still
+// be using what its allocator would hand out, and the memory is not given out again
+// before either stream is through with it.
+at::Tensor output(PyObject* out, const at::Tensor& x, at::ScalarType type, PyObject* stream, bitlin_stream_t raw, const char* what)
 {
-    if (out == Py_None) return at::empty(x.sizes(), x.options().dtype(type));
+    if (out == Py_None) {
+        if (stream == Py_None) return at::empty(x.sizes(), x.options().dtype(type));
+        const c10::DeviceIndex device = x.device().index();
+        const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(device);
+        at::Tensor t;
+        {
+            const c10::cuda::CUDAStreamGuard guard(
+                c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), device));
+            t = at::empty(x.sizes(), x.options().dtype(type));
+        }
+        if (current.stream() != raw) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current);
+        return t;
+    }
     const at::Tensor& t = tensor(out, what);
     if (t.sizes() != x.sizes()) refuse("%s must have the input's shape", what);
     return t;
@@ -153,10 +170,11 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n)
         const at::Tensor& x = tensor(a[2], "x");
         const bitlin_rows src = rows_of(x, "x");
         const int32_t* pos = positions(a[3], integer(a[1]), x.size(0));
-        const at::Tensor out = output(a[4], x, dtype_of(a[5], x.scalar_type()), "out");
+        const bitlin_stream_t stream = stream_of(a[7], x);
+        const at::Tensor out = output(a[4], x, dtype_of(a[5], x.scalar_type()), a[7], stream, "out");
         const bitlin_rows dst = rows_of(out, "out");
         check(bitlin_rope_apply(h, &src, size_of(x.size(0)), size_of(x.size(1)), size_of(x.size(2)), pos, &dst,
-                                PyObject_IsTrue(a[6]), stream_of(a[7], x)),
+                                PyObject_IsTrue(a[6]), stream),
               "bitlin_rope_apply", 0);
         return wrap(out, a[4]);
     } catch (const Refused&) {
@@ -180,6 +198,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (k.sizes() != v.sizes() || k.size(1) != kv_heads || k.size(2) != dim)
             refuse("k and v must be [tokens][kv_heads][head_dim]");
         const int64_t tokens = k.size(0);
+        const bitlin_stream_t stream = stream_of(a[12], k);
         bitlin_rope_t rope = nullptr;
         const int32_t* pos = nullptr;
         if (a[7] != Py_None) {
@@ -194,12 +213,12 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
             qr = rows_of(q, "q");
             if (q.size(0) != tokens || q.size(2) != dim) refuse("q must be [tokens][heads][head_dim]");
             heads = size_of(q.size(1));
-            out = output(a[11], q, type, "q_out");
+            out = output(a[11], q, type, a[12], stream, "q_out");
             or_ = rows_of(out, "q_out");
         }
         const bool has_q = a[10] != Py_None;
         check(bitlin_kv_append(h, batch, size_of(tokens), rope, pos, &kr, &vr, has_q ? &qr : nullptr, heads,
-                               has_q ? &or_ : nullptr, stream_of(a[12], k)),
+                               has_q ? &or_ : nullptr, stream),
               "bitlin_kv_append", bitlin_kv_cuda_error(h));
         if (has_q) return wrap(out, a[11]);
         Py_RETURN_NONE;
@@ -227,7 +246,8 @@ PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n)
             scale = PyFloat_AsDouble(a[5]);
             if (scale == -1.0 && PyErr_Occurred()) throw Refused();
         }
-        const at::Tensor out = output(a[7], q, dtype_of(a[8], type), "out");
+        const bitlin_stream_t stream = stream_of(a[10], q);
+        const at::Tensor out = output(a[7], q, dtype_of(a[8], type), a[10], stream, "out");
         const bitlin_rows dst = rows_of(out, "out");
         float* lse = nullptr;
         if (a[9] != Py_None) {
@@ -238,7 +258,7 @@ PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n)
             lse = static_cast<float*>(t.data_ptr());
         }
         check(bitlin_kv_attend(h, batch, size_of(q.size(0)), &qr, size_of(q.size(1)), (float)scale,
-                               PyObject_IsTrue(a[6]), &dst, lse, stream_of(a[10], q)),
+                               PyObject_IsTrue(a[6]), &dst, lse, stream),
               "bitlin_kv_attend", bitlin_kv_cuda_error(h));
         return wrap(out, a[7]);
     } catch (const Refused&) {

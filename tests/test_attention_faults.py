@@ -155,3 +155,34 @@ def test_closed_handles_are_refused(hrb):
     with pytest.raises(ValueError, match="closed"):
         cache.attend(q, batch)
     assert torch.equal(kp, before[0]) and torch.equal(vp, before[1])
+
+
+def stream_of_memory(t):
+    """The stream whose blocks of torch's allocator a tensor lies in."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's")
+
+
+@gpu
+def test_new_outputs_lie_on_the_stream_of_the_call(hrb):
+    """With `stream` and no output given, the output's memory is that stream's."""
+    batch, offsets, kp, vp, q = attend_case(hrb, 64, 16, 2, 4, [3, 1], [60, 9], torch.bfloat16, 38)
+    cache, rope = hrb.PagedKV(kp, vp), hrb.Rope(freqs(32))
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    k = torch.randn((4, 2, 64), generator=generator(39), device="cuda").bfloat16()
+    calls = (lambda s: rope.apply(q, pos, stream=s), lambda s: cache.append(k, k, batch, rope=rope, pos=pos, q=q, stream=s),
+             lambda s: cache.attend(q, batch, stream=s), lambda s: cache.attend(q, batch, dtype=torch.float32, stream=s))
+    for call in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        got = call(side)
+        assert stream_of_memory(got) == side.cuda_stream
+        assert stream_of_memory(call(torch.cuda.current_stream())) == torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got, want)
+        with torch.cuda.stream(side):
+            assert stream_of_memory(call(None)) == side.cuda_stream
+        torch.cuda.synchronize()
