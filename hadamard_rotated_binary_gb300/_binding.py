@@ -124,6 +124,24 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _new_output(shape, dtype, device, stream):
+    """A new tensor for a call's result.  A call on a stream of its own takes the memory on that
+    stream (the current one may still use what its allocator would hand out) and keeps it from
+    being handed out again before the current stream is through with it too."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    if stream.cuda_stream != current.cuda_stream:
+        out.record_stream(current)
+    return out
+
+
 def mlp_forward(gate_up: "BitLinear", down: "BitLinear", x, out=None, stream=None):
     """bitlin_mlp_forward: down(silu(gate) * up) with [gate | up] = gate_up(x)."""
     import torch
@@ -132,7 +150,7 @@ def mlp_forward(gate_up: "BitLinear", down: "BitLinear", x, out=None, stream=Non
         raise ValueError("x must be a contiguous float32 CUDA tensor [M][K]")
     M = int(x.shape[0])
     if out is None:
-        out = torch.empty((M, down.N), dtype=torch.float32, device=x.device)
+        out = _new_output((M, down.N), torch.float32, x.device, stream)
     st = lib().bitlin_mlp_forward(gate_up.handle, down.handle, x.data_ptr(), M, out.data_ptr(),
                                   _stream_handle(stream))
     if st != BITLIN_OK:
@@ -233,7 +251,7 @@ class BitLinear:
             raise ValueError("x must be a contiguous float32 CUDA tensor [M][K]")
         M = int(x2.shape[0])
         if out is None:
-            out = torch.empty((M, self.N), dtype=torch.float32, device=x2.device)
+            out = _new_output((M, self.N), torch.float32, x2.device, stream)
         self._check(lib().bitlin_forward(self._h, x2.data_ptr(), M, out.data_ptr(), _stream_handle(stream)),
                     "bitlin_forward")
         return out.reshape(-1) if squeeze else out
@@ -265,7 +283,7 @@ class BitLinear:
             raise ValueError("x must be a contiguous float32 CUDA tensor [M][K]")
         M = int(x.shape[0])
         if ids is None:
-            ids = torch.empty((M,), dtype=torch.int32, device=x.device)
+            ids = _new_output((M,), torch.int32, x.device, stream)
         self._check(lib().bitlin_argmax(self._h, x.data_ptr(), M, logits.data_ptr() if logits is not None else None,
                                         ids.data_ptr(), _stream_handle(stream)), "bitlin_argmax")
         return ids
@@ -279,7 +297,7 @@ class BitLinear:
             raise ValueError("ids must be a contiguous int32 CUDA tensor [M]")
         M = int(ids.shape[0])
         if out is None:
-            out = torch.empty((M, self.K), dtype=torch.float32, device=ids.device)
+            out = _new_output((M, self.K), torch.float32, ids.device, stream)
         self._check(lib().bitlin_embed(self._h, ids.data_ptr(), M, out.data_ptr(), _stream_handle(stream)),
                     "bitlin_embed")
         return out

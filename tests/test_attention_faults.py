@@ -186,3 +186,29 @@ def test_new_outputs_lie_on_the_stream_of_the_call(hrb):
         with torch.cuda.stream(side):
             assert stream_of_memory(call(None)) == side.cuda_stream
         torch.cuda.synchronize()
+
+
+@gpu
+def test_new_outputs_of_projections_lie_on_the_stream_of_the_call(hrb):
+    """The same for the one-bit matrices, which the attention side stands between."""
+    gen = generator(40)
+
+    def linear(n, k):
+        bits = torch.randint(-2**31, 2**31, (n, k // 32), generator=gen, device="cuda").to(torch.int32)
+        scales = (torch.rand((n, k // 128), generator=gen, device="cuda") * 0.02 + 0.005).half()
+        return hrb.BitLinear(bits, scales, torch.ones(k, device="cuda"))
+
+    lin, up = linear(1024, 1024), linear(2048, 1024)
+    x = torch.randn((2, 1024), generator=gen, device="cuda")
+    ids = torch.tensor([3, 1000], dtype=torch.int32, device="cuda")
+    for call in (lambda s: lin(x, stream=s), lambda s: lin.argmax(x, stream=s), lambda s: lin.embed(ids, stream=s),
+                 lambda s: hrb.mlp_forward(up, lin, x, stream=s)):
+        want = call(None)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        got = call(side)
+        assert stream_of_memory(got) == side.cuda_stream
+        assert stream_of_memory(call(torch.cuda.current_stream())) == torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got, want)
+        torch.cuda.synchronize()
