@@ -48,7 +48,7 @@ class Rope:
     def apply(self, x, pos, out=None, dtype=None, inverse: bool = False, stream=None):
         """bitlin_rope_apply: x [tokens][heads][dim] rotated by pos (int32 [axes][tokens]), into `out`
         (x itself is allowed) or a new tensor of `dtype` (x's where None)."""
-        return native.rope_apply(self._h, self.axes, x, pos, out, dtype, inverse, stream)
+        return native.rope_apply(self._h, self.device.index, self.axes, x, pos, out, dtype, inverse, stream)
 
     def close(self):
         if getattr(self, "_h", None):
@@ -74,6 +74,8 @@ class KVBatch:
         for t in (q_offsets, kv_lens, table):
             if t.dtype != torch.int32 or not t.is_cuda:
                 raise ValueError("q_offsets, kv_lens and table must be int32 CUDA tensors")
+            if t.device != kv_lens.device:
+                raise ValueError("q_offsets, kv_lens and table must be on one device")
         seqs = kv_lens.numel()
         if not (q_offsets.is_contiguous() and kv_lens.is_contiguous()) or q_offsets.numel() != seqs + 1:
             raise ValueError("q_offsets [seqs + 1] and kv_lens [seqs] must be contiguous")
@@ -82,6 +84,7 @@ class KVBatch:
         if table.stride(0) < table.shape[1] and seqs > 1:
             raise ValueError("table's rows must not overlap")
         self.q_offsets, self.kv_lens, self.table = q_offsets, kv_lens, table
+        self.device = kv_lens.device
         # the row length bounds what is read; rows of a wider table may be longer apart
         self._c = Batch(seqs, q_offsets.data_ptr(), kv_lens.data_ptr(), table.data_ptr(), table.shape[1],
                         table.stride(0))
@@ -100,6 +103,8 @@ class PagedKV:
             raise ValueError("k and v must be [pages][page_size][kv_heads][head_dim] of one type and layout")
         if not (k.is_cuda and v.is_cuda) or k.stride(3) != 1 or k.dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("k and v must be bfloat16 or float16 CUDA tensors with contiguous heads")
+        if k.device != v.device:
+            raise ValueError("k and v must be on one device")
         self.k, self.v = k, v
         self.device, self.dtype = k.device, k.dtype
         pages, page_size, self.kv_heads, self.head_dim = k.shape
@@ -116,21 +121,28 @@ class PagedKV:
         if st != BITLIN_OK:
             raise BitlinError(st, what, lib().bitlin_kv_cuda_error(self._h))
 
+    def _address_of(self, batch: KVBatch) -> int:
+        if batch.device != self.device:
+            raise ValueError("the batch must be on the cache's device")
+        return batch.address
+
     def append(self, k, v, batch: KVBatch, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None):
         """bitlin_kv_append: k and v [tokens][kv_heads][head_dim] to their places, k rotated; q
         [tokens][heads][head_dim], when given, is rotated too and returned in the cache's type."""
         if rope is not None and not rope._h:
             raise ValueError("the rope's handle is closed")  # (None would mean no rotation)
+        if rope is not None and rope.device != self.device:
+            raise ValueError("the rope must be on the cache's device")
         r, axes = (None, 0) if rope is None else (rope._h, rope.axes)
-        return native.kv_append(self._h, self.kv_heads, self.head_dim, self.dtype, batch.address, k, v, r, axes, pos, q,
-                                q_out, stream)
+        return native.kv_append(self._h, self.device.index, self.kv_heads, self.head_dim, self.dtype,
+                                self._address_of(batch), k, v, r, axes, pos, q, q_out, stream)
 
     def attend(self, q, batch: KVBatch, scale: float | None = None, causal: bool = True, out=None, dtype=None,
                lse=None, stream=None):
         """bitlin_kv_attend: attention of q [tokens][heads][head_dim] over the batch's sequences, into
         `out` or a new tensor of `dtype` (the cache's type, or float32); lse: float32 [tokens][heads]."""
-        return native.kv_attend(self._h, self.head_dim, self.dtype, batch.address, q, scale, causal, out, dtype, lse,
-                                stream)
+        return native.kv_attend(self._h, self.device.index, self.head_dim, self.dtype, self._address_of(batch), q, scale,
+                                causal, out, dtype, lse, stream)
 
     def set_wait_budget(self, ns: int):
         self._check(lib().bitlin_kv_set_wait_budget(self._h, int(ns)), "bitlin_kv_set_wait_budget")

@@ -78,12 +78,19 @@ int type_of(at::ScalarType t)
     return t == at::kFloat ? BITLIN_F32 : t == at::kBFloat16 ? BITLIN_BF16 : t == at::kHalf ? BITLIN_F16 : -1;
 }
 
+// A kernel reads what it is given on the device of its handle alone.
+void same_device(const at::Tensor& x, long device, const char* what)
+{
+    if (x.device().index() != device) refuse("%s must be on the handle's device", what);
+}
+
 // The C-ABI's view of a CUDA tensor [tokens][heads][dim] whose last dimension is contiguous.
-bitlin_rows rows_of(const at::Tensor& x, const char* what)
+bitlin_rows rows_of(const at::Tensor& x, long device, const char* what)
 {
     const int type = type_of(x.scalar_type());
     if (type < 0 || !x.is_cuda() || x.dim() != 3)
         refuse("%s must be a float32, bfloat16 or float16 CUDA tensor [tokens][heads][dim]", what);
+    same_device(x, device, what);
     if (x.stride(2) != 1 && x.size(2) != 1) refuse("%s's last dimension must be contiguous", what);
     // a dimension of one has no stride that matters
     const int64_t head = x.size(1) == 1 ? x.size(2) : x.stride(1);
@@ -132,11 +139,12 @@ bitlin_stream_t stream_of(PyObject* stream, const at::Tensor& x)
     return static_cast<bitlin_stream_t>(s);
 }
 
-const int32_t* positions(PyObject* pos, long axes, int64_t tokens)
+const int32_t* positions(PyObject* pos, long axes, int64_t tokens, long device)
 {
     const at::Tensor& t = tensor(pos, "pos");
     if (t.scalar_type() != at::kInt || !t.is_cuda() || !t.is_contiguous() || t.numel() != axes * tokens)
         refuse("pos must be a contiguous int32 CUDA tensor [axes][tokens]");
+    same_device(t, device, "pos");
     return static_cast<const int32_t*>(t.data_ptr());
 }
 
@@ -160,67 +168,69 @@ bool arguments(Py_ssize_t n, Py_ssize_t want)
     return n == want;
 }
 
-// (handle, axes, x, pos, out, dtype, inverse, stream)
+// (handle, device, axes, x, pos, out, dtype, inverse, stream)
 PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    if (!arguments(n, 8)) return nullptr;
+    if (!arguments(n, 9)) return nullptr;
     HANDLE_TH_ERRORS
     try {
         auto h = static_cast<bitlin_rope_t>(handle_of(a[0]));
-        const at::Tensor& x = tensor(a[2], "x");
-        const bitlin_rows src = rows_of(x, "x");
-        const int32_t* pos = positions(a[3], integer(a[1]), x.size(0));
-        const bitlin_stream_t stream = stream_of(a[7], x);
-        const at::Tensor out = output(a[4], x, dtype_of(a[5], x.scalar_type()), a[7], stream, "out");
-        const bitlin_rows dst = rows_of(out, "out");
+        const long device = integer(a[1]);
+        const at::Tensor& x = tensor(a[3], "x");
+        const bitlin_rows src = rows_of(x, device, "x");
+        const int32_t* pos = positions(a[4], integer(a[2]), x.size(0), device);
+        const bitlin_stream_t stream = stream_of(a[8], x);
+        const at::Tensor out = output(a[5], x, dtype_of(a[6], x.scalar_type()), a[8], stream, "out");
+        const bitlin_rows dst = rows_of(out, device, "out");
         check(bitlin_rope_apply(h, &src, size_of(x.size(0)), size_of(x.size(1)), size_of(x.size(2)), pos, &dst,
-                                PyObject_IsTrue(a[6]), stream),
+                                PyObject_IsTrue(a[7]), stream),
               "bitlin_rope_apply", 0);
-        return wrap(out, a[4]);
+        return wrap(out, a[5]);
     } catch (const Refused&) {
         return nullptr;
     }
     END_HANDLE_TH_ERRORS
 }
 
-// (handle, kv_heads, head_dim, cache dtype, batch, k, v, rope, axes, pos, q, q_out, stream)
+// (handle, device, kv_heads, head_dim, cache dtype, batch, k, v, rope, axes, pos, q, q_out, stream)
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    if (!arguments(n, 13)) return nullptr;
+    if (!arguments(n, 14)) return nullptr;
     HANDLE_TH_ERRORS
     try {
         auto h = static_cast<bitlin_kv_t>(handle_of(a[0]));
-        const long kv_heads = integer(a[1]), dim = integer(a[2]);
-        const at::ScalarType type = dtype_of(a[3], at::kFloat);
-        const auto* batch = static_cast<const bitlin_kv_batch*>(handle_of(a[4]));
-        const at::Tensor &k = tensor(a[5], "k"), &v = tensor(a[6], "v");
-        const bitlin_rows kr = rows_of(k, "k"), vr = rows_of(v, "v");
+        const long device = integer(a[1]);
+        const long kv_heads = integer(a[2]), dim = integer(a[3]);
+        const at::ScalarType type = dtype_of(a[4], at::kFloat);
+        const auto* batch = static_cast<const bitlin_kv_batch*>(handle_of(a[5]));
+        const at::Tensor &k = tensor(a[6], "k"), &v = tensor(a[7], "v");
+        const bitlin_rows kr = rows_of(k, device, "k"), vr = rows_of(v, device, "v");
         if (k.sizes() != v.sizes() || k.size(1) != kv_heads || k.size(2) != dim)
             refuse("k and v must be [tokens][kv_heads][head_dim]");
         const int64_t tokens = k.size(0);
-        const bitlin_stream_t stream = stream_of(a[12], k);
+        const bitlin_stream_t stream = stream_of(a[13], k);
         bitlin_rope_t rope = nullptr;
         const int32_t* pos = nullptr;
-        if (a[7] != Py_None) {
-            rope = static_cast<bitlin_rope_t>(handle_of(a[7]));
-            if (a[9] != Py_None) pos = positions(a[9], integer(a[8]), tokens);
+        if (a[8] != Py_None) {
+            rope = static_cast<bitlin_rope_t>(handle_of(a[8]));
+            if (a[10] != Py_None) pos = positions(a[10], integer(a[9]), tokens, device);
         }
         bitlin_rows qr = {}, or_ = {};
         at::Tensor out;
         int heads = 0;
-        if (a[10] != Py_None) {
-            const at::Tensor& q = tensor(a[10], "q");
-            qr = rows_of(q, "q");
+        if (a[11] != Py_None) {
+            const at::Tensor& q = tensor(a[11], "q");
+            qr = rows_of(q, device, "q");
             if (q.size(0) != tokens || q.size(2) != dim) refuse("q must be [tokens][heads][head_dim]");
             heads = size_of(q.size(1));
-            out = output(a[11], q, type, a[12], stream, "q_out");
-            or_ = rows_of(out, "q_out");
+            out = output(a[12], q, type, a[13], stream, "q_out");
+            or_ = rows_of(out, device, "q_out");
         }
-        const bool has_q = a[10] != Py_None;
+        const bool has_q = a[11] != Py_None;
         check(bitlin_kv_append(h, batch, size_of(tokens), rope, pos, &kr, &vr, has_q ? &qr : nullptr, heads,
                                has_q ? &or_ : nullptr, stream),
               "bitlin_kv_append", bitlin_kv_cuda_error(h));
-        if (has_q) return wrap(out, a[11]);
+        if (has_q) return wrap(out, a[12]);
         Py_RETURN_NONE;
     } catch (const Refused&) {
         return nullptr;
@@ -228,39 +238,41 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// (handle, head_dim, cache dtype, batch, q, scale, causal, out, dtype, lse, stream)
+// (handle, device, head_dim, cache dtype, batch, q, scale, causal, out, dtype, lse, stream)
 PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    if (!arguments(n, 11)) return nullptr;
+    if (!arguments(n, 12)) return nullptr;
     HANDLE_TH_ERRORS
     try {
         auto h = static_cast<bitlin_kv_t>(handle_of(a[0]));
-        const long dim = integer(a[1]);
-        const at::ScalarType type = dtype_of(a[2], at::kFloat);
-        const auto* batch = static_cast<const bitlin_kv_batch*>(handle_of(a[3]));
-        const at::Tensor& q = tensor(a[4], "q");
-        const bitlin_rows qr = rows_of(q, "q");
+        const long device = integer(a[1]);
+        const long dim = integer(a[2]);
+        const at::ScalarType type = dtype_of(a[3], at::kFloat);
+        const auto* batch = static_cast<const bitlin_kv_batch*>(handle_of(a[4]));
+        const at::Tensor& q = tensor(a[5], "q");
+        const bitlin_rows qr = rows_of(q, device, "q");
         if (q.size(2) != dim) refuse("q must be [tokens][heads][head_dim]");
         double scale = 1.0 / sqrt((double)dim);
-        if (a[5] != Py_None) {
-            scale = PyFloat_AsDouble(a[5]);
+        if (a[6] != Py_None) {
+            scale = PyFloat_AsDouble(a[6]);
             if (scale == -1.0 && PyErr_Occurred()) throw Refused();
         }
-        const bitlin_stream_t stream = stream_of(a[10], q);
-        const at::Tensor out = output(a[7], q, dtype_of(a[8], type), a[10], stream, "out");
-        const bitlin_rows dst = rows_of(out, "out");
+        const bitlin_stream_t stream = stream_of(a[11], q);
+        const at::Tensor out = output(a[8], q, dtype_of(a[9], type), a[11], stream, "out");
+        const bitlin_rows dst = rows_of(out, device, "out");
         float* lse = nullptr;
-        if (a[9] != Py_None) {
-            const at::Tensor& t = tensor(a[9], "lse");
+        if (a[10] != Py_None) {
+            const at::Tensor& t = tensor(a[10], "lse");
             if (t.scalar_type() != at::kFloat || !t.is_cuda() || !t.is_contiguous() || t.dim() != 2 ||
                 t.size(0) != q.size(0) || t.size(1) != q.size(1))
                 refuse("lse must be a contiguous float32 CUDA tensor [tokens][heads]");
+            same_device(t, device, "lse");
             lse = static_cast<float*>(t.data_ptr());
         }
         check(bitlin_kv_attend(h, batch, size_of(q.size(0)), &qr, size_of(q.size(1)), (float)scale,
-                               PyObject_IsTrue(a[6]), &dst, lse, stream),
+                               PyObject_IsTrue(a[7]), &dst, lse, stream),
               "bitlin_kv_attend", bitlin_kv_cuda_error(h));
-        return wrap(out, a[7]);
+        return wrap(out, a[8]);
     } catch (const Refused&) {
         return nullptr;
     }

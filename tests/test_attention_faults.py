@@ -212,3 +212,44 @@ def test_new_outputs_of_projections_lie_on_the_stream_of_the_call(hrb):
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(got, want)
         torch.cuda.synchronize()
+
+
+def test_batch_tensors_of_two_devices_are_refused(hrb):
+    """Checked by what the tensors say of themselves: no device is needed."""
+    class Elsewhere:
+        dtype, is_cuda = torch.int32, True
+
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+    for at in ((0, 0, 1), (0, 1, 0), (1, 0, 0)):
+        with pytest.raises(ValueError, match="one device"):
+            hrb.KVBatch(*(Elsewhere(i) for i in at))
+
+
+@gpu
+def test_tensors_of_another_device_are_refused(hrb):
+    """Handles that live on a second device, as far as the binding knows, refuse tensors of the first."""
+    batch, offsets, kp, vp, q = attend_case(hrb, 64, 16, 2, 4, [1], [9], torch.bfloat16, 41)
+    cache, rope = hrb.PagedKV(kp, vp), hrb.Rope(freqs(32))
+    here, there = cache.device, torch.device("cuda", 1)
+    pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k = torch.zeros((1, 2, 64), device="cuda").bfloat16()
+    calls = (lambda: cache.append(k, k, batch), lambda: cache.append(k, k, batch, rope=rope, pos=pos), lambda: cache.attend(q, batch))
+    rope.device = there
+    with pytest.raises(ValueError, match="x must be on the handle's device"):
+        rope.apply(q, pos)
+    with pytest.raises(ValueError, match="the rope must be on the cache's device"):
+        cache.append(k, k, batch, rope=rope, pos=pos)
+    cache.device = there
+    for call in calls:
+        with pytest.raises(ValueError, match="the batch must be on the cache's device"):
+            call()
+    batch.device = there
+    for call in calls:
+        with pytest.raises(ValueError, match="must be on the handle's device"):
+            call()
+    rope.device = cache.device = batch.device = here
+    for call in calls:
+        call()
+    assert cache.get_error() == 0
