@@ -62,13 +62,33 @@ class Rope:
             pass
 
 
+def _held(name: str):
+    """A tensor whose address a handle keeps: its contents may change, the tensor itself may not
+    (the old one's memory would be freed under the calls that read it).  Assigning the same tensor
+    again, as `batch.kv_lens += 1` does, is no change."""
+
+    def get(self):
+        return self.__dict__["_" + name]
+
+    def put(self, value):
+        if value is not self.__dict__.get("_" + name, value):
+            raise AttributeError(f"{name} cannot be replaced: change its contents, or make a new {type(self).__name__}")
+        self.__dict__["_" + name] = value
+
+    return property(get, put)
+
+
 class KVBatch:
     """The new tokens of a batch of sequences (a bitlin_kv_batch; holds the tensors).
 
     q_offsets  int32 CUDA [seqs + 1]: sequence s owns token rows q_offsets[s] .. q_offsets[s + 1] - 1
     kv_lens    int32 CUDA [seqs]: tokens in the cache, the new ones with them
     table      int32 CUDA [seqs][pages per sequence]
+
+    Calls read the tensors on the device: their contents may change between calls, the tensors stay.
     """
+
+    q_offsets, kv_lens, table = _held("q_offsets"), _held("kv_lens"), _held("table")
 
     def __init__(self, q_offsets, kv_lens, table):
         for t in (q_offsets, kv_lens, table):
@@ -97,6 +117,8 @@ class PagedKV:
     k, v  bfloat16 or float16 CUDA tensors [pages][page_size][kv_heads][head_dim] with the same
           strides, head_dim contiguous (a permuted view of another page layout is fine)
     """
+
+    k, v = _held("k"), _held("v")
 
     def __init__(self, k, v):
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:

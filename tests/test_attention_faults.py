@@ -9,7 +9,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from test_attention_side import (  # noqa: E402,F401
-    attend_case, attend64_long, check_attended, check_long, freqs, generator, gpu, hrb, make_batch, make_pools, shared_pages,
+    attend64, attend64_long, attend_case, check_attended, check_long, freqs, generator, gpu, hrb, make_batch, make_pools, shared_pages,
 )
 
 
@@ -253,3 +253,22 @@ def test_tensors_of_another_device_are_refused(hrb):
     for call in calls:
         call()
     assert cache.get_error() == 0
+
+
+@gpu
+def test_tensors_that_handles_point_to_cannot_be_replaced(hrb):
+    batch, offsets, kp, vp, q = attend_case(hrb, 64, 16, 1, 2, [1], [40], torch.bfloat16, 42)
+    cache = hrb.PagedKV(kp, vp)
+    want = cache.attend(q, batch)
+    for handle, names in ((batch, ("q_offsets", "kv_lens", "table")), (cache, ("k", "v"))):
+        for name in names:
+            held = getattr(handle, name)
+            with pytest.raises(AttributeError, match=name):
+                setattr(handle, name, held.clone())
+            assert getattr(handle, name) is held
+    assert torch.equal(cache.attend(q, batch), want)
+    # contents may change, also in the form that assigns the same tensor again
+    batch.kv_lens -= 8
+    assert cache.k is kp and cache.v is vp
+    ref = attend64(q, kp, vp, offsets, [32], batch.table, 0.125, True)
+    check_attended(cache.attend(q, batch), None, ref, torch.bfloat16)
