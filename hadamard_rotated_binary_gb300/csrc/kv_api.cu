@@ -18,6 +18,8 @@ constexpr long long kDefaultWaitBudgetNs = 2000000000LL;  // 2 s per bounded wai
 
 bitlin_status status_of(cudaError_t e)
 {
+    // what is reported here is not left for a later call to find
+    if (e != cudaSuccess) cudaGetLastError();
     return e == cudaSuccess ? BITLIN_OK : e == cudaErrorMemoryAllocation ? BITLIN_ENOMEM : BITLIN_ECUDA;
 }
 

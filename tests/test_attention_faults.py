@@ -272,3 +272,51 @@ def test_tensors_that_handles_point_to_cannot_be_replaced(hrb):
     assert cache.k is kp and cache.v is vp
     ref = attend64(q, kp, vp, offsets, [32], batch.table, 0.125, True)
     check_attended(cache.attend(q, batch), None, ref, torch.bfloat16)
+
+
+class InvalidCapture:
+    """A stream whose capture has been made invalid (by a wait, which a capture does not allow):
+    launches into it fail on the host."""
+
+    ERROR = 901  # cudaErrorStreamCaptureInvalidated
+
+    def __enter__(self):
+        import ctypes
+
+        self.cuda = ctypes.CDLL("libcuda.so.1")
+        self.stream = torch.cuda.Stream()
+        self.raw, self.graph = ctypes.c_void_p(self.stream.cuda_stream), ctypes.c_void_p()
+        torch.cuda.synchronize()
+        assert self.cuda.cuStreamBeginCapture_v2(self.raw, 2) == 0
+        assert self.cuda.cuStreamSynchronize(self.raw) != 0
+        return self.stream
+
+    def __exit__(self, *_):
+        import ctypes
+
+        assert self.cuda.cuStreamEndCapture(self.raw, ctypes.byref(self.graph)) == self.ERROR
+
+
+def calls_of(hrb, seed):
+    """A cache, and each call of the attention side on a stream, with outputs that are given."""
+    batch, offsets, kp, vp, q = attend_case(hrb, 64, 16, 2, 4, [1], [9], torch.bfloat16, seed)
+    cache, rope = hrb.PagedKV(kp, vp), hrb.Rope(freqs(32))
+    cache.attend(q, batch)
+    out, pos = torch.empty_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+    k = torch.zeros((1, 2, 64), device="cuda").bfloat16()
+    return cache, (lambda s: rope.apply(q, pos, out=out, stream=s), lambda s: cache.append(k, k, batch, stream=s),
+                   lambda s: cache.attend(q, batch, out=out, stream=s))
+
+
+@gpu
+def test_a_failed_call_does_not_fail_a_later_one(hrb):
+    cache, calls = calls_of(hrb, 43)
+    bits = torch.zeros((8, 32), dtype=torch.int32, device="cuda")
+    scales, signs = torch.ones((8, 8), device="cuda").half(), torch.ones(1024, device="cuda")
+    for call in calls:
+        with InvalidCapture() as stream:
+            with pytest.raises(hrb.BitlinError):
+                call(stream)
+        hrb.BitLinear(bits, scales, signs).close()  # (asks for the last error of its launches)
+        call(stream)
+    assert cache.get_error() == 0
