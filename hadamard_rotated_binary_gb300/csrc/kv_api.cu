@@ -23,7 +23,8 @@ bitlin_status status_of(cudaError_t e)
     return e == cudaSuccess ? BITLIN_OK : e == cudaErrorMemoryAllocation ? BITLIN_ENOMEM : BITLIN_ECUDA;
 }
 
-bitlin_status from_cuda(bitlin_kv_t h, cudaError_t e)
+template <typename Handle>
+bitlin_status from_cuda(Handle h, cudaError_t e)
 {
     if (e != cudaSuccess) h->last_cuda_error = (int)e;
     return status_of(e);
@@ -191,8 +192,10 @@ bitlin_status bitlin_rope_apply(bitlin_rope_t r, const bitlin_rows* x, int token
     p.heads = heads;
     p.dim = head_dim;
     p.inverse = inverse;
-    return status_of(bitlin_launch_turn(p, x->dtype, out->dtype, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(r, bitlin_launch_turn(p, x->dtype, out->dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
+
+int bitlin_rope_cuda_error(bitlin_rope_t r) { return r ? r->last_cuda_error : 0; }
 
 bitlin_status bitlin_rope_destroy(bitlin_rope_t r)
 {

@@ -114,6 +114,7 @@ struct bitlin_rope {
     int device = 0;
     int rotary = 0, axes = 0, adjacent = 0;
     bitlin_impl::Turn* turns = nullptr;
+    int last_cuda_error = 0;
 };
 
 struct bitlin_kv {

@@ -36,10 +36,15 @@ struct Refused {};
     throw Refused();
 }
 
-// Raises BitlinError for a call's status.
-void check(bitlin_status status, const char* call, int cuda_error)
+int cuda_error_of(bitlin_rope_t h) { return bitlin_rope_cuda_error(h); }
+int cuda_error_of(bitlin_kv_t h) { return bitlin_kv_cuda_error(h); }
+
+// Raises BitlinError for a call's status, with the CUDA error that the call left in its handle.
+template <typename Handle>
+void check(bitlin_status status, const char* call, Handle h)
 {
     if (status == BITLIN_OK) return;
+    const int cuda_error = status == BITLIN_ECUDA || status == BITLIN_ENOMEM ? cuda_error_of(h) : 0;
     PyObject* module = PyImport_ImportModule("hadamard_rotated_binary_gb300._binding");
     PyObject* type = module ? PyObject_GetAttrString(module, "BitlinError") : nullptr;
     PyObject* error = type ? PyObject_CallFunction(type, "isi", (int)status, call, cuda_error) : nullptr;
@@ -184,7 +189,7 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n)
         const bitlin_rows dst = rows_of(out, device, "out");
         check(bitlin_rope_apply(h, &src, size_of(x.size(0)), size_of(x.size(1)), size_of(x.size(2)), pos, &dst,
                                 PyObject_IsTrue(a[7]), stream),
-              "bitlin_rope_apply", 0);
+              "bitlin_rope_apply", h);
         return wrap(out, a[5]);
     } catch (const Refused&) {
         return nullptr;
@@ -229,7 +234,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
         const bool has_q = a[11] != Py_None;
         check(bitlin_kv_append(h, batch, size_of(tokens), rope, pos, &kr, &vr, has_q ? &qr : nullptr, heads,
                                has_q ? &or_ : nullptr, stream),
-              "bitlin_kv_append", bitlin_kv_cuda_error(h));
+              "bitlin_kv_append", h);
         if (has_q) return wrap(out, a[12]);
         Py_RETURN_NONE;
     } catch (const Refused&) {
@@ -271,7 +276,7 @@ PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n)
         }
         check(bitlin_kv_attend(h, batch, size_of(q.size(0)), &qr, size_of(q.size(1)), (float)scale,
                                PyObject_IsTrue(a[7]), &dst, lse, stream),
-              "bitlin_kv_attend", bitlin_kv_cuda_error(h));
+              "bitlin_kv_attend", h);
         return wrap(out, a[8]);
     } catch (const Refused&) {
         return nullptr;

@@ -406,6 +406,9 @@ bitlin_status bitlin_rope_create(bitlin_rope_t* out, int rotary_dim, int axes, c
 bitlin_status bitlin_rope_apply(bitlin_rope_t r, const bitlin_rows* x, int tokens, int heads, int head_dim,
                                 const int32_t* pos, const bitlin_rows* out, int inverse, bitlin_stream_t stream);
 
+/* The cudaError_t value behind the last BITLIN_ECUDA of this handle (0 if none). */
+int bitlin_rope_cuda_error(bitlin_rope_t r);
+
 /* Release the handle.  NULL is accepted.  Synchronizes the device. */
 bitlin_status bitlin_rope_destroy(bitlin_rope_t r);
 

@@ -320,3 +320,18 @@ def test_a_failed_call_does_not_fail_a_later_one(hrb):
         hrb.BitLinear(bits, scales, signs).close()  # (asks for the last error of its launches)
         call(stream)
     assert cache.get_error() == 0
+
+
+@gpu
+def test_errors_name_the_cuda_error_of_their_own_call(hrb):
+    for i in range(3):
+        cache, calls = calls_of(hrb, 44)
+        with InvalidCapture() as stream:
+            with pytest.raises(hrb.BitlinError, match=f"cudaError {InvalidCapture.ERROR}"):
+                calls[i](stream)
+        calls[i](stream)  # the handle goes on
+        with pytest.raises(hrb.BitlinError) as refused:  # an argument error has no such code
+            cache.attend(torch.zeros((1, 3, 64), device="cuda").bfloat16(), hrb.KVBatch(*(
+                torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 1], [1], [[0]]))))
+        assert "cudaError" not in str(refused.value)
+        assert cache.get_error() == 0
