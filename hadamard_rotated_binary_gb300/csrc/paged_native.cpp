@@ -149,6 +149,8 @@ const int32_t* positions(PyObject* pos, long axes, int64_t tokens, long device)
     const at::Tensor& t = tensor(pos, "pos");
     if (t.scalar_type() != at::kInt || !t.is_cuda() || !t.is_contiguous() || t.numel() != axes * tokens)
         refuse("pos must be a contiguous int32 CUDA tensor [axes][tokens]");
+    if (t.dim() > 1 && (t.dim() != 2 || t.size(0) != axes || t.size(1) != tokens))  // as many numbers in another order
+        refuse("pos must be [axes][tokens]");
     same_device(t, device, "pos");
     return static_cast<const int32_t*>(t.data_ptr());
 }

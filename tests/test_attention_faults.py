@@ -335,3 +335,19 @@ def test_errors_name_the_cuda_error_of_their_own_call(hrb):
                 torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 1], [1], [[0]]))))
         assert "cudaError" not in str(refused.value)
         assert cache.get_error() == 0
+
+
+@gpu
+def test_positions_in_another_order_are_refused(hrb):
+    batch, offsets, kp, vp, q = attend_case(hrb, 64, 16, 2, 4, [5], [9], torch.bfloat16, 45)
+    cache, rope = hrb.PagedKV(kp, vp), hrb.Rope(freqs(32), axis=[i % 3 for i in range(32)])
+    pos = torch.randint(0, 99, (3, 5), generator=generator(46), device="cuda", dtype=torch.int32)
+    k = q[:, :2].contiguous()
+    before = kp.clone()
+    for bad in (pos.t().contiguous(), pos[None], pos.view(1, 15)):
+        with pytest.raises(ValueError, match="axes"):
+            rope.apply(q, bad)
+        with pytest.raises(ValueError, match="axes"):
+            cache.append(k, k, batch, rope=rope, pos=bad)
+    assert torch.equal(kp, before)
+    assert torch.equal(rope.apply(q, pos.view(-1)), rope.apply(q, pos))
