@@ -2,7 +2,8 @@
 
 Each CUDA source is compiled in parallel with nvcc, then linked into
 ``hadamard_rotated_binary_gb300/libbitlin.so``; csrc/paged_native.cpp, which takes torch tensors,
-is compiled with g++ against the installed torch and linked into ``_paged_native.so`` beside it.
+is compiled with g++ against the installed torch, if there is one, and linked into
+``_paged_native.so`` beside it.
 Usage: ``python -m
 hadamard_rotated_binary_gb300.build``.
 """
@@ -55,16 +56,17 @@ def _fingerprint() -> str:
     return h.hexdigest()
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found: the compiled binding is built against it")
-    return list(spec.submodule_search_locations)[0]
+    return list(spec.submodule_search_locations)[0] if spec and spec.submodule_search_locations else None
 
 
 def _start_native(force: bool):
-    """Start compiling paged_native.cpp if it is out of date: (process, fingerprint), or None."""
+    """Start compiling paged_native.cpp if it is out of date: (process, fingerprint), or None.
+    Where there is no torch there is nothing to bind: the library alone is built."""
     torch = _torch_dir()
+    if torch is None:
+        return None
     h = hashlib.sha256()
     for f in (NATIVE_SRC, os.path.join(INCLUDE, "bitlin.h"), os.path.join(torch, "version.py")):
         with open(f, "rb") as fh:
@@ -103,9 +105,16 @@ def _finish_native(started) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build libbitlin.so and the compiled binding if their sources changed (or force); returns the library's path."""
+    """Build libbitlin.so and, where torch is installed, the compiled binding, if their sources
+    changed (or force); returns the library's path."""
     started = _start_native(force)
-    path = _build_library(force, verbose)
+    try:
+        path = _build_library(force, verbose)
+    except BaseException:
+        if started is not None:
+            started[0].kill()
+            started[0].communicate()
+        raise
     _finish_native(started)
     return path
 

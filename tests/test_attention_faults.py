@@ -351,3 +351,22 @@ def test_positions_in_another_order_are_refused(hrb):
             cache.append(k, k, batch, rope=rope, pos=bad)
     assert torch.equal(kp, before)
     assert torch.equal(rope.apply(q, pos.view(-1)), rope.apply(q, pos))
+
+
+def without_torch(code):
+    """Run in a Python of its own that finds no torch."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", "import sys\nsys.modules['torch'] = None\n" + code], cwd=root,
+                          capture_output=True, text=True, timeout=600)
+    assert done.returncode == 0, done.stderr
+
+
+def test_the_library_builds_without_torch(hrb):
+    without_torch("from hadamard_rotated_binary_gb300 import build\n"
+                  "assert build.build() == build.LIB\n"
+                  "import hadamard_rotated_binary_gb300 as m\n"
+                  "assert m.lib().bitlin_version() >= 100\n")
