@@ -13,6 +13,9 @@ use raises.
 """
 from __future__ import annotations
 
+import os as _os
+from importlib.util import find_spec as _find_spec
+
 from ._binding import (  # noqa: F401
     BITLIN_EDEVICE,
     BITLIN_EINDEX,
@@ -53,9 +56,6 @@ def __getattr__(name: str):
 __all__ = [
     "BitLinear",
     "BitlinError",
-    "Rope",
-    "PagedKV",
-    "KVBatch",
     "mlp_forward",
     "load_q1g128",
     "q1g128_words",
@@ -66,8 +66,10 @@ __all__ = [
     "PATH_DECODE",
     "PATH_PREFILL",
     "PATH_TC_EXACT",
-    "PAIRS_HALF",
-    "PAIRS_ADJACENT",
     "PERM_NONE",
     "PERM_SSM_TILED_TO_GROUPED",
 ]
+
+# `import *` takes the attention side too where it can be had: with torch, and built.
+if _find_spec("torch") is not None and _os.path.exists(_os.path.join(_os.path.dirname(__file__), "_paged_native.so")):
+    __all__ += _PAGED

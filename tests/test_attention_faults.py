@@ -370,3 +370,12 @@ def test_the_library_builds_without_torch(hrb):
                   "assert build.build() == build.LIB\n"
                   "import hadamard_rotated_binary_gb300 as m\n"
                   "assert m.lib().bitlin_version() >= 100\n")
+
+
+def test_import_star_without_torch(hrb):
+    without_torch("from hadamard_rotated_binary_gb300 import *\n"
+                  "BitLinear, load_q1g128, PATH_AUTO\n"
+                  "assert 'Rope' not in globals()\n")
+    names = {}
+    exec("from hadamard_rotated_binary_gb300 import *", names)
+    assert {"BitLinear", "Rope", "PagedKV", "KVBatch", "PAIRS_HALF", "PAIRS_ADJACENT"} <= set(names)
