@@ -98,6 +98,7 @@ def lib() -> ctypes.CDLL:
     L.bitlin_rope_cuda_error.argtypes = [P]
     L.bitlin_rope_destroy.argtypes = [P]
     L.bitlin_kv_create.argtypes = [ctypes.POINTER(P), P, P, i32, i32, i32, i32, i32, i64, i64, i64]
+    L.bitlin_kv_share.argtypes = [P, P]
     L.bitlin_kv_append.argtypes = [P, B, i32, P, P, R, R, R, i32, R, P]
     L.bitlin_kv_attend.argtypes = [P, B, i32, R, i32, ctypes.c_float, i32, R, P, P]
     L.bitlin_kv_get_error.argtypes = [P]
@@ -105,7 +106,7 @@ def lib() -> ctypes.CDLL:
     L.bitlin_kv_set_wait_budget.argtypes = [P, i64]
     L.bitlin_kv_test_stall.argtypes = [P, i32]
     L.bitlin_kv_destroy.argtypes = [P]
-    for name in ("bitlin_rope_create", "bitlin_rope_apply", "bitlin_rope_cuda_error", "bitlin_rope_destroy", "bitlin_kv_create", "bitlin_kv_append",
+    for name in ("bitlin_rope_create", "bitlin_rope_apply", "bitlin_rope_cuda_error", "bitlin_rope_destroy", "bitlin_kv_create", "bitlin_kv_share", "bitlin_kv_append",
                  "bitlin_kv_attend", "bitlin_kv_get_error", "bitlin_kv_cuda_error", "bitlin_kv_set_wait_budget",
                  "bitlin_kv_test_stall", "bitlin_kv_destroy"):
         getattr(L, name).restype = i32

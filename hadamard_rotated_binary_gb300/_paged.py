@@ -116,11 +116,14 @@ class PagedKV:
 
     k, v  bfloat16 or float16 CUDA tensors [pages][page_size][kv_heads][head_dim] with the same
           strides, head_dim contiguous (a permuted view of another page layout is fine)
+    share another layer's cache, with heads at least as large, whose workspace to use (40 MB at
+          head_dim 256) in place of one of its own: the calls on both must then follow one
+          another in stream order
     """
 
     k, v = _held("k"), _held("v")
 
-    def __init__(self, k, v):
+    def __init__(self, k, v, share: PagedKV | None = None):
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
             raise ValueError("k and v must be [pages][page_size][kv_heads][head_dim] of one type and layout")
         if not (k.is_cuda and v.is_cuda) or k.stride(3) != 1 or k.dtype not in (torch.bfloat16, torch.float16):
@@ -135,9 +138,11 @@ class PagedKV:
         with torch.cuda.device(k.device):
             st = lib().bitlin_kv_create(ctypes.byref(h), k.data_ptr(), v.data_ptr(), pages, page_size, self.kv_heads,
                                         self.head_dim, _CODES[k.dtype], page_stride, slot_stride, head_stride)
-        if st != BITLIN_OK:
-            raise BitlinError(st, "bitlin_kv_create")
-        self._h = h.value
+            if st != BITLIN_OK:
+                raise BitlinError(st, "bitlin_kv_create")
+            self._h = h.value
+            if share is not None:
+                self._check(lib().bitlin_kv_share(self._h, share._h), "bitlin_kv_share")
 
     def _check(self, st: int, what: str):
         if st != BITLIN_OK:

@@ -168,7 +168,7 @@ __device__ __forceinline__ Seq load_seq(const AttendParams& p, int s)
     q.place0 = raw - (min(max(hi, 0), kMaxLen) - q.row0);
     q.len = raw < cap ? raw : (int)cap;
     q.tiles = (q.rows + p.tile_tokens - 1) / p.tile_tokens;
-    if (q.len < raw) p.dev_error[kKvErrIndex] = 1;
+    if (q.len < raw) *p.index_error = 1;
     return q;
 }
 
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto checked = [&](int page) {
             if (page >= 0 && page < p.pages) return page;
-            p.dev_error[kKvErrIndex] = 1;
+            *p.index_error = 1;
             return -1;  // outside the pool: the copy fills zeros
         };
         auto next_stage = [&]() {
@@ -1296,18 +1296,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (threadIdx.x == 0 && sh->abort) p.dev_error[kKvErrTimeout] = 1;
+    if (threadIdx.x == 0 && sh->abort) *p.timed_out = 1;
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int DP, typename T, bool F32OUT>
+cudaError_t load()
+{
+    static PerDeviceOnce once;
+    int dev = 0;
+    return once.run(&dev, [](int) {
+        return cudaFuncSetAttribute(bitlin_attend<DP, T, F32OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
+    });
 }
 
 template <int DP, typename T, bool F32OUT>
 cudaError_t launch(const AttendParams& p, const void* tmap_q, const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s)
 {
-    static PerDeviceOnce once;
-    int dev = 0;
-    cudaError_t e = once.run(&dev, [](int) {
-        return cudaFuncSetAttribute(bitlin_attend<DP, T, F32OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
-    });
+    const cudaError_t e = load<DP, T, F32OUT>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_sms);
@@ -1332,6 +1338,19 @@ cudaError_t pick_dim(const AttendParams& p, const void* tmap_q, const void* tmap
     return launch<256, T, F32OUT>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
 }
 
+template <int DP, typename T>
+cudaError_t load_outputs()
+{
+    const cudaError_t e = load<DP, T, false>();
+    return e == cudaSuccess ? load<DP, T, true>() : e;
+}
+
+template <typename T>
+cudaError_t load_dim(int dim)
+{
+    return dim <= 64 ? load_outputs<64, T>() : dim <= 128 ? load_outputs<128, T>() : load_outputs<256, T>();
+}
+
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 }  // namespace
@@ -1348,13 +1367,16 @@ void bitlin_attend_boxes(int dim, int page_size, int* box_k, int* box_v)
 // of about 250 tiles): 1,161 without, 1,152 at 2, 1,167 at 4.
 int bitlin_attend_item_extra(int dim) { return dim > 128 ? 2 : 4; }
 
-size_t bitlin_attend_workspace(int dim, int num_sms, size_t* ml_offset, size_t* ticket_offset)
+KvWorkspaceParts bitlin_attend_workspace(int dim, int num_sms)
 {
     const size_t padded = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
     const size_t rows = (size_t)2 * num_sms * kRows;
-    *ml_offset = rows * padded * sizeof(float);
-    *ticket_offset = *ml_offset + rows * 2 * sizeof(float);
-    return *ticket_offset + num_sms * sizeof(int);
+    KvWorkspaceParts w;
+    w.timed_out = num_sms * sizeof(int);
+    w.ml = (w.timed_out + sizeof(int) + 255) / 256 * 256;
+    w.o = w.ml + rows * 2 * sizeof(float);
+    w.bytes = w.o + rows * padded * sizeof(float);
+    return w;
 }
 
 void bitlin_attend_rows(int tokens, int seqs, int group, int* tile_tokens, int* q_box)
@@ -1369,6 +1391,11 @@ void bitlin_attend_rows(int tokens, int seqs, int group, int* tile_tokens, int* 
         *q_box = few;
         *tile_tokens -= *tile_tokens % few;
     }
+}
+
+cudaError_t bitlin_attend_load(int dim, int dtype)
+{
+    return dtype == BITLIN_BF16 ? load_dim<__nv_bfloat16>(dim) : load_dim<__half>(dim);
 }
 
 cudaError_t bitlin_launch_attend(const AttendParams& p, int dtype, int out_dtype, const void* tmap_q,

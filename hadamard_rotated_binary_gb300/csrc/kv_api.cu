@@ -133,6 +133,24 @@ cudaError_t encode_queries(const bitlin_kv& h, const bitlin_rows& q, int tokens,
     return encode(tmap, h.dtype, 3, q.data, dims, strides, boxes);
 }
 
+// A workspace for the handle's calls, with zero tickets.
+cudaError_t new_workspace(bitlin_kv& h)
+{
+    const KvWorkspaceParts parts = bitlin_attend_workspace(h.dim, h.num_sms);
+    std::shared_ptr<KvWorkspace> w;
+    try {
+        w = std::make_shared<KvWorkspace>();
+    } catch (const std::bad_alloc&) {
+        return cudaErrorMemoryAllocation;
+    }
+    cudaError_t e = cudaMalloc(&w->data, parts.bytes);
+    if (e == cudaSuccess) e = cudaMemset(w->data, 0, parts.ml);
+    if (e != cudaSuccess) return e;
+    w->bytes = parts.bytes;
+    h.workspace = std::move(w);
+    return cudaSuccess;
+}
+
 }  // namespace
 
 extern "C" {
@@ -245,14 +263,27 @@ bitlin_status bitlin_kv_create(bitlin_kv_t* out, void* k, void* v, int pages, in
     cudaError_t e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = encode_pool(*h, k, box_k, h->tmap_k);
     if (e == cudaSuccess) e = encode_pool(*h, v, box_v, h->tmap_v);
-    if (e == cudaSuccess) e = cudaMalloc(&h->dev_error, 2 * sizeof(int));
-    if (e == cudaSuccess) e = cudaMemset(h->dev_error, 0, 2 * sizeof(int));
+    if (e == cudaSuccess) e = bitlin_attend_load(head_dim, dtype);
+    if (e == cudaSuccess) e = cudaMalloc(&h->index_error, sizeof(int));
+    if (e == cudaSuccess) e = cudaMemset(h->index_error, 0, sizeof(int));
+    if (e == cudaSuccess) e = new_workspace(*h);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
-        cudaFree(h->dev_error);
+        cudaFree(h->index_error);
         return status_of(e);
     }
     *out = h.release();
+    return BITLIN_OK;
+}
+
+bitlin_status bitlin_kv_share(bitlin_kv_t kv, bitlin_kv_t with)
+{
+    if (!kv || !with || kv->device != with->device) return BITLIN_EINVAL;
+    if (with->workspace->bytes < bitlin_attend_workspace(kv->dim, kv->num_sms).bytes) return BITLIN_EINVAL;
+    // the handle's own workspace may be freed here: not under its calls
+    const cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return from_cuda(kv, e);
+    kv->workspace = with->workspace;
     return BITLIN_OK;
 }
 
@@ -280,7 +311,7 @@ bitlin_status bitlin_kv_append(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
     p.slot_stride = kv->slot_stride;
     p.head_stride = kv->head_stride;
     p.batch = batch_of(batch);
-    p.dev_error = kv->dev_error;
+    p.index_error = kv->index_error;
     p.pages = kv->pages;
     p.page_size = kv->page_size;
     p.tokens = tokens;
@@ -303,18 +334,8 @@ bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
     if (kv->sticky != BITLIN_OK) return kv->sticky;
     if (tokens == 0) return BITLIN_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    size_t ml = 0, tickets = 0;
-    const size_t bytes = bitlin_attend_workspace(kv->dim, kv->num_sms, &ml, &tickets);
-    if (!kv->workspace) {
-        cudaError_t e = cudaMalloc(&kv->workspace, bytes);
-        // zeroed in stream order: the kernel sees zero tickets
-        if (e == cudaSuccess) e = cudaMemsetAsync(kv->workspace + tickets, 0, bytes - tickets, st);
-        if (e != cudaSuccess) {
-            cudaFree(kv->workspace);
-            kv->workspace = nullptr;
-            return from_cuda(kv, e);
-        }
-    }
+    const KvWorkspaceParts parts = bitlin_attend_workspace(kv->dim, kv->num_sms);
+    unsigned char* workspace = kv->workspace->data;
     AttendParams p = {};
     p.v_pool = kv->v;
     p.page_stride = kv->page_stride;
@@ -325,10 +346,11 @@ bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
     p.out_token = out->token_stride;
     p.out_head = out->head_stride;
     p.lse = lse;
-    p.ws_o = reinterpret_cast<float*>(kv->workspace);
-    p.ws_ml = reinterpret_cast<float*>(kv->workspace + ml);
-    p.tickets = reinterpret_cast<int*>(kv->workspace + tickets);
-    p.dev_error = kv->dev_error;
+    p.ws_o = reinterpret_cast<float*>(workspace + parts.o);
+    p.ws_ml = reinterpret_cast<float*>(workspace + parts.ml);
+    p.tickets = reinterpret_cast<int*>(workspace);
+    p.timed_out = reinterpret_cast<int*>(workspace + parts.timed_out);
+    p.index_error = kv->index_error;
     p.wait_budget_ns = kv->wait_budget_ns;
     p.pages = kv->pages;
     p.page_size = kv->page_size;
@@ -368,12 +390,14 @@ bitlin_status bitlin_kv_get_error(bitlin_kv_t kv)
 {
     if (!kv) return BITLIN_EINVAL;
     cudaError_t e = cudaDeviceSynchronize();
-    int v[2] = {0, 0};
-    if (e == cudaSuccess) e = cudaMemcpy(v, kv->dev_error, sizeof(v), cudaMemcpyDeviceToHost);
+    int timed_out = 0, index_error = 0;
+    const KvWorkspaceParts parts = bitlin_attend_workspace(kv->dim, kv->num_sms);
+    if (e == cudaSuccess) e = cudaMemcpy(&timed_out, kv->workspace->data + parts.timed_out, sizeof(int), cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess) e = cudaMemcpy(&index_error, kv->index_error, sizeof(int), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return from_cuda(kv, e);
-    if (v[kKvErrTimeout]) kv->sticky = BITLIN_ETIMEOUT;
-    if (kv->sticky != BITLIN_OK || !v[kKvErrIndex]) return kv->sticky;
-    e = cudaMemset(kv->dev_error + kKvErrIndex, 0, sizeof(int));
+    if (timed_out) kv->sticky = BITLIN_ETIMEOUT;
+    if (kv->sticky != BITLIN_OK || !index_error) return kv->sticky;
+    e = cudaMemset(kv->index_error, 0, sizeof(int));
     // before a later call, on whatever stream, can set it again
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     return e == cudaSuccess ? BITLIN_EINDEX : from_cuda(kv, e);
@@ -385,8 +409,7 @@ bitlin_status bitlin_kv_destroy(bitlin_kv_t kv)
 {
     if (!kv) return BITLIN_OK;
     cudaError_t e = cudaDeviceSynchronize();
-    cudaFree(kv->dev_error);
-    cudaFree(kv->workspace);
+    cudaFree(kv->index_error);
     delete kv;
     return e == cudaSuccess ? BITLIN_OK : BITLIN_ECUDA;
 }

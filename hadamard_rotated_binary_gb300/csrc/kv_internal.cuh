@@ -6,13 +6,11 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <memory>
+
 #include "bitlin_internal.cuh"
 
 namespace bitlin_impl {
-
-// Device-side error words of a cache handle.
-constexpr int kKvErrTimeout = 0;  // a bounded wait gave up
-constexpr int kKvErrIndex = 1;    // a place outside the table or a page outside the pool
 
 // A frequency as a fixed-point fraction of a turn per position, 2^-64 turns,
 // so that position * frequency modulo one turn is an exact wrapping product.
@@ -44,7 +42,7 @@ struct TurnParams {
     const Turn* turns;        // [rotary / 2], nullptr: no rotation
     int axes;
     const int32_t* pos;       // [axes][tokens], nullptr: the token's place
-    int* dev_error;
+    int* index_error;         // set: a place outside the table or a page outside the pool
     int pages, page_size;
     int tokens, heads, kv_heads, dim, rotary;
     int adjacent, inverse;
@@ -97,7 +95,8 @@ struct AttendParams {
     float* ws_o;               // [2 * CTAs][128][padded dim]: unnormalised parts of outputs
     float* ws_ml;              // [2 * CTAs][128][2]: their rows' log2 maxima and sums
     int* tickets;              // [CTAs], zero between calls
-    int* dev_error;
+    int* timed_out;            // set: a bounded wait gave up, and the tickets may not be zero
+    int* index_error;
     long long wait_budget_ns;
     int pages, page_size, page_shift;  // page_shift: log2 of a power of two, else -1
     int tokens, heads, kv_heads, group, dim, causal;
@@ -106,6 +105,20 @@ struct AttendParams {
     int box_k, box_v;          // slots of a page per TMA copy
     int stall_test;
     float scale;
+};
+
+// Attention's workspace.  Nothing in it outlives a call but zero tickets, so
+// handles whose calls run one after the other can share one.
+struct KvWorkspace {
+    unsigned char* data = nullptr;  // tickets, timed_out; then maxima and sums; then outputs
+    size_t bytes = 0;
+    KvWorkspace() = default;
+    KvWorkspace(const KvWorkspace&) = delete;
+    ~KvWorkspace() { cudaFree(data); }
+};
+
+struct KvWorkspaceParts {
+    size_t timed_out, ml, o, bytes;  // the tickets lie at 0
 };
 
 }  // namespace bitlin_impl
@@ -126,13 +139,12 @@ struct bitlin_kv {
     long long page_stride = 0, slot_stride = 0, head_stride = 0;
     int last_cuda_error = 0;
     bitlin_status sticky = BITLIN_OK;
-    int* dev_error = nullptr;  // [2]: kKvErr*
+    int* index_error = nullptr;
     long long wait_budget_ns = 0;
     int stall_test = 0;
     alignas(64) unsigned char tmap_k[128];  // TMA descriptors of the pools (CUtensorMaps)
     alignas(64) unsigned char tmap_v[128];
-    // attention's workspace, allocated by the first call
-    unsigned char* workspace = nullptr;
+    std::shared_ptr<bitlin_impl::KvWorkspace> workspace;
 };
 
 // Launchers (return a cudaError_t).
@@ -145,5 +157,7 @@ void bitlin_attend_rows(int tokens, int seqs, int group, int* tile_tokens, int* 
 int bitlin_attend_item_extra(int dim);
 // Slots per TMA copy of the key and value pools.
 void bitlin_attend_boxes(int dim, int page_size, int* box_k, int* box_v);
-// Bytes of the attention workspace, and where its parts begin (the outputs at 0).
-size_t bitlin_attend_workspace(int dim, int num_sms, size_t* ml_offset, size_t* ticket_offset);
+// The attention workspace's parts.
+bitlin_impl::KvWorkspaceParts bitlin_attend_workspace(int dim, int num_sms);
+// Load the kernels of a cache's calls (a first launch would, which a stream capture may not allow).
+cudaError_t bitlin_attend_load(int dim, int dtype);

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) bitlin_turn(const TurnParams p)
         int page = -1;
         if (place >= 0 && at < p.batch.table_pages) page = p.batch.table[seq * p.batch.table_stride + at];
         if (page < 0 || page >= p.pages) {
-            p.dev_error[kKvErrIndex] = 1;
+            *p.index_error = 1;
             return;
         }
         dst = static_cast<TO*>(p.pool[kind - 1]) + page * p.page_stride + (place - at * p.page_size) * p.slot_stride;

@@ -426,12 +426,27 @@ bitlin_status bitlin_rope_destroy(bitlin_rope_t r);
  *   strides     in elements, positive multiples of 8, below 2^39; no two
  *               elements may share memory.
  *
+ * Allocates the workspace of bitlin_kv_attend (see bitlin_kv_share).
+ * Synchronous.
  * Errors: BITLIN_EINVAL, BITLIN_ENOMEM, BITLIN_ECUDA, BITLIN_EDEVICE.  On
  * error *out is set to NULL.
  */
 bitlin_status bitlin_kv_create(bitlin_kv_t* out, void* k, void* v, int pages, int page_size, int kv_heads,
                                int head_dim, int dtype, long long page_stride, long long slot_stride,
                                long long head_stride);
+
+/*
+ * Use the workspace of `with` for kv's calls and give up kv's own (40 MB at
+ * head_dim 129..256, 20 at 65..128, 10 below).  For the layers of a model,
+ * which never run at once: create the caches one by one and let each share
+ * the first one's.  The workspace lives as long as a handle that uses it.
+ *
+ * The calls of all handles that share a workspace must follow one another in
+ * stream order.  A BITLIN_ETIMEOUT of one is one of all of them.
+ * Synchronizes the device.  Errors: BITLIN_EINVAL (NULL, another device, a
+ * workspace of smaller heads than kv's), BITLIN_ECUDA.
+ */
+bitlin_status bitlin_kv_share(bitlin_kv_t kv, bitlin_kv_t with);
 
 /*
  * Append the batch's new keys and values: row i of k and v goes to its place
@@ -484,10 +499,9 @@ bitlin_status bitlin_kv_append(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
  * Sums, the softmax's statistics and the output accumulate in f32.  Requires
  * heads % kv_heads == 0, heads / kv_heads <= 128.  kv_lens past the table's
  * row are cut to it, and pages outside [0, pages) read as zeros; both make the
- * next bitlin_kv_get_error return BITLIN_EINDEX.  Asynchronous; the first
- * call allocates workspace that the handle keeps (40 MB at head_dim 256), so
- * make it before a stream capture.
- * Calls on one handle share it: use one stream at a time.
+ * next bitlin_kv_get_error return BITLIN_EINDEX.  Asynchronous; allocates
+ * nothing.  Calls on one handle, and on handles that share a workspace, use
+ * it one after the other: keep them on one stream, or order them.
  * Errors: BITLIN_EINVAL, BITLIN_ENOMEM, BITLIN_ECUDA, the handle's sticky
  * error.
  */

@@ -379,3 +379,75 @@ def test_import_star_without_torch(hrb):
     names = {}
     exec("from hadamard_rotated_binary_gb300 import *", names)
     assert {"BitLinear", "Rope", "PagedKV", "KVBatch", "PAIRS_HALF", "PAIRS_ADJACENT"} <= set(names)
+
+
+@gpu
+def test_caches_share_a_workspace(hrb):
+    """Layers with heads of several sizes and types on one workspace, their calls in turn, each against a
+    cache of its own; handles closed in any order; no memory of their own."""
+    cases = [attend_case(hrb, dim, 16, 2, 4, new, lens, dtype, 47 + dim)
+             for dim, new, lens, dtype in ((256, [3, 1], [900, 5000], torch.bfloat16), (64, [1, 40], [7000, 300], torch.float16),
+                                           (128, [1, 1], [20, 30000], torch.bfloat16), (200, [2, 2], [3000, 3000], torch.bfloat16))]
+    want = []
+    for batch, _, kp, vp, q in cases:
+        cache = hrb.PagedKV(kp, vp)
+        want.append((cache.attend(q, batch), cache.attend(q, batch, dtype=torch.float32)))
+        cache.close()
+    first = hrb.PagedKV(cases[0][2], cases[0][3])
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    layers = [first] + [hrb.PagedKV(kp, vp, share=first) for _, _, kp, vp, _ in cases[1:]]
+    more = [hrb.PagedKV(cases[0][2], cases[0][3], share=layers[-1]) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert free - torch.cuda.mem_get_info()[0] < 16 << 20  # (one workspace has 40 MB)
+    for _ in range(3):
+        for cache, (batch, _, _, _, q), (out, wide) in zip(layers, cases, want):
+            assert torch.equal(cache.attend(q, batch), out)
+            assert torch.equal(cache.attend(q, batch, dtype=torch.float32), wide)
+    first.close()
+    layers[2].close()
+    for i in (1, 3):
+        assert torch.equal(layers[i].attend(cases[i][4], cases[i][0]), want[i][0])
+    assert torch.equal(more[5].attend(cases[0][4], cases[0][0]), want[0][0])
+    assert all(c.get_error() == 0 for c in [layers[1], layers[3]] + more)
+    # a workspace for smaller heads is refused, and so is a closed cache's
+    small = hrb.PagedKV(cases[1][2], cases[1][3])
+    for other in (small, first):
+        with pytest.raises(hrb.BitlinError):
+            hrb.PagedKV(cases[0][2], cases[0][3], share=other)
+
+
+@gpu
+def test_a_timeout_is_one_of_all_caches_that_share(hrb):
+    batch, offsets, kp, vp, q = attend_case(hrb, 128, 16, 2, 4, [40, 1], [300, 20], torch.bfloat16, 22)
+    one = hrb.PagedKV(kp, vp)
+    two, apart = hrb.PagedKV(kp, vp, share=one), hrb.PagedKV(kp, vp)
+    want = two.attend(q, batch)
+    assert one.get_error() == two.get_error() == 0
+    one.set_wait_budget(2_000_000)
+    one.test_stall(True)
+    one.attend(q, batch)
+    for cache in (two, one):
+        assert cache.get_error() == hrb.BITLIN_ETIMEOUT
+        with pytest.raises(hrb.BitlinError):
+            cache.attend(q, batch)
+    assert apart.get_error() == 0 and torch.equal(apart.attend(q, batch), want)
+
+
+@gpu
+def test_the_first_call_can_be_captured(hrb):
+    """Nothing is allocated or loaded by a handle's first call, of either output type."""
+    batch, offsets, kp, vp, q = attend_case(hrb, 72, 16, 2, 4, [3, 1], [900, 50], torch.float16, 48)
+    ref = attend64(q, kp, vp, offsets, [900, 50], batch.table, 72**-0.5, True)
+    for out_dtype in (torch.float16, torch.float32):
+        cache, out = hrb.PagedKV(kp, vp), torch.zeros(q.shape, dtype=out_dtype, device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            cache.attend(q, batch, out=out)
+        for _ in range(2):
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            check_attended(out, None, ref, torch.float16)
+        assert cache.get_error() == 0
