@@ -99,6 +99,31 @@ void set_out(TurnParams& p, const bitlin_rows* r)
     p.out_head = r->head_stride;
 }
 
+// f / (2 pi) modulo one turn, to one unit of 2^-64: the 24-bit significand of f
+// times 1 / (2 pi) to 192 bits (pi by Machin's formula), enough for f32's largest
+// exponent.
+Turn turns_per_place(float f)
+{
+    const uint64_t inverse[3] = {0x28be60db9391054aULL, 0x7f09d5f47d4d3770ULL, 0x36d8a5664f10e410ULL};
+    int exponent = 0;
+    const uint64_t significand = (uint64_t)ldexpf(frexpf(fabsf(f), &exponent), 24);
+    exponent -= 24;
+    uint64_t product[4];  // from the lowest word; its unit is 2^(exponent - 192)
+    uint64_t carry = 0;
+    for (int i = 0; i < 3; ++i) {
+        const unsigned __int128 x = (unsigned __int128)significand * inverse[2 - i] + carry;
+        product[i] = (uint64_t)x;
+        carry = (uint64_t)(x >> 64);
+    }
+    product[3] = carry;
+    const int shift = 128 - exponent;  // product >> shift is in 2^-64; at least 24
+    auto word = [&](int i) { return i < 4 ? product[i] : 0; };
+    const int at = shift / 64, by = shift % 64;
+    const uint64_t turns = by ? word(at) >> by | word(at + 1) << (64 - by) : word(at);
+    const uint64_t half = word((shift - 1) / 64) >> (shift - 1) % 64 & 1;
+    return f < 0 ? 0 - (turns + half) : turns + half;
+}
+
 // A tensor of 16-bit elements copied in boxes of 64 elements x `rows` (two of
 // its dimensions), 128-byte swizzle, zeros outside.  dims and strides (bytes)
 // from the innermost, whose stride is one element.
@@ -172,13 +197,8 @@ bitlin_status bitlin_rope_create(bitlin_rope_t* out, int rotary_dim, int axes, c
     std::unique_ptr<Turn[]> turns(new (std::nothrow) Turn[pairs]);
     std::unique_ptr<bitlin_rope> r(new (std::nothrow) bitlin_rope());
     if (!turns || !r) return BITLIN_ENOMEM;
-    for (int i = 0; i < pairs; ++i) {
-        // turns per place, modulo one turn, in 2^-64 (f64: 2^-54 of the frequency's own value)
-        double f = (double)inv_freq[i] / 6.283185307179586476925;
-        f -= floor(f);
-        if (f >= 1.0) f = 0.0;
-        turns[i] = ((uint64_t)ldexp(f, 64) & ~kAxisMask) | (Turn)(axis ? axis[i] : 0);
-    }
+    for (int i = 0; i < pairs; ++i)
+        turns[i] = ((turns_per_place(inv_freq[i]) + (kAxisMask + 1) / 2) & ~kAxisMask) | (Turn)(axis ? axis[i] : 0);
     r->device = dev;
     r->rotary = rotary_dim;
     r->axes = axes;

@@ -14,8 +14,8 @@ namespace bitlin_impl {
 
 // A frequency as a fixed-point fraction of a turn per position, 2^-64 turns,
 // so that position * frequency modulo one turn is an exact wrapping product.
-// The pair's axis lies in the low bits (2^-61 turns a position is below what
-// the frequency's own f32 says).
+// The pair's axis lies in the low bits, which leaves the frequency to 2^-62
+// turns: 2^-31 of a turn at the largest position.
 using Turn = uint64_t;
 constexpr int kAxisBits = 3;
 constexpr Turn kAxisMask = (1u << kAxisBits) - 1;

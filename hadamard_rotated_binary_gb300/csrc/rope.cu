@@ -4,10 +4,11 @@
 // Mathematics: pair i of a head turns by t = pos[axis[i]] * inv_freq[i],
 // (a, b) -> (a cos t - b sin t, b cos t + a sin t).  A frequency is held as a
 // 64-bit fixed-point fraction of a turn, so pos * frequency modulo one turn is
-// one wrapping integer product, exact at every int32 position; its top 32 bits
-// are the angle to 2^-33 of a turn, already within half a turn of zero.  There
-// the hardware's sine and cosine are good to 2^-21, enough for a 16-bit output
-// (2^-9 and 2^-12); an f32 output takes sincospi.
+// one wrapping integer product at every int32 position; its top 32 bits are the
+// angle to 2^-32 of a turn (and 2^-31 at most from the frequency's rounding),
+// already within half a turn of zero, and 24 of them enter the sine: 1e-7 at
+// most.  There the hardware's sine and cosine are good to 2^-21, enough for a
+// 16-bit output (2^-9 and 2^-12); an f32 output takes sincospi.
 //
 // Bound: HBM (each element is read once and written once).  A thread owns one
 // "unit" of a head: two chunks of VEC consecutive elements, half the rotated

@@ -395,10 +395,10 @@ bitlin_status bitlin_rope_create(bitlin_rope_t* out, int rotary_dim, int axes, c
  *   inverse  0, or 1 to turn by the negative angle: the transposed map, which
  *            is the gradient of the rotation.
  *
- * Angles are kept as a 64-bit fixed-point fraction of a turn, so the result
- * is good to 2e-7 (an f32 out) or 5e-7 (a 16-bit one, before its own
- * rounding) at every int32 position; each output is rounded
- * once to its type.  Asynchronous; allocates nothing.  tokens = 0 does nothing.
+ * Angles are formed as a 64-bit fixed-point fraction of a turn, so the result
+ * is good to 3.1e-7 (an f32 out) or 1e-6 (a 16-bit one, before its own
+ * rounding) of its pair's norm sqrt(a^2 + b^2), at every int32 position and
+ * every finite frequency; each output is rounded once to its type.  Asynchronous; allocates nothing.  tokens = 0 does nothing.
  * Errors: BITLIN_EINVAL (NULL, an unknown type, head_dim < rotary_dim,
  * heads < 1 or > 4096, tokens < 0, tokens * head_dim >= 2^32, a pointer that
  * is not aligned to its type), BITLIN_ECUDA.

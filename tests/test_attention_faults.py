@@ -451,3 +451,54 @@ def test_the_first_call_can_be_captured(hrb):
             torch.cuda.synchronize()
             check_attended(out, None, ref, torch.float16)
         assert cache.get_error() == 0
+
+
+def angles_mod_turn(inv_freq, positions):
+    """pos * freq modulo 2 pi, in f64, from 100 digits; [positions][freqs]."""
+    from decimal import Decimal, getcontext
+
+    getcontext().prec = 100
+
+    def arctan_inverse(x):
+        total = term = Decimal(1) / x
+        n = 1
+        while abs(term) > Decimal(10) ** -99:
+            term /= -x * x
+            n += 2
+            total += term / n
+        return total
+
+    turn = 2 * (16 * arctan_inverse(5) - 4 * arctan_inverse(239))
+    rows = []
+    for p in positions:
+        exact = [Decimal(float(torch.tensor(f, dtype=torch.float32))) * p / turn for f in inv_freq]
+        rows.append([float((x - x.to_integral_value()) * turn) for x in exact])
+    return torch.tensor(rows, dtype=torch.float64)
+
+
+@gpu
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_rope_bound_at_every_position_and_frequency(hrb, adjacent):
+    """The documented bound, of a pair's norm: for an f32 output the angle's 24 bits of half a turn
+    (2^-26 of a turn, 2^-32 cut off, 2^-31 from the frequency's rounding: 9.8e-8), sine and cosine
+    to one unit in the last place (sqrt(2) 2^-24), a product's and the sum's rounding (2 * 2^-24):
+    3.1e-7; for a 16-bit one the hardware's sine and cosine (2^-21.4 and 2^-21.2) and the angle's
+    rounding to radians instead: 1e-6, then its own."""
+    inv_freq = [1.0, -0.25, 7.5, 1e-9, 6.25, 6.2831855, 100.0, -31415.926, 3e38, 1e-45, 0.0, 1e10, 0.7, 1.25e-3, -1e20, 2.0**60]
+    positions = [0, 1, -1, 777, 131071, 2**24 + 1, 2**28 + 5, 2**31 - 1, -2**31, -2**31 + 1, 1234567891]
+    heads, pairs = 64, len(inv_freq)
+    x = torch.randn((len(positions), heads, 2 * pairs), generator=generator(49), device="cuda")
+    pos = torch.tensor([positions], dtype=torch.int32, device="cuda")
+    t = angles_mod_turn(inv_freq, positions)[:, None, :]
+    first, second = (slice(0, None, 2), slice(1, None, 2)) if adjacent else (slice(0, pairs), slice(pairs, None))
+    rope = hrb.Rope(inv_freq, adjacent=adjacent)
+    for dtype, rel, own, tiny in ((torch.float32, 3.1e-7, 0.0, 0.0), (torch.bfloat16, 1e-6, 2.0**-8, 0.0), (torch.float16, 1e-6, 2.0**-11, 2.0**-25)):
+        for inverse in (False, True):
+            y = rope.apply(x, pos, dtype=dtype, inverse=inverse).double().cpu()
+            a, b = x[..., first].double().cpu(), x[..., second].double().cpu()
+            sin = -torch.sin(t) if inverse else torch.sin(t)
+            norm = torch.sqrt(a * a + b * b)
+            for got, want in ((y[..., first], a * torch.cos(t) - b * sin), (y[..., second], b * torch.cos(t) + a * sin)):
+                bound = rel * norm
+                bound = bound + own * (want.abs() + bound) + tiny
+                assert bool(((got - want).abs() <= bound).all()), float(((got - want).abs() / norm).max())
