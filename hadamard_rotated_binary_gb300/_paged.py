@@ -124,7 +124,9 @@ class PagedKV:
     k, v = _held("k"), _held("v")
 
     def __init__(self, k, v, share: PagedKV | None = None):
-        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+        # a dimension of one has no stride that matters
+        strides = [[s if n > 1 else t.shape[-1] for n, s in zip(t.shape, t.stride())] for t in (k, v)]
+        if k.dim() != 4 or k.shape != v.shape or strides[0] != strides[1] or k.dtype != v.dtype:
             raise ValueError("k and v must be [pages][page_size][kv_heads][head_dim] of one type and layout")
         if not (k.is_cuda and v.is_cuda) or k.stride(3) != 1 or k.dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("k and v must be bfloat16 or float16 CUDA tensors with contiguous heads")
@@ -133,7 +135,7 @@ class PagedKV:
         self.k, self.v = k, v
         self.device, self.dtype = k.device, k.dtype
         pages, page_size, self.kv_heads, self.head_dim = k.shape
-        page_stride, slot_stride, head_stride = k.stride()[:3]
+        page_stride, slot_stride, head_stride = strides[0][:3]
         h = ctypes.c_void_p()
         with torch.cuda.device(k.device):
             st = lib().bitlin_kv_create(ctypes.byref(h), k.data_ptr(), v.data_ptr(), pages, page_size, self.kv_heads,

@@ -502,3 +502,28 @@ def test_rope_bound_at_every_position_and_frequency(hrb, adjacent):
                 bound = rel * norm
                 bound = bound + own * (want.abs() + bound) + tiny
                 assert bool(((got - want).abs() <= bound).all()), float(((got - want).abs() / norm).max())
+
+
+@gpu
+def test_pools_of_one_head_or_one_page(hrb):
+    """A dimension of one may have any stride, and another one in k than in v."""
+    for pages, kvh in ((6, 1), (1, 2), (1, 1)):
+        gen = generator(50)
+        lens = [16 * pages - 3]
+        batch, offsets, _ = make_batch(hrb, gen, [2], lens, 16, spare=0)
+        k, v = make_pools(gen, pages, 16, kvh, 64, torch.bfloat16)
+        q = torch.randn((2, 2 * kvh, 64), generator=gen, device="cuda").bfloat16()
+        want = hrb.PagedKV(k, v).attend(q, batch)
+        odd = [s if n > 1 else 1 for n, s in zip(k.shape, k.stride())]
+        far = [s if n > 1 else 8 * s + 8 for n, s in zip(k.shape, k.stride())]
+        for a, b in ((odd, odd), (odd, far), (far, k.stride())):
+            cache = hrb.PagedKV(k.as_strided(k.shape, a), v.as_strided(v.shape, b))
+            assert torch.equal(cache.attend(q, batch), want)
+            new = torch.randn((2, kvh, 64), generator=gen, device="cuda")
+            keep = k.clone(), v.clone()
+            cache.append(new, new, batch)
+            at = torch.arange(lens[0] - 2, lens[0], device="cuda")
+            assert torch.equal(v[batch.table[0, at // 16].long(), at % 16], new.bfloat16())
+            k.copy_(keep[0])
+            v.copy_(keep[1])
+            assert cache.get_error() == 0
