@@ -527,3 +527,88 @@ def test_pools_of_one_head_or_one_page(hrb):
             k.copy_(keep[0])
             v.copy_(keep[1])
             assert cache.get_error() == 0
+
+
+# ------------------------------------------------------------------ forms that had no test
+
+@gpu
+@pytest.mark.parametrize("dim,kvh,heads,rotary", [(64, 2, 6, 32), (80, 1, 3, 40), (256, 4, 24, 64)])
+def test_append_of_a_fused_projection(hrb, dim, kvh, heads, rotary):
+    """Queries, keys and values as slices of one projection, by head or side by side, and a table whose
+    rows are farther apart than they are long."""
+    from test_attention_side import check_rotated
+
+    gen = generator(51)
+    new, lens = [3, 1, 20], [40, 17, 20]
+    batch, offsets, pages = make_batch(hrb, gen, new, lens, 16)
+    apart = torch.full((3, batch.table.shape[1] + 5), -7, dtype=torch.int32, device="cuda")
+    apart[:, :-5] = batch.table
+    batch = hrb.KVBatch(batch.q_offsets, batch.kv_lens, apart[:, :-5])
+    T, inv_freq = offsets[-1], freqs(rotary // 2)
+    pos = torch.randint(0, 9000, (1, T), generator=gen, device="cuda", dtype=torch.int32)
+    rope = hrb.Rope(inv_freq)
+    for src in (torch.float32, torch.bfloat16):
+        side_by_side = torch.randn((T, (heads + 2 * kvh) * dim + 4), generator=gen, device="cuda").to(src)
+        parts = side_by_side[:, 2:-2].split((heads * dim, kvh * dim, kvh * dim), -1)
+        slices = [tuple(p.unflatten(-1, (-1, dim)) for p in parts)]
+        by_head = torch.randn((T, kvh, heads // kvh + 2, dim), generator=gen, device="cuda").to(src)
+        slices.append((by_head[:, :, 0], by_head[:, :, -2], by_head[:, :, -1]))
+        for q, k, v in slices:
+            assert not k.is_contiguous() and not v.is_contiguous()
+            kp, vp = make_pools(gen, pages, 16, kvh, dim, torch.bfloat16)
+            before = kp.clone(), vp.clone()
+            cache = hrb.PagedKV(kp, vp)
+            q_out = cache.append(k, v, batch, rope=rope, pos=pos, q=q)
+            check_rotated(q_out, q, pos, inv_freq, [0] * (rotary // 2), False)
+            at = [(s, lens[s] - new[s] + i) for s in range(3) for i in range(new[s])]
+            where = (torch.stack([apart[s, p // 16] for s, p in at]).long(), torch.tensor([p % 16 for _, p in at], device="cuda"))
+            check_rotated(kp[where], k, pos, inv_freq, [0] * (rotary // 2), False)
+            assert torch.equal(vp[where], v.bfloat16())
+            before[0][where], before[1][where] = kp[where], vp[where]
+            assert torch.equal(before[0], kp) and torch.equal(before[1], vp)
+            if q.shape[1] == heads:  # attention reads the same table
+                ref = attend64(q_out, kp, vp, offsets, lens, apart, dim**-0.5, True)
+                check_attended(cache.attend(q_out, batch), None, ref, torch.bfloat16)
+            assert cache.get_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("seqs", [31, 32, 33, 1023, 1024, 1025, 2500])
+def test_append_and_attend_of_many_sequences(hrb, seqs):
+    """The search for a token's sequence: 32 boundaries a round, over one, two and three rounds, with
+    sequences of no new token among them (the first, the last and runs of them)."""
+    from test_attention_side import check_rotated
+
+    gen = generator(52)
+    new = [0 if i in (0, seqs - 1) or i % 7 in (2, 3) or 500 < i < 560 else 1 + (i % 11 == 4) * 2 for i in range(seqs)]
+    lens = [n + (3 * i) % 29 for i, n in enumerate(new)]
+    batch, offsets, pages = make_batch(hrb, gen, new, lens, 8)
+    kp, vp = make_pools(gen, pages, 8, 1, 64, torch.float16)
+    T, inv_freq = offsets[-1], freqs(16)
+    k, v, q = (torch.randn((T, h, 64), generator=gen, device="cuda") for h in (1, 1, 2))
+    cache = hrb.PagedKV(kp, vp)
+    q_out = cache.append(k, v, batch, rope=hrb.Rope(inv_freq), q=q)
+    seq = torch.repeat_interleave(torch.arange(seqs), torch.tensor(new)).cuda()
+    place = torch.cat([torch.arange(n - m, n) for m, n in zip(new, lens)]).cuda()
+    where = batch.table[seq, place // 8].long(), place % 8
+    check_rotated(kp[where], k, place[None], inv_freq, [0] * 16, False)
+    check_rotated(q_out, q, place[None], inv_freq, [0] * 16, False)
+    assert torch.equal(vp[where], v.half())
+    out = cache.attend(q_out, batch, dtype=torch.float32)
+    check_attended(out, None, attend64(q_out, kp, vp, offsets, lens, batch.table, 0.125, True), torch.float16)
+    assert cache.get_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim,kvh,heads", [(64, 2, 8), (128, 1, 3), (256, 1, 6)])
+def test_attend_prompts_beside_single_tokens(hrb, dtype, dim, kvh, heads):
+    """A serving step that mixes a prompt with single tokens."""
+    new, lens = [1, 150, 1, 1, 9, 1], [500, 150, 33, 1, 300, 129]
+    batch, offsets, kp, vp, q = attend_case(hrb, dim, 16, kvh, heads, new, lens, dtype, 53, q_scale=2.0)
+    fill = attend64(q, kp, vp, offsets, lens, batch.table, dim**-0.5, True)
+    cache = hrb.PagedKV(kp, vp)
+    for out_dtype in (dtype, torch.float32):
+        lse = torch.empty(q.shape[:2], device="cuda")
+        check_attended(cache.attend(q, batch, dtype=out_dtype, lse=lse), lse, fill, dtype)
+    assert cache.get_error() == 0
