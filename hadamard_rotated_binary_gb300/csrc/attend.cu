@@ -1362,10 +1362,14 @@ void bitlin_attend_boxes(int dim, int page_size, int* box_k, int* box_v)
     *box_v = gcd(page_size, 8192 / padded);
 }
 
-// Measured, in us, on 4 prompts of 700-4,096 tokens (128 dims): 463 without,
-// 411 at 2, 377 at 4, 390 at 6; 2,048 tokens over 32,768 keys (256 dims, items
-// of about 250 tiles): 1,161 without, 1,152 at 2, 1,167 at 4.
-int bitlin_attend_item_extra(int dim) { return dim > 128 ? 2 : 4; }
+// Measured, in us, at 0/1/2/3/4/6: 4 prompts of 700-4,096 tokens at 64 dims
+// 335/290/257/232/233/245, at 128 414/355/315/284/262/277, at 256
+// 487/399/357/321/328/345; 4 chunks of 512 tokens over 4,096 keys at 256 dims
+// 183 at 2, 182 at 3, 188 at 4; a prompt of 4,000 beside 15 single tokens at 256
+// dims 239 at 2, 206 at 3, 210 at 4.  64 single tokens at 64/128/256 dims 168/191/167
+// without, 134/187/166 at 3, 135/186/166 at 4.  One long chunk or one token: no
+// difference past the spread.
+int bitlin_attend_item_extra(int dim) { return dim > 128 ? 3 : 4; }
 
 KvWorkspaceParts bitlin_attend_workspace(int dim, int num_sms)
 {
