@@ -27,14 +27,15 @@
 //         tensor memory, running maximum and sum, the weights P back over S as
 //         the A operand of P V; the item's epilogue;
 //   8-11  TMA: K and V pages through one ring of 16 KB chunks, in the order the
-//         MMAs use them (K0, K1, V0, K2, V1, ...); a chunk is 128 keys x 64 dims
+//         MMAs use them (K0, K1, V0, K2, V1, ...; up to 128 dims one K further
+//         ahead); a chunk is 128 keys x 64 dims
 //         of K or 8192 / DP keys x DP dims of V, page by page.  One warp's copies
 //         run one after the other at about 40 B a clock, whatever their boxes
 //         (measured: 31 B with 64-slot boxes, 62 from two warps, 91 from four,
 //         where L2 is the limit), and the tensor cores eat 64 B a clock at DP =
 //         256: four warps take the chunks in turn;
-//   12    MMA issue: S tiles alternate between two buffers, so Q K^T of the next
-//         tile runs while the softmax works on this one;
+//   12    MMA issue: S tiles take turns in two buffers (three up to 128 dims), so
+//         Q K^T of the next tile runs while the softmax works on this one;
 //   13    Q of the next item (TMA: the group's heads of its tokens, row by row).
 // The output stays in tensor memory; it is rescaled only when a row's maximum
 // grows by more than 2^8 (until then the weights are relative to the older
@@ -43,15 +44,22 @@
 // addition), so every kDrain tiles it is added, rounded to nearest, to an f32
 // copy in the workspace and starts again from zero.
 //
-// An f32 output's weights are two digits of the cache's type.  Two bf16 digits
-// hold 16 bits: the output is off by 1.6e-6 of its norm at 777 keys and 3.9e-6
-// at 131,072 (f32 arithmetic: 0.5e-6 and 1.1e-6).  A third digit, in shared
-// memory for want of tensor memory, with drains every 4 tiles, gives 1.0e-6 and
-// 2.4e-6 and takes 14.7 and 109.4 us instead of 14.0 and 100.1 (the ring is two
-// chunks shorter).  Three digits in the lanes that up to 32 rows leave idle (Q
-// loaded once per digit) give 0.7e-6 and 2.0e-6 and take 15.8 and 107.2 us, and
-// f32 prompts 807 us instead of 514.  Neither was kept: keys and values in bf16
-// are themselves rounded to 2e-3.
+// A 16-bit output's weights are rounded to the cache's type, which the tensor
+// cores multiply; their sum is that of the unrounded ones (lse needs it).  The
+// output is off by 2.1e-3 to 2.3e-3 of its norm in bf16 and 2.9e-4 in f16, its own
+// rounding included (alone 1.65e-3 and 2.1e-4).  Dividing by the sum of the rounded
+// ones instead gives 2.0e-3 to 2.1e-3 and 2.7e-4 and takes prompts 379 us for 362,
+// a chunk 1,208 for 1,178, drafts 53.5 for 51.3: not kept.
+// An f32 output's weights are two digits of that type.  Two bf16 digits hold 16
+// bits: the output is off by 1.3e-6 to 1.6e-6 of its norm at 777 keys and 3.5e-6
+// to 5.3e-6 at 131,072 (f32 arithmetic: 0.5e-6 to 0.8e-6 and 0.8e-6 to 1.4e-6).  A
+// third digit, in shared memory for want of tensor memory, with drains every 4
+// tiles, gave 1.0e-6 for 1.6e-6 and 2.4e-6 for 3.9e-6 on the same inputs and took
+// 14.7 and 109.4 us instead of 14.0 and 100.1 (the ring is two chunks shorter).
+// Three digits in the lanes that up to 32 rows leave idle (Q loaded once per
+// digit) gave 0.7e-6 and 2.0e-6 and took 15.8 and 107.2 us, and f32 prompts 807 us
+// instead of 514.  Neither was kept: keys and values in bf16 are themselves
+// rounded to 2e-3.
 //
 // Bound: single tokens by HBM (one over 131,072 keys, 537 MB, 106 us with
 // inputs changing from call to call: 5.1 TB/s; 64 over 100-8,000 keys each, 1.06
@@ -261,7 +269,12 @@ __device__ void locate(const AttendParams& p, Start* out)
     }
     least = __reduce_min_sync(0xffffffffu, least);
     most = __reduce_max_sync(0xffffffffu, most);
-    // Rounds of whole items when they cost about the same (within an eighth).
+    // Rounds of whole items when they cost about the same, within an eighth.
+    // Measured, in us, without rounds and with: 128 single tokens of 8 key heads
+    // over keys within 3 % of 4,000 330 and 324, within 10 % 320 and 313, within 20 %
+    // 305 and 301, within 40 % the same, within 80 % 213 and 226; 2,048 tokens over
+    // 32,768 keys, costs within 7 % (128 dims) 937 and 928, over 16,384, within 14 %,
+    // 458 and 468, over 8,192 227 and 239, over 4,096 112 and 124.
     const int rounds = items >= grid && most - least <= least / 8 ? (int)min(divide(items, grid), (long long)kRounds) : 0;
 
     // Cost of row tiles 0 .. qt-1 of a sequence.
@@ -1387,7 +1400,12 @@ void bitlin_attend_rows(int tokens, int seqs, int group, int* tile_tokens, int* 
 {
     // A tile's rows in one box where sequences bring many tokens; where they
     // bring few, boxes of the fewest tokens whose rows keep the swizzle's atoms
-    // of eight, so that single tokens do not fetch their neighbours' rows.
+    // of eight, so that single tokens do not fetch their neighbours' rows.  The
+    // boxes can cost the tile rows (21 tokens of 6 heads become 20).  Measured, in
+    // us, one box and boxes, at 256 dims, 6 heads to a key head: prompts of 700-4,096
+    // tokens 359 and 364, 2,048 tokens over 32,768 keys 1,170 and 1,219; 15 single
+    // tokens beside a prompt of 4,000, which the average below takes for many, 239
+    // and 231; 64 single tokens 165.3 and 165.0.  At 64 and 128 dims all within 0.5 %.
     *tile_tokens = kRows / group;
     *q_box = *tile_tokens;
     const int few = 8 / gcd(group, 8);
