@@ -44,6 +44,12 @@
 // addition), so every kDrain tiles it is added, rounded to nearest, to an f32
 // copy in the workspace and starts again from zero.
 //
+// The reference is rounded to f32 before it is subtracted, so the largest weight
+// may be off from 1 by half a step of it, in numerator and sum alike: nothing is
+// lost until that overflows the weights' type (a reference past 2^26 in an f16
+// cache, 2^30 in bf16).  Subtracting the maximum first would be exact, for an
+// instruction more per pair of scores.
+//
 // A 16-bit output's weights are rounded to the cache's type, which the tensor
 // cores multiply; their sum is that of the unrounded ones (lse needs it).  The
 // output is off by 2.1e-3 to 2.3e-3 of its norm in bf16 and 2.9e-4 in f16, its own
@@ -52,7 +58,10 @@
 // a chunk 1,208 for 1,178, drafts 53.5 for 51.3: not kept.
 // An f32 output's weights are two digits of that type.  Two bf16 digits hold 16
 // bits: the output is off by 1.3e-6 to 1.6e-6 of its norm at 777 keys and 3.5e-6
-// to 5.3e-6 at 131,072 (f32 arithmetic: 0.5e-6 to 0.8e-6 and 0.8e-6 to 1.4e-6).  A
+// to 5.3e-6 at 131,072 (f32 arithmetic: 0.5e-6 to 0.8e-6 and 0.8e-6 to 1.4e-6).
+// The larger part is what the tensor cores' additions lose between drains: an f16
+// cache, whose two digits hold 22 bits, has 1.35e-6 and 3.2e-6.  Drains every 4
+// tiles take a fifth of it away and cost f32 prompts and chunks 13 to 15 %.  A
 // third digit, in shared memory for want of tensor memory, with drains every 4
 // tiles, gave 1.0e-6 for 1.6e-6 and 2.4e-6 for 3.9e-6 on the same inputs and took
 // 14.7 and 109.4 us instead of 14.0 and 100.1 (the ring is two chunks shorter).
@@ -61,12 +70,12 @@
 // instead of 514.  Neither was kept: keys and values in bf16 are themselves
 // rounded to 2e-3.
 //
-// Bound: single tokens by HBM (one over 131,072 keys, 537 MB, 106 us with
+// Bound: single tokens by HBM (one over 131,072 keys, 537 MB, 104 us with
 // inputs changing from call to call: 5.1 TB/s; 64 over 100-8,000 keys each, 1.06
-// GB, 169 us: 6.3 TB/s) or, where keys are few, by the latency of one pass
+// GB, 171 us: 6.2 TB/s) or, where keys are few, by the latency of one pass
 // through the stages (777 keys 14.0 us in a graph); many tokens by the feeding of
 // K and V to one CTA's MMAs (2,048 over 32,768 keys 1.19 ms, 1.34 PFLOP/s; 4
-// prompts of 700-4,096 tokens 364 us).  With the softmax reduced to its
+// prompts of 700-4,096 tokens 362 us).  With the softmax reduced to its
 // handshakes the prompts take 343 us and the chunk 1,045: it is not the limit.
 #include <cuda.h>
 #include <math.h>

@@ -485,7 +485,9 @@ bitlin_status bitlin_kv_append(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
  *
  *   q      [tokens][heads][head_dim] in the cache's type, 16-byte aligned,
  *          strides positive multiples of 8.
- *   scale  usually 1/sqrt(head_dim); finite.
+ *   scale  usually 1/sqrt(head_dim); finite.  Scores are told apart as far as
+ *          f32 holds them; a row whose largest one is beyond 4e7 in magnitude
+ *          (f16 cache; 7e8 in bf16), infinite or NaN may come out as NaN.
  *   out    [tokens][heads][head_dim], 16-byte aligned, strides multiples of
  *          8; the cache's type, or BITLIN_F32 (what bitlin_forward reads).
  *          For a 16-bit out the probabilities are rounded to the cache's type

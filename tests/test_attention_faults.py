@@ -612,3 +612,27 @@ def test_attend_prompts_beside_single_tokens(hrb, dtype, dim, kvh, heads):
         lse = torch.empty(q.shape[:2], device="cuda")
         check_attended(cache.attend(q, batch, dtype=out_dtype, lse=lse), lse, fill, dtype)
     assert cache.get_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("dtype,most", [(torch.float16, 3.9e7), (torch.bfloat16, 6.9e8)])
+def test_scores_as_large_as_documented(hrb, dtype, most):
+    """Keys alike, with scores up to the documented size of either sign: the mean of the values, within the
+    weights' and the output's rounding.  (The reference is rounded before it is subtracted.)"""
+    batch, offsets, kp, vp, q = attend_case(hrb, 64, 16, 1, 2, [1, 3], [500, 40], dtype, 54)
+    kp.fill_(0.0)
+    kp[..., 0] = 1024.0
+    q.fill_(0.0)
+    q[:, 0, 0], q[:, 1, 0] = 1000.0, -1000.0
+    cache = hrb.PagedKV(kp, vp)
+    for i in range(25):
+        scale = most * (0.5 + i / 48) / 1.024e6
+        out, lse, _, size = attend64(q, kp, vp, offsets, [500, 40], batch.table, scale, True)
+        for out_dtype in (dtype, torch.float32):
+            got_lse = torch.empty(q.shape[:2], device="cuda")
+            got = cache.attend(q, batch, scale=scale, dtype=out_dtype, lse=got_lse).double().cpu()
+            u = 2.0**-8 if dtype == torch.bfloat16 else 2.0**-11
+            digits = u if out_dtype == dtype else u * u
+            own = u if out_dtype == dtype else 2.0**-24
+            assert bool(((got - out).abs() <= size * (digits + 2.0**-18) + own * (out.abs() + digits * size)).all())
+            assert bool(((got_lse.double().cpu() - lse).abs() <= 2.0**-21 * lse.abs()).all())
