@@ -56,19 +56,26 @@
 // rounding included (alone 1.65e-3 and 2.1e-4).  Dividing by the sum of the rounded
 // ones instead gives 2.0e-3 to 2.1e-3 and 2.7e-4 and takes prompts 379 us for 362,
 // a chunk 1,208 for 1,178, drafts 53.5 for 51.3: not kept.
-// An f32 output's weights are two digits of that type.  Two bf16 digits hold 16
-// bits: the output is off by 1.3e-6 to 1.6e-6 of its norm at 777 keys and 3.5e-6
-// to 5.3e-6 at 131,072 (f32 arithmetic: 0.5e-6 to 0.8e-6 and 0.8e-6 to 1.4e-6).
-// The larger part is what the tensor cores' additions lose between drains: an f16
-// cache, whose two digits hold 22 bits, has 1.35e-6 and 3.2e-6.  Drains every 4
-// tiles take a fifth of it away and cost f32 prompts and chunks 13 to 15 %.  A
-// third digit, in shared memory for want of tensor memory, with drains every 4
-// tiles, gave 1.0e-6 for 1.6e-6 and 2.4e-6 for 3.9e-6 on the same inputs and took
-// 14.7 and 109.4 us instead of 14.0 and 100.1 (the ring is two chunks shorter).
-// Three digits in the lanes that up to 32 rows leave idle (Q loaded once per
-// digit) gave 0.7e-6 and 2.0e-6 and took 15.8 and 107.2 us, and f32 prompts 807 us
-// instead of 514.  Neither was kept: keys and values in bf16 are themselves
-// rounded to 2e-3.
+// An f32 output's weights are several digits of that type, and what the tensor
+// cores' additions lose between drains matters as much.
+//   Many rows: two digits, one after the other into the same accumulator (16 bits of
+//   a weight in bf16, 22 in f16).
+//   Up to 8 rows (single tokens of 8 query heads to a key head): the queries lie in the tile once for each digit, eight
+//   lanes apart, and each copy's lanes hold one digit of the weights: three in bf16,
+//   two in f16, with accumulators of their own, half the additions into each, and
+//   no product more.  The epilogue adds the digits' outputs across the lanes.
+// Off by, of the output's norm (two digits in one accumulator -> this; f32
+// arithmetic): bf16 over 777 keys 1.5e-6 -> 0.8e-6 (0.6e-6), 131,072 4.2e-6 -> 2.2e-6
+// (1.0e-6), 64 tokens over 100-8,000 3.1e-6 -> 1.4e-6 (0.4e-6); f16 1.1e-6 -> 1.0e-6,
+// 3.4e-6 -> 2.4e-6 and 2.5e-6 -> 1.75e-6.  Times: bf16 777 keys 14.0 -> 14.4 us,
+// 131,072 102-109 -> 104-113, 64 tokens at 256/128/64 dims 194/191/167 -> 200/200/178;
+// f16 as before, at 64 dims 175 -> 154.  Two digits in lanes of their own in bf16
+// take no time either and leave 1.4e-6, 3.3e-6 and 2.6e-6.
+// Many rows have no idle lanes.  There a third digit in shared memory, for want of
+// tensor memory, with drains every 4 tiles, and drains every 4 tiles alone, were
+// measured and not kept: one token over 131,072 keys 3.9e-6 -> 2.4e-6 for 100 -> 109
+// us; f32 chunks 4.1e-6 -> 3.2e-6 for 449 -> 516 us.  (Keys and values in bf16 are
+// themselves rounded to 2e-3.)
 //
 // Bound: single tokens by HBM (one over 131,072 keys, 537 MB, 104 us with
 // inputs changing from call to call: 5.1 TB/s; 64 over 100-8,000 keys each, 1.06
@@ -104,6 +111,13 @@ constexpr int kMaxLen = 1 << 30;
 // one (4e-5, a hundredth of bf16's rounding).
 template <bool F32OUT>
 constexpr int kDrain = F32OUT ? 8 : 256;
+// Rows of a tile whose weights' digits lie in lanes of their own, and those digits:
+// 24 bits of a weight in bf16, 22 in f16.
+constexpr int kFewRows = 8;
+template <typename T>
+constexpr int kFewDigits = 3;
+template <>
+constexpr int kFewDigits<__half> = 2;
 
 template <int DP>
 struct Cfg {
@@ -566,8 +580,10 @@ __device__ __forceinline__ bool clean(uint32_t& w)
 // ---- the kernel -------------------------------------------------------------
 
 // F32OUT: the output is f32 and each weight is two digits of T, hi = T(w) and
-// lo = T(w - hi), multiplied into the same accumulator one after the other.
-template <int DP, typename T, bool F32OUT>
+// lo = T(w - hi), multiplied into the same accumulator one after the other.  FEW
+// (F32OUT, tiles of up to 8 rows): each weight is kFewDigits digits, digit d of row
+// r in lane 8 d + r, with an accumulator of its own.
+template <int DP, typename T, bool F32OUT, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
     bitlin_attend(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const __grid_constant__ AttendParams p)
@@ -792,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint32_t col = pcol + (key & ~31) + ((key & 31) >> 1);
                                 ptx::mma_bf16_ts(tmem + C::kOCol, col, v + (uint64_t)(kk * 2048 >> 4), idesc_o,
                                                  !fresh || c > 0 || kk > 0 ? 1u : 0u);
-                                if (F32OUT)
+                                if (F32OUT && !FEW)
                                     ptx::mma_bf16_ts(tmem + C::kOCol, col + 16, v + (uint64_t)(kk * 2048 >> 4), idesc_o, 1u);
                             }
                             ptx::mma_commit(&sh->empty[stage]);
@@ -823,13 +839,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 // Boxes of q_box tokens x the group's heads x 64 dims; dims past the
                 // head's are zeros (K's are, and a zero times what lies there must stay zero).
-                const int boxes = (w.tokens() + p.q_box - 1) / p.q_box, bytes = p.q_box * p.group * 128;
+                // FEW: the tile's one box, once for each digit.
+                const int boxes = FEW ? kFewDigits<T> : (w.tokens() + p.q_box - 1) / p.q_box;
+                const int bytes = p.q_box * p.group * 128, apart = FEW ? kFewRows * 128 : bytes;
                 if (lane == 0) ptx::mbar_arrive_expect_tx(&sh->q_full, boxes * bytes * NC);
                 __syncwarp();
                 for (int k = lane; k < boxes * NC; k += 32) {
                     const int c = k % NC, box = k / NC;
-                    ptx::tma_load_3d(tile_q + c * kChunkBytes + box * bytes, &tmap_q, 64 * c, w.head * p.group,
-                                     w.q.row0 + w.qt * p.tile_tokens + box * p.q_box, &sh->q_full);
+                    ptx::tma_load_3d(tile_q + c * kChunkBytes + box * apart, &tmap_q, 64 * c, w.head * p.group,
+                                     w.q.row0 + w.qt * p.tile_tokens + (FEW ? 0 : box * p.q_box), &sh->q_full);
                 }
             }
             // The last copies must land before the CTA may exit.
@@ -858,7 +876,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool negative = p.scale < 0.f;
         const float sign = negative ? -1.f : 1.f, mul = sign * sl2;
         const float limit = exp2f(kLazy + kShift<T>);
-        const int my_token = r / p.group, my_head = r - my_token * p.group;
+        const int digit = FEW ? r / kFewRows : 0, my_row = FEW ? r % kFewRows : r;
+        const int my_token = my_row / p.group, my_head = my_row - my_token * p.group;
+        // 0 or -1: whether this lane takes a weight's first and second digit off it before it rounds it to its own
+        const float off1 = FEW && digit > 0 ? -1.f : 0.f, off2 = FEW && digit > 1 ? -1.f : 0.f;
         int gt = 0, consumed = 0;                // tiles and ring chunks before this part
         int part = 0, joined = 0, paired = 0;    // parts before this one, meetings so far
         bool ok = true;
@@ -871,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; w.valid() && ok; w.next(), ++part) {
             const int n = w.j1 - w.j0;
             const int tokens = w.tokens();
-            const bool valid = my_token < tokens;
+            const bool valid = my_token < tokens && (!FEW || digit < kFewDigits<T>);
             const bool active = 32 * quad < tokens * p.group;     // the warp has a valid row
             const int first = w.q.place0 + w.qt * p.tile_tokens;  // place of the first token
             const int lim_first = p.causal ? min(max(first + 1, 0), w.q.len) : w.q.len;
@@ -979,7 +1000,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (k & 2) add1 = __fadd2_rn(add1, e);
                                 else add0 = __fadd2_rn(add0, e);
                                 hi[k / 2] = pack2<T>(e.x, e.y);
-                                if (F32OUT) {
+                                if (FEW) {
+                                    float2 rest = __ffma2_rn(unpack2<T>(hi[k / 2]), make_float2(off1, off1), e);
+                                    hi[k / 2] = pack2<T>(rest.x, rest.y);
+                                    if (kFewDigits<T> > 2) {
+                                        rest = __ffma2_rn(unpack2<T>(hi[k / 2]), make_float2(off2, off2), rest);
+                                        hi[k / 2] = pack2<T>(rest.x, rest.y);
+                                    }
+                                } else if (F32OUT) {
                                     const float2 f = unpack2<T>(hi[k / 2]);
                                     lo[k / 2] = pack2<T>(e.x - f.x, e.y - f.y);
                                 }
@@ -1036,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 16; ++k) x[k] = hi[c + k];
                         ptx::tmem_st16(taddr + 2 * c, x);
-                        if (F32OUT) {
+                        if (F32OUT && !FEW) {
 #pragma unroll
                             for (int k = 0; k < 16; ++k) x[k] = lo[c + k];
                             ptx::tmem_st16(taddr + 2 * c + 16, x);
@@ -1145,6 +1173,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (c + 16 < HALF) x[k] = __ldcg(ws_o + ((c + 16) / 4 + k) * ws_col);
                         }
                     }
+                    if (FEW) {
+                        // the digits' products, smallest first
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float second = __shfl_down_sync(0xffffffffu, o[k], kFewRows);
+                            const float third = kFewDigits<T> > 2 ? __shfl_down_sync(0xffffffffu, o[k], 2 * kFewRows) : 0.f;
+                            o[k] += second + third;
+                        }
+                    }
                     if (bad && valid) {
 #pragma unroll 1
                         for (int key = max(lim_first, w.j0 * kKeys); key < min(lim, w.j1 * kKeys); ++key) {
@@ -1159,7 +1196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    if (valid) {
+                    if (valid && digit == 0) {
                         if (!whole) {
 #pragma unroll
                             for (int k = 0; k < 16; k += 4)
@@ -1190,13 +1227,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_before();
             ptx::mbar_arrive(&sh->o_free);
             if (whole) {
-                if (valid && side == 0 && p.lse)
+                if (valid && side == 0 && digit == 0 && p.lse)
                     p.lse[token * p.heads + head] = sum == 0.f ? -INFINITY : 0.6931471805599453f * (base + log2f(sum));
                 continue;
             }
 
             // ---- a part of an item: the last one to arrive joins them
-            if (valid && side == 0)
+            if (valid && side == 0 && digit == 0)
                 __stcg(reinterpret_cast<float2*>(p.ws_ml) + slot * kRows + r, make_float2(sum == 0.f ? -INFINITY : base, sum));
             const int from = cta_of(start, w.line + p.item_extra);
             const int to = cta_of(start, w.line + p.item_extra + w.tiles - 1);
@@ -1322,20 +1359,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int DP, typename T, bool F32OUT>
+template <int DP, typename T, bool F32OUT, bool FEW>
 cudaError_t load()
 {
     static PerDeviceOnce once;
     int dev = 0;
     return once.run(&dev, [](int) {
-        return cudaFuncSetAttribute(bitlin_attend<DP, T, F32OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
+        return cudaFuncSetAttribute(bitlin_attend<DP, T, F32OUT, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
     });
 }
 
-template <int DP, typename T, bool F32OUT>
+template <int DP, typename T, bool F32OUT, bool FEW>
 cudaError_t launch(const AttendParams& p, const void* tmap_q, const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s)
 {
-    const cudaError_t e = load<DP, T, F32OUT>();
+    const cudaError_t e = load<DP, T, F32OUT, FEW>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_sms);
@@ -1347,24 +1384,35 @@ cudaError_t launch(const AttendParams& p, const void* tmap_q, const void* tmap_k
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, bitlin_attend<DP, T, F32OUT>, *static_cast<const CUtensorMap*>(tmap_q),
+    return cudaLaunchKernelEx(&cfg, bitlin_attend<DP, T, F32OUT, FEW>, *static_cast<const CUtensorMap*>(tmap_q),
                               *static_cast<const CUtensorMap*>(tmap_k), *static_cast<const CUtensorMap*>(tmap_v), p);
 }
 
-template <typename T, bool F32OUT>
+template <typename T, bool F32OUT, bool FEW>
 cudaError_t pick_dim(const AttendParams& p, const void* tmap_q, const void* tmap_k, const void* tmap_v, int num_sms,
                      cudaStream_t s)
 {
-    if (p.dim <= 64) return launch<64, T, F32OUT>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
-    if (p.dim <= 128) return launch<128, T, F32OUT>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
-    return launch<256, T, F32OUT>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
+    if (p.dim <= 64) return launch<64, T, F32OUT, FEW>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
+    if (p.dim <= 128) return launch<128, T, F32OUT, FEW>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
+    return launch<256, T, F32OUT, FEW>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
+}
+
+template <typename T>
+cudaError_t pick_output(const AttendParams& p, int out_dtype, const void* tmap_q, const void* tmap_k, const void* tmap_v,
+                        int num_sms, cudaStream_t s)
+{
+    if (out_dtype != BITLIN_F32) return pick_dim<T, false, false>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
+    return p.few ? pick_dim<T, true, true>(p, tmap_q, tmap_k, tmap_v, num_sms, s)
+                 : pick_dim<T, true, false>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
 }
 
 template <int DP, typename T>
 cudaError_t load_outputs()
 {
-    const cudaError_t e = load<DP, T, false>();
-    return e == cudaSuccess ? load<DP, T, true>() : e;
+    cudaError_t e = load<DP, T, false, false>();
+    if (e == cudaSuccess) e = load<DP, T, true, false>();
+    if (e == cudaSuccess) e = load<DP, T, true, true>();
+    return e;
 }
 
 template <typename T>
@@ -1405,8 +1453,16 @@ KvWorkspaceParts bitlin_attend_workspace(int dim, int num_sms)
     return w;
 }
 
-void bitlin_attend_rows(int tokens, int seqs, int group, int* tile_tokens, int* q_box)
+void bitlin_attend_rows(int tokens, int seqs, int group, int out_dtype, int* tile_tokens, int* q_box, int* few_rows)
 {
+    // An f32 output of a few rows a sequence: room for every digit in the tile.  The
+    // lengths lie on the device: as many tokens as sequences are taken for one each
+    // (another spread of them takes more tiles, each of which reads its keys).
+    *few_rows = out_dtype == BITLIN_F32 && group <= kFewRows && (tokens == seqs || tokens <= kFewRows / group);
+    if (*few_rows) {
+        *tile_tokens = *q_box = kFewRows / group;
+        return;
+    }
     // A tile's rows in one box where sequences bring many tokens; where they
     // bring few, boxes of the fewest tokens whose rows keep the swizzle's atoms
     // of eight, so that single tokens do not fetch their neighbours' rows.  The
@@ -1432,10 +1488,6 @@ cudaError_t bitlin_attend_load(int dim, int dtype)
 cudaError_t bitlin_launch_attend(const AttendParams& p, int dtype, int out_dtype, const void* tmap_q,
                                  const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s)
 {
-    const bool f32 = out_dtype == BITLIN_F32;
-    if (dtype == BITLIN_BF16)
-        return f32 ? pick_dim<__nv_bfloat16, true>(p, tmap_q, tmap_k, tmap_v, num_sms, s)
-                   : pick_dim<__nv_bfloat16, false>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
-    return f32 ? pick_dim<__half, true>(p, tmap_q, tmap_k, tmap_v, num_sms, s)
-               : pick_dim<__half, false>(p, tmap_q, tmap_k, tmap_v, num_sms, s);
+    return dtype == BITLIN_BF16 ? pick_output<__nv_bfloat16>(p, out_dtype, tmap_q, tmap_k, tmap_v, num_sms, s)
+                                : pick_output<__half>(p, out_dtype, tmap_q, tmap_k, tmap_v, num_sms, s);
 }

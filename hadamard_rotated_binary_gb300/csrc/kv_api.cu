@@ -381,7 +381,7 @@ bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
     p.group = heads / kv->kv_heads;
     p.dim = kv->dim;
     p.causal = causal;
-    bitlin_attend_rows(tokens, batch->seqs, p.group, &p.tile_tokens, &p.q_box);
+    bitlin_attend_rows(tokens, batch->seqs, p.group, out->dtype, &p.tile_tokens, &p.q_box, &p.few);
     p.item_extra = bitlin_attend_item_extra(kv->dim);
     bitlin_attend_boxes(kv->dim, kv->page_size, &p.box_k, &p.box_v);
     p.stall_test = kv->stall_test;

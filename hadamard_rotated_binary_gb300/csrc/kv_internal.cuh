@@ -101,6 +101,7 @@ struct AttendParams {
     int pages, page_size, page_shift;  // page_shift: log2 of a power of two, else -1
     int tokens, heads, kv_heads, group, dim, causal;
     int tile_tokens, q_box;    // tokens of a 128-row tile, and of one copy of its queries
+    int few;                   // tiles of up to 8 rows, the weights' digits in lanes of their own
     int item_extra;            // key tiles that an item's begin and end cost
     int box_k, box_v;          // slots of a page per TMA copy
     int stall_test;
@@ -151,8 +152,8 @@ struct bitlin_kv {
 cudaError_t bitlin_launch_turn(const bitlin_impl::TurnParams& p, int src_dtype, int dst_dtype, cudaStream_t s);
 cudaError_t bitlin_launch_attend(const bitlin_impl::AttendParams& p, int dtype, int out_dtype, const void* tmap_q,
                                  const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s);
-// Tokens of a row tile, and of one TMA copy of its queries.
-void bitlin_attend_rows(int tokens, int seqs, int group, int* tile_tokens, int* q_box);
+// Tokens of a row tile, and of one TMA copy of its queries; whether its rows are few.
+void bitlin_attend_rows(int tokens, int seqs, int group, int out_dtype, int* tile_tokens, int* q_box, int* few_rows);
 // What an item of attention's work costs beside its key tiles, in key tiles.
 int bitlin_attend_item_extra(int dim);
 // Slots per TMA copy of the key and value pools.

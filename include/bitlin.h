@@ -491,14 +491,17 @@ bitlin_status bitlin_kv_append(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
  *   out    [tokens][heads][head_dim], 16-byte aligned, strides multiples of
  *          8; the cache's type, or BITLIN_F32 (what bitlin_forward reads).
  *          For a 16-bit out the probabilities are rounded to the cache's type
- *          before they meet the values; for an f32 out each is split into two
- *          digits of that type, 16 bits in bf16 and 22 in f16 (an infinite
- *          value may come out of them as NaN).  Measured against 64 bits, in
- *          relative norm: a bf16 out is off by 2.1e-3 to 2.3e-3 (its own
- *          rounding alone: 1.65e-3), an f16 one by 2.9e-4 (2.1e-4); an f32 out
- *          over a bf16 cache by 1.3e-6 to 1.6e-6 at 777 keys and 3.5e-6 to
- *          5.3e-6 at 131,072 (f32 arithmetic throughout: 0.5e-6 to 0.8e-6 and
- *          0.8e-6 to 1.4e-6).
+ *          before they meet the values; for an f32 out each is split into
+ *          digits of that type: two, 16 bits in bf16 and 22 in f16, or, for
+ *          single tokens (tokens = seqs, or few tokens, of up to 8 query heads
+ *          to a key head), three in bf16 with all 24 (an infinite value may
+ *          come out of them as NaN).  Measured against 64 bits, in relative
+ *          norm (in brackets the output's own rounding alone, or f32
+ *          arithmetic throughout): a bf16 out 2.1e-3 to 2.3e-3 (1.65e-3), an
+ *          f16 one 2.9e-4 (2.1e-4); an f32 out of single tokens 0.8e-6 to
+ *          1.2e-6 over 777 keys (0.4e-6 to 0.7e-6) and 2.0e-6 to 2.5e-6 over
+ *          131,072 (0.5e-6 to 1.4e-6), of prompts 0.3e-6 to 1.1e-6 (0.2e-6 to
+ *          0.5e-6), of chunks over a long cache up to 4.1e-6 (1.0e-6).
  *   lse    device pointer, float [tokens][heads], or NULL.
  *
  * Sums, the softmax's statistics and the output accumulate in f32.  Requires

@@ -9,7 +9,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from test_attention_side import (  # noqa: E402,F401
-    attend64, attend64_long, attend_case, check_attended, check_long, freqs, generator, gpu, hrb, make_batch, make_pools, shared_pages,
+    attend64, attend64_long, attend_case, check_attended, check_long, fill_past, freqs, generator, gpu, hrb, make_batch, make_pools, shared_pages,
 )
 
 
@@ -636,3 +636,49 @@ def test_scores_as_large_as_documented(hrb, dtype, most):
             own = u if out_dtype == dtype else 2.0**-24
             assert bool(((got - out).abs() <= size * (digits + 2.0**-18) + own * (out.abs() + digits * size)).all())
             assert bool(((got_lse.double().cpu() - lse).abs() <= 2.0**-21 * lse.abs()).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim,heads", [(64, 1), (128, 6), (256, 8)])
+@pytest.mark.parametrize("heavy", [0, 1])
+def test_f32_outputs_of_single_tokens_hold_whole_weights(hrb, dtype, dim, heads, heavy):
+    """Two keys of exact scores, one of weight 1 and value 0, one of weight w and value 1: w / (1 + w).
+
+    In units of 2^-24 of w: the argument of 2^x for |x| < 8 is rounded (4) and its factor too (8), ex2 is
+    good to 3, the digits hold all bits or 22 (2), the sum of two products is cut at 2, and sum,
+    reciprocal and product round three times (3): with x's by ln 2, 18.3 units, 1.1e-6.  (Two digits of
+    bf16 are off by up to 7.6e-6.)"""
+    seqs = 300
+    gen = generator(55)
+    batch, offsets, pages = make_batch(hrb, gen, [1] * seqs, [2] * seqs, 8)
+    kp, vp = make_pools(gen, pages, 8, 1, dim, dtype, fill=0.0)
+    score = torch.linspace(-5.4, 5.4 if heavy else 0.0, seqs, device="cuda").to(dtype)
+    page = batch.table[:, 0].long()
+    kp[page, heavy, 0, 0] = score
+    vp[page, heavy] = 1.0
+    q = torch.zeros((seqs, heads, dim), dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    got = hrb.PagedKV(kp, vp).attend(q, batch, scale=1.0, dtype=torch.float32).double().cpu()
+    w = torch.exp(score.double().cpu())[:, None, None]
+    want = (w / (1 + w)).expand_as(got)
+    assert bool(((got - want).abs() <= 1.1e-6 * want).all()), float(((got - want).abs() / want).max())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("new", [[1, 1, 1, 1], [3, 0, 0, 1], [0, 4, 0, 0], [0, 0, 1, 0], [2, 0, 0, 0], [60] + [0] * 58 + [1]])
+@pytest.mark.parametrize("kvh,heads", [(1, 8), (2, 10), (1, 6), (2, 2), (1, 9)])
+def test_f32_outputs_of_few_tokens_however_spread(hrb, dtype, new, kvh, heads):
+    """As many tokens as sequences, or fewer, spread in any way, and more than were counted on."""
+    lens = [n + (37 * i + 5) % 300 for i, n in enumerate(new)]
+    batch, offsets, kp, vp, q = attend_case(hrb, 72, 16, kvh, heads, new, lens, dtype, 56, q_scale=2.0)
+    fill_past(batch, kp, vp, lens, math.nan)
+    cache = hrb.PagedKV(kp, vp)
+    for causal in (True, False):
+        ref = attend64(q, kp, vp, offsets, lens, batch.table, 72**-0.5, causal)
+        lse = torch.empty(q.shape[:2], device="cuda")
+        out = cache.attend(q, batch, causal=causal, dtype=torch.float32, lse=lse)
+        check_attended(out, lse, ref, dtype)
+        assert torch.equal(out, cache.attend(q, batch, causal=causal, dtype=torch.float32))
+    assert cache.get_error() == 0
