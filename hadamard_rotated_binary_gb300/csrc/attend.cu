@@ -67,10 +67,10 @@
 // Off by, of the output's norm (two digits in one accumulator -> this; f32
 // arithmetic): bf16 over 777 keys 1.5e-6 -> 0.8e-6 (0.6e-6), 131,072 4.2e-6 -> 2.2e-6
 // (1.0e-6), 64 tokens over 100-8,000 3.1e-6 -> 1.4e-6 (0.4e-6); f16 1.1e-6 -> 1.0e-6,
-// 3.4e-6 -> 2.4e-6 and 2.5e-6 -> 1.75e-6.  Times: bf16 777 keys 14.0 -> 14.4 us,
-// 131,072 102-109 -> 104-113, 64 tokens at 256/128/64 dims 194/191/167 -> 200/200/178;
-// f16 as before, at 64 dims 175 -> 154.  Two digits in lanes of their own in bf16
-// take no time either and leave 1.4e-6, 3.3e-6 and 2.6e-6.
+// 3.4e-6 -> 2.4e-6 and 2.5e-6 -> 1.75e-6.  Times: bf16 777 keys 14.0 -> 14.2 us,
+// 131,072 102-111 -> 103-116 (103.3 and 101.9 where most lie), 64 tokens at
+// 256/128/64 dims 194/191/166 -> 200/196/163; f16 194/191/175 -> 196/194/162.  Two
+// digits in lanes of their own in bf16 leave 1.4e-6, 3.3e-6 and 2.6e-6.
 // Many rows have no idle lanes.  There a third digit in shared memory, for want of
 // tensor memory, with drains every 4 tiles, and drains every 4 tiles alone, were
 // measured and not kept: one token over 131,072 keys 3.9e-6 -> 2.4e-6 for 100 -> 109
@@ -553,6 +553,16 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t v)
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+// The digits of a weight are runs of its significand: what it is up to a run's end
+// less what it is up to its begin, which masks give.  (Digits rounded one after the
+// other took 200 us for 196 on 64 tokens of 128 dims, 178 for 162 at 64 dims.)
+template <typename T>
+__device__ __forceinline__ uint32_t first_digits(int n)  // mask of the first n
+{
+    return n == 0 ? 0u : n >= kFewDigits<T> ? 0xFFFFFFFFu : kFewDigits<T> == 2 ? 0xFFFFE000u : n == 1 ? 0xFFFF0000u : 0xFFFFFF00u;
+}
+__device__ __forceinline__ float run(float x, uint32_t mask) { return __uint_as_float(__float_as_uint(x) & mask); }
+
 // Exponent bits of a 16-bit element: all ones is an infinity or a NaN.
 template <typename T>
 constexpr uint32_t kExpBits = 0x7F80u;
@@ -878,8 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float limit = exp2f(kLazy + kShift<T>);
         const int digit = FEW ? r / kFewRows : 0, my_row = FEW ? r % kFewRows : r;
         const int my_token = my_row / p.group, my_head = my_row - my_token * p.group;
-        // 0 or -1: whether this lane takes a weight's first and second digit off it before it rounds it to its own
-        const float off1 = FEW && digit > 0 ? -1.f : 0.f, off2 = FEW && digit > 1 ? -1.f : 0.f;
+        const uint32_t digit_to = first_digits<T>(digit + 1), digit_from = first_digits<T>(digit);
         int gt = 0, consumed = 0;                // tiles and ring chunks before this part
         int part = 0, joined = 0, paired = 0;    // parts before this one, meetings so far
         bool ok = true;
@@ -999,15 +1008,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
                                 if (k & 2) add1 = __fadd2_rn(add1, e);
                                 else add0 = __fadd2_rn(add0, e);
-                                hi[k / 2] = pack2<T>(e.x, e.y);
                                 if (FEW) {
-                                    float2 rest = __ffma2_rn(unpack2<T>(hi[k / 2]), make_float2(off1, off1), e);
-                                    hi[k / 2] = pack2<T>(rest.x, rest.y);
-                                    if (kFewDigits<T> > 2) {
-                                        rest = __ffma2_rn(unpack2<T>(hi[k / 2]), make_float2(off2, off2), rest);
-                                        hi[k / 2] = pack2<T>(rest.x, rest.y);
-                                    }
-                                } else if (F32OUT) {
+                                    hi[k / 2] = pack2<T>(run(e.x, digit_to) - run(e.x, digit_from),
+                                                         run(e.y, digit_to) - run(e.y, digit_from));
+                                    continue;
+                                }
+                                hi[k / 2] = pack2<T>(e.x, e.y);
+                                if (F32OUT) {
                                     const float2 f = unpack2<T>(hi[k / 2]);
                                     lo[k / 2] = pack2<T>(e.x - f.x, e.y - f.y);
                                 }
