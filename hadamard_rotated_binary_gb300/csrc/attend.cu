@@ -60,10 +60,11 @@
 // cores' additions lose between drains matters as much.
 //   Many rows: two digits, one after the other into the same accumulator (16 bits of
 //   a weight in bf16, 22 in f16).
-//   Up to 8 rows (single tokens of 8 query heads to a key head): the queries lie in the tile once for each digit, eight
-//   lanes apart, and each copy's lanes hold one digit of the weights: three in bf16,
-//   two in f16, with accumulators of their own, half the additions into each, and
-//   no product more.  The epilogue adds the digits' outputs across the lanes.
+//   Up to 8 rows (single tokens of up to 8 query heads to a key head): the queries
+//   lie in the tile once for each digit, eight lanes apart, and each copy's lanes
+//   hold one digit of the weights: three in bf16 (all 24 bits), two in f16, with
+//   accumulators of their own, half the additions into each, and no product more.
+//   The epilogue adds the digits' outputs across the lanes.
 // Off by, of the output's norm (two digits in one accumulator -> this; f32
 // arithmetic): bf16 over 777 keys 1.5e-6 -> 0.8e-6 (0.6e-6), 131,072 4.2e-6 -> 2.2e-6
 // (1.0e-6), 64 tokens over 100-8,000 3.1e-6 -> 1.4e-6 (0.4e-6); f16 1.1e-6 -> 1.0e-6,
@@ -77,10 +78,10 @@
 // us; f32 chunks 4.1e-6 -> 3.2e-6 for 449 -> 516 us.  (Keys and values in bf16 are
 // themselves rounded to 2e-3.)
 //
-// Bound: single tokens by HBM (one over 131,072 keys, 537 MB, 104 us with
-// inputs changing from call to call: 5.1 TB/s; 64 over 100-8,000 keys each, 1.06
-// GB, 171 us: 6.2 TB/s) or, where keys are few, by the latency of one pass
-// through the stages (777 keys 14.0 us in a graph); many tokens by the feeding of
+// Bound: single tokens by HBM (one over 131,072 keys, 537 MB, 103 to 116 us
+// with inputs changing from call to call: 4.6 to 5.2 TB/s; 64 over 100-8,000 keys
+// each, 1.06 GB, 167 to 171 us: 6.2 to 6.3 TB/s) or, where keys are few, by the latency of one pass
+// through the stages (777 keys 14.2 us); many tokens by the feeding of
 // K and V to one CTA's MMAs (2,048 over 32,768 keys 1.19 ms, 1.34 PFLOP/s; 4
 // prompts of 700-4,096 tokens 362 us).  With the softmax reduced to its
 // handshakes the prompts take 343 us and the chunk 1,045: it is not the limit.
