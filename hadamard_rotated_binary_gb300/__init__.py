@@ -41,7 +41,7 @@ from ._binding import (  # noqa: F401
     q1g128_words,
 )
 
-_PAGED = ("KVBatch", "PAIRS_ADJACENT", "PAIRS_HALF", "PagedKV", "Rope")
+_PAGED = ("KVBatch", "PAIRS_ADJACENT", "PAIRS_HALF", "PagedKV", "QuantKV", "Rope")
 
 
 def __getattr__(name: str):

@@ -42,6 +42,21 @@ class Batch(ctypes.Structure):
                 ("table", ctypes.c_void_p), ("table_pages", ctypes.c_int), ("table_stride", ctypes.c_longlong)]
 
 
+class QuantPools(ctypes.Structure):
+    """bitlin_kvq_pools: a 4-bit cache's pools, strides in bytes."""
+
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+                + [(n, ctypes.c_int) for n in ("pages", "page_size", "kv_heads", "head_dim")]
+                + [(n, ctypes.c_longlong) for n in ("page_stride", "slot_stride", "head_stride", "scale_page_stride",
+                                                    "scale_slot_stride", "scale_head_stride")])
+
+
+class HeadNorms(ctypes.Structure):
+    """bitlin_head_norms: weights of queries' and keys' norms."""
+
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("eps", ctypes.c_double)]
+
+
 def library_path() -> str:
     return os.path.join(PKG, "libbitlin.so")
 
@@ -109,6 +124,23 @@ def lib() -> ctypes.CDLL:
     for name in ("bitlin_rope_create", "bitlin_rope_apply", "bitlin_rope_cuda_error", "bitlin_rope_destroy", "bitlin_kv_create", "bitlin_kv_share", "bitlin_kv_append",
                  "bitlin_kv_attend", "bitlin_kv_get_error", "bitlin_kv_cuda_error", "bitlin_kv_set_wait_budget",
                  "bitlin_kv_test_stall", "bitlin_kv_destroy"):
+        getattr(L, name).restype = i32
+    N, f64, size = ctypes.POINTER(HeadNorms), ctypes.c_double, ctypes.c_size_t
+    L.bitlin_rope_apply_normed.argtypes = [P, R, i32, i32, i32, P, P, f64, R, P]
+    L.bitlin_rope_gradient_scratch.argtypes = [i32, i32, i32]
+    L.bitlin_rope_gradient_scratch.restype = size
+    L.bitlin_rope_gradient.argtypes = [P, R, R, i32, i32, i32, P, P, f64, R, P, P, size, P]
+    L.bitlin_kv_append_normed.argtypes = [P, B, i32, P, P, R, R, R, i32, R, N, P]
+    L.bitlin_kvq_create.argtypes = [ctypes.POINTER(P), ctypes.POINTER(QuantPools), i32]
+    L.bitlin_kvq_share.argtypes = [P, P]
+    L.bitlin_kvq_append.argtypes = [P, B, i32, P, P, R, R, R, i32, R, N, P]
+    L.bitlin_kvq_read.argtypes = [P, B, i32, R, R, P]
+    L.bitlin_kvq_attend.argtypes = [P, B, i32, R, i32, ctypes.c_float, i32, R, P, P, P]
+    for name in ("bitlin_kvq_get_error", "bitlin_kvq_cuda_error", "bitlin_kvq_destroy"):
+        getattr(L, name).argtypes = [P]
+    for name in ("bitlin_rope_apply_normed", "bitlin_rope_gradient", "bitlin_kv_append_normed", "bitlin_kvq_create", "bitlin_kvq_share",
+                 "bitlin_kvq_append", "bitlin_kvq_read", "bitlin_kvq_attend", "bitlin_kvq_get_error", "bitlin_kvq_cuda_error",
+                 "bitlin_kvq_destroy"):
         getattr(L, name).restype = i32
     for name in ("bitlin_create", "bitlin_create_q1g128", "bitlin_forward", "bitlin_forward_host", "bitlin_embed", "bitlin_mlp_forward",
                  "bitlin_argmax", "bitlin_set_path", "bitlin_plan", "bitlin_set_wait_budget", "bitlin_test_stall", "bitlin_destroy", "bitlin_get_error",

@@ -1,4 +1,5 @@
-"""Binding of the attention side: rotary positions, the paged cache and attention over it.
+"""Binding of the attention side: rotary positions, norms of heads, the paged caches in 16 and in
+4 bits and attention over them.
 
 Handles live here (ctypes, as in ``_binding``); the calls on tensors are marshalled by the compiled
 ``_paged_native`` (csrc/paged_native.cpp)."""
@@ -8,7 +9,7 @@ import ctypes
 
 import torch
 
-from ._binding import BITLIN_OK, Batch, BitlinError, lib
+from ._binding import BITLIN_OK, Batch, BitlinError, QuantPools, lib
 
 lib()  # libbitlin.so first: the compiled binding is linked against it
 
@@ -45,10 +46,19 @@ class Rope:
             raise BitlinError(st, "bitlin_rope_create")
         self._h = h.value
 
-    def apply(self, x, pos, out=None, dtype=None, inverse: bool = False, stream=None):
+    def apply(self, x, pos, out=None, dtype=None, inverse: bool = False, stream=None, norm=None, eps: float = 1e-6):
         """bitlin_rope_apply: x [tokens][heads][dim] rotated by pos (int32 [axes][tokens]), into `out`
-        (x itself is allowed) or a new tensor of `dtype` (x's where None)."""
-        return native.rope_apply(self._h, self.device.index, self.axes, x, pos, out, dtype, inverse, stream)
+        (x itself is allowed) or a new tensor of `dtype` (x's where None).
+
+        norm  float32 [dim]: each head is first divided by its root mean square (eps added to the
+              mean) and multiplied by this weight, in the same pass (bitlin_rope_apply_normed).
+        """
+        return native.rope_apply(self._h, self.device.index, self.axes, x, pos, out, dtype, inverse, stream, norm, eps)
+
+    def gradient(self, dy, x, pos, norm, eps: float = 1e-6, dx=None, stream=None):
+        """bitlin_rope_gradient: the gradient of apply(x, pos, norm=norm, eps=eps) from that of its
+        output: (dx in x's type, the weight's in float32).  dx: x, dy, or a tensor to write to."""
+        return native.rope_gradient(self._h, self.device.index, self.axes, dy, x, pos, norm, eps, dx, stream)
 
     def close(self):
         if getattr(self, "_h", None):
@@ -111,6 +121,17 @@ class KVBatch:
         self.address = ctypes.addressof(self._c)
 
 
+def _rope_of(rope: Rope | None, device):
+    """(handle, axes) of an append's rope."""
+    if rope is None:
+        return None, 0
+    if not rope._h:
+        raise ValueError("the rope's handle is closed")  # (None would mean no rotation)
+    if rope.device != device:
+        raise ValueError("the rope must be on the cache's device")
+    return rope._h, rope.axes
+
+
 class PagedKV:
     """One layer's paged cache (a bitlin_kv handle on the caller's pools, which it keeps alive).
 
@@ -155,16 +176,17 @@ class PagedKV:
             raise ValueError("the batch must be on the cache's device")
         return batch.address
 
-    def append(self, k, v, batch: KVBatch, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None):
+    def append(self, k, v, batch: KVBatch, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None,
+               q_norm=None, k_norm=None, eps: float = 1e-6):
         """bitlin_kv_append: k and v [tokens][kv_heads][head_dim] to their places, k rotated; q
-        [tokens][heads][head_dim], when given, is rotated too and returned in the cache's type."""
-        if rope is not None and not rope._h:
-            raise ValueError("the rope's handle is closed")  # (None would mean no rotation)
-        if rope is not None and rope.device != self.device:
-            raise ValueError("the rope must be on the cache's device")
-        r, axes = (None, 0) if rope is None else (rope._h, rope.axes)
+        [tokens][heads][head_dim], when given, is rotated too and returned in the cache's type.
+
+        q_norm, k_norm  float32 [head_dim]: each head of q and of k is normed before its rotation,
+                        in the same pass (see Rope.apply).
+        """
+        r, axes = _rope_of(rope, self.device)
         return native.kv_append(self._h, self.device.index, self.kv_heads, self.head_dim, self.dtype,
-                                self._address_of(batch), k, v, r, axes, pos, q, q_out, stream)
+                                self._address_of(batch), k, v, r, axes, pos, q, q_out, stream, q_norm, k_norm, eps)
 
     def attend(self, q, batch: KVBatch, scale: float | None = None, causal: bool = True, out=None, dtype=None,
                lse=None, stream=None):
@@ -185,6 +207,105 @@ class PagedKV:
     def close(self):
         if getattr(self, "_h", None):
             lib().bitlin_kv_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class QuantKV:
+    """One layer's paged cache in 4 bits (a bitlin_kvq handle on the caller's pools, which it keeps
+    alive).  `QuantKV.pools` makes pools in the layout that is read fastest.
+
+    k, v              uint8 CUDA tensors [pages][page_size][kv_heads][head_dim / 2], head_dim 64, 128
+                      or 256, with the same strides (multiples of 16): two elements a byte
+    k_scale, v_scale  uint8 CUDA tensors [pages][page_size][kv_heads][4] with the same strides
+                      (multiples of 4): a scale for each quarter of a head
+    dtype             bfloat16 or float16: of queries, and of outputs unless they are asked for in
+                      float32
+    share             another 4-bit cache, whose workspace to use in place of one of its own: the
+                      calls on both must then follow one another in stream order
+    """
+
+    k, v, k_scale, v_scale = _held("k"), _held("v"), _held("k_scale"), _held("v_scale")
+
+    def __init__(self, k, v, k_scale, v_scale, dtype=torch.bfloat16, share: QuantKV | None = None):
+        parts = (k, v, k_scale, v_scale)
+        if any(t.dtype != torch.uint8 or not t.is_cuda or t.dim() != 4 or t.device != k.device for t in parts):
+            raise ValueError("k, v and their scales must be 4-dimensional uint8 CUDA tensors on one device")
+        if k.shape != v.shape or k_scale.shape != v_scale.shape or k_scale.shape != k.shape[:3] + (4,):
+            raise ValueError("k and v must be [pages][page_size][kv_heads][head_dim / 2], the scales [pages][page_size][kv_heads][4]")
+        if any(t.stride(3) != 1 for t in parts):
+            raise ValueError("heads must be contiguous")
+        # a dimension of one has no stride that matters
+        strides = [[s if n > 1 else max(t.shape[3], 16) for n, s in zip(t.shape, t.stride())][:3] for t in parts]
+        if strides[0] != strides[1] or strides[2] != strides[3]:
+            raise ValueError("k and v must have one layout, and their scales one")
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("dtype must be bfloat16 or float16")
+        self.k, self.v, self.k_scale, self.v_scale = parts
+        self.device, self.dtype = k.device, dtype
+        pages, page_size, self.kv_heads, self.head_dim = *k.shape[:3], 2 * k.shape[3]
+        pools = QuantPools(*(t.data_ptr() for t in parts), pages, page_size, self.kv_heads, self.head_dim,
+                           *strides[0], *strides[2])
+        h = ctypes.c_void_p()
+        with torch.cuda.device(k.device):
+            st = lib().bitlin_kvq_create(ctypes.byref(h), ctypes.byref(pools), _CODES[dtype])
+            if st != BITLIN_OK:
+                raise BitlinError(st, "bitlin_kvq_create")
+            self._h = h.value
+            if share is not None:
+                st = lib().bitlin_kvq_share(self._h, share._h)
+                if st != BITLIN_OK:
+                    raise BitlinError(st, "bitlin_kvq_share", lib().bitlin_kvq_cuda_error(self._h))
+
+    @staticmethod
+    def pools(pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
+        """(k, v, k_scale, v_scale) of zeros, the slots of a head side by side in memory."""
+        def pool(n):
+            return torch.zeros((pages, kv_heads, page_size, n), dtype=torch.uint8, device=device).transpose(1, 2)
+        return pool(head_dim // 2), pool(head_dim // 2), pool(4), pool(4)
+
+    def _address_of(self, batch: KVBatch) -> int:
+        if batch.device != self.device:
+            raise ValueError("the batch must be on the cache's device")
+        return batch.address
+
+    def append(self, k, v, batch: KVBatch, rope: Rope | None = None, pos=None, q=None, q_out=None, stream=None,
+               q_norm=None, k_norm=None, eps: float = 1e-6):
+        """bitlin_kvq_append: as PagedKV.append, to 4 bits; q is returned in the handle's dtype."""
+        r, axes = _rope_of(rope, self.device)
+        return native.kvq_append(self._h, self.device.index, self.kv_heads, self.head_dim, self.dtype,
+                                 self._address_of(batch), k, v, r, axes, pos, q, q_out, stream, q_norm, k_norm, eps)
+
+    def read(self, batch: KVBatch, tokens: int, k=None, v=None, dtype=None, stream=None):
+        """bitlin_kvq_read: what the cache holds at the places of the batch's rows, as (k, v)
+        [tokens][kv_heads][head_dim], into `k` and `v` or new tensors of `dtype` (the handle's)."""
+        return native.kvq_read(self._h, self.device.index, self.kv_heads, self.head_dim, self._address_of(batch), tokens,
+                               k, v, dtype or self.dtype, stream)
+
+    def attend(self, q, batch: KVBatch, scale: float | None = None, causal: bool = True, out=None, dtype=None,
+               lse=None, stream=None, through: PagedKV | None = None):
+        """bitlin_kvq_attend: as PagedKV.attend, over the 4-bit cache.
+
+        through  a 16-bit cache of the same pages, page size, heads and dtype whose pools are
+                 scratch (one serves all layers): calls of more tokens than sequences read the
+                 pages back into it and attend there, which is faster for prompts.
+        """
+        if through is not None and not through._h:
+            raise ValueError("through's handle is closed")
+        return native.kvq_attend(self._h, self.device.index, self.head_dim, self.dtype, self._address_of(batch), q, scale,
+                                 causal, out, dtype, lse, stream, None if through is None else through._h)
+
+    def get_error(self) -> int:
+        return lib().bitlin_kvq_get_error(self._h)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().bitlin_kvq_destroy(self._h)
             self._h = None
 
     def __del__(self):

@@ -7,6 +7,7 @@
 #include <memory>
 #include <new>
 
+#include "kv_checks.cuh"
 #include "kv_internal.cuh"
 #include "tensormap.cuh"
 
@@ -15,89 +16,6 @@ using namespace bitlin_impl;
 namespace {
 
 constexpr long long kDefaultWaitBudgetNs = 2000000000LL;  // 2 s per bounded wait
-
-bitlin_status status_of(cudaError_t e)
-{
-    // what is reported here is not left for a later call to find
-    if (e != cudaSuccess) cudaGetLastError();
-    return e == cudaSuccess ? BITLIN_OK : e == cudaErrorMemoryAllocation ? BITLIN_ENOMEM : BITLIN_ECUDA;
-}
-
-template <typename Handle>
-bitlin_status from_cuda(Handle h, cudaError_t e)
-{
-    if (e != cudaSuccess) h->last_cuda_error = (int)e;
-    return status_of(e);
-}
-
-// The current device, when it is one this library runs on.
-bitlin_status current_device(int* dev)
-{
-    int major = 0, minor = 0;
-    if (cudaGetDevice(dev) != cudaSuccess) return BITLIN_EDEVICE;
-    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev);
-    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev);
-    return major == 10 && minor == 3 ? BITLIN_OK : BITLIN_EDEVICE;
-}
-
-bool on_device(int device)
-{
-    int dev = -1;
-    return cudaGetDevice(&dev) == cudaSuccess && dev == device;
-}
-
-int type_size(int dtype) { return dtype == BITLIN_F32 ? 4 : 2; }
-
-// A call of no tokens may have no memory.
-bool rows_ok(const bitlin_rows* r, int tokens)
-{
-    return r && (r->data || tokens == 0) && (r->dtype == BITLIN_F32 || r->dtype == BITLIN_BF16 || r->dtype == BITLIN_F16) &&
-           reinterpret_cast<uintptr_t>(r->data) % type_size(r->dtype) == 0;
-}
-
-// Rows that are moved 16 bytes at a time (TMA, vector stores).
-bool rows_wide(const bitlin_rows* r)
-{
-    return reinterpret_cast<uintptr_t>(r->data) % 16 == 0 && r->token_stride > 0 && r->head_stride > 0 &&
-           r->token_stride % 8 == 0 && r->head_stride % 8 == 0 && r->token_stride < (1LL << 38) &&
-           r->head_stride < (1LL << 38);
-}
-
-bool sizes_ok(int tokens, int heads, int dim)
-{
-    return tokens >= 0 && heads >= 1 && heads <= 4096 && (unsigned long long)tokens * (unsigned)dim < (1ULL << 32);
-}
-
-bool batch_ok(const bitlin_kv_batch* b)
-{
-    return b && b->seqs >= 1 && b->q_offsets && b->kv_lens && b->table && b->table_pages >= 1 &&
-           (b->seqs == 1 || b->table_stride >= b->table_pages);
-}
-
-KvBatch batch_of(const bitlin_kv_batch* b) { return {b->q_offsets, b->kv_lens, b->table, b->table_stride, b->table_pages, b->seqs}; }
-
-void set_source(TurnParams& p, int i, const bitlin_rows* r)
-{
-    p.src[i] = r->data;
-    p.src_token[i] = r->token_stride;
-    p.src_head[i] = r->head_stride;
-}
-
-void set_rope(TurnParams& p, bitlin_rope_t r, const int32_t* pos)
-{
-    p.turns = r ? r->turns : nullptr;
-    p.rotary = r ? r->rotary : 0;
-    p.axes = r ? r->axes : 0;
-    p.adjacent = r ? r->adjacent : 0;
-    p.pos = pos;
-}
-
-void set_out(TurnParams& p, const bitlin_rows* r)
-{
-    p.out = r->data;
-    p.out_token = r->token_stride;
-    p.out_head = r->head_stride;
-}
 
 // f / (2 pi) modulo one turn, to one unit of 2^-64: the 24-bit significand of f
 // times 1 / (2 pi) to 192 bits (pi by Machin's formula), enough for f32's largest
@@ -233,6 +151,67 @@ bitlin_status bitlin_rope_apply(bitlin_rope_t r, const bitlin_rows* x, int token
     return from_cuda(r, bitlin_launch_turn(p, x->dtype, out->dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+bitlin_status bitlin_rope_apply_normed(bitlin_rope_t r, const bitlin_rows* x, int tokens, int heads, int head_dim,
+                                       const int32_t* pos, const float* weight, double eps, const bitlin_rows* out,
+                                       bitlin_stream_t stream)
+{
+    if (!r || !rows_ok(x, tokens) || !rows_ok(out, tokens) || (!pos && tokens) || !sizes_ok(tokens, heads, head_dim)) return BITLIN_EINVAL;
+    if (head_dim < r->rotary || head_dim > kNormMaxDim || !weight_ok(weight) || !eps_ok(eps) || !on_device(r->device)) return BITLIN_EINVAL;
+    if (tokens == 0) return BITLIN_OK;
+    NormTurnParams p = {};
+    set_source(p.t, 0, x);
+    set_out(p.t, out);
+    set_rope(p.t, r, pos);
+    p.t.tokens = tokens;
+    p.t.heads = heads;
+    p.t.dim = head_dim;
+    p.weight[0] = weight;
+    p.eps = eps;
+    return from_cuda(r, bitlin_launch_norm_turn(p, x->dtype, out->dtype, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t bitlin_rope_gradient_scratch(int tokens, int heads, int head_dim)
+{
+    if (!sizes_ok(tokens, heads, head_dim) || head_dim < 1 || head_dim > kNormMaxDim) return 0;
+    return sizeof(float) * head_dim * bitlin_norm_grad_blocks(tokens, heads);
+}
+
+bitlin_status bitlin_rope_gradient(bitlin_rope_t r, const bitlin_rows* dy, const bitlin_rows* x, int tokens, int heads,
+                                   int head_dim, const int32_t* pos, const float* weight, double eps,
+                                   const bitlin_rows* dx, float* dweight, float* scratch, size_t scratch_bytes,
+                                   bitlin_stream_t stream)
+{
+    if (!r || !rows_ok(dy, tokens) || !rows_ok(x, tokens) || !rows_ok(dx, tokens) || (!pos && tokens) || dx->dtype != x->dtype) return BITLIN_EINVAL;
+    if (!sizes_ok(tokens, heads, head_dim) || head_dim < r->rotary || head_dim > kNormMaxDim || !eps_ok(eps)) return BITLIN_EINVAL;
+    if (!weight_ok(weight) || !weight_ok(dweight) || !on_device(r->device)) return BITLIN_EINVAL;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (tokens == 0) return from_cuda(r, cudaMemsetAsync(dweight, 0, head_dim * sizeof(float), s));
+    if (!weight_ok(scratch) || scratch_bytes < bitlin_rope_gradient_scratch(tokens, heads, head_dim)) return BITLIN_ESCRATCH;
+    NormGradParams p = {};
+    p.dy = dy->data;
+    p.dy_token = dy->token_stride;
+    p.dy_head = dy->head_stride;
+    p.x = x->data;
+    p.x_token = x->token_stride;
+    p.x_head = x->head_stride;
+    p.dx = dx->data;
+    p.dx_token = dx->token_stride;
+    p.dx_head = dx->head_stride;
+    p.weight = weight;
+    p.eps = eps;
+    p.turns = r->turns;
+    p.pos = pos;
+    p.partial = scratch;
+    p.dweight = dweight;
+    p.tokens = tokens;
+    p.heads = heads;
+    p.dim = head_dim;
+    p.rotary = r->rotary;
+    p.axes = r->axes;
+    p.adjacent = r->adjacent;
+    return from_cuda(r, bitlin_launch_norm_grad(p, dy->dtype, x->dtype, s));
+}
+
 int bitlin_rope_cuda_error(bitlin_rope_t r) { return r ? r->last_cuda_error : 0; }
 
 bitlin_status bitlin_rope_destroy(bitlin_rope_t r)
@@ -311,35 +290,35 @@ bitlin_status bitlin_kv_append(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
                                const int32_t* pos, const bitlin_rows* k, const bitlin_rows* v,
                                const bitlin_rows* q, int heads, const bitlin_rows* q_out, bitlin_stream_t stream)
 {
-    if (!kv || !batch_ok(batch) || !rows_ok(k, tokens) || !rows_ok(v, tokens) || k->dtype != v->dtype) return BITLIN_EINVAL;
-    if (!sizes_ok(tokens, q ? heads : 1, kv->dim) || (rope && rope->rotary > kv->dim)) return BITLIN_EINVAL;
-    if (q && (!rows_ok(q, tokens) || !rows_ok(q_out, tokens) || q->dtype != k->dtype || q_out->dtype != kv->dtype)) return BITLIN_EINVAL;
+    return bitlin_kv_append_normed(kv, batch, tokens, rope, pos, k, v, q, heads, q_out, nullptr, stream);
+}
+
+bitlin_status bitlin_kv_append_normed(bitlin_kv_t kv, const bitlin_kv_batch* batch, int tokens, bitlin_rope_t rope,
+                                      const int32_t* pos, const bitlin_rows* k, const bitlin_rows* v,
+                                      const bitlin_rows* q, int heads, const bitlin_rows* q_out,
+                                      const bitlin_head_norms* norms, bitlin_stream_t stream)
+{
+    if (!kv || !append_ok(batch, tokens, k, v, q, heads, q_out, kv->dim, kv->dtype, rope) || !norms_ok(norms)) return BITLIN_EINVAL;
     if (!on_device(kv->device) || (rope && rope->device != kv->device)) return BITLIN_EINVAL;
     if (kv->sticky != BITLIN_OK) return kv->sticky;
     if (tokens == 0) return BITLIN_OK;
-    TurnParams p = {};
-    if (q) {
-        set_source(p, 0, q);
-        set_out(p, q_out);
-    }
-    set_source(p, 1, k);
-    set_source(p, 2, v);
-    set_rope(p, rope, pos);
+    NormTurnParams n = {};
+    TurnParams& p = n.t;
+    set_append(p, batch, tokens, rope, pos, k, v, q, heads, q_out);
     p.pool[0] = kv->k;
     p.pool[1] = kv->v;
     p.page_stride = kv->page_stride;
     p.slot_stride = kv->slot_stride;
     p.head_stride = kv->head_stride;
-    p.batch = batch_of(batch);
     p.index_error = kv->index_error;
     p.pages = kv->pages;
     p.page_size = kv->page_size;
-    p.tokens = tokens;
-    p.heads = q ? heads : 0;
     p.kv_heads = kv->kv_heads;
     p.dim = kv->dim;
-    p.append = 1;
-    return from_cuda(kv, bitlin_launch_turn(p, k->dtype, kv->dtype, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!norms || (!norms->q && !norms->k)) return from_cuda(kv, bitlin_launch_turn(p, k->dtype, kv->dtype, s));
+    set_norms(n, norms);
+    return from_cuda(kv, bitlin_launch_norm_turn(n, k->dtype, kv->dtype, false, s));
 }
 
 bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q,

@@ -84,6 +84,32 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// A call of the rotation kernel with a norm of each head before it, and the
+// append to a cache in 4 bits (t.pool then holds codes, strides in bytes).
+struct NormTurnParams {
+    TurnParams t;
+    const float* weight[2];   // q's, k's; nullptr: no norm
+    double eps;
+    uint8_t* scales[2];       // k's, v's (4-bit cache)
+    long long scale_page, scale_slot, scale_head;
+    int team;                 // lanes to a row, set by the launcher
+};
+
+// The gradient of a norm and rotation (dx in x's type).
+struct NormGradParams {
+    const void *dy, *x;
+    void* dx;
+    long long dy_token, dy_head, x_token, x_head, dx_token, dx_head;
+    const float* weight;
+    double eps;
+    const Turn* turns;
+    const int32_t* pos;
+    float* partial;           // [blocks][dim]
+    float* dweight;           // [dim]
+    int tokens, heads, dim, rotary, axes, adjacent;
+    int team, blocks;         // set by the launcher
+};
+
 // One call of the attention kernel.
 struct AttendParams {
     const void* v_pool;        // for the rare values that are put back (see attend.cu)
@@ -105,6 +131,51 @@ struct AttendParams {
     int item_extra;            // key tiles that an item's begin and end cost
     int box_k, box_v;          // slots of a page per TMA copy
     int stall_test;
+    float scale;
+};
+
+// A paged cache in 4 bits (strides in bytes).
+struct QuantPools {
+    const uint8_t* codes[2];   // k, v
+    const uint8_t* scales[2];
+    long long page_stride, slot_stride, head_stride;
+    long long scale_page, scale_slot, scale_head;
+    int pages, page_size, kv_heads, dim;
+};
+
+// Rows of the batch's new tokens read back from it.
+struct QuantReadParams {
+    QuantPools pool;
+    KvBatch batch;
+    void* out[2];
+    long long out_token[2], out_head[2];
+    int* index_error;
+    int tokens;
+};
+
+// The batch's pages as 16-bit ones.
+struct QuantUnpackParams {
+    QuantPools pool;
+    KvBatch batch;
+    void* out[2];
+    long long page_stride, slot_stride, head_stride;
+    int* index_error;
+};
+
+// Attention over it.
+struct QuantAttendParams {
+    QuantPools pool;
+    KvBatch batch;
+    const void* q;
+    long long q_token, q_head;
+    void* out;
+    long long out_token, out_head;
+    float* lse;
+    float* ws_o;
+    float* ws_ml;
+    int* tickets;
+    int* index_error;
+    int tokens, heads, group, causal;
     float scale;
 };
 
@@ -148,7 +219,25 @@ struct bitlin_kv {
     std::shared_ptr<bitlin_impl::KvWorkspace> workspace;
 };
 
+struct bitlin_kvq {
+    int device = 0;
+    int num_sms = 0;
+    int dtype = 0;
+    bitlin_impl::QuantPools pool = {};
+    int last_cuda_error = 0;
+    int* index_error = nullptr;
+    std::shared_ptr<bitlin_impl::KvWorkspace> workspace;
+};
+
 // Launchers (return a cudaError_t).
+cudaError_t bitlin_launch_norm_turn(const bitlin_impl::NormTurnParams& p, int src_dtype, int dst_dtype, bool quant, cudaStream_t s);
+int bitlin_norm_grad_blocks(int tokens, int heads);
+cudaError_t bitlin_launch_norm_grad(const bitlin_impl::NormGradParams& p, int dy_dtype, int x_dtype, cudaStream_t s);
+cudaError_t bitlin_launch_quant_read(const bitlin_impl::QuantReadParams& p, int dst_dtype, cudaStream_t s);
+cudaError_t bitlin_launch_quant_unpack(const bitlin_impl::QuantUnpackParams& p, int dst_dtype, int num_sms, cudaStream_t s);
+cudaError_t bitlin_launch_quant_attend(const bitlin_impl::QuantAttendParams& p, int dtype, int out_dtype, int num_sms, cudaStream_t s);
+cudaError_t bitlin_quant_attend_load(int dim, int dtype);
+bitlin_impl::KvWorkspaceParts bitlin_quant_attend_workspace(int dim, int num_sms);
 cudaError_t bitlin_launch_turn(const bitlin_impl::TurnParams& p, int src_dtype, int dst_dtype, cudaStream_t s);
 cudaError_t bitlin_launch_attend(const bitlin_impl::AttendParams& p, int dtype, int out_dtype, const void* tmap_q,
                                  const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s);

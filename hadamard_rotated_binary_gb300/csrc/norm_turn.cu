@@ -1,0 +1,702 @@
+// A norm of each head with its rotation in the same pass, the append of such
+// rows to a paged cache in 16 or 4 bits, and the gradient.
+//
+// Mathematics: n = x / sqrt(mean(x^2) + eps), y = R (w * n) with R the rotation
+// of pairs by their positions (see rope.cu).  Backwards, with g = R^T dy and
+// h = w * g: dx = r (h - n mean(h n)), r = 1 / sqrt(mean(x^2) + eps), and
+// dw = sum over rows of g * n.
+//
+// Bound: HBM; each element is read once and written once.  A team of 8 to 32
+// lanes holds a row: a lane owns two chunks of four elements, half the rotated
+// (or the passed-through) part apart, so pairs stay in a thread; the sum of
+// squares is five shuffles at most.  A team takes four heads of a token: the
+// angles are computed once for them and their loads are in flight together.
+// Where sizes, strides or alignment do not allow chunks, a lane takes up to four
+// pairs of single elements.
+//
+// In 4 bits the codes are those of the exact real-valued row, whatever the order
+// of the kernel's sums: a row is computed in 32 bits with a bound on its error
+// (24 units of 2^-24 of |a| + |b|: sum of squares 9 / 2, rsqrt 4, products 2,
+// angle, sine and cosine 4, rotation 2), and an element (or a group's scale)
+// that lies within it of a border between two codes is computed again in 64 bits,
+// one row in some 300.  Rows that neither a norm nor a rotation touches are exact.
+#include "kv_internal.cuh"
+#include "ptx.cuh"
+#include "quant.cuh"
+
+using namespace bitlin_impl;
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kHeadsPerTeam = 4;
+constexpr int kMaxDim = 256;
+constexpr float kRowError = 24.f * 5.9604645e-8f;
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Chunk {
+    T v[VEC];
+};
+
+__device__ __forceinline__ float team_sum(float v, int team)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        if (o < team) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ double team_sum(double v, int team)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        if (o < team) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Where unit u of a row has its two chunks of VEC elements.
+template <int VEC>
+struct Unit {
+    int lo, hi;
+    bool held, has_hi, turns;  // in the row at all; its second chunk; inside the rotated part
+};
+
+template <int VEC>
+__device__ __forceinline__ Unit<VEC> unit_of(int u, int dim, int rotary, int adjacent)
+{
+    Unit<VEC> x;
+    const int rotated = rotary / 2 / VEC;
+    x.turns = u < rotated;
+    if (VEC > 1) {
+        x.lo = x.turns ? u * VEC : rotary + (u - rotated) * VEC;
+        x.hi = x.lo + (x.turns ? rotary : dim - rotary) / 2;
+        x.held = u < dim / (2 * VEC);
+        x.has_hi = x.held;
+    } else {
+        x.lo = x.turns ? (adjacent ? 2 * u : u) : rotary + 2 * (u - rotated);
+        x.hi = x.turns && !adjacent ? x.lo + rotary / 2 : x.lo + 1;
+        x.held = x.lo < dim;
+        x.has_hi = x.hi < dim;
+    }
+    return x;
+}
+
+// Pair of the unit's element j.
+template <int VEC>
+__device__ __forceinline__ int pair_of(const Unit<VEC>& x, int u, int j, int adjacent)
+{
+    if (!adjacent) return x.lo + j;
+    return VEC == 1 ? u : j < VEC / 2 ? x.lo / 2 + j : x.hi / 2 + j - VEC / 2;
+}
+
+// The angle of a pair as a fraction of a turn in 2^-64, signed.
+__device__ __forceinline__ long long fraction(Turn w, const int32_t* pos, int tokens, int t, int place)
+{
+    const int axis = (int)(w & kAxisMask);
+    const long long at = pos ? pos[(long long)axis * tokens + t] : place;
+    return (long long)((uint64_t)at * (w & ~kAxisMask));
+}
+
+template <int VEC>
+__device__ __forceinline__ void rotate(float (&x)[VEC], float (&y)[VEC], const float (&cs)[VEC], const float (&sn)[VEC], int adjacent)
+{
+    if (VEC > 1 && adjacent) {
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+            const int k = VEC / 2 + j, e = 2 * j < VEC ? 2 * j : 0, f = e + 1 < VEC ? e + 1 : 0;
+            const float x0 = x[e], x1 = x[f], y0 = y[e], y1 = y[f];
+            x[e] = x0 * cs[j] - x1 * sn[j];
+            x[f] = x1 * cs[j] + x0 * sn[j];
+            y[e] = y0 * cs[k] - y1 * sn[k];
+            y[f] = y1 * cs[k] + y0 * sn[k];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const float x0 = x[j];
+            x[j] = x0 * cs[j] - y[j] * sn[j];
+            y[j] = y[j] * cs[j] + x0 * sn[j];
+        }
+    }
+}
+
+// Elements of |a| + |b| of each output of a pair.
+template <int VEC>
+__device__ __forceinline__ void sizes(const float (&x)[VEC], const float (&y)[VEC], float (&ex)[VEC], float (&ey)[VEC], bool turning, int adjacent)
+{
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        if (!turning) {
+            ex[j] = fabsf(x[j]);
+            ey[j] = fabsf(y[j]);
+        } else if (VEC > 1 && adjacent) {
+            ex[j] = fabsf(x[j]) + fabsf(x[j ^ 1]);
+            ey[j] = fabsf(y[j]) + fabsf(y[j ^ 1]);
+        } else {
+            ex[j] = ey[j] = fabsf(x[j]) + fabsf(y[j]);
+        }
+    }
+}
+
+// One row's value of element d in 64 bits.
+template <typename TI>
+struct Exact {
+    const TI* row;
+    const float* weight;
+    const Turn* turns;  // nullptr: not rotated
+    const int32_t* pos;
+    double r;
+    int tokens, t, place, rotary, adjacent;
+
+    __device__ double normed(int d) const
+    {
+        const double x = (double)to_f32(row[d]);
+        return weight ? x * r * (double)weight[d] : x;
+    }
+    __device__ double operator()(int d) const
+    {
+        double v;
+        if (!turns || d >= rotary) {
+            v = normed(d);
+        } else {
+            const int half = rotary / 2;
+            const int f = adjacent ? d >> 1 : d < half ? d : d - half;
+            const bool first = adjacent ? !(d & 1) : d < half;
+            const int other = adjacent ? d ^ 1 : first ? d + half : d - half;
+            double sn, cs;
+            sincospi((double)fraction(turns[f], pos, tokens, t, place) * 0x1p-63, &sn, &cs);
+            v = normed(d) * cs + (first ? -sn : sn) * normed(other);
+        }
+        return v == v ? v : 0.0;  // a NaN is stored as zero
+    }
+};
+
+// Store a row's 8 elements d0.. of each lane u < D / 8 in 4 bits.  x: the values,
+// err: how far each may be off (all zero: exact).  All lanes of the warp take part.
+template <typename TI>
+__device__ __forceinline__ void store_codes(const float (&x)[8], const float (&err)[8], bool exact, bool active, int u, int dim, int team,
+                                            const Exact<TI>& again, double eps, uint8_t* codes, uint8_t* scales)
+{
+    const int d0 = 8 * u, width = dim / 32;  // lanes of a group
+    float amax = 0.f, emax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        amax = fmaxf(amax, fabsf(x[j]));
+        emax = fmaxf(emax, err[j]);
+    }
+#pragma unroll
+    for (int o = 4; o; o >>= 1) {
+        if (o < width) {
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            emax = fmaxf(emax, __shfl_xor_sync(0xffffffffu, emax, o));
+        }
+    }
+    uint32_t scale = quant_scale_code(amax);
+    const bool which = active && !exact && quant_scale_code(fmaxf(amax - emax, 0.f)) != quant_scale_code(amax + emax);
+    float s = quant_scale(scale);
+    float inv = s > 0.f ? 1.f / s : 0.f;
+    uint32_t word = 0, doubt = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float c = rintf(fminf(fmaxf(x[j] * inv, -9.f), 9.f));
+        const float rest = fmaf(-c, s, x[j]);  // exact
+        const float over = fabsf(rest) - 0.5f * s;
+        if (exact) {
+            if (over > 0.f || (over == 0.f && ((int)c & 1))) c += rest > 0.f ? 1.f : -1.f;
+        } else if (fabsf(over) <= err[j]) {
+            doubt |= 1u << j;
+        } else if (over > 0.f) {
+            c += rest > 0.f ? 1.f : -1.f;
+        }
+        const int code = min(max((int)c, -7), 7) + 8;
+        word |= (uint32_t)(s > 0.f ? code : 8) << (4 * j);
+    }
+    if (!active || s == 0.f) doubt = 0;
+    if (__any_sync(0xffffffffu, which || doubt)) {
+        // Rare: borders decided in 64 bits.
+        Exact<TI> e = again;
+        double sum = 0;
+        if (active)
+            for (int j = 0; j < 8; ++j) {
+                const double v = (double)to_f32(e.row[d0 + j]);
+                sum += v * v;
+            }
+        sum = team_sum(sum, team);
+        e.r = 1.0 / sqrt(sum / dim + eps);
+        double top = 0;
+        if (which) {
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) top = fmax(top, fabs(e(d0 + j)));
+        }
+#pragma unroll
+        for (int o = 4; o; o >>= 1)
+            if (o < width) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (which) {
+            scale = quant_scale_code(top);
+            s = quant_scale(scale);
+            doubt = s > 0.f ? 0xffu : 0u;
+            if (s == 0.f) word = 0x88888888u;
+        }
+        for (int j = 0; doubt; ++j, doubt >>= 1) {
+            if (!(doubt & 1)) continue;
+            const double c = fmin(fmax(rint(e(d0 + j) / (double)s), -7.0), 7.0);
+            word = (word & ~(0xfu << (4 * j))) | (uint32_t)((int)c + 8) << (4 * j);
+        }
+        __syncwarp();
+    }
+    if (active) {
+        *reinterpret_cast<uint32_t*>(codes + d0 / 2) = word;
+        if ((u & (width - 1)) == 0) scales[u / width] = (uint8_t)scale;
+    }
+}
+
+template <typename TI, typename TO, int VEC, bool QUANT>
+__global__ void __launch_bounds__(kThreads) bitlin_norm_turn(const NormTurnParams np)
+{
+    constexpr int NU = VEC == 1 ? 4 : 1;  // units of a lane
+    __shared__ float buffer[QUANT ? kThreads / 32 : 1][2][QUANT ? kMaxDim : 1];
+    ptx::griddep_wait();
+    const TurnParams& p = np.t;
+    const int lane = threadIdx.x & 31, u0 = lane & (np.team - 1);
+    const uint32_t idx = (blockIdx.x * (uint32_t)kThreads + threadIdx.x) / (uint32_t)np.team;
+    const int t = (int)min(idx, (uint32_t)(p.tokens - 1));
+    bool active = idx < (uint32_t)p.tokens;
+
+    int kind = 0, group = blockIdx.y;  // q, k or v, and which heads of it
+    if (group >= p.q_groups) {
+        group -= p.q_groups;
+        kind = 1;
+        if (group >= p.kv_groups) {
+            group -= p.kv_groups;
+            kind = 2;
+        }
+    }
+    const int heads = kind == 0 ? p.heads : p.kv_heads;
+    const int h0 = group * kHeadsPerTeam;
+
+    // the token's place in its sequence (all lanes take part in the search)
+    int place = 0, seq = 0;
+    if (p.append) {
+        const uint32_t first = __shfl_sync(0xffffffffu, (uint32_t)t, 0);
+        seq = warp_sequence_of(p.batch, (int)first);
+        while (seq < p.batch.seqs && p.batch.q_offsets[seq + 1] <= t) ++seq;
+        if (seq >= p.batch.seqs) active = false;  // padding
+        else place = p.batch.kv_lens[seq] - (p.batch.q_offsets[seq + 1] - t);
+    }
+
+    // where the row goes
+    TO* dst = nullptr;
+    uint8_t *codes = nullptr, *scales = nullptr;
+    long long dst_head = 0;
+    if (kind == 0) {
+        dst = static_cast<TO*>(p.out) + t * p.out_token;
+        dst_head = p.out_head;
+    } else if (active) {
+        const int at = place / p.page_size;
+        int page = -1;
+        if (place >= 0 && at < p.batch.table_pages) page = p.batch.table[seq * p.batch.table_stride + at];
+        if (page < 0 || page >= p.pages) {
+            *p.index_error = 1;
+            active = false;
+        } else {
+            const long long slot = place - at * p.page_size;
+            dst_head = p.head_stride;
+            if (QUANT) {
+                codes = static_cast<uint8_t*>(p.pool[kind - 1]) + page * p.page_stride + slot * p.slot_stride;
+                scales = np.scales[kind - 1] + page * np.scale_page + slot * np.scale_slot;
+            } else {
+                dst = static_cast<TO*>(p.pool[kind - 1]) + page * p.page_stride + slot * p.slot_stride;
+            }
+        }
+    }
+    if (__ballot_sync(0xffffffffu, active) == 0) return;
+    const TI* src = static_cast<const TI*>(p.src[kind]) + t * p.src_token[kind];
+    const long long src_head = p.src_head[kind];
+    const float* weight = kind == 2 ? nullptr : np.weight[kind];
+    const bool rotating = p.turns != nullptr && kind != 2;
+
+    Unit<VEC> unit[NU];
+    float cs[NU][VEC], sn[NU][VEC], wx[NU][VEC], wy[NU][VEC];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+        const int u = u0 + 32 * i;
+        unit[i] = unit_of<VEC>(u, p.dim, p.rotary, p.adjacent);
+        unit[i].turns = unit[i].turns && rotating;
+        const bool mine = active && unit[i].held;
+        if (mine && unit[i].turns) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int f = pair_of<VEC>(unit[i], u, j, p.adjacent);
+                const int32_t frac = (int32_t)(fraction(p.turns[f], p.pos, p.tokens, t, place) >> 32);
+                if (sizeof(TO) == 2 && !(QUANT && kind == 1)) {
+                    const float angle = (float)frac * 1.4629180792671596e-9f;  // 2^-32 of a turn, in radians
+                    sn[i][j] = __sinf(angle);
+                    cs[i][j] = __cosf(angle);
+                } else {
+                    sincospif((float)frac * 4.656612873077393e-10f /* 2^-31: half turns */, &sn[i][j], &cs[i][j]);
+                }
+            }
+        }
+        if (weight) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                wx[i][j] = mine ? weight[unit[i].lo + j] : 0.f;
+                wy[i][j] = mine && unit[i].has_hi ? weight[unit[i].hi + j] : 0.f;
+            }
+        }
+    }
+
+    Chunk<TI, VEC> a[kHeadsPerTeam][NU] = {}, b[kHeadsPerTeam][NU] = {};
+#pragma unroll
+    for (int h = 0; h < kHeadsPerTeam; ++h) {
+        if (h0 + h < heads && active) {
+            const TI* row = src + (h0 + h) * src_head;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                if (unit[i].held) a[h][i] = *reinterpret_cast<const Chunk<TI, VEC>*>(row + unit[i].lo);
+                if (unit[i].has_hi) b[h][i] = *reinterpret_cast<const Chunk<TI, VEC>*>(row + unit[i].hi);
+            }
+        }
+    }
+    float r[kHeadsPerTeam];
+    if (weight) {
+#pragma unroll
+        for (int h = 0; h < kHeadsPerTeam; ++h) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                float part = 0.f;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float x = to_f32(a[h][i].v[j]), y = to_f32(b[h][i].v[j]);
+                    part += fmaf(x, x, y * y);
+                }
+                sum += part;
+            }
+            r[h] = rsqrtf(team_sum(sum, np.team) / p.dim + (float)np.eps);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < kHeadsPerTeam; ++h) {
+        if (h0 + h >= heads) break;
+        float x[NU][VEC], y[NU][VEC], ex[NU][VEC], ey[NU][VEC];
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                x[i][j] = to_f32(a[h][i].v[j]);
+                y[i][j] = to_f32(b[h][i].v[j]);
+                if (weight) {
+                    x[i][j] *= r[h] * wx[i][j];
+                    y[i][j] *= r[h] * wy[i][j];
+                }
+            }
+            if (QUANT) sizes<VEC>(x[i], y[i], ex[i], ey[i], unit[i].turns, p.adjacent);
+            if (unit[i].turns) rotate<VEC>(x[i], y[i], cs[i], sn[i], p.adjacent);
+        }
+        if (!QUANT || kind == 0) {
+            if (!active) continue;
+            TO* row = dst + (h0 + h) * dst_head;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                Chunk<TO, VEC> c, d;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    c.v[j] = from_f32<TO>(x[i][j]);
+                    d.v[j] = from_f32<TO>(y[i][j]);
+                }
+                if (unit[i].held) *reinterpret_cast<Chunk<TO, VEC>*>(row + unit[i].lo) = c;
+                if (unit[i].has_hi) *reinterpret_cast<Chunk<TO, VEC>*>(row + unit[i].hi) = d;
+            }
+        } else {
+            // through shared memory to 8 consecutive elements a lane
+            const bool exact = !weight && !rotating;
+            float* values = buffer[threadIdx.x >> 5][0] + lane / np.team * p.dim;
+            float* errors = buffer[threadIdx.x >> 5][1] + lane / np.team * p.dim;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                if (!unit[i].held) continue;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    values[unit[i].lo + j] = x[i][j];
+                    errors[unit[i].lo + j] = ex[i][j];
+                    if (unit[i].has_hi) {
+                        values[unit[i].hi + j] = y[i][j];
+                        errors[unit[i].hi + j] = ey[i][j];
+                    }
+                }
+            }
+            __syncwarp();
+            const bool mine = active && u0 < p.dim / 8;
+            float v[8], e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = mine ? values[8 * u0 + j] : 0.f;
+                e[j] = mine && !exact ? kRowError * errors[8 * u0 + j] : 0.f;
+                if (v[j] != v[j]) v[j] = 0.f;
+            }
+            __syncwarp();
+            const Exact<TI> again = {src + (h0 + h) * src_head, weight, rotating ? p.turns : nullptr, p.pos, 0.0,
+                                     p.tokens, t, place, p.rotary, p.adjacent};
+            store_codes<TI>(v, e, exact, mine, u0, p.dim, np.team, again, np.eps, codes + (h0 + h) * dst_head,
+                            scales + (h0 + h) * np.scale_head);
+        }
+    }
+}
+
+// ---- the gradient -------------------------------------------------------------
+
+template <typename TY, typename TX, int VEC>
+__global__ void __launch_bounds__(kThreads) bitlin_norm_grad(const NormGradParams p)
+{
+    constexpr int NU = VEC == 1 ? 4 : 1;
+    constexpr int kHeads = 2;
+    __shared__ float sums[kThreads / 8][kMaxDim];  // a row for each team
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31, u0 = lane & (p.team - 1);
+    const int teams = kThreads / p.team, me = threadIdx.x / p.team;
+    const int groups = (p.heads + kHeads - 1) / kHeads;
+    const long long items = (long long)p.tokens * groups;
+
+    Unit<VEC> unit[NU];
+    float wx[NU][VEC], wy[NU][VEC], dwx[NU][VEC] = {}, dwy[NU][VEC] = {};
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+        unit[i] = unit_of<VEC>(u0 + 32 * i, p.dim, p.rotary, p.adjacent);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            wx[i][j] = unit[i].held ? p.weight[unit[i].lo + j] : 0.f;
+            wy[i][j] = unit[i].has_hi ? p.weight[unit[i].hi + j] : 0.f;
+        }
+    }
+    for (long long base = (long long)blockIdx.x * teams; base < items; base += (long long)gridDim.x * teams) {
+        const bool active = base + me < items;
+        const long long item = active ? base + me : items - 1;
+        const int t = (int)(item / groups), h0 = (int)(item - (long long)t * groups) * kHeads;
+        Chunk<TX, VEC> a[kHeads][NU] = {}, b[kHeads][NU] = {};
+        Chunk<TY, VEC> ga[kHeads][NU] = {}, gb[kHeads][NU] = {};
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+            if (h0 + h >= p.heads || !active) continue;
+            const TX* x = static_cast<const TX*>(p.x) + t * p.x_token + (h0 + h) * p.x_head;
+            const TY* dy = static_cast<const TY*>(p.dy) + t * p.dy_token + (h0 + h) * p.dy_head;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                if (unit[i].held) {
+                    a[h][i] = *reinterpret_cast<const Chunk<TX, VEC>*>(x + unit[i].lo);
+                    ga[h][i] = *reinterpret_cast<const Chunk<TY, VEC>*>(dy + unit[i].lo);
+                }
+                if (unit[i].has_hi) {
+                    b[h][i] = *reinterpret_cast<const Chunk<TX, VEC>*>(x + unit[i].hi);
+                    gb[h][i] = *reinterpret_cast<const Chunk<TY, VEC>*>(dy + unit[i].hi);
+                }
+            }
+        }
+        float cs[NU][VEC], sn[NU][VEC];
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            if (!unit[i].held || !unit[i].turns) continue;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int f = pair_of<VEC>(unit[i], u0 + 32 * i, j, p.adjacent);
+                const int32_t frac = (int32_t)(fraction(p.turns[f], p.pos, p.tokens, t, 0) >> 32);
+                sincospif((float)frac * 4.656612873077393e-10f, &sn[i][j], &cs[i][j]);
+                sn[i][j] = -sn[i][j];  // back
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+            float gx[NU][VEC], gy[NU][VEC];
+            float squares = 0.f, products = 0.f;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    gx[i][j] = to_f32(ga[h][i].v[j]);
+                    gy[i][j] = to_f32(gb[h][i].v[j]);
+                }
+                if (unit[i].held && unit[i].turns) rotate<VEC>(gx[i], gy[i], cs[i], sn[i], p.adjacent);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float x = to_f32(a[h][i].v[j]), y = to_f32(b[h][i].v[j]);
+                    squares += fmaf(x, x, y * y);
+                    products += fmaf(gx[i][j] * wx[i][j], x, gy[i][j] * wy[i][j] * y);
+                }
+            }
+            squares = team_sum(squares, p.team);
+            products = team_sum(products, p.team);
+            const float r = rsqrtf(squares / p.dim + (float)p.eps);
+            const float mean = products * r / p.dim * r;  // mean(h n) r: n = x r
+            if (h0 + h >= p.heads || !active) continue;
+            TX* dx = static_cast<TX*>(p.dx) + t * p.dx_token + (h0 + h) * p.dx_head;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                Chunk<TX, VEC> c, d;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float x = to_f32(a[h][i].v[j]), y = to_f32(b[h][i].v[j]);
+                    dwx[i][j] = fmaf(gx[i][j], x * r, dwx[i][j]);
+                    dwy[i][j] = fmaf(gy[i][j], y * r, dwy[i][j]);
+                    c.v[j] = from_f32<TX>(r * (gx[i][j] * wx[i][j] - x * mean));
+                    d.v[j] = from_f32<TX>(r * (gy[i][j] * wy[i][j] - y * mean));
+                }
+                if (unit[i].held) *reinterpret_cast<Chunk<TX, VEC>*>(dx + unit[i].lo) = c;
+                if (unit[i].has_hi) *reinterpret_cast<Chunk<TX, VEC>*>(dx + unit[i].hi) = d;
+            }
+        }
+    }
+    // the block's sum, teams in their order
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            if (unit[i].held) sums[me][unit[i].lo + j] = dwx[i][j];
+            if (unit[i].has_hi) sums[me][unit[i].hi + j] = dwy[i][j];
+        }
+    __syncthreads();
+    for (int d = threadIdx.x; d < p.dim; d += kThreads) {
+        float sum = 0.f;
+        for (int k = 0; k < teams; ++k) sum += sums[k][d];
+        p.partial[(long long)blockIdx.x * p.dim + d] = sum;
+    }
+}
+
+// The blocks' sums joined in a fixed order: 32 elements to a block, 32 rows at a time.
+__global__ void __launch_bounds__(1024) bitlin_norm_grad_join(const float* partial, float* dweight, int blocks, int dim)
+{
+    __shared__ float sums[32][33];
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
+    float sum = 0.f;
+    if (d < dim)
+        for (int k = row; k < blocks; k += 32) sum += partial[(long long)k * dim + d];
+    sums[row][lane] = sum;
+    __syncthreads();
+    if (row == 0 && d < dim) {
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) sum += sums[k][lane];
+        dweight[d] = sum;
+    }
+}
+
+// ---- launches -------------------------------------------------------------------
+
+cudaLaunchConfig_t config(dim3 grid, int threads, cudaStream_t s, cudaLaunchAttribute* attr)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// Lanes to a row of `dim` elements: a power of two of them, eight elements each.
+int team_of(int dim, int vec)
+{
+    if (vec == 1) return 32;
+    int team = 8;
+    while (team * 8 < dim) team *= 2;
+    return team;
+}
+
+template <typename TI, typename TO, int VEC, bool QUANT>
+cudaError_t launch(NormTurnParams& p, cudaStream_t s)
+{
+    p.team = team_of(p.t.dim, VEC);
+    p.t.q_groups = (p.t.heads + kHeadsPerTeam - 1) / kHeadsPerTeam;
+    p.t.kv_groups = p.t.append ? (p.t.kv_heads + kHeadsPerTeam - 1) / kHeadsPerTeam : 0;
+    const uint64_t threads = (uint64_t)p.t.tokens * p.team;
+    cudaLaunchAttribute attr = {};
+    const cudaLaunchConfig_t cfg =
+        config(dim3((unsigned)((threads + kThreads - 1) / kThreads), p.t.q_groups + 2 * p.t.kv_groups), kThreads, s, &attr);
+    return cudaLaunchKernelEx(&cfg, bitlin_norm_turn<TI, TO, VEC, QUANT>, p);
+}
+
+// Whether rows of this tensor can be read or written four elements at a time.
+bool chunked(const void* data, long long token, long long head, int size)
+{
+    return reinterpret_cast<uintptr_t>(data) % (uintptr_t)(size * 4) == 0 && token % 4 == 0 && head % 4 == 0;
+}
+
+template <typename TI, typename TO, bool QUANT>
+cudaError_t pick(const NormTurnParams& np, cudaStream_t s)
+{
+    NormTurnParams p = np;
+    const TurnParams& t = p.t;
+    bool wide = t.rotary % 8 == 0 && (t.dim - t.rotary) % 8 == 0;
+    if (t.heads)
+        wide = wide && chunked(t.src[0], t.src_token[0], t.src_head[0], sizeof(TI)) && chunked(t.out, t.out_token, t.out_head, sizeof(TO));
+    if (t.append)
+        for (int i = 1; i < 3; ++i) wide = wide && chunked(t.src[i], t.src_token[i], t.src_head[i], sizeof(TI));
+    return wide ? launch<TI, TO, 4, QUANT>(p, s) : launch<TI, TO, 1, QUANT>(p, s);
+}
+
+template <typename TI>
+cudaError_t pick_out(const NormTurnParams& p, int dst_dtype, bool quant, cudaStream_t s)
+{
+    if (quant) return dst_dtype == BITLIN_BF16 ? pick<TI, __nv_bfloat16, true>(p, s) : pick<TI, __half, true>(p, s);
+    switch (dst_dtype) {
+    case BITLIN_F32: return pick<TI, float, false>(p, s);
+    case BITLIN_BF16: return pick<TI, __nv_bfloat16, false>(p, s);
+    default: return pick<TI, __half, false>(p, s);
+    }
+}
+
+template <typename TY, typename TX>
+cudaError_t grad(const NormGradParams& np, cudaStream_t s)
+{
+    NormGradParams p = np;
+    const bool wide = p.rotary % 8 == 0 && (p.dim - p.rotary) % 8 == 0 && chunked(p.dy, p.dy_token, p.dy_head, sizeof(TY)) &&
+                      chunked(p.x, p.x_token, p.x_head, sizeof(TX)) && chunked(p.dx, p.dx_token, p.dx_head, sizeof(TX));
+    p.team = team_of(p.dim, wide ? 4 : 1);
+    p.blocks = bitlin_norm_grad_blocks(p.tokens, p.heads);
+    cudaLaunchAttribute attr = {};
+    cudaLaunchConfig_t cfg = config(dim3(p.blocks), kThreads, s, &attr);
+    cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, bitlin_norm_grad<TY, TX, 4>, p) : cudaLaunchKernelEx(&cfg, bitlin_norm_grad<TY, TX, 1>, p);
+    if (e != cudaSuccess) return e;
+    cfg = config(dim3((p.dim + 31) / 32), 1024, s, &attr);
+    return cudaLaunchKernelEx(&cfg, bitlin_norm_grad_join, (const float*)p.partial, p.dweight, p.blocks, p.dim);
+}
+
+template <typename TY>
+cudaError_t grad_x(const NormGradParams& p, int x_dtype, cudaStream_t s)
+{
+    switch (x_dtype) {
+    case BITLIN_F32: return grad<TY, float>(p, s);
+    case BITLIN_BF16: return grad<TY, __nv_bfloat16>(p, s);
+    default: return grad<TY, __half>(p, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t bitlin_launch_norm_turn(const NormTurnParams& p, int src_dtype, int dst_dtype, bool quant, cudaStream_t s)
+{
+    switch (src_dtype) {
+    case BITLIN_F32: return pick_out<float>(p, dst_dtype, quant, s);
+    case BITLIN_BF16: return pick_out<__nv_bfloat16>(p, dst_dtype, quant, s);
+    default: return pick_out<__half>(p, dst_dtype, quant, s);
+    }
+}
+
+int bitlin_norm_grad_blocks(int tokens, int heads)
+{
+    // eight blocks to each of the 152 SMs, or as many as there are tokens and pairs of heads for
+    const long long items = (long long)tokens * ((heads + 1) / 2);
+    const long long blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
+    return (int)(blocks < 1216 ? blocks : 1216);
+}
+
+cudaError_t bitlin_launch_norm_grad(const NormGradParams& p, int dy_dtype, int x_dtype, cudaStream_t s)
+{
+    switch (dy_dtype) {
+    case BITLIN_F32: return grad_x<float>(p, x_dtype, s);
+    case BITLIN_BF16: return grad_x<__nv_bfloat16>(p, x_dtype, s);
+    default: return grad_x<__half>(p, x_dtype, s);
+    }
+}

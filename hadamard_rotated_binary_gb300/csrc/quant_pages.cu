@@ -1,0 +1,152 @@
+// Rows of a 4-bit cache read back, and its pages as 16-bit ones.
+//
+// A value is (nibble - 8) * scale, exact in every output type (see quant.cuh).
+// Bound: HBM, the writes of the 16-bit values above all.  A thread takes 8
+// elements (a 32-bit word) of one head; a warp's words are consecutive.
+#include "kv_internal.cuh"
+#include "ptx.cuh"
+#include "quant.cuh"
+
+using namespace bitlin_impl;
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kHeadsPerThread = 4;
+
+template <typename T>
+__device__ __forceinline__ void store8(T* dst, uint32_t word, uint32_t scale_byte, bool wide)
+{
+    const float s = quant_scale(scale_byte);
+    T v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = from_f32<T>((float)((int)(word >> (4 * j) & 15) - 8) * s);
+    if (wide) {
+#pragma unroll
+        for (int j = 0; j < (int)sizeof(T) / 2; ++j) reinterpret_cast<uint4*>(dst)[j] = reinterpret_cast<const uint4*>(v)[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dst[j] = v[j];
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) bitlin_quant_read(const QuantReadParams p, int wide)
+{
+    ptx::griddep_wait();
+    const int units = p.pool.dim / 8;
+    const uint32_t idx = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
+    const uint32_t token = idx / (uint32_t)units;
+    const int u = (int)(idx - token * (uint32_t)units);
+    const int t = (int)min(token, (uint32_t)(p.tokens - 1));
+    const int warp_first = (int)min((idx - (threadIdx.x & 31)) / (uint32_t)units, (uint32_t)(p.tokens - 1));
+    int seq = warp_sequence_of(p.batch, warp_first);
+    while (seq < p.batch.seqs && p.batch.q_offsets[seq + 1] <= t) ++seq;
+    if (token >= (uint32_t)p.tokens || seq >= p.batch.seqs) return;
+    const int place = p.batch.kv_lens[seq] - (p.batch.q_offsets[seq + 1] - t);
+    const int at = place / p.pool.page_size;
+    int page = -1;
+    if (place >= 0 && at < p.batch.table_pages) page = p.batch.table[seq * p.batch.table_stride + at];
+    const int groups = (p.pool.kv_heads + kHeadsPerThread - 1) / kHeadsPerThread;
+    const int kind = blockIdx.y >= groups, h0 = (blockIdx.y - kind * groups) * kHeadsPerThread;
+    const bool inside = page >= 0 && page < p.pool.pages;
+    if (!inside) *p.index_error = 1;
+    const long long slot = place - (long long)at * p.pool.page_size;
+    const uint8_t* codes = p.pool.codes[kind] + page * p.pool.page_stride + slot * p.pool.slot_stride + 4 * u;
+    const uint8_t* scales = p.pool.scales[kind] + page * p.pool.scale_page + slot * p.pool.scale_slot + 8 * u / (p.pool.dim / 4);
+    T* out = static_cast<T*>(p.out[kind]) + t * p.out_token[kind] + 8 * u;
+    uint32_t word[kHeadsPerThread], scale[kHeadsPerThread];
+#pragma unroll
+    for (int i = 0; i < kHeadsPerThread; ++i) {
+        word[i] = scale[i] = 0;
+        if (inside && h0 + i < p.pool.kv_heads) {
+            word[i] = *reinterpret_cast<const uint32_t*>(codes + (h0 + i) * p.pool.head_stride);
+            scale[i] = scales[(h0 + i) * p.pool.scale_head];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kHeadsPerThread; ++i)
+        if (h0 + i < p.pool.kv_heads) store8<T>(out + (h0 + i) * p.out_head[kind], word[i], scale[i], wide);
+}
+
+// Block (x, s): every gridDim.x-th page of sequence s.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) bitlin_quant_unpack(const QuantUnpackParams p)
+{
+    ptx::griddep_wait();
+    const int seq = blockIdx.y;
+    if (p.batch.q_offsets[seq + 1] <= p.batch.q_offsets[seq]) return;  // nothing asks for it
+    const int units = p.pool.dim / 8;
+    const int len = min(max(p.batch.kv_lens[seq], 0), 1 << 30);
+    const int want = (int)(((long long)len + p.pool.page_size - 1) / p.pool.page_size);
+    const int pages = min(want, p.batch.table_pages);
+    if (pages < want) *p.index_error = 1;
+    for (int at = blockIdx.x; at < pages; at += gridDim.x) {
+        const int page = p.batch.table[seq * p.batch.table_stride + at];
+        if (page < 0 || page >= p.pool.pages) {  // attention reads it as zeros
+            *p.index_error = 1;
+            continue;
+        }
+        const int slots = min(p.pool.page_size, len - at * p.pool.page_size);
+        const int words = slots * units;
+        for (int head = 0; head < p.pool.kv_heads; ++head) {
+            for (int i = threadIdx.x; i < 2 * words; i += kThreads) {
+                const int kind = i >= words, slot = (i - kind * words) / units, u = i - kind * words - slot * units;
+                const uint32_t word = *reinterpret_cast<const uint32_t*>(
+                    p.pool.codes[kind] + page * p.pool.page_stride + slot * p.pool.slot_stride + head * p.pool.head_stride + 4 * u);
+                const uint32_t scale =
+                    p.pool.scales[kind][page * p.pool.scale_page + slot * p.pool.scale_slot + head * p.pool.scale_head + 8 * u / (p.pool.dim / 4)];
+                T* out = static_cast<T*>(p.out[kind]) + page * p.page_stride + slot * p.slot_stride + head * p.head_stride + 8 * u;
+                store8<T>(out, word, scale, true);
+            }
+        }
+    }
+}
+
+cudaLaunchConfig_t config(dim3 grid, cudaStream_t s, cudaLaunchAttribute* attr)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <typename T>
+cudaError_t read(const QuantReadParams& p, cudaStream_t s)
+{
+    bool wide = true;
+    for (int i = 0; i < 2; ++i) {
+        const int n = 16 / sizeof(T);
+        wide = wide && reinterpret_cast<uintptr_t>(p.out[i]) % 16 == 0 && p.out_token[i] % n == 0 && p.out_head[i] % n == 0;
+    }
+    const uint64_t threads = (uint64_t)p.tokens * (p.pool.dim / 8);
+    const int groups = (p.pool.kv_heads + kHeadsPerThread - 1) / kHeadsPerThread;
+    cudaLaunchAttribute attr = {};
+    const cudaLaunchConfig_t cfg = config(dim3((unsigned)((threads + kThreads - 1) / kThreads), 2 * groups), s, &attr);
+    return cudaLaunchKernelEx(&cfg, bitlin_quant_read<T>, p, (int)wide);
+}
+
+}  // namespace
+
+cudaError_t bitlin_launch_quant_read(const QuantReadParams& p, int dst_dtype, cudaStream_t s)
+{
+    switch (dst_dtype) {
+    case BITLIN_F32: return read<float>(p, s);
+    case BITLIN_BF16: return read<__nv_bfloat16>(p, s);
+    default: return read<__half>(p, s);
+    }
+}
+
+cudaError_t bitlin_launch_quant_unpack(const QuantUnpackParams& p, int dst_dtype, int num_sms, cudaStream_t s)
+{
+    const int want = (8 * num_sms + p.batch.seqs - 1) / p.batch.seqs;
+    cudaLaunchAttribute attr = {};
+    const cudaLaunchConfig_t cfg = config(dim3(want < p.batch.table_pages ? want : p.batch.table_pages, p.batch.seqs), s, &attr);
+    return dst_dtype == BITLIN_BF16 ? cudaLaunchKernelEx(&cfg, bitlin_quant_unpack<__nv_bfloat16>, p)
+                                    : cudaLaunchKernelEx(&cfg, bitlin_quant_unpack<__half>, p);
+}

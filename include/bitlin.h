@@ -406,6 +406,49 @@ bitlin_status bitlin_rope_create(bitlin_rope_t* out, int rotary_dim, int axes, c
 bitlin_status bitlin_rope_apply(bitlin_rope_t r, const bitlin_rows* x, int tokens, int heads, int head_dim,
                                 const int32_t* pos, const bitlin_rows* out, int inverse, bitlin_stream_t stream);
 
+/*
+ * As bitlin_rope_apply (forward), after a norm of each head:
+ *     n = x / sqrt(mean(x^2) + eps) * weight,  out = n rotated,
+ * in one pass: the norms of queries and keys that stand between a projection
+ * and the rotation.
+ *
+ *   weight  device pointer, float [head_dim].
+ *   eps     finite, >= 0.  A head of zeros with eps = 0 comes out as NaN.
+ *
+ * out is good to 2e-6 (an f32 out) or 3.4e-6 (a 16-bit one, before its own
+ * rounding) of its pair's norm (of the element itself past rotary_dim); each
+ * output is rounded once to its type.  Requires head_dim <= 256.  out
+ * may be x itself.  Otherwise as bitlin_rope_apply.
+ */
+bitlin_status bitlin_rope_apply_normed(bitlin_rope_t r, const bitlin_rows* x, int tokens, int heads, int head_dim,
+                                       const int32_t* pos, const float* weight, double eps, const bitlin_rows* out,
+                                       bitlin_stream_t stream);
+
+/* Bytes of scratch that bitlin_rope_gradient needs for these sizes (0 for sizes it refuses). */
+size_t bitlin_rope_gradient_scratch(int tokens, int heads, int head_dim);
+
+/*
+ * The gradient of bitlin_rope_apply_normed: from dy, that of its output, to
+ * dx, that of x, and dweight, the weight's, summed over tokens and heads.
+ *
+ *   dy       any of the three types, any strides.
+ *   x        the forward call's input; dx in x's type, any strides.  dx may be
+ *            x or dy itself (same data, type and strides), else it overlaps
+ *            neither.
+ *   dweight  device pointer, float [head_dim]; overwritten.  tokens = 0 sets
+ *            it to zero.
+ *   scratch  device pointer, bitlin_rope_gradient_scratch bytes, float
+ *            aligned; in use until the call's work is done.
+ *
+ * Sums are held in f32 and joined in a fixed order: the same call gives the
+ * same bits.  Asynchronous.  Errors: as bitlin_rope_apply_normed, and
+ * BITLIN_ESCRATCH (NULL or too small).
+ */
+bitlin_status bitlin_rope_gradient(bitlin_rope_t r, const bitlin_rows* dy, const bitlin_rows* x, int tokens, int heads,
+                                   int head_dim, const int32_t* pos, const float* weight, double eps,
+                                   const bitlin_rows* dx, float* dweight, float* scratch, size_t scratch_bytes,
+                                   bitlin_stream_t stream);
+
 /* The cudaError_t value behind the last BITLIN_ECUDA of this handle (0 if none). */
 int bitlin_rope_cuda_error(bitlin_rope_t r);
 
@@ -474,6 +517,21 @@ bitlin_status bitlin_kv_append(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
                                const int32_t* pos, const bitlin_rows* k, const bitlin_rows* v,
                                const bitlin_rows* q, int heads, const bitlin_rows* q_out, bitlin_stream_t stream);
 
+/* Norms of each head before its rotation (see bitlin_rope_apply_normed): device
+ * pointers, float [head_dim]; NULL: none. */
+typedef struct {
+    const float* q;
+    const float* k;
+    double eps;
+} bitlin_head_norms;
+
+/* bitlin_kv_append with norms of k and q before their rotation (norms NULL, or
+ * without weights: none).  A norm without a rope is allowed. */
+bitlin_status bitlin_kv_append_normed(bitlin_kv_t kv, const bitlin_kv_batch* batch, int tokens, bitlin_rope_t rope,
+                                      const int32_t* pos, const bitlin_rows* k, const bitlin_rows* v,
+                                      const bitlin_rows* q, int heads, const bitlin_rows* q_out,
+                                      const bitlin_head_norms* norms, bitlin_stream_t stream);
+
 /*
  * Attention of the batch's new tokens over their sequences in the cache:
  *     s_j = scale * (q . k_j),  out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),
@@ -532,6 +590,109 @@ int bitlin_kv_cuda_error(bitlin_kv_t kv);
 /* Release the handle's own memory (not the pools).  NULL is accepted.
  * Synchronizes the device. */
 bitlin_status bitlin_kv_destroy(bitlin_kv_t kv);
+
+/* ------------------------------------------------------------------------
+ * The cache in 4 bits.  A head's elements are four groups of head_dim / 4 with
+ * a scale each: 4 bits an element and a byte a group, 4.125 to 4.5 bits an
+ * element together.
+ *
+ * Scales: 5 bits of exponent, 3 of significand (byte << 7 is the scale as a
+ * float16), at most 60 (byte 167).  A group's is its largest magnitude / 7
+ * rounded to the nearest scale, ties to even; so groups whose magnitudes are
+ * all below 2.7e-5 are stored as zeros, and elements beyond 420 saturate.
+ * Elements: clamp(round(x / scale), -7, 7) + 8, ties to even; element 2i of a
+ * head in the low and 2i + 1 in the high half of its byte i.  What is read
+ * back, and what attention reads, is (nibble - 8) * scale, which bf16 and f16
+ * hold exactly.  An infinity is stored as the largest value, a NaN as zero.
+ * ------------------------------------------------------------------------ */
+
+/* Opaque handle on one layer's paged cache in 4 bits (the pools stay the caller's). */
+typedef struct bitlin_kvq* bitlin_kvq_t;
+
+/* Its pools: byte i of head h of slot s of page g is
+ * k[g * page_stride + s * slot_stride + h * head_stride + i], i < head_dim / 2,
+ * for v alike; group j's scale is k_scale[g * scale_page_stride +
+ * s * scale_slot_stride + h * scale_head_stride + j], j < 4.  Strides in bytes. */
+typedef struct {
+    void *k, *v;             /* 16-byte aligned */
+    void *k_scale, *v_scale; /* 4-byte aligned */
+    int pages, page_size;    /* page_size 1 .. 65536 */
+    int kv_heads, head_dim;  /* 1 .. 4096; 64, 128 or 256 */
+    long long page_stride, slot_stride, head_stride;                   /* positive multiples of 16 */
+    long long scale_page_stride, scale_slot_stride, scale_head_stride; /* positive multiples of 4 */
+} bitlin_kvq_pools;
+
+/*
+ * A handle on a 4-bit cache in the caller's memory.  The slots of a head side
+ * by side (slot_stride = head_dim / 2, scale_slot_stride = 4) are read fastest.
+ *
+ *   dtype  BITLIN_BF16 or BITLIN_F16: of the queries, of a 16-bit attention
+ *          output and of what the append makes of q.
+ *
+ * Allocates the workspace of bitlin_kvq_attend (see bitlin_kvq_share).
+ * Synchronous.  Errors: BITLIN_EINVAL, BITLIN_ENOMEM, BITLIN_ECUDA,
+ * BITLIN_EDEVICE.  On error *out is set to NULL.
+ */
+bitlin_status bitlin_kvq_create(bitlin_kvq_t* out, const bitlin_kvq_pools* pools, int dtype);
+
+/* As bitlin_kv_share, between 4-bit caches.  The calls of all handles that
+ * share a workspace must follow one another in stream order. */
+bitlin_status bitlin_kvq_share(bitlin_kvq_t kvq, bitlin_kvq_t with);
+
+/*
+ * As bitlin_kv_append_normed: k (normed and rotated) and v go to their places
+ * in 4 bits, q to q_out in the handle's type.  A code is that of the exact
+ * real-valued row, whatever the order of the kernel's sums: where 32 bits do
+ * not tell on which side of a border a value lies, 64 decide.
+ */
+bitlin_status bitlin_kvq_append(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, int tokens, bitlin_rope_t rope,
+                                const int32_t* pos, const bitlin_rows* k, const bitlin_rows* v,
+                                const bitlin_rows* q, int heads, const bitlin_rows* q_out,
+                                const bitlin_head_norms* norms, bitlin_stream_t stream);
+
+/*
+ * Read rows back: row i of k and v, [tokens][kv_heads][head_dim], becomes what
+ * the cache holds at the row's place (see bitlin_kv_batch): the rows of the
+ * append that took the same batch, or, with q_offsets that count all tokens
+ * of the sequences, whole sequences.
+ *
+ *   k, v  one type for both (any of the three), any strides.
+ *
+ * Rows past q_offsets[seqs] are left alone.  A row without a place in the
+ * pool reads as zeros and makes the next bitlin_kvq_get_error return
+ * BITLIN_EINDEX.  Asynchronous; allocates nothing.  Errors: BITLIN_EINVAL,
+ * BITLIN_ECUDA.
+ */
+bitlin_status bitlin_kvq_read(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* k,
+                              const bitlin_rows* v, bitlin_stream_t stream);
+
+/*
+ * As bitlin_kv_attend, over a 4-bit cache.
+ *
+ *   through  NULL, or a 16-bit cache of the handle's type and of the same
+ *            pages, page_size, kv_heads and head_dim, whose pools are scratch
+ *            (one for all layers of a model will do).  Calls of more tokens
+ *            than sequences then read the sequences' pages back into it and
+ *            attend there.  Without it such calls are right, but slow where
+ *            sequences bring many tokens.
+ *
+ * Calls that share a `through` must follow one another in stream order, as
+ * those that share a workspace must.  Errors: as bitlin_kv_attend; the sticky
+ * error is that of `through`.
+ */
+bitlin_status bitlin_kvq_attend(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q,
+                                int heads, float scale, int causal, const bitlin_rows* out, float* lse,
+                                bitlin_kv_t through, bitlin_stream_t stream);
+
+/* As bitlin_kv_get_error: BITLIN_EINDEX (once, then cleared) or BITLIN_ECUDA.  Synchronizes. */
+bitlin_status bitlin_kvq_get_error(bitlin_kvq_t kvq);
+
+/* The cudaError_t value behind the last BITLIN_ECUDA of this handle (0 if none). */
+int bitlin_kvq_cuda_error(bitlin_kvq_t kvq);
+
+/* Release the handle's own memory (not the pools).  NULL is accepted.
+ * Synchronizes the device. */
+bitlin_status bitlin_kvq_destroy(bitlin_kvq_t kvq);
 
 /* A static, human-readable description of a status value. */
 const char* bitlin_status_string(bitlin_status s);
