@@ -237,7 +237,7 @@ cudaError_t bitlin_launch_quant_read(const bitlin_impl::QuantReadParams& p, int 
 cudaError_t bitlin_launch_quant_unpack(const bitlin_impl::QuantUnpackParams& p, int dst_dtype, int num_sms, cudaStream_t s);
 cudaError_t bitlin_launch_quant_attend(const bitlin_impl::QuantAttendParams& p, int dtype, int out_dtype, int num_sms, cudaStream_t s);
 cudaError_t bitlin_quant_attend_load(int dim, int dtype);
-bitlin_impl::KvWorkspaceParts bitlin_quant_attend_workspace(int dim, int num_sms);
+bitlin_impl::KvWorkspaceParts bitlin_quant_attend_workspace(int num_sms);
 cudaError_t bitlin_launch_turn(const bitlin_impl::TurnParams& p, int src_dtype, int dst_dtype, cudaStream_t s);
 cudaError_t bitlin_launch_attend(const bitlin_impl::AttendParams& p, int dtype, int out_dtype, const void* tmap_q,
                                  const void* tmap_k, const void* tmap_v, int num_sms, cudaStream_t s);

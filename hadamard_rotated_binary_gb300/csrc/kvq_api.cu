@@ -50,7 +50,7 @@ QuantPools pools_of(const bitlin_kvq_pools* p)
 // A workspace for the handle's calls, with zero tickets.
 cudaError_t new_workspace(bitlin_kvq& h)
 {
-    const KvWorkspaceParts parts = bitlin_quant_attend_workspace(h.pool.dim, h.num_sms);
+    const KvWorkspaceParts parts = bitlin_quant_attend_workspace(h.num_sms);
     std::shared_ptr<KvWorkspace> w;
     try {
         w = std::make_shared<KvWorkspace>();
@@ -106,7 +106,6 @@ bitlin_status bitlin_kvq_create(bitlin_kvq_t* out, const bitlin_kvq_pools* pools
 bitlin_status bitlin_kvq_share(bitlin_kvq_t kvq, bitlin_kvq_t with)
 {
     if (!kvq || !with || kvq->device != with->device) return BITLIN_EINVAL;
-    if (with->workspace->bytes < bitlin_quant_attend_workspace(kvq->pool.dim, kvq->num_sms).bytes) return BITLIN_EINVAL;
     // the handle's own workspace may be freed here: not under its calls
     const cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return from_cuda(kvq, e);
@@ -192,7 +191,7 @@ bitlin_status bitlin_kvq_attend(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, 
         if (st == BITLIN_ECUDA || st == BITLIN_ENOMEM) kvq->last_cuda_error = through->last_cuda_error;
         return st;
     }
-    const KvWorkspaceParts parts = bitlin_quant_attend_workspace(kvq->pool.dim, kvq->num_sms);
+    const KvWorkspaceParts parts = bitlin_quant_attend_workspace(kvq->num_sms);
     unsigned char* workspace = kvq->workspace->data;
     QuantAttendParams p = {};
     p.pool = kvq->pool;
