@@ -176,6 +176,9 @@ struct QuantAttendParams {
     int* tickets;
     int* index_error;
     int tokens, heads, group, causal;
+    int bf16;                  // the type of q and of a 16-bit output
+    uint32_t magic;            // two float16 1024s (see quant.cuh)
+    int page_shift;            // log2 of a page size that is a power of two, else -1
     float scale;
 };
 
@@ -235,8 +238,8 @@ int bitlin_norm_grad_blocks(int tokens, int heads);
 cudaError_t bitlin_launch_norm_grad(const bitlin_impl::NormGradParams& p, int dy_dtype, int x_dtype, cudaStream_t s);
 cudaError_t bitlin_launch_quant_read(const bitlin_impl::QuantReadParams& p, int dst_dtype, cudaStream_t s);
 cudaError_t bitlin_launch_quant_unpack(const bitlin_impl::QuantUnpackParams& p, int dst_dtype, int num_sms, cudaStream_t s);
-cudaError_t bitlin_launch_quant_attend(const bitlin_impl::QuantAttendParams& p, int dtype, int out_dtype, int num_sms, cudaStream_t s);
-cudaError_t bitlin_quant_attend_load(int dim, int dtype);
+cudaError_t bitlin_launch_quant_attend(const bitlin_impl::QuantAttendParams& p, int out_dtype, int num_sms, cudaStream_t s);
+cudaError_t bitlin_quant_attend_load(int dim);
 bitlin_impl::KvWorkspaceParts bitlin_quant_attend_workspace(int num_sms);
 cudaError_t bitlin_launch_turn(const bitlin_impl::TurnParams& p, int src_dtype, int dst_dtype, cudaStream_t s);
 cudaError_t bitlin_launch_attend(const bitlin_impl::AttendParams& p, int dtype, int out_dtype, const void* tmap_q,

@@ -90,7 +90,7 @@ bitlin_status bitlin_kvq_create(bitlin_kvq_t* out, const bitlin_kvq_pools* pools
     h->dtype = dtype;
     h->pool = pools_of(pools);
     cudaError_t e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = bitlin_quant_attend_load(h->pool.dim, dtype);
+    if (e == cudaSuccess) e = bitlin_quant_attend_load(h->pool.dim);
     if (e == cudaSuccess) e = cudaMalloc(&h->index_error, sizeof(int));
     if (e == cudaSuccess) e = cudaMemset(h->index_error, 0, sizeof(int));
     if (e == cudaSuccess) e = new_workspace(*h);
@@ -212,7 +212,11 @@ bitlin_status bitlin_kvq_attend(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, 
     p.group = heads / kvq->pool.kv_heads;
     p.causal = causal;
     p.scale = scale;
-    return from_cuda(kvq, bitlin_launch_quant_attend(p, kvq->dtype, out->dtype, kvq->num_sms, s));
+    p.bf16 = kvq->dtype == BITLIN_BF16;
+    p.magic = 0x64006400u;
+    const int size = kvq->pool.page_size;
+    p.page_shift = size & (size - 1) ? -1 : __builtin_ctz((unsigned)size);
+    return from_cuda(kvq, bitlin_launch_quant_attend(p, out->dtype, kvq->num_sms, s));
 }
 
 bitlin_status bitlin_kvq_get_error(bitlin_kvq_t kvq)

@@ -46,14 +46,18 @@ __device__ __forceinline__ QuantScale2 quant_scale2(uint32_t pair_of_bytes)  // 
     q.high_add = __hmul2(s, __float2half2_rn(-72.f));
     return q;
 }
-__device__ __forceinline__ __half2 quant_low(uint32_t word, const QuantScale2& s)
+// `magic` is 0x64006400, two float16 1024s, in a register: masked and joined in one
+// operation (as a constant it would take a second one beside the mask).
+__device__ __forceinline__ __half2 quant_low(uint32_t word, const QuantScale2& s, uint32_t magic)
 {
-    const uint32_t bits = (word & 0x000f000fu) | 0x64006400u;
+    uint32_t bits;
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(bits) : "r"(word), "r"(magic));
     return __hfma2(*reinterpret_cast<const __half2*>(&bits), s.low, s.low_add);
 }
-__device__ __forceinline__ __half2 quant_high(uint32_t word, const QuantScale2& s)
+__device__ __forceinline__ __half2 quant_high(uint32_t word, const QuantScale2& s, uint32_t magic)
 {
-    const uint32_t bits = (word & 0x00f000f0u) | 0x64006400u;
+    uint32_t bits;
+    asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;" : "=r"(bits) : "r"(word), "r"(magic));
     return __hfma2(*reinterpret_cast<const __half2*>(&bits), s.high, s.high_add);
 }
 
