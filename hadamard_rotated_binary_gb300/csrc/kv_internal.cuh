@@ -178,6 +178,10 @@ struct QuantAttendParams {
     int tokens, heads, group, causal;
     int bf16;                  // the type of q and of a 16-bit output
     uint32_t magic;            // two float16 1024s (see quant.cuh)
+    int group_inverse;         // 2^16 / group, rounded up: divides numbers below 256
+    // the pools' strides in units of the largest power of two that divides them
+    uint32_t unit, page_units, slot_units, head_units;
+    uint32_t scale_unit, scale_page_units, scale_slot_units, scale_head_units;
     int page_shift;            // log2 of a page size that is a power of two, else -1
     float scale;
 };
@@ -227,6 +231,7 @@ struct bitlin_kvq {
     int num_sms = 0;
     int dtype = 0;
     bitlin_impl::QuantPools pool = {};
+    uint32_t unit = 0, scale_unit = 0;  // powers of two that divide the pools' strides
     int last_cuda_error = 0;
     int* index_error = nullptr;
     std::shared_ptr<bitlin_impl::KvWorkspace> workspace;

@@ -11,6 +11,21 @@ using namespace bitlin_impl;
 
 namespace {
 
+// The largest power of two that divides three strides.
+uint32_t unit_of(long long page, long long slot, long long head)
+{
+    const long long all = page | slot | head;
+    const long long low = all & -all;
+    return low < (1 << 30) ? (uint32_t)low : 1u << 30;
+}
+
+// Whether every slot lies less than 2^32 units from the first.
+bool reaches(const bitlin_kvq_pools* p, uint32_t unit, long long page, long long slot, long long head)
+{
+    const __int128 last = (__int128)(p->pages - 1) * page + (__int128)(p->page_size - 1) * slot + (__int128)(p->kv_heads - 1) * head;
+    return last / unit < ((__int128)1 << 32);
+}
+
 bool pool_ok(const bitlin_kvq_pools* p)
 {
     if (!p) return false;
@@ -24,7 +39,9 @@ bool pool_ok(const bitlin_kvq_pools* p)
         if (stride < 16 || stride % 16 || stride >= (1LL << 39)) return false;
     for (long long stride : {p->scale_page_stride, p->scale_slot_stride, p->scale_head_stride})
         if (stride < 4 || stride % 4 || stride >= (1LL << 39)) return false;
-    return true;
+    return reaches(p, unit_of(p->page_stride, p->slot_stride, p->head_stride), p->page_stride, p->slot_stride, p->head_stride) &&
+           reaches(p, unit_of(p->scale_page_stride, p->scale_slot_stride, p->scale_head_stride), p->scale_page_stride, p->scale_slot_stride,
+                   p->scale_head_stride);
 }
 
 QuantPools pools_of(const bitlin_kvq_pools* p)
@@ -89,6 +106,8 @@ bitlin_status bitlin_kvq_create(bitlin_kvq_t* out, const bitlin_kvq_pools* pools
     h->device = dev;
     h->dtype = dtype;
     h->pool = pools_of(pools);
+    h->unit = unit_of(pools->page_stride, pools->slot_stride, pools->head_stride);
+    h->scale_unit = unit_of(pools->scale_page_stride, pools->scale_slot_stride, pools->scale_head_stride);
     cudaError_t e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = bitlin_quant_attend_load(h->pool.dim);
     if (e == cudaSuccess) e = cudaMalloc(&h->index_error, sizeof(int));
@@ -214,6 +233,15 @@ bitlin_status bitlin_kvq_attend(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, 
     p.scale = scale;
     p.bf16 = kvq->dtype == BITLIN_BF16;
     p.magic = 0x64006400u;
+    p.group_inverse = (65536 + p.group - 1) / p.group;
+    p.unit = kvq->unit;
+    p.page_units = (uint32_t)(kvq->pool.page_stride / kvq->unit);
+    p.slot_units = (uint32_t)(kvq->pool.slot_stride / kvq->unit);
+    p.head_units = (uint32_t)(kvq->pool.head_stride / kvq->unit);
+    p.scale_unit = kvq->scale_unit;
+    p.scale_page_units = (uint32_t)(kvq->pool.scale_page / kvq->scale_unit);
+    p.scale_slot_units = (uint32_t)(kvq->pool.scale_slot / kvq->scale_unit);
+    p.scale_head_units = (uint32_t)(kvq->pool.scale_head / kvq->scale_unit);
     const int size = kvq->pool.page_size;
     p.page_shift = size & (size - 1) ? -1 : __builtin_ctz((unsigned)size);
     return from_cuda(kvq, bitlin_launch_quant_attend(p, out->dtype, kvq->num_sms, s));

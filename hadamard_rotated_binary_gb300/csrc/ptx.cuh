@@ -263,11 +263,11 @@ __device__ __forceinline__ void prefetch_tmap(const void* tmap)
 }
 
 // ---- asynchronous copies of a thread, matrix products of a warp ---------------
-// `valid` bytes of the 16 (or 4) come from src, zeros for the rest.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int valid)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// `valid` bytes of the 4 come from src, zeros for the rest.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int valid)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid) : "memory");
@@ -282,7 +282,7 @@ __device__ __forceinline__ void cp_async_wait()
 // D += A B, 16 x 8 x 16 in f16 with an f32 D.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));

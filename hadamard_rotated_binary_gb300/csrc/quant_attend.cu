@@ -19,14 +19,14 @@
 // one fused multiply-add makes two values of them.  In P V the inner dimension is
 // the keys: words of two keys are joined halfword by halfword first.
 //
-// Work: an item is (sequence, key head, tile of rows) and costs its steps of keys
-// and one more.  All items lie end to end on one line, which is cut into equal parts,
-// one for each of the CTAs that run at once; so a long context splits over all SMs
-// and ragged batches balance, with no length known on the host.  In a CTA's part of
-// an item the eight warps take tiles of 16 or 32 keys in turn, each with its own ring
-// of copies in flight, maximum, sum and output, and meet only at its end.  A CTA that
+// Work: an item is (sequence, key head, tile of rows) and costs its steps of keys (a
+// tile of 32 for each warp of a CTA) and some more.  All items lie end to end on one
+// line, which is cut into equal parts, one for each of the CTAs that run at once; so a
+// long context splits over all SMs and ragged batches balance, with no length known on
+// the host.  In a CTA's part of an item the warps take tiles in turn, each with its own
+// ring of copies in flight, maximum, sum and output, and meet only at its end.  A CTA that
 // has only a part of an item leaves its unnormalised output with the rows' references
-// and sums in the workspace; the last of the item's CTAs to do so joins the parts
+// and sums in the workspace; the last of the item's CTAs to be through joins the parts
 // in their order (results do not depend on which one is last).
 //
 // Weights are relative to 2^7 of the running reference, which follows a row's
@@ -44,43 +44,44 @@ using namespace bitlin_impl;
 namespace {
 
 constexpr int kMaxLen = 1 << 30;
-constexpr int kItemExtra = 1;     // steps that an item's begin and end cost
+constexpr int KT = 32;            // keys of a tile
 constexpr float kShift = 7.f;     // log2 of the largest weight when its reference is set
 constexpr float kLazy = 8.f;      // log2 of the growth that another reference waits for
-constexpr int kSlotFloats = 4096; // of a part's output in the workspace: rows x dim
-constexpr int kSlotRows = 64;
-constexpr int kJoin = 8;          // groups of parts come in multiples of this many
-constexpr int kBatch = 4;         // parts in flight while they are joined
 
 template <int D, int NT>
 struct Cfg {
-    // Warps of a CTA, so that two CTAs on an SM leave a thread the registers it needs.
-    static constexpr int kWarps = D == 64 ? 8 : D == 256 && NT == 2 ? 8 : 6;
+    // Warps of a CTA and CTAs on an SM, so that a thread has the registers it needs.
+    static constexpr int kWarps = D == 256 && NT == 1 ? 6 : 8;
+    static constexpr int kBlocks = D == 256 && NT == 2 ? 1 : 2;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int KT = 32;                          // keys of a warp's tile
-    static constexpr int kStep = kWarps * KT;              // keys of a CTA's step
     static constexpr int kRows = 8 * NT;
     static constexpr int kRow = D / 2;                     // bytes of a head's codes
     static constexpr int kCodes = KT * kRow;
     static constexpr int kSlot = kCodes + KT * 4;          // a tile's K or V, and its scales
-    static constexpr int kLead = D == 256 ? 1 : 2;         // tiles that copies run ahead
+    static constexpr int kLead = D == 256 || (D == 128 && NT == 2) ? 1 : 2;  // tiles that copies run ahead
     static constexpr int kSlots = 2 * kLead + 1;
-    static constexpr int kRing = kWarps * kSlots * kSlot;
+    static constexpr int kRing = kSlots * kSlot;
     static constexpr int kQ = NT * (D / 32) * 512;
-    static constexpr int kMerge = kWarps * 8 * D * 4;      // eight rows of every warp, over the ring
-    static constexpr int kBytes = (kRing > kMerge ? kRing : kMerge) + kQ;
-    static constexpr int kBlocks = D == 256 && NT == 2 ? 1 : 2;  // CTAs on an SM
-    static_assert(kRows * D <= kSlotFloats && kRows <= kSlotRows, "workspace");
+    static constexpr int kStep = kWarps * KT;              // keys of a step
+    // Steps that an item's begin and end cost.  Measured, in us, 64 tokens over 100-8,000 keys, at 1/2/3:
+    // 256 dims 69.0/69.4/70.6, 128 dims 81.0/73.7/74.7, 64 dims 62.1/54.6/52.0.
+    static constexpr int kExtra = D == 256 ? 1 : D == 128 ? 2 : 3;
+    // Eight rows of every warp, over the rings: float2s, with a gap after each lane's dimensions and rows
+    // so far apart that the stores of 16 lanes (4 lanes' dimensions of 4 rows) meet no bank twice.
+    static constexpr int kMergeRow = D / 2 + 8 + 10;
+    static constexpr int kMerge = kWarps * 8 * kMergeRow * 8;
+    static constexpr int kBytes = (kWarps * kRing > kMerge ? kWarps * kRing : kMerge) + kQ;
+    static constexpr int kPart = kRows * D;                // floats of a part's output in the workspace
 };
 
 struct Seq {
     int row0, tokens;  // its token rows
     int place0;        // place of the first
     int len;           // keys held
-    int tiles, steps;  // row tiles, steps of keys
+    int tiles, steps;  // tiles of rows, steps of keys
 };
 
-template <int STEP, int ROWS>
+template <class C>
 __device__ __forceinline__ Seq load_seq(const QuantAttendParams& p, int s)
 {
     Seq q;
@@ -92,66 +93,131 @@ __device__ __forceinline__ Seq load_seq(const QuantAttendParams& p, int s)
     q.place0 = raw - (min(max(hi, 0), kMaxLen) - q.row0);
     q.len = raw < cap ? raw : (int)cap;
     if (q.len < raw && q.tokens) *p.index_error = 1;
-    q.tiles = (int)(((long long)q.tokens * p.group + ROWS - 1) / ROWS);
-    q.steps = max(1, (q.len + STEP - 1) / STEP);
+    q.tiles = (int)(((long long)q.tokens * p.group + C::kRows - 1) / C::kRows);
+    q.steps = max(1, (q.len + C::kStep - 1) / C::kStep);
     return q;
 }
 
-// Where this CTA's part of the line begins and how long it is.
-struct Start {
-    long long per;    // length of a part; the first `extra` CTAs have one more
-    long long extra;
-    long long begin, length;
-    long long skip;   // from the beginning of sequence `seq` to the part
-    int seq;
+// What a CTA has of the line, and the item that it works on; in shared memory, so that
+// the loop over the keys does not hold it in registers.
+struct Work {
+    long long per, extra;  // length of a CTA's part; the first `extra` CTAs have one more
+    long long left;        // of this CTA's part
+    long long line;        // where the item begins on the line
+    Seq w;
+    int seq, item, cost, from, to;
+    int head, row0, rows;
+    int j0, j1;            // steps of the part
+    int end, lim_first;    // keys that the item's last row sees, and its first
+    bool some, whole;      // whether there is a part, and whether it is all of the item
 };
 
-__device__ __forceinline__ int cta_of(const Start& s, long long x)
+// x / n for n > 0; the sizes at hand nearly always fit 32 bits.
+__device__ __forceinline__ long long divide(long long x, long long n)
 {
-    const long long longer = s.extra * (s.per + 1);
-    return (int)(x < longer ? x / (s.per + 1) : s.extra + (x - longer) / s.per);
+    return ((x | n) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)n) : x / n;
 }
 
-// One warp.
-template <int STEP, int ROWS>
-__device__ void locate(const QuantAttendParams& p, Start* out)
+// The CTA whose part of the line holds x.
+__device__ __forceinline__ int cta_of(const Work& s, long long x)
 {
-    const int lane = threadIdx.x & 31, grid = (int)gridDim.x, me = (int)blockIdx.x;
-    auto cost = [&](int s) -> long long {
-        if (s >= p.batch.seqs) return 0;
-        const Seq q = load_seq<STEP, ROWS>(p, s);
-        return (long long)q.tiles * p.pool.kv_heads * (q.steps + kItemExtra);
-    };
-    long long total = 0;
-    for (int base = 0; base < p.batch.seqs; base += 32) total += cost(base + lane);
+    const long long longer = s.extra * (s.per + 1);
+    return (int)(x < longer ? divide(x, s.per + 1) : s.extra + divide(x - longer, s.per));
+}
+
+// Keys that a row of the item sees.
+__device__ __forceinline__ int limit(const QuantAttendParams& p, const Work& k, int row)
+{
+    return p.causal ? min(max(k.w.place0 + (k.row0 + row) / p.group + 1, 0), k.w.len) : k.w.len;
+}
+
+// Cost of all items of a sequence (0 past the last one).
+template <class C>
+__device__ __forceinline__ long long seq_cost(const QuantAttendParams& p, int s)
+{
+    if (s >= p.batch.seqs) return 0;
+    const Seq q = load_seq<C>(p, s);
+    return (long long)q.tiles * p.pool.kv_heads * (q.steps + C::kExtra);
+}
+
+// One warp: where this CTA's part of the line begins.
+template <class C>
+__device__ void locate(const QuantAttendParams& p, Work* out)
+{
+    const int lane = threadIdx.x & 31, ctas = (int)gridDim.x, me = (int)blockIdx.x;
+    long long total = 0, mine = 0;
+    for (int base = 0; base < p.batch.seqs; base += 32) total += mine = seq_cost<C>(p, base + lane);
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    Start s;
-    s.per = total / grid;
-    s.extra = total - s.per * grid;
-    s.begin = s.per * me + min((long long)me, s.extra);
-    s.length = s.per + (me < s.extra);
-    s.skip = 0;
-    s.seq = p.batch.seqs;
-    long long before = 0;
-    for (int base = 0; base < p.batch.seqs && s.length > 0; base += 32) {
-        const long long mine = cost(base + lane);
+    const long long per = divide(total, ctas), extra = total - per * ctas;
+    const long long begin = per * me + min((long long)me, extra), left = per + (me < extra);
+    long long before = 0, skip = 0;
+    int seq = p.batch.seqs;
+    for (int base = 0; base < p.batch.seqs && left > 0; base += 32) {
+        if (p.batch.seqs > 32) mine = seq_cost<C>(p, base + lane);
         long long upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long u = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += u;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, before + upto > s.begin);
+        const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
         if (past) {
             const int l = __ffs(past) - 1;
-            s.seq = base + l;
-            s.skip = s.begin - (before + __shfl_sync(0xffffffffu, upto - mine, l));
+            seq = base + l;
+            skip = begin - (before + __shfl_sync(0xffffffffu, upto - mine, l));
             break;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (lane == 0) *out = s;
+    if (lane != 0) return;
+    Work k = {};
+    k.per = per;
+    k.extra = extra;
+    k.left = left;
+    k.seq = seq;
+    if (left > 0) {
+        k.w = load_seq<C>(p, seq);
+        k.cost = k.w.steps + C::kExtra;
+        k.item = (int)divide(skip, k.cost);
+        k.from = (int)(skip - (long long)k.item * k.cost);
+        k.line = begin - k.from;
+    }
+    k.item -= 1;  // what next_item moves on from
+    k.line -= k.cost;
+    *out = k;
+}
+
+// One thread: the next item of this CTA's part, if there is one.
+template <class C>
+__device__ void next_item(const QuantAttendParams& p, Work* out)
+{
+    Work k = *out;
+    k.some = false;
+    while (k.left > 0 && !k.some) {
+        k.item += 1;
+        k.line += k.cost;
+        while (k.item >= k.w.tiles * p.pool.kv_heads) {  // the next sequence with rows
+            k.item = 0;
+            k.w = load_seq<C>(p, ++k.seq);
+            k.cost = k.w.steps + C::kExtra;
+        }
+        k.to = (int)min((long long)k.cost, k.from + k.left);
+        k.left -= k.to - k.from;
+        k.j0 = max(k.from - C::kExtra, 0);
+        k.j1 = k.to - C::kExtra;
+        k.from = 0;
+        k.some = k.j1 > k.j0;  // (else its begin alone: nothing to do)
+    }
+    if (k.some) {
+        k.whole = k.j0 == 0 && k.j1 == k.w.steps;
+        k.head = k.item / k.w.tiles;
+        k.row0 = (k.item - k.head * k.w.tiles) * C::kRows;
+        k.rows = min(C::kRows, k.w.tokens * p.group - k.row0);
+        k.end = limit(p, k, k.rows - 1);
+        k.lim_first = limit(p, k, 0);
+    }
+    *out = k;
 }
 
 // A 16-bit value of the call's type, and two of them.
@@ -185,114 +251,127 @@ __device__ __forceinline__ int v_at(int key, int x)
     return at ^ (turn << 4);
 }
 
+// The CTA that does the item's first step, and the one that does its last.
+__device__ __forceinline__ int first_cta(const Work& k) { return cta_of(k, k.line + k.cost - k.w.steps); }
+__device__ __forceinline__ int last_cta(const Work& k) { return cta_of(k, k.line + k.cost - 1); }
+// Where part k of an item that begins at CTA `from` lies in the workspace: the first
+// in its CTA's second slot, the others in their first.
+__device__ __forceinline__ long long part_slot(int from, int k) { return 2LL * (from + k) + (k == 0 ? 1 : 0); }
+
+// Parts of an item that a CTA reads at once, of `all`: so many groups of so many.
+__device__ __forceinline__ int group_of(int all) { return all <= 16 ? all : 8 * ((int)(sqrtf((float)all) * 0.125f) + 1); }
+
+// An item of which a CTA has a part.
+struct Shared {
+    int first, last;  // its CTAs; first = -1: there is none
+    int token, head, row0, rows;
+};
+
+__device__ __forceinline__ float weight(float2 x, float ref) { return x.y == 0.f ? 0.f : ptx::ex2(x.x - ref); }  // (a sum of zero: no key)
+
+// The token row and the head of a row of a tile.
+struct Place {
+    long long token;
+    int head;
+};
+__device__ __forceinline__ Place place_of(const QuantAttendParams& p, int first_token, int head, int at)
+{
+    const int token = at / p.group;
+    return {first_token + token, head * p.group + at - token * p.group};
+}
+
+// Four elements of a row's output from element d on.
+template <int DIGITS>
+__device__ __forceinline__ void write_four(const QuantAttendParams& p, Place at, int d, float4 x)
+{
+    const long long to = at.token * p.out_token + at.head * p.out_head + d;
+    if (DIGITS > 1) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = x;
+    else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to) = make_uint2(half_words(x.x, x.y, p.bf16), half_words(x.z, x.w, p.bf16));
+}
+__device__ __forceinline__ void write_lse(const QuantAttendParams& p, Place at, float2 ml)
+{
+    p.lse[at.token * p.heads + at.head] = ml.y == 0.f ? -INFINITY : 0.6931471805599453f * (ml.x + log2f(ml.y));
+}
+
 template <int D, int NT, int DIGITS>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bitlin_quant_attend(const QuantAttendParams p)
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bitlin_quant_attend(const __grid_constant__ QuantAttendParams p)
 {
     using C = Cfg<D, NT>;
-    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
-    constexpr int KT = C::KT, SUBS = KT / 16, KW = D / 32, VW = D / 64, MT = D / 16;
+    constexpr int SUBS = KT / 16, KW = D / 32, VW = D / 64, MT = D / 16;
     constexpr int CPR = D / 32, COPIES = KT * CPR / 32;  // 16-byte chunks of a key, and copies of a lane
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ Start start;
+    constexpr int kWarps = C::kWarps;
+    __shared__ Work work;
     __shared__ float factor[C::kRows];
     __shared__ float2 warp_ml[kWarps][C::kRows];  // references and sums of the warps
     __shared__ float warp_weight[kWarps][C::kRows];
     __shared__ float2 row_ml[C::kRows];           // and of all of them
-    __shared__ int last;
-    unsigned char* ring = smem;
-    uint4* qf = reinterpret_cast<uint4*>(smem + (C::kBytes - C::kQ));
-    float* merge = reinterpret_cast<float*>(smem);
+    __shared__ Shared shared[2];                  // the items that began in an earlier CTA, and go on in the next
+    __shared__ int joins[2], count_of[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    unsigned char* my_ring = smem + warp * C::kRing;
+    uint4* qf = reinterpret_cast<uint4*>(smem + (C::kBytes - C::kQ));
+    const uint32_t my_ring_s = ptx::smem_u32(my_ring);
 
     ptx::griddep_wait();
-    if (warp == 0) locate<C::kStep, C::kRows>(p, &start);
-    __syncthreads();
-    long long left = start.length, skip = start.skip;
-    if (left <= 0) return;
-    long long line = start.begin - start.skip;  // where the current item begins
-    int seq = start.seq;
-    Seq w = load_seq<C::kStep, C::kRows>(p, seq);
-    int cost = w.steps + kItemExtra;
-    int item = (int)(skip / cost);
-    line += (long long)item * cost;
-    int from_step = (int)(skip - (long long)item * cost);
-    unsigned char* my_ring = ring + warp * C::kSlots * C::kSlot;
-    const uint32_t my_ring_s = ptx::smem_u32(my_ring);
+    if (warp == 0) locate<C>(p, &work);
+    if (threadIdx.x < 2) shared[threadIdx.x].first = -1;
     // Where this lane's copies of a tile go: chunk x of keys row, row + 32 / CPR, ...
     const int copy_row = lane / CPR, copy_x = lane & (CPR - 1);
     const uint32_t k_to = k_at<D>(copy_row, copy_x), v_to = v_at<D>(copy_row, copy_x);
-    const bool one_page = p.pool.page_size % KT == 0;  // a tile lies in one page
-    const long long copy_stride = (32 / CPR) * p.pool.slot_stride;
     const uint32_t magic = p.magic;
-    auto page_index = [&](int key) { return p.page_shift >= 0 ? key >> p.page_shift : key / p.pool.page_size; };
 
-    for (; left > 0; from_step = 0, line += cost, ++item) {
-        while (item >= w.tiles * p.pool.kv_heads) {  // the next sequence with rows
-            item = 0;
-            w = load_seq<C::kStep, C::kRows>(p, ++seq);
-            cost = w.steps + kItemExtra;
-        }
-        const int to_step = (int)min((long long)cost, from_step + left);
-        left -= to_step - from_step;
-        const int j0 = max(from_step - kItemExtra, 0), j1 = to_step - kItemExtra;
-        if (j1 <= j0) continue;  // its begin alone: nothing to do
-        const bool whole = j0 == 0 && j1 == w.steps;
-        const int head = item / w.tiles, row0 = (item - head * w.tiles) * C::kRows;
-        const int rows = min(C::kRows, w.tokens * p.group - row0);
-        auto limit = [&](int row) {  // keys that a row sees
-            return p.causal ? min(max(w.place0 + (row0 + row) / p.group + 1, 0), w.len) : w.len;
-        };
-        const int end = limit(rows - 1), lim_first = limit(0);
-        const int first = (j0 * kWarps + warp) * KT;  // this warp's first key
-        const int stop = min(end, j1 * C::kStep);
+    for (;;) {
+        if (threadIdx.x == 0) next_item<C>(p, &work);
+        __syncthreads();  // (and the ring and the queries of the item before are through)
+        if (!work.some) break;
+        const int head = work.head, end = work.end, lim_first = work.lim_first;
+        const int first = (work.j0 * kWarps + warp) * KT;  // this warp's first key
+        const int stop = min(end, work.j1 * C::kStep);
         const int n = stop > first ? (stop - first + C::kStep - 1) / C::kStep : 0;  // and its tiles
 
-        __syncthreads();  // (the ring and the queries of the item before are through)
+        // this warp's queries are on their way first: eight elements to a lane
+        constexpr int LPR = D / 8, RPS = 32 / LPR, SETS = C::kRows / RPS, QS = (SETS + kWarps - 1) / kWarps;  // lanes of a row, rows of a set, sets, of a warp
+        const int q_row = lane / LPR, q_unit = lane & (LPR - 1);
+        uint4 raw[QS];
+        {
+            const int token0 = work.row0 / p.group, in_group = work.row0 - token0 * p.group;
+            const uint16_t* from = static_cast<const uint16_t*>(p.q) + (long long)(work.w.row0 + token0) * p.q_token + head * p.group * p.q_head + 8 * q_unit;
+#pragma unroll
+            for (int j = 0; j < QS; ++j) {
+                const int q = (warp + j * kWarps) * RPS + q_row, at = in_group + q, token = (at * p.group_inverse) >> 16;
+                raw[j] = make_uint4(0, 0, 0, 0);
+                if (q < work.rows) raw[j] = *reinterpret_cast<const uint4*>(from + token * p.q_token + (at - token * p.group) * p.q_head);
+            }
+        }
 
-        // ---- copies: K and V of a tile one after the other through the ring
-        const int32_t* table = p.batch.table + seq * p.batch.table_stride;
-        const long long lane_at = head * p.pool.head_stride + (one_page ? copy_row * p.pool.slot_stride + 16 * copy_x : 0);
-        const long long lane_scale = head * p.pool.scale_head + (one_page ? lane * p.pool.scale_slot : 0);
+        // ---- copies: K and V of a tile one after the other through the ring.  A lane looks up one key;
+        // where its codes and scale lie, in units of the pools' strides, goes round by shuffles.  Keys that
+        // are not there get scales of zero and whatever codes lie at the pool's begin: values of zero.
+        const int32_t* table = p.batch.table + work.seq * p.batch.table_stride;
         auto page_of = [&](int i) {  // the table's entry for this lane's key of tile i
-            const int key = first + i * C::kStep + (one_page ? 0 : lane);
-            return i < n && key < end ? __ldg(table + page_index(key)) : -2;
+            const int key = first + i * C::kStep + lane;
+            return i < n && key < end ? __ldg(table + (p.page_shift >= 0 ? key >> p.page_shift : key / p.pool.page_size)) : -2;
         };
-        // Of the tile in issue: its first key's codes and scales (this lane's part of them) or, where
-        // a tile may span pages, this lane's key's; -1: zeros.
-        long long at = 0, scale_at = 0;
+        uint32_t at = 0, scale_at = 0;  // of this lane's key of the tile in issue
+        bool held = false;
         auto aim = [&](int i, int page) {
-            const int key = first + i * C::kStep + (one_page ? 0 : lane);
-            const bool inside = page >= 0 && page < p.pool.pages;
-            if (page != -2 && !inside) *p.index_error = 1;
+            const int key = first + i * C::kStep + lane;
+            held = page >= 0 && page < p.pool.pages;
+            if (page != -2 && !held) *p.index_error = 1;
             const int slot = p.page_shift >= 0 ? key & (p.pool.page_size - 1) : key % p.pool.page_size;
-            at = page * p.pool.page_stride + slot * p.pool.slot_stride + lane_at;
-            scale_at = page * p.pool.scale_page + slot * p.pool.scale_slot + lane_scale;
-            if (!inside) at = scale_at = -1;
+            at = held ? page * p.page_units + slot * p.slot_units + head * p.head_units : 0;
+            scale_at = held ? page * p.scale_page_units + slot * p.scale_slot_units + head * p.scale_head_units : 0;
         };
         auto issue = [&](int i, int kind, int slot) {
             if (i < n) {
                 const uint32_t to = my_ring_s + slot * C::kSlot, dst = to + (kind ? v_to : k_to), turned = kind && D == 256 ? dst ^ 64 : dst;
-                const int held = end - (first + i * C::kStep);  // keys of the tile
-                // (v_at turns by bits 1 and 2 of the key, of which D == 256 changes one here)
-                auto to_of = [&](int j) { return (j & 1 ? turned : dst) + j * (32 / CPR) * C::kRow; };
-                if (one_page) {
-                    const uint8_t* from = p.pool.codes[kind] + (at < 0 ? 0 : at);
-                    const int rows_held = at < 0 ? 0 : held;
+                const uint8_t* from = p.pool.codes[kind] + 16 * copy_x;
 #pragma unroll
-                    for (int j = 0; j < COPIES; ++j) {
-                        const bool mine = copy_row + j * (32 / CPR) < rows_held;
-                        ptx::cp_async16(to_of(j), mine ? from : p.pool.codes[kind], mine ? 16 : 0);
-                        from += copy_stride;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < COPIES; ++j) {
-                        const long long off = __shfl_sync(0xffffffffu, at, copy_row + j * (32 / CPR));
-                        ptx::cp_async16(to_of(j), p.pool.codes[kind] + (off < 0 ? 0 : off + 16 * copy_x), off < 0 ? 0 : 16);
-                    }
-                }
-                const bool mine = scale_at >= 0 && lane < held;
-                ptx::cp_async4(to + C::kCodes + 4 * lane, p.pool.scales[kind] + (mine ? scale_at : 0), mine ? 4 : 0);
+                for (int j = 0; j < COPIES; ++j)  // (v_at turns by bits 1 and 2 of the key, of which D == 256 changes one here)
+                    ptx::cp_async16((j & 1 ? turned : dst) + j * (32 / CPR) * C::kRow,
+                                    from + (uint64_t)__shfl_sync(0xffffffffu, at, copy_row + j * (32 / CPR)) * p.unit);
+                ptx::cp_async4(to + C::kCodes + 4 * lane, p.pool.scales[kind] + (uint64_t)scale_at * p.scale_unit, held ? 4 : 0);
             }
             ptx::cp_async_commit();
         };
@@ -311,32 +390,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
         }
 
         // ---- queries: a power of two brings a row's largest magnitude to 2^14 .. 2^15
-        for (int q = warp; q < C::kRows; q += kWarps) {
-            constexpr int E = D / 32;
-            float x[E], top = 0.f;
-            const int row = row0 + q, token = row / p.group;
-            const uint16_t* from = static_cast<const uint16_t*>(p.q) + (long long)(w.row0 + token) * p.q_token +
-                                   (head * p.group + row - token * p.group) * p.q_head;
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                x[j] = q < rows ? half_word(from[lane * E + j], p.bf16) : 0.f;
-                top = fmaxf(top, fabsf(x[j]));
-            }
+        for (int j = 0; j < QS; ++j) {
+            if (warp + j * kWarps >= SETS) break;
+            const uint32_t words[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+            float x[8];
+            int top = 0;  // magnitudes compare as integers; zero, infinity and NaN are left as they are
 #pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            int by = 0;
-            if (top > 0.f && top < INFINITY) {
-                frexpf(top, &by);
-                by = min(15 - by, 120);
+            for (int e = 0; e < 8; ++e) {
+                x[e] = half_word(words[e / 2] >> 16 * (e & 1), p.bf16);
+                top = max(top, __float_as_int(fabsf(x[e])));
             }
-            const float up = ldexpf(1.f, by);
-            if (lane == 0) factor[q] = p.scale * 1.4426950408889634f * ldexpf(1.f, -by);
-            __half* to = reinterpret_cast<__half*>(qf + (q / 8) * KW * 32);
+            if (LPR == 32) {
+                top = __reduce_max_sync(0xffffffffu, top);
+            } else {
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const int d = lane * E + j, quarter = d / (D / 4), in = d - quarter * (D / 4), i = in & 7;
-                to[((in >> 3) * 32 + (q & 7) * 4 + quarter) * 8 + (i < 4 ? 2 * i : 2 * i - 7)] = __float2half_rn(x[j] * up);
+                for (int o = LPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
             }
+            const int by = top > 0 && top < 0x7f800000 ? min(14 + 127 - (top >> 23), 120) : 0;
+            // a negative scale goes to the queries: products and scores then grow together
+            const float up = copysignf(__int_as_float((127 + by) << 23), p.scale);
+            const int q = (warp + j * kWarps) * RPS + q_row;
+            if (q_unit == 0) factor[q] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * __int_as_float((127 - by) << 23), 1e-36f);
+            auto two = [&](int e) {
+                const __half2 h = __floats2half2_rn(x[e] * up, x[e + 4] * up);
+                return *reinterpret_cast<const uint32_t*>(&h);
+            };
+            qf[(q / 8 * KW + q_unit % (LPR / 4)) * 32 + (q & 7) * 4 + q_unit / (LPR / 4)] = make_uint4(two(0), two(1), two(2), two(3));
         }
         __syncthreads();
 
@@ -365,28 +445,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
             __syncwarp();
 
             // S = K Q^T, keys down, queries across
-            float s[SUBS][NT][4] = {};
+            float s[SUBS][NT][4];
             {
                 const unsigned char* stage = my_ring + slot * C::kSlot;
-                const uint32_t* scales = reinterpret_cast<const uint32_t*>(stage + C::kCodes);
+                const uint32_t* scales = reinterpret_cast<const uint32_t*>(stage + C::kCodes) + r;
 #pragma unroll
-                for (int b = 0; b < SUBS; ++b) {
+                for (int b = 0; b < SUBS; ++b, stage += 16 * C::kRow, scales += 16) {
+                    float x0[NT][4] = {}, x1[NT][4] = {};  // two, so that a product does not wait for the one before
                     QuantScale2 q2[2];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) q2[k] = quant_scale2(__byte_perm(scales[16 * b + 8 * k + r], 0, 0x4040 + 0x0101 * c));
+                    for (int k = 0; k < 2; ++k) q2[k] = quant_scale2(__byte_perm(scales[8 * k], 0, 0x4040 + 0x0101 * c));
                     constexpr int H = KW < 4 ? KW : 4;  // words at a time
 #pragma unroll
                     for (int h = 0; h < KW / H; ++h) {
                         uint32_t word[2][H];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const int key = 16 * b + 8 * k + r;
                             if (KW == 2) {
-                                const uint2 x = *reinterpret_cast<const uint2*>(stage + key * C::kRow + 8 * c);
+                                const uint2 x = *reinterpret_cast<const uint2*>(stage + (8 * k + r) * C::kRow + 8 * c);
                                 word[k][0] = x.x;
                                 word[k][1] = x.y;
                             } else {
-                                const uint4 x = *reinterpret_cast<const uint4*>(stage + k_at<D>(key, c * (KW / 4) + h));
+                                const uint4 x = *reinterpret_cast<const uint4*>(stage + k_at<D>(8 * k + r, c * (KW / 4) + h));
                                 word[k][0] = x.x;
                                 word[k][1] = x.y;
                                 word[k][H - 2] = x.z;
@@ -406,28 +486,30 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
                                 const uint4 q = qf[(t * KW + h * H + x) * 32 + lane];
-                                ptx::mma_f16(s[b][t], u(a[0][0]), u(a[1][0]), u(a[0][1]), u(a[1][1]), q.x, q.y);
-                                ptx::mma_f16(s[b][t], u(a[0][2]), u(a[1][2]), u(a[0][3]), u(a[1][3]), q.z, q.w);
+                                ptx::mma_f16(x0[t], u(a[0][0]), u(a[1][0]), u(a[0][1]), u(a[1][1]), q.x, q.y);
+                                ptx::mma_f16(x1[t], u(a[0][2]), u(a[1][2]), u(a[0][3]), u(a[1][3]), q.z, q.w);
                             }
                         }
                     }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float x = x0[t][k] + x1[t][k];
+                            if (b == 0) s[0][t][k] = x;
+                            else s[1][t][k] = x;
+                        }
                 }
             }
 
             // weights
             bool ask = false;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int b = 0; b < SUBS; ++b) s[b][t][k] *= sl2[t][k & 1];
             if (key0 + KT > lim_first) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int lim = min(limit(8 * t + 2 * c + k), end) - key0 - r;
+                        const int lim = min(limit(p, work, 8 * t + 2 * c + k), end) - key0 - r;
 #pragma unroll
                         for (int b = 0; b < SUBS; ++b) {
                             if (16 * b >= lim) s[b][t][k] = -INFINITY;
@@ -443,6 +525,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
                     top[t][k] = fmaxf(s[0][t][k], s[0][t][k + 2]);
 #pragma unroll
                     for (int b = 1; b < SUBS; ++b) top[t][k] = fmaxf(top[t][k], fmaxf(s[b][t][k], s[b][t][k + 2]));
+                    top[t][k] *= sl2[t][k];
                     ask |= top[t][k] > base[t][k] + (kShift + kLazy);
                 }
             if (__any_sync(0xffffffffu, ask)) {
@@ -471,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float x = ptx::ex2(s[b][t][2 * k] - base[t][0]), y = ptx::ex2(s[b][t][2 * k + 1] - base[t][1]);
+                        const float x = ptx::ex2(fmaf(s[b][t][2 * k], sl2[t][0], -base[t][0])), y = ptx::ex2(fmaf(s[b][t][2 * k + 1], sl2[t][1], -base[t][1]));
                         sum[t][0] += x;
                         sum[t][1] += y;
                         const __half2 hi = __floats2half2_rn(x, y);
@@ -491,16 +574,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
 
             // O += V^T P^T, dimensions down, queries across
             const unsigned char* stage = my_ring + slot * C::kSlot;
-            const uint32_t* scales = reinterpret_cast<const uint32_t*>(stage + C::kCodes);
+            const uint32_t* scales = reinterpret_cast<const uint32_t*>(stage + C::kCodes) + 2 * c;
             slot = next(slot);
 #pragma unroll
-            for (int b = 0; b < SUBS; ++b) {
+            for (int b = 0; b < SUBS; ++b, stage += 16 * C::kRow, scales += 16) {
                 QuantScale2 q2[2];
-                uint32_t word[2][2][VW];
+                uint32_t word[2][2][VW], pb[NT][DIGITS][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int g = 0; g < DIGITS; ++g)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) pb[t][g][k] = b ? pf[1][t][g][k] : pf[0][t][g][k];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int key = 16 * b + 8 * k + 2 * c;
-                    const uint2 two = *reinterpret_cast<const uint2*>(scales + key);
+                    const int key = 8 * k + 2 * c;
+                    const uint2 two = *reinterpret_cast<const uint2*>(scales + 8 * k);
                     const uint32_t g = r >> 1;
                     q2[k] = quant_scale2(__byte_perm(two.x, two.y, g | (g + 4) << 8) & 0x00ff00ffu);
 #pragma unroll
@@ -540,7 +629,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
 #pragma unroll
                                 for (int g = 0; g < DIGITS; ++g)
                                     ptx::mma_f16(acc[4 * x + 2 * h + d][t], u(a[0][2 * d]), u(a[0][2 * d + 1]), u(a[1][2 * d]), u(a[1][2 * d + 1]),
-                                                 pf[b][t][g][0], pf[b][t][g][1]);
+                                                 pb[t][g][0], pb[t][g][1]);
                     }
                 }
             }
@@ -561,23 +650,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
 
         // (row q of eight, dimensions 2 i and 2 i + 1) of a warp's output in shared memory
         auto merge_at = [&](int who, int q, int i) {
-            return reinterpret_cast<float2*>(merge) + (who * 8 + q) * (D / 2) + (i ^ ((i / MT ^ (q >> 1 << 2)) & (MT - 1)));
+            return reinterpret_cast<float2*>(smem) + (who * 8 + q) * C::kMergeRow + i + i / MT;
         };
-        const int from = cta_of(start, line + kItemExtra), parts = cta_of(start, line + kItemExtra + w.steps - 1) - from + 1;
-        float2* ws_ml = reinterpret_cast<float2*>(p.ws_ml);
-        // the first part lies in its CTA's second slot, the others in their first
-        auto slot_of = [&](int k) { return 2LL * (from + k) + (k == 0 ? 1 : 0); };
-        const long long my_slot = slot_of((int)blockIdx.x - from);
-        auto weight = [](float2 x, float ref) { return x.y == 0.f ? 0.f : ptx::ex2(x.x - ref); };  // (a sum of zero: no key)
-        auto write_lse = [&](int row, float2 ml) {
-            const int at = row0 + row, token = at / p.group;
-            p.lse[(long long)(w.row0 + token) * p.heads + head * p.group + at - token * p.group] =
-                ml.y == 0.f ? -INFINITY : 0.6931471805599453f * (ml.x + log2f(ml.y));
-        };
-        auto out_at = [&](int row) {
-            const int at = row0 + row, token = at / p.group;
-            return (long long)(w.row0 + token) * p.out_token + (head * p.group + at - token * p.group) * p.out_head;
-        };
+        const int rows = work.rows;
+        const bool whole = work.whole;
         for (int row = warp; row < rows; row += kWarps) {
             const float2 x = lane < kWarps ? warp_ml[lane][row] : make_float2(0.f, 0.f);
             float ref = x.y == 0.f ? -INFINITY : x.x;
@@ -591,6 +667,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
             if (lane < kWarps) warp_weight[lane][row] = f;
             if (lane == 0) row_ml[row] = make_float2(ref, total);
         }
+        const int from = first_cta(work);
+        const long long slot_of_part = part_slot(from, (int)blockIdx.x - from);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (8 * t >= rows) break;
@@ -598,108 +676,125 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) *merge_at(warp, 2 * c + k, r * MT + i) = make_float2(acc[i][t][k], acc[i][t][k + 2]);
+                for (int e = 0; e < 2; ++e) merge_at(warp, 2 * c + e, r * MT)[i] = make_float2(acc[i][t][e], acc[i][t][e + 2]);
             __syncthreads();
-            for (int at = threadIdx.x; at < 8 * (D / 2); at += kThreads) {
-                const int q = at / (D / 2), i = at - q * (D / 2), row = 8 * t + q;
-                if (row >= rows) break;
-                float2 o = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    const float2 v = *merge_at(k, q, i);
-                    const float f = warp_weight[k][row];
-                    o.x = fmaf(f, v.x, o.x);
-                    o.y = fmaf(f, v.y, o.y);
-                }
+            // a warp takes a row, a lane four of its elements at a time
+            for (int q = warp; q < 8 && 8 * t + q < rows; q += kWarps) {
+                const int row = 8 * t + q;
                 const float2 ml = row_ml[row];
-                if (whole) {
-                    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
-                    const long long to = out_at(row) + 2 * i;
-                    if (DIGITS > 1) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + to) = make_float2(o.x * inv, o.y * inv);
-                    else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + to) = half_words(o.x * inv, o.y * inv, p.bf16);
-                    if (p.lse && i == 0) write_lse(row, ml);
-                } else {
-                    __stcg(reinterpret_cast<float2*>(p.ws_o + my_slot * kSlotFloats + row * D) + i, o);
-                    if (i == 0) __stcg(ws_ml + my_slot * kSlotRows + row, ml);
+                const float scale = !whole ? 1.f : ml.y == 0.f ? 0.f : 1.f / ml.y;
+                const Place place = place_of(p, work.w.row0, head, work.row0 + row);
+#pragma unroll
+                for (int e = 0; e < (D + 127) / 128; ++e) {
+                    const int d = 4 * (lane + 32 * e);
+                    if (d >= D) break;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < kWarps; ++k) {
+                        const float2* v = merge_at(k, q, d / 2);
+                        const float2 x = v[0], y = v[1];
+                        const float f = warp_weight[k][row];
+                        o = make_float4(fmaf(f, x.x, o.x), fmaf(f, x.y, o.y), fmaf(f, y.x, o.z), fmaf(f, y.y, o.w));
+                    }
+                    o = make_float4(o.x * scale, o.y * scale, o.z * scale, o.w * scale);
+                    if (whole) write_four<DIGITS>(p, place, d, o);
+                    else __stcg(reinterpret_cast<float4*>(p.ws_o + slot_of_part * C::kPart + row * D + d), o);
+                }
+                if (lane == 0) {
+                    if (!whole) __stcg(reinterpret_cast<float2*>(p.ws_ml) + slot_of_part * C::kRows + row, ml);
+                    else if (p.lse) write_lse(p, place, ml);
                 }
             }
         }
-        if (whole) continue;
+        if (!whole && threadIdx.x == 0) shared[from == (int)blockIdx.x] = {from, last_cta(work), work.w.row0, head, work.row0, rows};
+    }
 
-        // ---- a part of an item: the last CTA to arrive joins them.  Many parts are joined
-        // in groups first, by the last CTA of each group, so that no CTA reads them all.
-        const int group = parts <= 2 * kJoin ? parts : (int)(sqrtf((float)parts) / kJoin + 1.f) * kJoin;
-        const int groups = (parts + group - 1) / group, mine = ((int)blockIdx.x - from) / group;
-        for (int level = groups > 1 ? 0 : 1; level < 2; ++level) {
-            const int head_part = level ? 0 : mine * group;                                  // the first of those that are joined here,
-            const int count = level ? groups : min(group, parts - head_part), each = level && groups > 1 ? group : 1;  // how many, how far apart
-            const int joined = level && groups == 1 ? parts : count;
-            if (joined > 1) {
-                __syncthreads();
-                if (threadIdx.x == 0) {
+    // ---- items that CTAs share: the last one to come joins the parts.  Many parts are joined
+    // in groups first, by the last CTA of each group, so that no CTA reads them all.
+    constexpr int V = D == 256 ? 2 : 1;  // 16 bytes of a lane and part
+    constexpr int kBatch = 8;            // parts in flight
+    const bool busy = D >= 128 || lane < 16;
+    bool alive[2] = {shared[0].first >= 0, shared[1].first >= 0};
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+        __syncthreads();
+        if (threadIdx.x < 2) {
+            const Shared item = shared[threadIdx.x];
+            int mode = alive[threadIdx.x] ? 1 : 0;  // 0: no more to do, 1: goes on to the next level, 2: joins
+            if (mode) {
+                const int all = item.last - item.first + 1, group = group_of(all), groups = (all + group - 1) / group;
+                const int first = level ? 0 : ((int)blockIdx.x - item.first) / group * group;
+                const int count = !level ? min(group, all - first) : groups > 1 ? groups : all;
+                if (level ? count > 1 : groups > 1 && count > 1) {
                     // (carries what the other threads wrote before they met, and brings
                     // what the other CTAs' threads wrote before theirs).  A group of several
-                    // begins at a CTA that lies inside this item, an item at its own first.
-                    int* ticket = p.tickets + level * (int)gridDim.x + from + head_part;
-                    last = ptx::atom_add_acq_rel(ticket, 1) == joined - 1;
-                    if (last) *ticket = 0;
+                    // begins at a CTA that lies inside the item, an item at its own first.
+                    int* ticket = p.tickets + level * (int)gridDim.x + item.first + first;
+                    mode = ptx::atom_add_acq_rel(ticket, 1) == count - 1 ? 2 : 0;
+                    if (mode) *ticket = 0;
                 }
-                __syncthreads();
-                if (!last) break;
-                for (int row = warp; row < rows; row += kWarps) {
-                    constexpr int V = D == 256 ? 2 : 1;  // 16 bytes of a lane and part
-                    const bool busy = D >= 128 || lane < 16;
-                    const int k0 = lane;
-                    float2 x = make_float2(0.f, 0.f);
-                    if (k0 < joined) x = __ldcg(ws_ml + slot_of(head_part + k0 * each) * kSlotRows + row);
-                    float ref = x.y == 0.f ? -INFINITY : x.x;
+                count_of[threadIdx.x] = count;
+            }
+            joins[threadIdx.x] = mode;
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            alive[which] = joins[which] != 0;
+            if (joins[which] != 2) continue;
+            const Shared item = shared[which];
+            const int group = group_of(item.last - item.first + 1), count = count_of[which];
+            const int first = level ? 0 : ((int)blockIdx.x - item.first) / group * group;
+            const int each = level && item.last - item.first + 1 > group ? group : 1;  // how far the parts are apart
+            auto slot_of = [&](int k) { return part_slot(item.first, first + k * each); };
+#pragma unroll 1
+            for (int row = warp; row < item.rows; row += kWarps) {
+                float4 v[kBatch][V], o[V] = {};
+                auto load = [&](int k) {
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-                    if (ref == -INFINITY) ref = 0.f;
-                    const float f = weight(x, ref);
-                    float total = f * x.y;
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-                    float4 o[V] = {};
-                    for (int k = 0; k < joined; k += kBatch) {
-                        float4 v[kBatch][V];
-#pragma unroll
-                        for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-                            for (int e = 0; e < V; ++e)
-                                if (k + j < joined && busy)
-                                    v[j][e] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot_of(head_part + (k + j) * each) * kSlotFloats + row * D) + lane + 32 * e);
-#pragma unroll
-                        for (int j = 0; j < kBatch; ++j) {
-                            const float g = __shfl_sync(0xffffffffu, f, (k + j) & 31);
-                            if (k + j < joined && busy) {
-#pragma unroll
-                                for (int e = 0; e < V; ++e)
-                                    o[e] = make_float4(fmaf(g, v[j][e].x, o[e].x), fmaf(g, v[j][e].y, o[e].y), fmaf(g, v[j][e].z, o[e].z),
-                                                       fmaf(g, v[j][e].w, o[e].w));
-                            }
-                        }
-                    }
-                    if (level == 0) {
-                        float* to = p.ws_o + slot_of(head_part) * kSlotFloats + row * D;
-                        __syncwarp();
+                    for (int j = 0; j < kBatch; ++j)
 #pragma unroll
                         for (int e = 0; e < V; ++e)
-                            if (busy) __stcg(reinterpret_cast<float4*>(to) + lane + 32 * e, o[e]);
-                        if (lane == 0) __stcg(ws_ml + slot_of(head_part) * kSlotRows + row, make_float2(ref, total));
-                    } else {
-                        const float inv = total == 0.f ? 0.f : 1.f / total;
-                        const long long to = out_at(row) + 4 * lane;
+                            if (k + j < count && busy) v[j][e] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot_of(k + j) * C::kPart + row * D) + lane + 32 * e);
+                };
+                load(0);
+                float2 x = make_float2(0.f, 0.f);
+                if (lane < count) x = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot_of(lane) * C::kRows + row);
+                float ref = x.y == 0.f ? -INFINITY : x.x;
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            const float4 y = make_float4(o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv);
-                            if (!busy) continue;
-                            if (DIGITS > 1) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to + 128 * e) = y;
-                            else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to + 128 * e) =
-                                make_uint2(half_words(y.x, y.y, p.bf16), half_words(y.z, y.w, p.bf16));
+                for (int s = 16; s; s >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, s));
+                if (ref == -INFINITY) ref = 0.f;
+                const float f = weight(x, ref);
+                float total = f * x.y;
+#pragma unroll
+                for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
+#pragma unroll 1
+                for (int k = 0; k < count; k += kBatch) {
+                    if (k) load(k);
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+                        const float g = __shfl_sync(0xffffffffu, f, (k + j) & 31);
+                        if (k + j < count && busy) {
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                o[e] = make_float4(fmaf(g, v[j][e].x, o[e].x), fmaf(g, v[j][e].y, o[e].y), fmaf(g, v[j][e].z, o[e].z),
+                                                   fmaf(g, v[j][e].w, o[e].w));
                         }
-                        if (p.lse && lane == 0) write_lse(row, make_float2(ref, total));
                     }
+                }
+                const float scale = !level ? 1.f : total == 0.f ? 0.f : 1.f / total;
+                const Place place = place_of(p, item.token, item.head, item.row0 + row);
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float4 y = make_float4(o[e].x * scale, o[e].y * scale, o[e].z * scale, o[e].w * scale);
+                    if (!busy) continue;
+                    if (level) write_four<DIGITS>(p, place, 4 * (lane + 32 * e), y);
+                    else __stcg(reinterpret_cast<float4*>(p.ws_o + slot_of(0) * C::kPart + row * D) + lane + 32 * e, y);
+                }
+                if (lane == 0) {
+                    if (!level) __stcg(reinterpret_cast<float2*>(p.ws_ml) + slot_of(0) * C::kRows + row, make_float2(ref, total));
+                    else if (p.lse) write_lse(p, place, make_float2(ref, total));
                 }
             }
         }
@@ -762,18 +857,27 @@ cudaError_t load_all()
     return e;
 }
 
-constexpr int kMostBlocks = 2;  // CTAs on an SM
+// The largest of all kernels' parts, two of a CTA, per SM.
+template <int D, int NT>
+constexpr size_t most_floats(size_t other)
+{
+    const size_t mine = (size_t)2 * Cfg<D, NT>::kBlocks * Cfg<D, NT>::kPart;
+    return mine > other ? mine : other;
+}
+constexpr size_t kPartFloats = most_floats<64, 1>(most_floats<64, 2>(most_floats<128, 1>(most_floats<128, 2>(most_floats<256, 1>(most_floats<256, 2>(0))))));
+constexpr int kMostBlocks = 2, kMostRows = 16;
 
 }  // namespace
 
+// Tickets, zero between calls; then references and sums; then outputs.
 KvWorkspaceParts bitlin_quant_attend_workspace(int num_sms)
 {
-    const size_t slots = (size_t)2 * kMostBlocks * num_sms;
+    const size_t ctas = (size_t)kMostBlocks * num_sms;
     KvWorkspaceParts w;
-    w.timed_out = 2 * kMostBlocks * num_sms * sizeof(int);  // (no kernel here waits)
+    w.timed_out = 2 * ctas * sizeof(int);  // (no kernel here waits)
     w.ml = (w.timed_out + sizeof(int) + 255) / 256 * 256;
-    w.o = w.ml + slots * kSlotRows * 2 * sizeof(float);
-    w.bytes = w.o + slots * kSlotFloats * sizeof(float);
+    w.o = (w.ml + 2 * ctas * kMostRows * 2 * sizeof(float) + 255) / 256 * 256;
+    w.bytes = w.o + (size_t)num_sms * kPartFloats * sizeof(float);
     return w;
 }
 

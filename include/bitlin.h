@@ -626,6 +626,9 @@ typedef struct {
  * A handle on a 4-bit cache in the caller's memory.  The slots of a head side
  * by side (slot_stride = head_dim / 2, scale_slot_stride = 4) are read fastest.
  *
+ * A pool's last slot must lie less than 2^32 times the largest power of two
+ * that divides its three strides from its first (64 GB at strides of 16 bytes).
+ *
  *   dtype  BITLIN_BF16 or BITLIN_F16: of the queries, of a 16-bit attention
  *          output and of what the append makes of q.
  *
