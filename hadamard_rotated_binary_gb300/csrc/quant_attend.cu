@@ -51,14 +51,15 @@ constexpr float kLazy = 8.f;      // log2 of the growth that another reference w
 template <int D, int NT>
 struct Cfg {
     // Warps of a CTA and CTAs on an SM, so that a thread has the registers it needs.
-    static constexpr int kWarps = D == 256 && NT == 1 ? 6 : 8;
-    static constexpr int kBlocks = D == 256 && NT == 2 ? 1 : 2;
+    static constexpr int kOutputs = D / 32 * NT * 8;       // a thread's part of the output, in registers
+    static constexpr int kBlocks = kOutputs > 64 ? 1 : 2;
+    static constexpr int kWarps = kOutputs == 48 || kOutputs == 64 ? 6 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRows = 8 * NT;
     static constexpr int kRow = D / 2;                     // bytes of a head's codes
     static constexpr int kCodes = KT * kRow;
     static constexpr int kSlot = kCodes + KT * 4;          // a tile's K or V, and its scales
-    static constexpr int kLead = D == 256 || (D == 128 && NT == 2) ? 1 : 2;  // tiles that copies run ahead
+    static constexpr int kLead = D == 256 ? 1 : 2;  // tiles that copies run ahead
     static constexpr int kSlots = 2 * kLead + 1;
     static constexpr int kRing = kSlots * kSlot;
     static constexpr int kQ = NT * (D / 32) * 512;
@@ -829,31 +830,42 @@ cudaError_t launch(const QuantAttendParams& p, int num_sms, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, bitlin_quant_attend<D, NT, DIGITS>, p);
 }
 
-template <int NT, int DIGITS>
-cudaError_t pick_dim(const QuantAttendParams& p, int num_sms, cudaStream_t s)
+// Tiles of 8 rows: by a sequence's rows on average, as far as the host knows them, up to
+// what leaves a thread's part of the output in registers.  Measured, in us, 16 sequences
+// of 1,000-6,000 keys with 5 tokens of 4 heads to a key head, 128 dims: 16 rows 51.3, 24 43.2.
+template <int D, int DIGITS>
+cudaError_t pick_rows(const QuantAttendParams& p, int num_sms, cudaStream_t s)
 {
-    switch (p.pool.dim) {
-    case 64: return launch<64, NT, DIGITS>(p, num_sms, s);
-    case 128: return launch<128, NT, DIGITS>(p, num_sms, s);
-    default: return launch<256, NT, DIGITS>(p, num_sms, s);
-    }
+    constexpr int kMost = D == 256 ? 2 : 3;
+    const long long rows = (long long)p.tokens * p.group, seqs = p.batch.seqs;
+    if (rows <= 8 * seqs) return launch<D, 1, DIGITS>(p, num_sms, s);
+    if (kMost == 2 || rows <= 16 * seqs) return launch<D, 2, DIGITS>(p, num_sms, s);
+    return launch<D, kMost, DIGITS>(p, num_sms, s);
 }
 
 template <int DIGITS>
-cudaError_t pick_rows(const QuantAttendParams& p, int num_sms, cudaStream_t s)
+cudaError_t pick_dim(const QuantAttendParams& p, int num_sms, cudaStream_t s)
 {
-    // A sequence's rows on average, as far as the host knows them.
-    const bool few = (long long)p.tokens * p.group <= 8LL * p.batch.seqs;
-    return few ? pick_dim<1, DIGITS>(p, num_sms, s) : pick_dim<2, DIGITS>(p, num_sms, s);
+    switch (p.pool.dim) {
+    case 64: return pick_rows<64, DIGITS>(p, num_sms, s);
+    case 128: return pick_rows<128, DIGITS>(p, num_sms, s);
+    default: return pick_rows<256, DIGITS>(p, num_sms, s);
+    }
 }
 
-template <int D>
+template <int D, int NT>
+cudaError_t load_digits()
+{
+    const cudaError_t e = load<D, NT, 1>();
+    return e == cudaSuccess ? load<D, NT, 2>() : e;
+}
+
+template <int D, int MOST>
 cudaError_t load_all()
 {
-    cudaError_t e = load<D, 1, 1>();
-    if (e == cudaSuccess) e = load<D, 2, 1>();
-    if (e == cudaSuccess) e = load<D, 1, 2>();
-    if (e == cudaSuccess) e = load<D, 2, 2>();
+    cudaError_t e = load_digits<D, 1>();
+    if (e == cudaSuccess) e = load_digits<D, 2>();
+    if (e == cudaSuccess && MOST > 2) e = load_digits<D, MOST>();
     return e;
 }
 
@@ -864,8 +876,9 @@ constexpr size_t most_floats(size_t other)
     const size_t mine = (size_t)2 * Cfg<D, NT>::kBlocks * Cfg<D, NT>::kPart;
     return mine > other ? mine : other;
 }
-constexpr size_t kPartFloats = most_floats<64, 1>(most_floats<64, 2>(most_floats<128, 1>(most_floats<128, 2>(most_floats<256, 1>(most_floats<256, 2>(0))))));
-constexpr int kMostBlocks = 2, kMostRows = 16;
+constexpr size_t kPartFloats =
+    most_floats<64, 1>(most_floats<64, 2>(most_floats<64, 3>(most_floats<128, 1>(most_floats<128, 2>(most_floats<128, 3>(most_floats<256, 1>(most_floats<256, 2>(0))))))));
+constexpr int kMostBlocks = 2, kMostRows = 24;
 
 }  // namespace
 
@@ -883,10 +896,10 @@ KvWorkspaceParts bitlin_quant_attend_workspace(int num_sms)
 
 cudaError_t bitlin_quant_attend_load(int dim)
 {
-    return dim == 64 ? load_all<64>() : dim == 128 ? load_all<128>() : load_all<256>();
+    return dim == 64 ? load_all<64, 3>() : dim == 128 ? load_all<128, 3>() : load_all<256, 2>();
 }
 
 cudaError_t bitlin_launch_quant_attend(const QuantAttendParams& p, int out_dtype, int num_sms, cudaStream_t s)
 {
-    return out_dtype == BITLIN_F32 ? pick_rows<2>(p, num_sms, s) : pick_rows<1>(p, num_sms, s);
+    return out_dtype == BITLIN_F32 ? pick_dim<2>(p, num_sms, s) : pick_dim<1>(p, num_sms, s);
 }

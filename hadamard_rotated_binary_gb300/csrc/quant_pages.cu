@@ -13,14 +13,34 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kHeadsPerThread = 4;
+constexpr int kUnpackThreads = 256;
+
+// A word's eight values, two by two, as f16.
+__device__ __forceinline__ void eight_halves(uint32_t word, uint32_t scale_byte, uint32_t (&v)[4])
+{
+    const QuantScale2 s = quant_scale2(scale_byte * 0x00010001u);
+    const uint32_t magic = 0x64006400u;
+    const __half2 a = quant_low(word, s, magic), b = quant_high(word, s, magic);  // elements 0 and 4, 1 and 5
+    const __half2 c = quant_low(word >> 8, s, magic), d = quant_high(word >> 8, s, magic);
+    auto bits = [](const __half2& x) { return *reinterpret_cast<const uint32_t*>(&x); };
+    v[0] = __byte_perm(bits(a), bits(b), 0x5410);
+    v[1] = __byte_perm(bits(c), bits(d), 0x5410);
+    v[2] = __byte_perm(bits(a), bits(b), 0x7632);
+    v[3] = __byte_perm(bits(c), bits(d), 0x7632);
+}
 
 template <typename T>
 __device__ __forceinline__ void store8(T* dst, uint32_t word, uint32_t scale_byte, bool wide)
 {
-    const float s = quant_scale(scale_byte);
-    T v[8];
+    uint32_t h[4];
+    eight_halves(word, scale_byte, h);
+    alignas(16) T v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = from_f32<T>((float)((int)(word >> (4 * j) & 15) - 8) * s);
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+        v[2 * j] = from_f32<T>(f.x);
+        v[2 * j + 1] = from_f32<T>(f.y);
+    }
     if (wide) {
 #pragma unroll
         for (int j = 0; j < (int)sizeof(T) / 2; ++j) reinterpret_cast<uint4*>(dst)[j] = reinterpret_cast<const uint4*>(v)[j];
@@ -69,14 +89,18 @@ __global__ void __launch_bounds__(kThreads) bitlin_quant_read(const QuantReadPar
         if (h0 + i < p.pool.kv_heads) store8<T>(out + (h0 + i) * p.out_head[kind], word[i], scale[i], wide);
 }
 
-// Block (x, s): every gridDim.x-th page of sequence s.
+// Block (x, s): every gridDim.x-th page of sequence s.  A warp takes the slots of one head
+// of K or of V, a word to a lane: 32 / (D / 8) slots at a time, eight times in flight.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) bitlin_quant_unpack(const QuantUnpackParams p)
+__global__ void __launch_bounds__(kUnpackThreads) bitlin_quant_unpack(const QuantUnpackParams p)
 {
+    constexpr int kBatch = 8;
     ptx::griddep_wait();
     const int seq = blockIdx.y;
     if (p.batch.q_offsets[seq + 1] <= p.batch.q_offsets[seq]) return;  // nothing asks for it
-    const int units = p.pool.dim / 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int units = p.pool.dim / 8, u = lane & (units - 1), slots = 32 / units, mine = lane / units;
+    const int group = 8 * (8 * u / (p.pool.dim / 4));  // the group's byte in a head's scales, in bits
     const int len = min(max(p.batch.kv_lens[seq], 0), 1 << 30);
     const int want = (int)(((long long)len + p.pool.page_size - 1) / p.pool.page_size);
     const int pages = min(want, p.batch.table_pages);
@@ -87,17 +111,27 @@ __global__ void __launch_bounds__(kThreads) bitlin_quant_unpack(const QuantUnpac
             *p.index_error = 1;
             continue;
         }
-        const int slots = min(p.pool.page_size, len - at * p.pool.page_size);
-        const int words = slots * units;
-        for (int head = 0; head < p.pool.kv_heads; ++head) {
-            for (int i = threadIdx.x; i < 2 * words; i += kThreads) {
-                const int kind = i >= words, slot = (i - kind * words) / units, u = i - kind * words - slot * units;
-                const uint32_t word = *reinterpret_cast<const uint32_t*>(
-                    p.pool.codes[kind] + page * p.pool.page_stride + slot * p.pool.slot_stride + head * p.pool.head_stride + 4 * u);
-                const uint32_t scale =
-                    p.pool.scales[kind][page * p.pool.scale_page + slot * p.pool.scale_slot + head * p.pool.scale_head + 8 * u / (p.pool.dim / 4)];
-                T* out = static_cast<T*>(p.out[kind]) + page * p.page_stride + slot * p.slot_stride + head * p.head_stride + 8 * u;
-                store8<T>(out, word, scale, true);
+        const int held = min(p.pool.page_size, len - at * p.pool.page_size);
+        for (int i = warp; i < 2 * p.pool.kv_heads; i += kUnpackThreads / 32) {
+            const int kind = i & 1, head = i >> 1;
+            const uint8_t* codes = p.pool.codes[kind] + page * p.pool.page_stride + head * p.pool.head_stride + 4 * u;
+            const uint8_t* scales = p.pool.scales[kind] + page * p.pool.scale_page + head * p.pool.scale_head;
+            T* out = static_cast<T*>(p.out[kind]) + page * p.page_stride + head * p.head_stride + 8 * u;
+            for (int first = mine; first < held; first += slots * kBatch) {
+                uint32_t word[kBatch], scale[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int slot = first + j * slots;
+                    if (slot < held) {
+                        word[j] = *reinterpret_cast<const uint32_t*>(codes + slot * p.pool.slot_stride);
+                        scale[j] = *reinterpret_cast<const uint32_t*>(scales + slot * p.pool.scale_slot);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int slot = first + j * slots;
+                    if (slot < held) store8<T>(out + slot * p.slot_stride, word[j], scale[j] >> group & 0xff, true);
+                }
             }
         }
     }
@@ -144,9 +178,11 @@ cudaError_t bitlin_launch_quant_read(const QuantReadParams& p, int dst_dtype, cu
 
 cudaError_t bitlin_launch_quant_unpack(const QuantUnpackParams& p, int dst_dtype, int num_sms, cudaStream_t s)
 {
-    const int want = (8 * num_sms + p.batch.seqs - 1) / p.batch.seqs;
+    // blocks for sixteen to an SM, or for a page each
+    const int want = (16 * num_sms + p.batch.seqs - 1) / p.batch.seqs;
     cudaLaunchAttribute attr = {};
-    const cudaLaunchConfig_t cfg = config(dim3(want < p.batch.table_pages ? want : p.batch.table_pages, p.batch.seqs), s, &attr);
+    cudaLaunchConfig_t cfg = config(dim3(want < p.batch.table_pages ? want : p.batch.table_pages, p.batch.seqs), s, &attr);
+    cfg.blockDim = dim3(kUnpackThreads);
     return dst_dtype == BITLIN_BF16 ? cudaLaunchKernelEx(&cfg, bitlin_quant_unpack<__nv_bfloat16>, p)
                                     : cudaLaunchKernelEx(&cfg, bitlin_quant_unpack<__half>, p);
 }

@@ -674,10 +674,13 @@ bitlin_status bitlin_kvq_read(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, in
  *
  *   through  NULL, or a 16-bit cache of the handle's type and of the same
  *            pages, page_size, kv_heads and head_dim, whose pools are scratch
- *            (one for all layers of a model will do).  Calls of more tokens
- *            than sequences then read the sequences' pages back into it and
- *            attend there.  Without it such calls are right, but slow where
- *            sequences bring many tokens.
+ *            (one for all layers of a model will do).  Calls whose sequences
+ *            bring many rows (more than 80 new tokens times query heads of a
+ *            key head on average) then read the sequences' pages back into it
+ *            and attend there.  Without it such calls are right, but slower.
+ *   out      For a 16-bit out the probabilities are rounded to f16 before they
+ *            meet the values (through 16-bit pages: to the handle's type); for
+ *            an f32 out they are split in two f16 digits, 22 bits.
  *
  * Calls that share a `through` must follow one another in stream order, as
  * those that share a workspace must.  Errors: as bitlin_kv_attend; the sticky

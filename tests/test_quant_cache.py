@@ -534,15 +534,22 @@ def test_attention(hrb, case):
     assert cache.kv.get_error() == hrb.BITLIN_OK
 
 
+THROUGH = [c for c in ATTENDED if c[2] % 8 == 0] + [
+    ([300, 80], [25, 25], 32, 2, 4, 128, torch.float16, torch.float16, True, "heads"),
+    ([300, 80, 4], [60, 0, 9], 48, 2, 6, 256, torch.bfloat16, torch.float32, True, "slots"),
+    ([130, 0, 64], [130, 5, 0], 8, 3, 4, 64, torch.bfloat16, torch.bfloat16, False, "heads"),
+]
+
+
 @gpu
-@pytest.mark.parametrize("case", [c for c in ATTENDED if c[2] % 8 == 0], ids=str)
+@pytest.mark.parametrize("case", THROUGH, ids=str)
 def test_attention_through_16_bit_pages(hrb, case):
     lens, new, page, kvh, group, dim, dtype, out, causal, pools = case
     need = sum(-(-n // page) for n in lens) + 2
     scratch = [torch.full((need, page, kvh, dim), math.nan, dtype=dtype, device="cuda") for _ in range(2)]
     through = hrb.PagedKV(*scratch)
     cache, _, offsets, q, y, lse = attended(hrb, case, through=through)
-    many = offsets[-1] > len(lens)
+    many = offsets[-1] * group > 80 * len(lens)
     check_attended(y, lse, reference(cache, offsets, lens, q, causal), dtype if many else torch.float16)
     assert cache.kv.get_error() == hrb.BITLIN_OK and through.get_error() == hrb.BITLIN_OK
 
@@ -554,8 +561,8 @@ def test_attention_over_pages_outside_and_lengths_past_the_table(hrb, many):
     gen = torch.Generator(device="cuda").manual_seed(3)
     cache = Cache(hrb, gen, lens, page, kvh, dim, torch.float16).random(gen)
     through = hrb.PagedKV(*(torch.zeros((8, page, kvh, dim), dtype=torch.float16, device="cuda") for _ in range(2))) if many else None
-    new = [2, 2] if many else [1, 1]
-    q = torch.randn((sum(new), 4, dim), generator=gen, device="cuda").half()
+    new = [30, 30] if many else [1, 1]  # 60 rows, or 2, of 8 query heads: the first through 16-bit pages
+    q = torch.randn((sum(new), 8, dim), generator=gen, device="cuda").half()
     batch, offsets = batch_of(hrb, new, cache)
     k, v = cache.values()
     old = int(cache.table[1, 1])
