@@ -92,7 +92,10 @@ struct NormTurnParams {
     double eps;
     uint8_t* scales[2];       // k's, v's (4-bit cache)
     long long scale_page, scale_slot, scale_head;
-    int team;                 // lanes to a row, set by the launcher
+    // set by the launcher
+    int team;                 // lanes to a row
+    int kv_heads_per_team;    // heads of k (or v) that a team takes one after the other
+    float inverse_dim, eps_f;
 };
 
 // The gradient of a norm and rotation (dx in x's type).
@@ -107,7 +110,9 @@ struct NormGradParams {
     float* partial;           // [blocks][dim]
     float* dweight;           // [dim]
     int tokens, heads, dim, rotary, axes, adjacent;
-    int team, blocks;         // set by the launcher
+    // set by the launcher
+    int team, blocks;
+    float inverse_dim, eps_f;
 };
 
 // One call of the attention kernel.

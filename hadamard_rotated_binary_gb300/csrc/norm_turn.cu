@@ -171,82 +171,297 @@ struct Exact {
     }
 };
 
-// Store a row's 8 elements d0.. of each lane u < D / 8 in 4 bits.  x: the values,
-// err: how far each may be off (all zero: exact).  All lanes of the warp take part.
+// Codes of a lane's 8 elements d0.. and their group's scale in 64 bits: of the elements in
+// `doubt` alone, or, where the scale itself is in doubt (`which`, the same for all lanes of a
+// group), of all.  The whole warp takes part.
+struct Codes {
+    uint32_t word, scale;
+};
 template <typename TI>
-__device__ __forceinline__ void store_codes(const float (&x)[8], const float (&err)[8], bool exact, bool active, int u, int dim, int team,
-                                            const Exact<TI>& again, double eps, uint8_t* codes, uint8_t* scales)
+__device__ __noinline__ Codes codes_again(Codes c, Exact<TI> e, uint32_t doubt, bool which, bool active, int d0, int dim, int team, double eps)
 {
+    const int width = dim / 32;
+    double sum = 0;
+    if (active)
+        for (int j = 0; j < 8; ++j) {
+            const double v = (double)to_f32(e.row[d0 + j]);
+            sum += v * v;
+        }
+    sum = team_sum(sum, team);
+    e.r = 1.0 / sqrt(sum / dim + eps);
+    double top = 0;
+    if (which) {
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) top = fmax(top, fabs(e(d0 + j)));
+    }
+#pragma unroll
+    for (int o = 4; o; o >>= 1)
+        if (o < width) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (which) {
+        c.scale = quant_scale_code(top);
+        doubt = c.scale ? 0xffu : 0u;
+        if (!c.scale) c.word = 0x88888888u;
+    }
+    const double s = (double)quant_scale(c.scale);
+    for (int j = 0; doubt; ++j, doubt >>= 1) {
+        if (!(doubt & 1)) continue;
+        const double code = fmin(fmax(rint(e(d0 + j) / s), -7.0), 7.0);
+        c.word = (c.word & ~(0xfu << (4 * j))) | (uint32_t)((int)code + 8) << (4 * j);
+    }
+    __syncwarp();
+    return c;
+}
+
+// Store a row's 8 elements d0.. of each lane u < D / 8 in 4 bits.  x: the values, err: how far
+// each may be off (EXACT: not at all).  All lanes of the warp take part.
+//
+// x / s comes from a product and one correction, which for 16-bit values lies on the right
+// side of every border (and on the border itself where x / s does); an f32 value's rest
+// x - c s, which is exact, decides.  Adding 1.5 2^23 + 8 rounds to the nearest (ties to even)
+// and leaves code + 8 in the low bits.
+template <typename TI, bool EXACT>
+__device__ __forceinline__ void store_codes(float (&x)[8], const float (&err)[8], bool active, int u, int dim, int team, const Exact<TI>& again,
+                                            double eps, uint8_t* codes, uint8_t* scales)
+{
+    constexpr float kRound = 12582912.f + 8.f;
     const int d0 = 8 * u, width = dim / 32;  // lanes of a group
     float amax = 0.f, emax = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+        if (x[j] != x[j]) x[j] = 0.f;  // a NaN is stored as zero
         amax = fmaxf(amax, fabsf(x[j]));
-        emax = fmaxf(emax, err[j]);
+        if (!EXACT) emax = fmaxf(emax, err[j]);
     }
 #pragma unroll
     for (int o = 4; o; o >>= 1) {
         if (o < width) {
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            emax = fmaxf(emax, __shfl_xor_sync(0xffffffffu, emax, o));
+            if (!EXACT) emax = fmaxf(emax, __shfl_xor_sync(0xffffffffu, emax, o));
         }
     }
-    uint32_t scale = quant_scale_code(amax);
-    const bool which = active && !exact && quant_scale_code(fmaxf(amax - emax, 0.f)) != quant_scale_code(amax + emax);
-    float s = quant_scale(scale);
-    float inv = s > 0.f ? 1.f / s : 0.f;
-    uint32_t word = 0, doubt = 0;
+    Codes c;
+    c.scale = quant_scale_code(amax);
+    const float s = quant_scale(c.scale), half = 0.5f * s, limit = 7.25f * s;
+    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+    float near = 0.f;  // the largest distance from a code, with its error
+    uint32_t bits = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float c = rintf(fminf(fmaxf(x[j] * inv, -9.f), 9.f));
-        const float rest = fmaf(-c, s, x[j]);  // exact
-        const float over = fabsf(rest) - 0.5f * s;
-        if (exact) {
-            if (over > 0.f || (over == 0.f && ((int)c & 1))) c += rest > 0.f ? 1.f : -1.f;
-        } else if (fabsf(over) <= err[j]) {
-            doubt |= 1u << j;
-        } else if (over > 0.f) {
-            c += rest > 0.f ? 1.f : -1.f;
+    for (int j = 7; j >= 0; --j) {
+        x[j] = fminf(fmaxf(x[j], -limit), limit);  // (the same code, 7 or -7)
+        float q = x[j] * inv;
+        q = fmaf(fmaf(-q, s, x[j]), inv, q) + kRound;
+        if (!EXACT || sizeof(TI) == 4) {
+            const float rest = fabsf(fmaf(kRound - q, s, x[j]));
+            near = fmaxf(near, EXACT ? rest : rest + err[j]);
         }
-        const int code = min(max((int)c, -7), 7) + 8;
-        word |= (uint32_t)(s > 0.f ? code : 8) << (4 * j);
+        bits = bits * 16 + __float_as_uint(q);
     }
-    if (!active || s == 0.f) doubt = 0;
-    if (__any_sync(0xffffffffu, which || doubt)) {
-        // Rare: borders decided in 64 bits.
-        Exact<TI> e = again;
-        double sum = 0;
-        if (active)
+    // (the sum of the 1.5 2^23s, which the low bits of each stand above)
+    constexpr uint32_t kBias = 0x4b400000u * 0x11111111u;
+    c.word = bits - kBias;
+    if (EXACT && sizeof(TI) == 4) {
+        // an f32 value nearer to a border than its quotient's rounding: decided by its rest
+        if (near >= half && s > 0.f) {
+#pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const double v = (double)to_f32(e.row[d0 + j]);
-                sum += v * v;
+                float code = (float)((int)(c.word >> (4 * j) & 15) - 8);
+                const float rest = fmaf(-code, s, x[j]);
+                if (fabsf(rest) > half || (fabsf(rest) == half && ((int)code & 1))) code += rest > 0.f ? 1.f : -1.f;
+                c.word = (c.word & ~(0xfu << (4 * j))) | (uint32_t)((int)code + 8) << (4 * j);
             }
-        sum = team_sum(sum, team);
-        e.r = 1.0 / sqrt(sum / dim + eps);
-        double top = 0;
-        if (which) {
-#pragma unroll 1
-            for (int j = 0; j < 8; ++j) top = fmax(top, fabs(e(d0 + j)));
         }
+    }
+    if (!EXACT) {
+        // Does a border lie within an element's error, or between two scales within the largest's?
+        const float above = 3.5f * (s + quant_scale(c.scale + 1)), below = c.scale ? 3.5f * (s + quant_scale(c.scale - 1)) : -1.f;
+        const bool which = active && ((amax + emax >= above && c.scale < kQuantTopScale) || amax - emax <= below);
+        if (__any_sync(0xffffffffu, active && (which || (near >= half && s > 0.f)))) {
+            uint32_t doubt = 0;
 #pragma unroll
-        for (int o = 4; o; o >>= 1)
-            if (o < width) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (which) {
-            scale = quant_scale_code(top);
-            s = quant_scale(scale);
-            doubt = s > 0.f ? 0xffu : 0u;
-            if (s == 0.f) word = 0x88888888u;
+            for (int j = 0; j < 8; ++j) {
+                const float rest = fmaf(-(float)((int)(c.word >> (4 * j) & 15) - 8), s, x[j]);
+                if (fabsf(rest) + err[j] >= half) doubt |= 1u << j;
+            }
+            if (!active || s == 0.f) doubt = 0;
+            c = codes_again<TI>(c, again, doubt, which, active, d0, dim, team, eps);
         }
-        for (int j = 0; doubt; ++j, doubt >>= 1) {
-            if (!(doubt & 1)) continue;
-            const double c = fmin(fmax(rint(e(d0 + j) / (double)s), -7.0), 7.0);
-            word = (word & ~(0xfu << (4 * j))) | (uint32_t)((int)c + 8) << (4 * j);
-        }
-        __syncwarp();
     }
     if (active) {
-        *reinterpret_cast<uint32_t*>(codes + d0 / 2) = word;
-        if ((u & (width - 1)) == 0) scales[u / width] = (uint8_t)scale;
+        *reinterpret_cast<uint32_t*>(codes + d0 / 2) = c.word;
+        if ((u & (width - 1)) == 0) scales[u / width] = (uint8_t)c.scale;
+    }
+}
+
+// Where a token's row of k or v goes: its place in its sequence, its page and slot.
+struct Home {
+    int place, page, slot;
+    bool active;  // false: padding, or no place in the pool
+};
+// All lanes of a warp take part, with ascending tokens.
+__device__ __forceinline__ Home home_of(const TurnParams& p, int t, bool active, bool pages)
+{
+    Home r = {0, 0, 0, active};
+    if (!p.append) return r;
+    const int first = __shfl_sync(0xffffffffu, t, 0);
+    int seq = warp_sequence_of(p.batch, first);
+    while (seq < p.batch.seqs && p.batch.q_offsets[seq + 1] <= t) ++seq;
+    if (seq >= p.batch.seqs) {
+        r.active = false;
+        return r;
+    }
+    r.place = p.batch.kv_lens[seq] - (p.batch.q_offsets[seq + 1] - t);
+    if (!pages || !active) return r;
+    const int at = r.place / p.page_size;
+    r.page = -1;
+    if (r.place >= 0 && at < p.batch.table_pages) r.page = p.batch.table[seq * p.batch.table_stride + at];
+    r.slot = r.place - at * p.page_size;
+    if (r.page < 0 || r.page >= p.pages) {
+        *p.index_error = 1;
+        r.active = false;
+    }
+    return r;
+}
+
+// The k or v rows of heads h0 .. h1 - 1 of a token to a 4-bit cache: a lane ends with eight
+// consecutive elements of a row.  It starts with them too, unless pairs lie half the rotated
+// part apart: those are rotated in two chunks and go through shared memory.
+template <typename TI, int VEC>
+__device__ __forceinline__ void quant_rows(const NormTurnParams& np, int kind, int h0, int h1, int t, bool token, float* values, float* errors)
+{
+    constexpr int NU = VEC == 1 ? 4 : 1;
+    const TurnParams& p = np.t;
+    const int u0 = threadIdx.x & (np.team - 1);
+    const TI* src = static_cast<const TI*>(p.src[kind]) + t * p.src_token[kind];
+    const float* weight = kind == 2 ? nullptr : np.weight[1];
+    const bool rotating = p.turns != nullptr && kind != 2;
+    const bool apart = VEC == 1 || (rotating && !p.adjacent);
+    const bool exact = !weight && !rotating;
+
+    Unit<VEC> unit[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+        const int u = u0 + 32 * i;
+        unit[i] = unit_of<VEC>(u, p.dim, p.rotary, p.adjacent);
+        if (!apart) {
+            unit[i].lo = 8 * u;
+            unit[i].hi = 8 * u + 4;
+            unit[i].turns = 8 * u < p.rotary;
+        }
+        unit[i].turns = unit[i].turns && rotating;
+        unit[i].held = unit[i].held && token;
+        unit[i].has_hi = unit[i].has_hi && token;
+    }
+    Chunk<TI, VEC> a[NU] = {}, b[NU] = {};
+    auto load = [&](int h) {
+        const TI* row = src + h * p.src_head[kind];
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            if (unit[i].held) a[i] = *reinterpret_cast<const Chunk<TI, VEC>*>(row + unit[i].lo);
+            if (unit[i].has_hi) b[i] = *reinterpret_cast<const Chunk<TI, VEC>*>(row + unit[i].hi);
+        }
+    };
+    load(h0);
+    float cs[NU][VEC], sn[NU][VEC], wx[NU][VEC], wy[NU][VEC];
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            wx[i][j] = weight && unit[i].held ? weight[unit[i].lo + j] : 1.f;
+            wy[i][j] = weight && unit[i].has_hi ? weight[unit[i].hi + j] : 1.f;
+        }
+
+    const Home home = home_of(p, t, token, true);
+    if (__ballot_sync(0xffffffffu, home.active) == 0) return;
+    const int place = home.place;
+    const bool mine = home.active && u0 < p.dim / 8;
+    uint8_t* codes = static_cast<uint8_t*>(p.pool[kind - 1]) + home.page * p.page_stride + home.slot * p.slot_stride;
+    uint8_t* scales = np.scales[kind - 1] + home.page * np.scale_page + home.slot * np.scale_slot;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+        const int u = u0 + 32 * i;
+        if (unit[i].held && unit[i].turns) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int f = pair_of<VEC>(unit[i], u, j, p.adjacent);
+                const int32_t frac = (int32_t)(fraction(p.turns[f], p.pos, p.tokens, t, place) >> 32);
+                sincospif((float)frac * 4.656612873077393e-10f /* 2^-31: half turns */, &sn[i][j], &cs[i][j]);
+            }
+        }
+    }
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h) {
+        alignas(16) float x[NU][VEC], y[NU][VEC], ex[NU][VEC], ey[NU][VEC];
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                x[i][j] = to_f32(a[i].v[j]);
+                y[i][j] = to_f32(b[i].v[j]);
+            }
+        if (h + 1 < h1) load(h + 1);
+        if (weight) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                float part = 0.f;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) part += fmaf(x[i][j], x[i][j], y[i][j] * y[i][j]);
+                sum += part;
+            }
+            const float r = rsqrtf(fmaf(team_sum(sum, np.team), np.inverse_dim, np.eps_f));
+#pragma unroll
+            for (int i = 0; i < NU; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    x[i][j] *= r * wx[i][j];
+                    y[i][j] *= r * wy[i][j];
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            sizes<VEC>(x[i], y[i], ex[i], ey[i], unit[i].turns, p.adjacent);
+            if (unit[i].turns) rotate<VEC>(x[i], y[i], cs[i], sn[i], p.adjacent);
+        }
+        alignas(16) float v[8] = {}, e[8] = {};
+        if (!apart) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = x[0][j % VEC];
+                v[4 + j] = y[0][j % VEC];
+                e[j] = ex[0][j % VEC];
+                e[4 + j] = ey[0][j % VEC];
+            }
+        } else {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                if (unit[i].held) {
+                    *reinterpret_cast<Chunk<float, VEC>*>(values + unit[i].lo) = *reinterpret_cast<const Chunk<float, VEC>*>(x[i]);
+                    *reinterpret_cast<Chunk<float, VEC>*>(errors + unit[i].lo) = *reinterpret_cast<const Chunk<float, VEC>*>(ex[i]);
+                }
+                if (unit[i].has_hi) {
+                    *reinterpret_cast<Chunk<float, VEC>*>(values + unit[i].hi) = *reinterpret_cast<const Chunk<float, VEC>*>(y[i]);
+                    *reinterpret_cast<Chunk<float, VEC>*>(errors + unit[i].hi) = *reinterpret_cast<const Chunk<float, VEC>*>(ey[i]);
+                }
+            }
+            __syncwarp();
+            if (mine) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    *reinterpret_cast<float4*>(v + j) = *reinterpret_cast<const float4*>(values + 8 * u0 + j);
+                    *reinterpret_cast<float4*>(e + j) = *reinterpret_cast<const float4*>(errors + 8 * u0 + j);
+                }
+            }
+        }
+        uint8_t *row_codes = codes + h * p.head_stride, *row_scales = scales + h * np.scale_head;
+        const Exact<TI> again = {src + h * p.src_head[kind], weight, rotating ? p.turns : nullptr, p.pos, 0.0, p.tokens, t, place, p.rotary, p.adjacent};
+        if (exact) {
+            store_codes<TI, true>(v, e, mine, u0, p.dim, np.team, again, np.eps, row_codes, row_scales);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] *= kRowError;
+            store_codes<TI, false>(v, e, mine, u0, p.dim, np.team, again, np.eps, row_codes, row_scales);
+        }
     }
 }
 
@@ -254,81 +469,74 @@ template <typename TI, typename TO, int VEC, bool QUANT>
 __global__ void __launch_bounds__(kThreads) bitlin_norm_turn(const NormTurnParams np)
 {
     constexpr int NU = VEC == 1 ? 4 : 1;  // units of a lane
-    __shared__ float buffer[QUANT ? kThreads / 32 : 1][2][QUANT ? kMaxDim : 1];
+    __shared__ __align__(16) float buffer[QUANT ? kThreads / 32 : 1][2][QUANT ? kMaxDim : 4];
     ptx::griddep_wait();
     const TurnParams& p = np.t;
     const int lane = threadIdx.x & 31, u0 = lane & (np.team - 1);
     const uint32_t idx = (blockIdx.x * (uint32_t)kThreads + threadIdx.x) / (uint32_t)np.team;
     const int t = (int)min(idx, (uint32_t)(p.tokens - 1));
-    bool active = idx < (uint32_t)p.tokens;
+    const bool token = idx < (uint32_t)p.tokens;
 
-    int kind = 0, group = blockIdx.y;  // q, k or v, and which heads of it
-    if (group >= p.q_groups) {
-        group -= p.q_groups;
-        kind = 1;
+    // k, v or q, and which heads of it (the blocks that take longest come first)
+    int kind = 1, group = blockIdx.y;
+    if (group >= p.kv_groups) {
+        group -= p.kv_groups;
+        kind = 2;
         if (group >= p.kv_groups) {
             group -= p.kv_groups;
-            kind = 2;
+            kind = 0;
         }
     }
     const int heads = kind == 0 ? p.heads : p.kv_heads;
-    const int h0 = group * kHeadsPerTeam;
-
-    // the token's place in its sequence (all lanes take part in the search)
-    int place = 0, seq = 0;
-    if (p.append) {
-        const uint32_t first = __shfl_sync(0xffffffffu, (uint32_t)t, 0);
-        seq = warp_sequence_of(p.batch, (int)first);
-        while (seq < p.batch.seqs && p.batch.q_offsets[seq + 1] <= t) ++seq;
-        if (seq >= p.batch.seqs) active = false;  // padding
-        else place = p.batch.kv_lens[seq] - (p.batch.q_offsets[seq + 1] - t);
+    const int h0 = group * (QUANT && kind ? np.kv_heads_per_team : kHeadsPerTeam);
+    if (QUANT && kind) {
+        float* row = buffer[threadIdx.x >> 5][0] + lane / np.team * p.dim;
+        quant_rows<TI, VEC>(np, kind, h0, min(h0 + np.kv_heads_per_team, heads), t, token, row, row + kMaxDim);
+        return;
     }
-
-    // where the row goes
-    TO* dst = nullptr;
-    uint8_t *codes = nullptr, *scales = nullptr;
-    long long dst_head = 0;
-    if (kind == 0) {
-        dst = static_cast<TO*>(p.out) + t * p.out_token;
-        dst_head = p.out_head;
-    } else if (active) {
-        const int at = place / p.page_size;
-        int page = -1;
-        if (place >= 0 && at < p.batch.table_pages) page = p.batch.table[seq * p.batch.table_stride + at];
-        if (page < 0 || page >= p.pages) {
-            *p.index_error = 1;
-            active = false;
-        } else {
-            const long long slot = place - at * p.page_size;
-            dst_head = p.head_stride;
-            if (QUANT) {
-                codes = static_cast<uint8_t*>(p.pool[kind - 1]) + page * p.page_stride + slot * p.slot_stride;
-                scales = np.scales[kind - 1] + page * np.scale_page + slot * np.scale_slot;
-            } else {
-                dst = static_cast<TO*>(p.pool[kind - 1]) + page * p.page_stride + slot * p.slot_stride;
-            }
-        }
-    }
-    if (__ballot_sync(0xffffffffu, active) == 0) return;
     const TI* src = static_cast<const TI*>(p.src[kind]) + t * p.src_token[kind];
     const long long src_head = p.src_head[kind];
     const float* weight = kind == 2 ? nullptr : np.weight[kind];
     const bool rotating = p.turns != nullptr && kind != 2;
 
     Unit<VEC> unit[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+        unit[i] = unit_of<VEC>(u0 + 32 * i, p.dim, p.rotary, p.adjacent);
+        unit[i].turns = unit[i].turns && rotating;
+    }
+    Chunk<TI, VEC> a[kHeadsPerTeam][NU] = {}, b[kHeadsPerTeam][NU] = {};
+#pragma unroll
+    for (int h = 0; h < kHeadsPerTeam; ++h) {
+        if (h0 + h < heads && token) {
+            const TI* row = src + (h0 + h) * src_head;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                if (unit[i].held) a[h][i] = *reinterpret_cast<const Chunk<TI, VEC>*>(row + unit[i].lo);
+                if (unit[i].has_hi) b[h][i] = *reinterpret_cast<const Chunk<TI, VEC>*>(row + unit[i].hi);
+            }
+        }
+    }
+
+    const Home home = home_of(p, t, token, kind != 0);
+    const bool active = home.active;
+    const int place = home.place;
+    TO* dst = kind == 0 ? static_cast<TO*>(p.out) + t * p.out_token
+                        : static_cast<TO*>(p.pool[kind - 1]) + home.page * p.page_stride + home.slot * p.slot_stride;
+    const long long dst_head = kind == 0 ? p.out_head : p.head_stride;
+    if (__ballot_sync(0xffffffffu, active) == 0) return;
+
     float cs[NU][VEC], sn[NU][VEC], wx[NU][VEC], wy[NU][VEC];
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
         const int u = u0 + 32 * i;
-        unit[i] = unit_of<VEC>(u, p.dim, p.rotary, p.adjacent);
-        unit[i].turns = unit[i].turns && rotating;
         const bool mine = active && unit[i].held;
         if (mine && unit[i].turns) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 const int f = pair_of<VEC>(unit[i], u, j, p.adjacent);
                 const int32_t frac = (int32_t)(fraction(p.turns[f], p.pos, p.tokens, t, place) >> 32);
-                if (sizeof(TO) == 2 && !(QUANT && kind == 1)) {
+                if (sizeof(TO) == 2) {
                     const float angle = (float)frac * 1.4629180792671596e-9f;  // 2^-32 of a turn, in radians
                     sn[i][j] = __sinf(angle);
                     cs[i][j] = __cosf(angle);
@@ -346,18 +554,6 @@ __global__ void __launch_bounds__(kThreads) bitlin_norm_turn(const NormTurnParam
         }
     }
 
-    Chunk<TI, VEC> a[kHeadsPerTeam][NU] = {}, b[kHeadsPerTeam][NU] = {};
-#pragma unroll
-    for (int h = 0; h < kHeadsPerTeam; ++h) {
-        if (h0 + h < heads && active) {
-            const TI* row = src + (h0 + h) * src_head;
-#pragma unroll
-            for (int i = 0; i < NU; ++i) {
-                if (unit[i].held) a[h][i] = *reinterpret_cast<const Chunk<TI, VEC>*>(row + unit[i].lo);
-                if (unit[i].has_hi) b[h][i] = *reinterpret_cast<const Chunk<TI, VEC>*>(row + unit[i].hi);
-            }
-        }
-    }
     float r[kHeadsPerTeam];
     if (weight) {
 #pragma unroll
@@ -373,13 +569,13 @@ __global__ void __launch_bounds__(kThreads) bitlin_norm_turn(const NormTurnParam
                 }
                 sum += part;
             }
-            r[h] = rsqrtf(team_sum(sum, np.team) / p.dim + (float)np.eps);
+            r[h] = rsqrtf(fmaf(team_sum(sum, np.team), np.inverse_dim, np.eps_f));
         }
     }
 #pragma unroll
     for (int h = 0; h < kHeadsPerTeam; ++h) {
         if (h0 + h >= heads) break;
-        float x[NU][VEC], y[NU][VEC], ex[NU][VEC], ey[NU][VEC];
+        float x[NU][VEC], y[NU][VEC];
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
 #pragma unroll
@@ -391,55 +587,20 @@ __global__ void __launch_bounds__(kThreads) bitlin_norm_turn(const NormTurnParam
                     y[i][j] *= r[h] * wy[i][j];
                 }
             }
-            if (QUANT) sizes<VEC>(x[i], y[i], ex[i], ey[i], unit[i].turns, p.adjacent);
             if (unit[i].turns) rotate<VEC>(x[i], y[i], cs[i], sn[i], p.adjacent);
         }
-        if (!QUANT || kind == 0) {
-            if (!active) continue;
-            TO* row = dst + (h0 + h) * dst_head;
+        if (!active) continue;
+        TO* row = dst + (h0 + h) * dst_head;
 #pragma unroll
-            for (int i = 0; i < NU; ++i) {
-                Chunk<TO, VEC> c, d;
+        for (int i = 0; i < NU; ++i) {
+            Chunk<TO, VEC> c, d;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    c.v[j] = from_f32<TO>(x[i][j]);
-                    d.v[j] = from_f32<TO>(y[i][j]);
-                }
-                if (unit[i].held) *reinterpret_cast<Chunk<TO, VEC>*>(row + unit[i].lo) = c;
-                if (unit[i].has_hi) *reinterpret_cast<Chunk<TO, VEC>*>(row + unit[i].hi) = d;
+            for (int j = 0; j < VEC; ++j) {
+                c.v[j] = from_f32<TO>(x[i][j]);
+                d.v[j] = from_f32<TO>(y[i][j]);
             }
-        } else {
-            // through shared memory to 8 consecutive elements a lane
-            const bool exact = !weight && !rotating;
-            float* values = buffer[threadIdx.x >> 5][0] + lane / np.team * p.dim;
-            float* errors = buffer[threadIdx.x >> 5][1] + lane / np.team * p.dim;
-#pragma unroll
-            for (int i = 0; i < NU; ++i) {
-                if (!unit[i].held) continue;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    values[unit[i].lo + j] = x[i][j];
-                    errors[unit[i].lo + j] = ex[i][j];
-                    if (unit[i].has_hi) {
-                        values[unit[i].hi + j] = y[i][j];
-                        errors[unit[i].hi + j] = ey[i][j];
-                    }
-                }
-            }
-            __syncwarp();
-            const bool mine = active && u0 < p.dim / 8;
-            float v[8], e[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = mine ? values[8 * u0 + j] : 0.f;
-                e[j] = mine && !exact ? kRowError * errors[8 * u0 + j] : 0.f;
-                if (v[j] != v[j]) v[j] = 0.f;
-            }
-            __syncwarp();
-            const Exact<TI> again = {src + (h0 + h) * src_head, weight, rotating ? p.turns : nullptr, p.pos, 0.0,
-                                     p.tokens, t, place, p.rotary, p.adjacent};
-            store_codes<TI>(v, e, exact, mine, u0, p.dim, np.team, again, np.eps, codes + (h0 + h) * dst_head,
-                            scales + (h0 + h) * np.scale_head);
+            if (unit[i].held) *reinterpret_cast<Chunk<TO, VEC>*>(row + unit[i].lo) = c;
+            if (unit[i].has_hi) *reinterpret_cast<Chunk<TO, VEC>*>(row + unit[i].hi) = d;
         }
     }
 }
@@ -525,8 +686,8 @@ __global__ void __launch_bounds__(kThreads) bitlin_norm_grad(const NormGradParam
             }
             squares = team_sum(squares, p.team);
             products = team_sum(products, p.team);
-            const float r = rsqrtf(squares / p.dim + (float)p.eps);
-            const float mean = products * r / p.dim * r;  // mean(h n) r: n = x r
+            const float r = rsqrtf(fmaf(squares, p.inverse_dim, p.eps_f));
+            const float mean = products * p.inverse_dim * r * r;  // mean(h n) r: n = x r
             if (h0 + h >= p.heads || !active) continue;
             TX* dx = static_cast<TX*>(p.dx) + t * p.dx_token + (h0 + h) * p.dx_head;
 #pragma unroll
@@ -568,8 +729,10 @@ __global__ void __launch_bounds__(1024) bitlin_norm_grad_join(const float* parti
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
     float sum = 0.f;
-    if (d < dim)
+    if (d < dim) {
+#pragma unroll 8
         for (int k = row; k < blocks; k += 32) sum += partial[(long long)k * dim + d];
+    }
     sums[row][lane] = sum;
     __syncthreads();
     if (row == 0 && d < dim) {
@@ -608,8 +771,13 @@ template <typename TI, typename TO, int VEC, bool QUANT>
 cudaError_t launch(NormTurnParams& p, cudaStream_t s)
 {
     p.team = team_of(p.t.dim, VEC);
+    p.inverse_dim = 1.f / p.t.dim;
+    p.eps_f = (float)p.eps;
     p.t.q_groups = (p.t.heads + kHeadsPerTeam - 1) / kHeadsPerTeam;
-    p.t.kv_groups = p.t.append ? (p.t.kv_heads + kHeadsPerTeam - 1) / kHeadsPerTeam : 0;
+    // k and v to 4 bits: a team takes as many heads of a token as leave 24 teams to an SM's share of warps
+    const long long rows = 2LL * p.t.tokens * p.t.kv_heads * p.team / 32, most = rows / (24 * 152);
+    p.kv_heads_per_team = !QUANT ? kHeadsPerTeam : most < 1 ? 1 : most < p.t.kv_heads ? (int)most : p.t.kv_heads;
+    p.t.kv_groups = p.t.append ? (p.t.kv_heads + p.kv_heads_per_team - 1) / p.kv_heads_per_team : 0;
     const uint64_t threads = (uint64_t)p.t.tokens * p.team;
     cudaLaunchAttribute attr = {};
     const cudaLaunchConfig_t cfg =
@@ -654,6 +822,8 @@ cudaError_t grad(const NormGradParams& np, cudaStream_t s)
     const bool wide = p.rotary % 8 == 0 && (p.dim - p.rotary) % 8 == 0 && chunked(p.dy, p.dy_token, p.dy_head, sizeof(TY)) &&
                       chunked(p.x, p.x_token, p.x_head, sizeof(TX)) && chunked(p.dx, p.dx_token, p.dx_head, sizeof(TX));
     p.team = team_of(p.dim, wide ? 4 : 1);
+    p.inverse_dim = 1.f / p.dim;
+    p.eps_f = (float)p.eps;
     p.blocks = bitlin_norm_grad_blocks(p.tokens, p.heads);
     cudaLaunchAttribute attr = {};
     cudaLaunchConfig_t cfg = config(dim3(p.blocks), kThreads, s, &attr);
