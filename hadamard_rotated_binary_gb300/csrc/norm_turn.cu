@@ -31,6 +31,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kHeadsPerTeam = 4;
 constexpr int kMaxDim = 256;
+constexpr int kGradHeads = 4, kGradBlocks = 4;  // heads that a team of the gradient takes, blocks on an SM
 constexpr float kRowError = 24.f * 5.9604645e-8f;
 
 template <typename T, int VEC>
@@ -38,11 +39,60 @@ struct alignas(sizeof(T) * VEC) Chunk {
     T v[VEC];
 };
 
+// A chunk's elements, 16-bit ones two by two.
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const Chunk<T, VEC>& c, float (&x)[VEC])
+{
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) x[j] = to_f32(c.v[j]);
+}
+template <>
+__device__ __forceinline__ void unpack(const Chunk<__nv_bfloat16, 4>& c, float (&x)[4])
+{
+    const uint2 w = *reinterpret_cast<const uint2*>(&c);
+    x[0] = __uint_as_float(w.x << 16);
+    x[1] = __uint_as_float(w.x & 0xffff0000u);
+    x[2] = __uint_as_float(w.y << 16);
+    x[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+template <>
+__device__ __forceinline__ void unpack(const Chunk<__half, 4>& c, float (&x)[4])
+{
+    const uint2 w = *reinterpret_cast<const uint2*>(&c);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+    x[0] = a.x;
+    x[1] = a.y;
+    x[2] = b.x;
+    x[3] = b.y;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Chunk<T, VEC> pack(const float (&x)[VEC])
+{
+    Chunk<T, VEC> c;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) c.v[j] = from_f32<T>(x[j]);
+    return c;
+}
+template <>
+__device__ __forceinline__ Chunk<__nv_bfloat16, 4> pack(const float (&x)[4])
+{
+    const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(x[0], x[1]), __floats2bfloat162_rn(x[2], x[3])};
+    return *reinterpret_cast<const Chunk<__nv_bfloat16, 4>*>(w);
+}
+template <>
+__device__ __forceinline__ Chunk<__half, 4> pack(const float (&x)[4])
+{
+    const __half2 w[2] = {__floats2half2_rn(x[0], x[1]), __floats2half2_rn(x[2], x[3])};
+    return *reinterpret_cast<const Chunk<__half, 4>*>(w);
+}
+
 __device__ __forceinline__ float team_sum(float v, int team)
 {
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        if (o < team) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 16; o; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, v, o);
+        v += o < team ? other : 0.f;
+    }
     return v;
 }
 
@@ -212,32 +262,36 @@ __device__ __noinline__ Codes codes_again(Codes c, Exact<TI> e, uint32_t doubt, 
     return c;
 }
 
-// Store a row's 8 elements d0.. of each lane u < D / 8 in 4 bits.  x: the values, err: how far
-// each may be off (EXACT: not at all).  All lanes of the warp take part.
+// Store a row's 8 elements d0.. of each lane u < D / 8 in 4 bits.  x: the values, size: |a| + |b|
+// of each, kRowError of which it may be off (EXACT: nothing).  All lanes of the warp take part.
 //
 // x / s comes from a product and one correction, which for 16-bit values lies on the right
 // side of every border (and on the border itself where x / s does); an f32 value's rest
 // x - c s, which is exact, decides.  Adding 1.5 2^23 + 8 rounds to the nearest (ties to even)
 // and leaves code + 8 in the low bits.
-template <typename TI, bool EXACT>
-__device__ __forceinline__ void store_codes(float (&x)[8], const float (&err)[8], bool active, int u, int dim, int team, const Exact<TI>& again,
+template <typename TI, bool EXACT, typename Again>
+__device__ __forceinline__ void store_codes(float (&x)[8], const float (&size)[8], bool active, int u, int dim, int team, Again again,
                                             double eps, uint8_t* codes, uint8_t* scales)
 {
     constexpr float kRound = 12582912.f + 8.f;
-    const int d0 = 8 * u, width = dim / 32;  // lanes of a group
-    float amax = 0.f, emax = 0.f;
+    const int d0 = 8 * u, width = dim / 32;  // lanes of a group: 2, 4 or 8
+    float amax = 0.f, emax = 0.f, finite = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        if (x[j] != x[j]) x[j] = 0.f;  // a NaN is stored as zero
+        finite = fmaf(x[j], 0.f, finite);
         amax = fmaxf(amax, fabsf(x[j]));
-        if (!EXACT) emax = fmaxf(emax, err[j]);
+        if (!EXACT) emax = fmaxf(emax, size[j]);
+    }
+    if (finite != 0.f) {  // (an infinity or a NaN, which is stored as zero)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (x[j] != x[j]) x[j] = 0.f;
     }
 #pragma unroll
     for (int o = 4; o; o >>= 1) {
-        if (o < width) {
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            if (!EXACT) emax = fmaxf(emax, __shfl_xor_sync(0xffffffffu, emax, o));
-        }
+        const int lane = o < width ? o : 0;  // (0: its own)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, lane));
+        if (!EXACT) emax = fmaxf(emax, __shfl_xor_sync(0xffffffffu, emax, lane));
     }
     Codes c;
     c.scale = quant_scale_code(amax);
@@ -252,7 +306,7 @@ __device__ __forceinline__ void store_codes(float (&x)[8], const float (&err)[8]
         q = fmaf(fmaf(-q, s, x[j]), inv, q) + kRound;
         if (!EXACT || sizeof(TI) == 4) {
             const float rest = fabsf(fmaf(kRound - q, s, x[j]));
-            near = fmaxf(near, EXACT ? rest : rest + err[j]);
+            near = fmaxf(near, EXACT ? rest : fmaf(size[j], kRowError, rest));
         }
         bits = bits * 16 + __float_as_uint(q);
     }
@@ -273,6 +327,7 @@ __device__ __forceinline__ void store_codes(float (&x)[8], const float (&err)[8]
     }
     if (!EXACT) {
         // Does a border lie within an element's error, or between two scales within the largest's?
+        emax *= kRowError;
         const float above = 3.5f * (s + quant_scale(c.scale + 1)), below = c.scale ? 3.5f * (s + quant_scale(c.scale - 1)) : -1.f;
         const bool which = active && ((amax + emax >= above && c.scale < kQuantTopScale) || amax - emax <= below);
         if (__any_sync(0xffffffffu, active && (which || (near >= half && s > 0.f)))) {
@@ -280,10 +335,10 @@ __device__ __forceinline__ void store_codes(float (&x)[8], const float (&err)[8]
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float rest = fmaf(-(float)((int)(c.word >> (4 * j) & 15) - 8), s, x[j]);
-                if (fabsf(rest) + err[j] >= half) doubt |= 1u << j;
+                if (fmaf(size[j], kRowError, fabsf(rest)) >= half) doubt |= 1u << j;
             }
             if (!active || s == 0.f) doubt = 0;
-            c = codes_again<TI>(c, again, doubt, which, active, d0, dim, team, eps);
+            c = codes_again<TI>(c, again(), doubt, which, active, d0, dim, team, eps);
         }
     }
     if (active) {
@@ -331,7 +386,6 @@ __device__ __forceinline__ void quant_rows(const NormTurnParams& np, int kind, i
     constexpr int NU = VEC == 1 ? 4 : 1;
     const TurnParams& p = np.t;
     const int u0 = threadIdx.x & (np.team - 1);
-    const TI* src = static_cast<const TI*>(p.src[kind]) + t * p.src_token[kind];
     const float* weight = kind == 2 ? nullptr : np.weight[1];
     const bool rotating = p.turns != nullptr && kind != 2;
     const bool apart = VEC == 1 || (rotating && !p.adjacent);
@@ -352,15 +406,17 @@ __device__ __forceinline__ void quant_rows(const NormTurnParams& np, int kind, i
         unit[i].has_hi = unit[i].has_hi && token;
     }
     Chunk<TI, VEC> a[NU] = {}, b[NU] = {};
-    auto load = [&](int h) {
-        const TI* row = src + h * p.src_head[kind];
+    const long long src_head = p.src_head[kind], code_head = p.head_stride, scale_head = np.scale_head;
+    const TI* row = static_cast<const TI*>(p.src[kind]) + t * p.src_token[kind] + h0 * src_head;
+    auto load = [&]() {
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
             if (unit[i].held) a[i] = *reinterpret_cast<const Chunk<TI, VEC>*>(row + unit[i].lo);
             if (unit[i].has_hi) b[i] = *reinterpret_cast<const Chunk<TI, VEC>*>(row + unit[i].hi);
         }
+        row += src_head;
     };
-    load(h0);
+    load();
     float cs[NU][VEC], sn[NU][VEC], wx[NU][VEC], wy[NU][VEC];
 #pragma unroll
     for (int i = 0; i < NU; ++i)
@@ -374,8 +430,8 @@ __device__ __forceinline__ void quant_rows(const NormTurnParams& np, int kind, i
     if (__ballot_sync(0xffffffffu, home.active) == 0) return;
     const int place = home.place;
     const bool mine = home.active && u0 < p.dim / 8;
-    uint8_t* codes = static_cast<uint8_t*>(p.pool[kind - 1]) + home.page * p.page_stride + home.slot * p.slot_stride;
-    uint8_t* scales = np.scales[kind - 1] + home.page * np.scale_page + home.slot * np.scale_slot;
+    uint8_t* codes = static_cast<uint8_t*>(p.pool[kind - 1]) + home.page * p.page_stride + home.slot * p.slot_stride + h0 * code_head;
+    uint8_t* scales = np.scales[kind - 1] + home.page * np.scale_page + home.slot * np.scale_slot + h0 * scale_head;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
         const int u = u0 + 32 * i;
@@ -389,16 +445,14 @@ __device__ __forceinline__ void quant_rows(const NormTurnParams& np, int kind, i
         }
     }
 #pragma unroll 1
-    for (int h = h0; h < h1; ++h) {
+    for (int h = h0; h < h1; ++h, codes += code_head, scales += scale_head) {
         alignas(16) float x[NU][VEC], y[NU][VEC], ex[NU][VEC], ey[NU][VEC];
 #pragma unroll
-        for (int i = 0; i < NU; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                x[i][j] = to_f32(a[i].v[j]);
-                y[i][j] = to_f32(b[i].v[j]);
-            }
-        if (h + 1 < h1) load(h + 1);
+        for (int i = 0; i < NU; ++i) {
+            unpack(a[i], x[i]);
+            unpack(b[i], y[i]);
+        }
+        if (h + 1 < h1) load();
         if (weight) {
             float sum = 0.f;
 #pragma unroll
@@ -408,7 +462,8 @@ __device__ __forceinline__ void quant_rows(const NormTurnParams& np, int kind, i
                 for (int j = 0; j < VEC; ++j) part += fmaf(x[i][j], x[i][j], y[i][j] * y[i][j]);
                 sum += part;
             }
-            const float r = rsqrtf(fmaf(team_sum(sum, np.team), np.inverse_dim, np.eps_f));
+            sum = team_sum(sum, np.team);
+            const float r = rsqrtf(fmaf(sum, np.inverse_dim, np.eps_f));
 #pragma unroll
             for (int i = 0; i < NU; ++i)
 #pragma unroll
@@ -453,20 +508,17 @@ __device__ __forceinline__ void quant_rows(const NormTurnParams& np, int kind, i
                 }
             }
         }
-        uint8_t *row_codes = codes + h * p.head_stride, *row_scales = scales + h * np.scale_head;
-        const Exact<TI> again = {src + h * p.src_head[kind], weight, rotating ? p.turns : nullptr, p.pos, 0.0, p.tokens, t, place, p.rotary, p.adjacent};
-        if (exact) {
-            store_codes<TI, true>(v, e, mine, u0, p.dim, np.team, again, np.eps, row_codes, row_scales);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] *= kRowError;
-            store_codes<TI, false>(v, e, mine, u0, p.dim, np.team, again, np.eps, row_codes, row_scales);
-        }
+        auto again = [&]() {
+            const TI* mine = static_cast<const TI*>(p.src[kind]) + t * p.src_token[kind] + h * src_head;
+            return Exact<TI>{mine, weight, rotating ? p.turns : nullptr, p.pos, 0.0, p.tokens, t, place, p.rotary, p.adjacent};
+        };
+        if (exact) store_codes<TI, true>(v, e, mine, u0, p.dim, np.team, again, np.eps, codes, scales);
+        else store_codes<TI, false>(v, e, mine, u0, p.dim, np.team, again, np.eps, codes, scales);
     }
 }
 
 template <typename TI, typename TO, int VEC, bool QUANT>
-__global__ void __launch_bounds__(kThreads) bitlin_norm_turn(const NormTurnParams np)
+__global__ void __launch_bounds__(kThreads, QUANT ? 7 : 1) bitlin_norm_turn(const NormTurnParams np)
 {
     constexpr int NU = VEC == 1 ? 4 : 1;  // units of a lane
     __shared__ __align__(16) float buffer[QUANT ? kThreads / 32 : 1][2][QUANT ? kMaxDim : 4];
@@ -561,46 +613,45 @@ __global__ void __launch_bounds__(kThreads) bitlin_norm_turn(const NormTurnParam
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                float part = 0.f;
+                float x[VEC], y[VEC], part = 0.f;
+                unpack(a[h][i], x);
+                unpack(b[h][i], y);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float x = to_f32(a[h][i].v[j]), y = to_f32(b[h][i].v[j]);
-                    part += fmaf(x, x, y * y);
-                }
+                for (int j = 0; j < VEC; ++j) part += fmaf(x[j], x[j], y[j] * y[j]);
                 sum += part;
             }
-            r[h] = rsqrtf(fmaf(team_sum(sum, np.team), np.inverse_dim, np.eps_f));
+            r[h] = sum;
         }
-    }
 #pragma unroll
-    for (int h = 0; h < kHeadsPerTeam; ++h) {
+        for (int o = 16; o; o >>= 1) {
+            if (o < np.team) {
+#pragma unroll
+                for (int h = 0; h < kHeadsPerTeam; ++h) r[h] += __shfl_xor_sync(0xffffffffu, r[h], o);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < kHeadsPerTeam; ++h) r[h] = rsqrtf(fmaf(r[h], np.inverse_dim, np.eps_f));
+    }
+    if (!active) return;
+    dst += h0 * dst_head;
+#pragma unroll
+    for (int h = 0; h < kHeadsPerTeam; ++h, dst += dst_head) {
         if (h0 + h >= heads) break;
-        float x[NU][VEC], y[NU][VEC];
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
+            float x[VEC], y[VEC];
+            unpack(a[h][i], x);
+            unpack(b[h][i], y);
+            if (weight) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                x[i][j] = to_f32(a[h][i].v[j]);
-                y[i][j] = to_f32(b[h][i].v[j]);
-                if (weight) {
-                    x[i][j] *= r[h] * wx[i][j];
-                    y[i][j] *= r[h] * wy[i][j];
+                for (int j = 0; j < VEC; ++j) {
+                    x[j] *= r[h] * wx[i][j];
+                    y[j] *= r[h] * wy[i][j];
                 }
             }
-            if (unit[i].turns) rotate<VEC>(x[i], y[i], cs[i], sn[i], p.adjacent);
-        }
-        if (!active) continue;
-        TO* row = dst + (h0 + h) * dst_head;
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-            Chunk<TO, VEC> c, d;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                c.v[j] = from_f32<TO>(x[i][j]);
-                d.v[j] = from_f32<TO>(y[i][j]);
-            }
-            if (unit[i].held) *reinterpret_cast<Chunk<TO, VEC>*>(row + unit[i].lo) = c;
-            if (unit[i].has_hi) *reinterpret_cast<Chunk<TO, VEC>*>(row + unit[i].hi) = d;
+            if (unit[i].turns) rotate<VEC>(x, y, cs[i], sn[i], p.adjacent);
+            if (unit[i].held) *reinterpret_cast<Chunk<TO, VEC>*>(dst + unit[i].lo) = pack<TO, VEC>(x);
+            if (unit[i].has_hi) *reinterpret_cast<Chunk<TO, VEC>*>(dst + unit[i].hi) = pack<TO, VEC>(y);
         }
     }
 }
@@ -608,10 +659,10 @@ __global__ void __launch_bounds__(kThreads) bitlin_norm_turn(const NormTurnParam
 // ---- the gradient -------------------------------------------------------------
 
 template <typename TY, typename TX, int VEC>
-__global__ void __launch_bounds__(kThreads) bitlin_norm_grad(const NormGradParams p)
+__global__ void __launch_bounds__(kThreads, kGradBlocks) bitlin_norm_grad(const NormGradParams p)
 {
     constexpr int NU = VEC == 1 ? 4 : 1;
-    constexpr int kHeads = 2;
+    constexpr int kHeads = kGradHeads;
     __shared__ float sums[kThreads / 8][kMaxDim];  // a row for each team
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31, u0 = lane & (p.team - 1);
@@ -667,42 +718,44 @@ __global__ void __launch_bounds__(kThreads) bitlin_norm_grad(const NormGradParam
         }
 #pragma unroll
         for (int h = 0; h < kHeads; ++h) {
-            float gx[NU][VEC], gy[NU][VEC];
+            float x[NU][VEC], y[NU][VEC], gx[NU][VEC], gy[NU][VEC];
             float squares = 0.f, products = 0.f;
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    gx[i][j] = to_f32(ga[h][i].v[j]);
-                    gy[i][j] = to_f32(gb[h][i].v[j]);
-                }
+                unpack(a[h][i], x[i]);
+                unpack(b[h][i], y[i]);
+                unpack(ga[h][i], gx[i]);
+                unpack(gb[h][i], gy[i]);
                 if (unit[i].held && unit[i].turns) rotate<VEC>(gx[i], gy[i], cs[i], sn[i], p.adjacent);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    const float x = to_f32(a[h][i].v[j]), y = to_f32(b[h][i].v[j]);
-                    squares += fmaf(x, x, y * y);
-                    products += fmaf(gx[i][j] * wx[i][j], x, gy[i][j] * wy[i][j] * y);
+                    squares += fmaf(x[i][j], x[i][j], y[i][j] * y[i][j]);
+                    products += fmaf(gx[i][j] * wx[i][j], x[i][j], gy[i][j] * wy[i][j] * y[i][j]);
                 }
             }
-            squares = team_sum(squares, p.team);
-            products = team_sum(products, p.team);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                if (o < p.team) {
+                    squares += __shfl_xor_sync(0xffffffffu, squares, o);
+                    products += __shfl_xor_sync(0xffffffffu, products, o);
+                }
+            }
             const float r = rsqrtf(fmaf(squares, p.inverse_dim, p.eps_f));
             const float mean = products * p.inverse_dim * r * r;  // mean(h n) r: n = x r
             if (h0 + h >= p.heads || !active) continue;
             TX* dx = static_cast<TX*>(p.dx) + t * p.dx_token + (h0 + h) * p.dx_head;
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                Chunk<TX, VEC> c, d;
+                float c[VEC], d[VEC];
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    const float x = to_f32(a[h][i].v[j]), y = to_f32(b[h][i].v[j]);
-                    dwx[i][j] = fmaf(gx[i][j], x * r, dwx[i][j]);
-                    dwy[i][j] = fmaf(gy[i][j], y * r, dwy[i][j]);
-                    c.v[j] = from_f32<TX>(r * (gx[i][j] * wx[i][j] - x * mean));
-                    d.v[j] = from_f32<TX>(r * (gy[i][j] * wy[i][j] - y * mean));
+                    dwx[i][j] = fmaf(gx[i][j], x[i][j] * r, dwx[i][j]);
+                    dwy[i][j] = fmaf(gy[i][j], y[i][j] * r, dwy[i][j]);
+                    c[j] = r * (gx[i][j] * wx[i][j] - x[i][j] * mean);
+                    d[j] = r * (gy[i][j] * wy[i][j] - y[i][j] * mean);
                 }
-                if (unit[i].held) *reinterpret_cast<Chunk<TX, VEC>*>(dx + unit[i].lo) = c;
-                if (unit[i].has_hi) *reinterpret_cast<Chunk<TX, VEC>*>(dx + unit[i].hi) = d;
+                if (unit[i].held) *reinterpret_cast<Chunk<TX, VEC>*>(dx + unit[i].lo) = pack<TX, VEC>(c);
+                if (unit[i].has_hi) *reinterpret_cast<Chunk<TX, VEC>*>(dx + unit[i].hi) = pack<TX, VEC>(d);
             }
         }
     }
@@ -856,10 +909,10 @@ cudaError_t bitlin_launch_norm_turn(const NormTurnParams& p, int src_dtype, int 
 
 int bitlin_norm_grad_blocks(int tokens, int heads)
 {
-    // eight blocks to each of the 152 SMs, or as many as there are tokens and pairs of heads for
-    const long long items = (long long)tokens * ((heads + 1) / 2);
+    // as many as run at once on 152 SMs, or as there are tokens and heads for
+    const long long items = (long long)tokens * ((heads + kGradHeads - 1) / kGradHeads);
     const long long blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
-    return (int)(blocks < 1216 ? blocks : 1216);
+    return (int)(blocks < kGradBlocks * 152 ? blocks : kGradBlocks * 152);
 }
 
 cudaError_t bitlin_launch_norm_grad(const NormGradParams& p, int dy_dtype, int x_dtype, cudaStream_t s)
