@@ -296,7 +296,8 @@ __device__ __forceinline__ void store_codes(float (&x)[8], const float (&size)[8
     Codes c;
     c.scale = quant_scale_code(amax);
     const float s = quant_scale(c.scale), half = 0.5f * s, limit = 7.25f * s;
-    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+    float inv = ptx::rcp(s);  // 1 / s, corrected once
+    inv = s > 0.f ? fmaf(fmaf(-s, inv, 1.f), inv, inv) : 0.f;
     float near = 0.f;  // the largest distance from a code, with its error
     uint32_t bits = 0;
 #pragma unroll
@@ -357,6 +358,10 @@ __device__ __forceinline__ Home home_of(const TurnParams& p, int t, bool active,
 {
     Home r = {0, 0, 0, active};
     if (!p.append) return r;
+    if (!pages && p.pos) {  // a row of q needs no place: is it padding?
+        r.active = active && t < p.batch.q_offsets[p.batch.seqs];
+        return r;
+    }
     const int first = __shfl_sync(0xffffffffu, t, 0);
     int seq = warp_sequence_of(p.batch, first);
     while (seq < p.batch.seqs && p.batch.q_offsets[seq + 1] <= t) ++seq;

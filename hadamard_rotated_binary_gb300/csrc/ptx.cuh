@@ -250,6 +250,13 @@ __device__ __forceinline__ int atom_add_acq_rel(int* p, int v)
     return old;
 }
 
+__device__ __forceinline__ float rcp(float x)  // to one unit in the last place
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
