@@ -31,7 +31,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kHeadsPerTeam = 4;
 constexpr int kMaxDim = 256;
-constexpr int kGradHeads = 4, kGradBlocks = 4;  // heads that a team of the gradient takes, blocks on an SM
+constexpr int kGradHeads = 4;     // heads that a team of the gradient takes
+constexpr int kGradThreads = 256; // two blocks on an SM, the sums of each a row to join
 constexpr float kRowError = 24.f * 5.9604645e-8f;
 
 template <typename T, int VEC>
@@ -664,14 +665,14 @@ __global__ void __launch_bounds__(kThreads, QUANT ? 7 : 1) bitlin_norm_turn(cons
 // ---- the gradient -------------------------------------------------------------
 
 template <typename TY, typename TX, int VEC>
-__global__ void __launch_bounds__(kThreads, kGradBlocks) bitlin_norm_grad(const NormGradParams p)
+__global__ void __launch_bounds__(kGradThreads, 2) bitlin_norm_grad(const NormGradParams p)
 {
     constexpr int NU = VEC == 1 ? 4 : 1;
     constexpr int kHeads = kGradHeads;
-    __shared__ float sums[kThreads / 8][kMaxDim];  // a row for each team
+    __shared__ float sums[8 * kGradThreads];  // a row for each team
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31, u0 = lane & (p.team - 1);
-    const int teams = kThreads / p.team, me = threadIdx.x / p.team;
+    const int teams = kGradThreads / p.team, me = threadIdx.x / p.team;
     const int groups = (p.heads + kHeads - 1) / kHeads;
     const long long items = (long long)p.tokens * groups;
 
@@ -769,13 +770,13 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) bitlin_norm_grad(const 
     for (int i = 0; i < NU; ++i)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            if (unit[i].held) sums[me][unit[i].lo + j] = dwx[i][j];
-            if (unit[i].has_hi) sums[me][unit[i].hi + j] = dwy[i][j];
+            if (unit[i].held) sums[me * p.dim + unit[i].lo + j] = dwx[i][j];
+            if (unit[i].has_hi) sums[me * p.dim + unit[i].hi + j] = dwy[i][j];
         }
     __syncthreads();
-    for (int d = threadIdx.x; d < p.dim; d += kThreads) {
+    for (int d = threadIdx.x; d < p.dim; d += kGradThreads) {
         float sum = 0.f;
-        for (int k = 0; k < teams; ++k) sum += sums[k][d];
+        for (int k = 0; k < teams; ++k) sum += sums[k * p.dim + d];
         p.partial[(long long)blockIdx.x * p.dim + d] = sum;
     }
 }
@@ -884,7 +885,7 @@ cudaError_t grad(const NormGradParams& np, cudaStream_t s)
     p.eps_f = (float)p.eps;
     p.blocks = bitlin_norm_grad_blocks(p.tokens, p.heads);
     cudaLaunchAttribute attr = {};
-    cudaLaunchConfig_t cfg = config(dim3(p.blocks), kThreads, s, &attr);
+    cudaLaunchConfig_t cfg = config(dim3(p.blocks), kGradThreads, s, &attr);
     cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, bitlin_norm_grad<TY, TX, 4>, p) : cudaLaunchKernelEx(&cfg, bitlin_norm_grad<TY, TX, 1>, p);
     if (e != cudaSuccess) return e;
     cfg = config(dim3((p.dim + 31) / 32), 1024, s, &attr);
@@ -914,10 +915,10 @@ cudaError_t bitlin_launch_norm_turn(const NormTurnParams& p, int src_dtype, int 
 
 int bitlin_norm_grad_blocks(int tokens, int heads)
 {
-    // as many as run at once on 152 SMs, or as there are tokens and heads for
+    // two to each of 152 SMs, or as many as there are tokens and heads for
     const long long items = (long long)tokens * ((heads + kGradHeads - 1) / kGradHeads);
-    const long long blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
-    return (int)(blocks < kGradBlocks * 152 ? blocks : kGradBlocks * 152);
+    const long long blocks = (items + kGradThreads / 32 - 1) / (kGradThreads / 32);
+    return (int)(blocks < 304 ? blocks : 304);
 }
 
 cudaError_t bitlin_launch_norm_grad(const NormGradParams& p, int dy_dtype, int x_dtype, cudaStream_t s)

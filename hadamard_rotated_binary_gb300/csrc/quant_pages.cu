@@ -12,7 +12,7 @@ using namespace bitlin_impl;
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kHeadsPerThread = 4;
+constexpr int kHeadsPerThread = 8;
 constexpr int kUnpackThreads = 256;
 
 // A word's eight values, two by two, as f16.
@@ -29,6 +29,20 @@ __device__ __forceinline__ void eight_halves(uint32_t word, uint32_t scale_byte,
     v[3] = __byte_perm(bits(c), bits(d), 0x7632);
 }
 
+// Two f16 values as two of T.
+template <typename T>
+__device__ __forceinline__ uint32_t two_of(uint32_t h)
+{
+    return h;
+}
+template <>
+__device__ __forceinline__ uint32_t two_of<__nv_bfloat16>(uint32_t h)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 template <typename T>
 __device__ __forceinline__ void store8(T* dst, uint32_t word, uint32_t scale_byte, bool wide)
 {
@@ -37,9 +51,13 @@ __device__ __forceinline__ void store8(T* dst, uint32_t word, uint32_t scale_byt
     alignas(16) T v[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-        v[2 * j] = from_f32<T>(f.x);
-        v[2 * j + 1] = from_f32<T>(f.y);
+        if (sizeof(T) == 4 || !wide) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+            v[2 * j] = from_f32<T>(f.x);
+            v[2 * j + 1] = from_f32<T>(f.y);
+        } else {
+            reinterpret_cast<uint32_t*>(v)[j] = two_of<T>(h[j]);
+        }
     }
     if (wide) {
 #pragma unroll
