@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, QUANT ? 7 : 1) bitlin_norm_turn(cons
     ptx::griddep_wait();
     const TurnParams& p = np.t;
     const int lane = threadIdx.x & 31, u0 = lane & (np.team - 1);
-    const uint32_t idx = (blockIdx.x * (uint32_t)kThreads + threadIdx.x) / (uint32_t)np.team;
+    const uint32_t idx = blockIdx.x * (uint32_t)(kThreads / np.team) + threadIdx.x / (uint32_t)np.team;  // the team's token
     const int t = (int)min(idx, (uint32_t)(p.tokens - 1));
     const bool token = idx < (uint32_t)p.tokens;
 
@@ -833,14 +833,14 @@ cudaError_t launch(NormTurnParams& p, cudaStream_t s)
     p.inverse_dim = 1.f / p.t.dim;
     p.eps_f = (float)p.eps;
     p.t.q_groups = (p.t.heads + kHeadsPerTeam - 1) / kHeadsPerTeam;
-    // k and v to 4 bits: a team takes as many heads of a token as leave 24 teams to an SM's share of warps
+    // k and v to 4 bits: a team takes as many heads of a token as leave 24 warps to an SM
     const long long rows = 2LL * p.t.tokens * p.t.kv_heads * p.team / 32, most = rows / (24 * 152);
     p.kv_heads_per_team = !QUANT ? kHeadsPerTeam : most < 1 ? 1 : most < p.t.kv_heads ? (int)most : p.t.kv_heads;
     p.t.kv_groups = p.t.append ? (p.t.kv_heads + p.kv_heads_per_team - 1) / p.kv_heads_per_team : 0;
-    const uint64_t threads = (uint64_t)p.t.tokens * p.team;
+    const int teams = kThreads / p.team;
     cudaLaunchAttribute attr = {};
     const cudaLaunchConfig_t cfg =
-        config(dim3((unsigned)((threads + kThreads - 1) / kThreads), p.t.q_groups + 2 * p.t.kv_groups), kThreads, s, &attr);
+        config(dim3((unsigned)(((long long)p.t.tokens + teams - 1) / teams), p.t.q_groups + 2 * p.t.kv_groups), kThreads, s, &attr);
     return cudaLaunchKernelEx(&cfg, bitlin_norm_turn<TI, TO, VEC, QUANT>, p);
 }
 

@@ -107,48 +107,49 @@ __global__ void __launch_bounds__(kThreads) bitlin_quant_read(const QuantReadPar
         if (h0 + i < p.pool.kv_heads) store8<T>(out + (h0 + i) * p.out_head[kind], word[i], scale[i], wide);
 }
 
-// Block (x, s): every gridDim.x-th page of sequence s.  A warp takes the slots of one head
+// Block (x, y): every gridDim.x-th page of every gridDim.y-th sequence.  A warp takes the slots of one head
 // of K or of V, a word to a lane: 32 / (D / 8) slots at a time, eight times in flight.
 template <typename T>
 __global__ void __launch_bounds__(kUnpackThreads) bitlin_quant_unpack(const QuantUnpackParams p)
 {
     constexpr int kBatch = 8;
     ptx::griddep_wait();
-    const int seq = blockIdx.y;
-    if (p.batch.q_offsets[seq + 1] <= p.batch.q_offsets[seq]) return;  // nothing asks for it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int units = p.pool.dim / 8, u = lane & (units - 1), slots = 32 / units, mine = lane / units;
     const int group = 8 * (8 * u / (p.pool.dim / 4));  // the group's byte in a head's scales, in bits
-    const int len = min(max(p.batch.kv_lens[seq], 0), 1 << 30);
-    const int want = (int)(((long long)len + p.pool.page_size - 1) / p.pool.page_size);
-    const int pages = min(want, p.batch.table_pages);
-    if (pages < want) *p.index_error = 1;
-    for (int at = blockIdx.x; at < pages; at += gridDim.x) {
-        const int page = p.batch.table[seq * p.batch.table_stride + at];
-        if (page < 0 || page >= p.pool.pages) {  // attention reads it as zeros
-            *p.index_error = 1;
-            continue;
-        }
-        const int held = min(p.pool.page_size, len - at * p.pool.page_size);
-        for (int i = warp; i < 2 * p.pool.kv_heads; i += kUnpackThreads / 32) {
-            const int kind = i & 1, head = i >> 1;
-            const uint8_t* codes = p.pool.codes[kind] + page * p.pool.page_stride + head * p.pool.head_stride + 4 * u;
-            const uint8_t* scales = p.pool.scales[kind] + page * p.pool.scale_page + head * p.pool.scale_head;
-            T* out = static_cast<T*>(p.out[kind]) + page * p.page_stride + head * p.head_stride + 8 * u;
-            for (int first = mine; first < held; first += slots * kBatch) {
-                uint32_t word[kBatch], scale[kBatch];
+    for (int seq = blockIdx.y; seq < p.batch.seqs; seq += gridDim.y) {
+        if (p.batch.q_offsets[seq + 1] <= p.batch.q_offsets[seq]) continue;  // nothing asks for it
+        const int len = min(max(p.batch.kv_lens[seq], 0), 1 << 30);
+        const int want = (int)(((long long)len + p.pool.page_size - 1) / p.pool.page_size);
+        const int pages = min(want, p.batch.table_pages);
+        if (pages < want) *p.index_error = 1;
+        for (int at = blockIdx.x; at < pages; at += gridDim.x) {
+            const int page = p.batch.table[seq * p.batch.table_stride + at];
+            if (page < 0 || page >= p.pool.pages) {  // attention reads it as zeros
+                *p.index_error = 1;
+                continue;
+            }
+            const int held = min(p.pool.page_size, len - at * p.pool.page_size);
+            for (int i = warp; i < 2 * p.pool.kv_heads; i += kUnpackThreads / 32) {
+                const int kind = i & 1, head = i >> 1;
+                const uint8_t* codes = p.pool.codes[kind] + page * p.pool.page_stride + head * p.pool.head_stride + 4 * u;
+                const uint8_t* scales = p.pool.scales[kind] + page * p.pool.scale_page + head * p.pool.scale_head;
+                T* out = static_cast<T*>(p.out[kind]) + page * p.page_stride + head * p.head_stride + 8 * u;
+                for (int first = mine; first < held; first += slots * kBatch) {
+                    uint32_t word[kBatch], scale[kBatch];
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int slot = first + j * slots;
-                    if (slot < held) {
-                        word[j] = *reinterpret_cast<const uint32_t*>(codes + slot * p.pool.slot_stride);
-                        scale[j] = *reinterpret_cast<const uint32_t*>(scales + slot * p.pool.scale_slot);
+                    for (int j = 0; j < kBatch; ++j) {
+                        const int slot = first + j * slots;
+                        if (slot < held) {
+                            word[j] = *reinterpret_cast<const uint32_t*>(codes + slot * p.pool.slot_stride);
+                            scale[j] = *reinterpret_cast<const uint32_t*>(scales + slot * p.pool.scale_slot);
+                        }
                     }
-                }
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int slot = first + j * slots;
-                    if (slot < held) store8<T>(out + slot * p.slot_stride, word[j], scale[j] >> group & 0xff, true);
+                    for (int j = 0; j < kBatch; ++j) {
+                        const int slot = first + j * slots;
+                        if (slot < held) store8<T>(out + slot * p.slot_stride, word[j], scale[j] >> group & 0xff, true);
+                    }
                 }
             }
         }
@@ -199,7 +200,7 @@ cudaError_t bitlin_launch_quant_unpack(const QuantUnpackParams& p, int dst_dtype
     // blocks for sixteen to an SM, or for a page each
     const int want = (16 * num_sms + p.batch.seqs - 1) / p.batch.seqs;
     cudaLaunchAttribute attr = {};
-    cudaLaunchConfig_t cfg = config(dim3(want < p.batch.table_pages ? want : p.batch.table_pages, p.batch.seqs), s, &attr);
+    cudaLaunchConfig_t cfg = config(dim3(want < p.batch.table_pages ? want : p.batch.table_pages, p.batch.seqs < 65535 ? p.batch.seqs : 65535), s, &attr);
     cfg.blockDim = dim3(kUnpackThreads);
     return dst_dtype == BITLIN_BF16 ? cudaLaunchKernelEx(&cfg, bitlin_quant_unpack<__nv_bfloat16>, p)
                                     : cudaLaunchKernelEx(&cfg, bitlin_quant_unpack<__half>, p);

@@ -855,3 +855,39 @@ def test_refusals(hrb):
     with pytest.raises(ValueError):
         kv.append(q[:, :2], q[:, :2], batch, rope=closed)
     assert kv.get_error() == hrb.BITLIN_OK
+
+
+@gpu
+def test_more_sequences_than_a_grid_has_rows(hrb):
+    """70,000 sequences of 1 to 8 keys, through 16-bit pages and directly; a few of them compared."""
+    seqs, page, dim, heads = 70000, 8, 64, 96
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    parts = hrb.QuantKV.pools(seqs, page, 1, dim)
+    kv = hrb.QuantKV(*parts, dtype=torch.float16)
+    lens = torch.arange(seqs, dtype=torch.int32, device="cuda") % 8 + 1
+    table = torch.randperm(seqs, generator=gen, device="cuda").to(torch.int32)[:, None].contiguous()
+    offsets = torch.cat([lens.new_zeros(1), lens.cumsum(0).to(torch.int32)])
+    k, v = (torch.randn((int(offsets[-1]), 1, dim), generator=gen, device="cuda").half() for _ in range(2))
+    every = hrb.KVBatch(offsets, lens, table)
+    kv.append(k, v, every)
+    back = kv.read(every, k.shape[0], dtype=torch.float32)
+    one = hrb.KVBatch(torch.arange(seqs + 1, dtype=torch.int32, device="cuda"), lens, table)
+    q = torch.randn((seqs, heads, dim), generator=gen, device="cuda").half()
+    through = hrb.PagedKV(*(torch.empty((seqs, page, 1, dim), dtype=torch.float16, device="cuda") for _ in range(2)))
+    outs = [kv.attend(q, one, through=t) for t in (None, through)]
+    for s in (0, 7, 65534, 65535, 65536, 69999):
+        at = slice(int(offsets[s]), int(offsets[s + 1]))
+        kk, vv = (x[at, 0].double().cpu() for x in back)
+        want = torch.softmax(q[s].double().cpu() @ kk.t() / dim**0.5, -1) @ vv
+        for y in outs:  # weights and output in f16, values up to 4
+            assert bool(((y[s].double().cpu() - want).abs() <= 2 * 2.0**-11 * 4).all())
+    assert kv.get_error() == hrb.BITLIN_OK
+
+
+@gpu
+def test_as_many_heads_as_a_row_tile_and_more(hrb):
+    """Groups of up to 128 query heads, tokens that straddle row tiles, ragged new tokens."""
+    for group, new, dim in ((128, [1, 1], 256), (127, [2, 1], 128), (5, [7, 1], 256), (24, [1, 1], 128), (25, [1, 3], 64)):
+        case = ([200, 77], new, 16, 2, group, dim, torch.bfloat16, torch.float32, True, "heads")
+        cache, _, offsets, q, y, lse = attended(hrb, case)
+        check_attended(y, lse, reference(cache, offsets, case[0], q, True), torch.float16)
