@@ -6,7 +6,7 @@
 // m and sum per row; exp(x) = 2^(x log2 e).
 //
 // A row is one query head of one token; the heads / kv_heads query heads that read
-// a key head share a tile of 8 or 16 rows (tokens outermost), so a single token of
+// a key head share a tile of 8, 16 or 24 rows (tokens outermost), so a single token of
 // a grouped model reads each key once.
 //
 // Codes become f16 in registers, where they are the A operand of 16 x 8 x 16
@@ -32,7 +32,20 @@
 // Weights are relative to 2^7 of the running reference, which follows a row's
 // maximum only when that grows by more than 2^8: f16 holds them up to 2^15, and what
 // its smallest step loses is 2^-32 of the largest weight.  They are rounded to f16 for
-// a 16-bit output and split in two f16 digits (22 bits) for an f32 one.
+// a 16-bit output and split in two f16 digits (22 bits) for an f32 one.  The products'
+// additions truncate (3.4e-8 of an output per addition of positive values, measured), so
+// an f32 output is added outside them, rounded: off by 1e-7 to 8e-7 of its norm from
+// 2,000 to 131,072 keys an item, where f32 arithmetic in torch is by 1e-7 to 1.1e-6, for
+// 5 us in 76 (64 tokens over 100-8,000 keys).
+//
+// Bound: HBM, and the issue of the codes' conversion beside it (at 256 dims some 1,200
+// instructions of a warp for 32 keys, 620 of them masks, shifts, permutations and
+// fused multiply-adds of the codes).  The loop over the keys moves 5.7 TB/s at 256 dims;
+// an item's begin takes 2 us and its end 1.5, which the other CTA on the SM covers in
+// part, a call's begin 4 us and its last join 4.  Measured (GB300, inputs changing from
+// call to call): one token over 131,072 keys, 138 MB, 45 us (f32 out); 64 over 100-8,000
+// keys, 282 MB, 70 us (4.0 TB/s), with heads of 128 dims 74 and of 64 (149 MB) 52; one
+// over 777 keys 11 us; 16 x 5 drafted tokens over 1,000-6,000 keys, 128 dims, 43 us.
 #include <math.h>
 
 #include "kv_internal.cuh"
@@ -626,11 +639,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
 #pragma unroll
                         for (int d = 0; d < 2; ++d)
 #pragma unroll
-                            for (int t = 0; t < NT; ++t)
+                            for (int t = 0; t < NT; ++t) {
+                                float(&o)[4] = acc[4 * x + 2 * h + d][t];
+                                if (DIGITS == 1) {
+                                    ptx::mma_f16(o, u(a[0][2 * d]), u(a[0][2 * d + 1]), u(a[1][2 * d]), u(a[1][2 * d + 1]), pb[t][0][0], pb[t][0][1]);
+                                } else {
+                                    // (the products' additions truncate: these are rounded)
+                                    float part[4] = {};
 #pragma unroll
-                                for (int g = 0; g < DIGITS; ++g)
-                                    ptx::mma_f16(acc[4 * x + 2 * h + d][t], u(a[0][2 * d]), u(a[0][2 * d + 1]), u(a[1][2 * d]), u(a[1][2 * d + 1]),
-                                                 pb[t][g][0], pb[t][g][1]);
+                                    for (int g = 0; g < DIGITS; ++g)
+                                        ptx::mma_f16(part, u(a[0][2 * d]), u(a[0][2 * d + 1]), u(a[1][2 * d]), u(a[1][2 * d + 1]), pb[t][g][0], pb[t][g][1]);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) o[k] += part[k];
+                                }
+                            }
                     }
                 }
             }

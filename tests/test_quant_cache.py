@@ -885,6 +885,27 @@ def test_more_sequences_than_a_grid_has_rows(hrb):
 
 
 @gpu
+@pytest.mark.parametrize("dim", [64, 256])
+def test_long_sums_of_f32_outputs_are_rounded_not_truncated(hrb, dim):
+    """The mean of 65,536 positive values, by more items than CTAs, so that each is summed in one
+    place: 700 to 1,400 additions of 16 keys each, rounded at random by 2^-25 of the sum at most,
+    are off by 2^-20 together; truncated ones would be by 2^-14."""
+    n, seqs, page = 65536, 400, 64
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    parts = hrb.QuantKV.pools(n // page, page, 1, dim)  # all sequences read the same pages
+    for p in parts[:2]:
+        p.copy_(17 * torch.randint(9, 16, p.shape, generator=gen, device="cuda"))
+    for p in parts[2:]:
+        p.copy_(torch.randint(96, 104, p.shape, generator=gen, device="cuda"))
+    kv = hrb.QuantKV(*parts)
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda")[None].repeat(seqs, 1).contiguous()
+    batch = hrb.KVBatch(torch.arange(seqs + 1, dtype=torch.int32, device="cuda"), i32([n] * seqs), table)
+    y = kv.attend(torch.zeros((seqs, 2, dim), dtype=torch.bfloat16, device="cuda"), batch, dtype=torch.float32)
+    want = decode64(parts[1], parts[3]).mean((0, 1, 2))
+    assert float((y.double().cpu() - want).norm() / (want.norm() * (2 * seqs) ** 0.5)) <= 2.0**-20
+
+
+@gpu
 def test_as_many_heads_as_a_row_tile_and_more(hrb):
     """Groups of up to 128 query heads, tokens that straddle row tiles, ragged new tokens."""
     for group, new, dim in ((128, [1, 1], 256), (127, [2, 1], 128), (5, [7, 1], 256), (24, [1, 1], 128), (25, [1, 3], 64)):
