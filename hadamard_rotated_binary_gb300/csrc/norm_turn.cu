@@ -20,7 +20,8 @@
 // (24 units of 2^-24 of |a| + |b|: sum of squares 9 / 2, rsqrt 4, products 2,
 // angle, sine and cosine 4, rotation 2), and an element (or a group's scale)
 // that lies within it of a border between two codes is computed again in 64 bits,
-// one row in some 300.  Rows that neither a norm nor a rotation touches are exact.
+// one row in some 300; so is a row whose squares leave the range of 32 bits.  Rows
+// that neither a norm nor a rotation touches are exact.
 // There a lane ends with eight consecutive elements (pairs half the rotated part
 // apart go through shared memory), and a team takes several heads one after the
 // other where there are tokens enough: what comes before a row, and its place,
@@ -31,9 +32,8 @@
 // 41, 38, before 16-bit chunks were taken apart by words); 4,097 x 24 x 256 f32 32.8 us
 // (6.1 TB/s), its gradient 50 us (6.0 TB/s; two heads at a time 53, blocks of 128 whose
 // sums are 608 rows to join 51); prompts of 8,191 tokens to 4 bits with their queries
-// 66 us, issue at 80 % of its rate: a k row of 128 takes a warp half as many instructions
-// again as a q row, a v row half of one; at 64 and 72 registers 66, at 96 80.  One token's
-// queries 2.1 us in a graph.
+// and read back 76 us, issue at 80 % of its rate, with 72 registers of a thread (64 the
+// same, 96 eight to eleven more).  One token's queries 2.1 us in a graph.
 #include "kv_internal.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -278,14 +278,15 @@ __device__ __noinline__ Codes codes_again(Codes c, Exact<TI> e, uint32_t doubt, 
 }
 
 // Store a row's 8 elements d0.. of each lane u < D / 8 in 4 bits.  x: the values, size: |a| + |b|
-// of each, kRowError of which it may be off (EXACT: nothing).  All lanes of the warp take part.
+// of each, kRowError of which it may be off (EXACT: nothing; `far`: anything).  All lanes of the
+// warp take part.
 //
 // x / s comes from a product and one correction, which for 16-bit values lies on the right
 // side of every border (and on the border itself where x / s does); an f32 value's rest
 // x - c s, which is exact, decides.  Adding 1.5 2^23 + 8 rounds to the nearest (ties to even)
 // and leaves code + 8 in the low bits.
 template <typename TI, bool EXACT, typename Again>
-__device__ __forceinline__ void store_codes(float (&x)[8], const float (&size)[8], bool active, int u, int dim, int team, Again again,
+__device__ __forceinline__ void store_codes(float (&x)[8], const float (&size)[8], bool far, bool active, int u, int dim, int team, Again again,
                                             double eps, uint8_t* codes, uint8_t* scales)
 {
     constexpr float kRound = 12582912.f + 8.f;
@@ -345,7 +346,7 @@ __device__ __forceinline__ void store_codes(float (&x)[8], const float (&size)[8
         // Does a border lie within an element's error, or between two scales within the largest's?
         emax *= kRowError;
         const float above = 3.5f * (s + quant_scale(c.scale + 1)), below = c.scale ? 3.5f * (s + quant_scale(c.scale - 1)) : -1.f;
-        const bool which = active && ((amax + emax >= above && c.scale < kQuantTopScale) || amax - emax <= below);
+        const bool which = active && (far || (amax + emax >= above && c.scale < kQuantTopScale) || amax - emax <= below);
         if (__any_sync(0xffffffffu, active && (which || (near >= half && s > 0.f)))) {
             uint32_t doubt = 0;
 #pragma unroll
@@ -473,6 +474,7 @@ __device__ __forceinline__ void quant_rows(const NormTurnParams& np, int kind, i
             unpack(b[i], y[i]);
         }
         if (h + 1 < h1) load();
+        bool far = false;  // the squares leave what 32 bits hold well
         if (weight) {
             float sum = 0.f;
 #pragma unroll
@@ -483,7 +485,8 @@ __device__ __forceinline__ void quant_rows(const NormTurnParams& np, int kind, i
                 sum += part;
             }
             sum = team_sum(sum, np.team);
-            const float r = rsqrtf(fmaf(sum, np.inverse_dim, np.eps_f));
+            const float mean = fmaf(sum, np.inverse_dim, np.eps_f), r = rsqrtf(mean);
+            far = !(sum <= 3e38f && mean >= 1e-30f);
 #pragma unroll
             for (int i = 0; i < NU; ++i)
 #pragma unroll
@@ -532,8 +535,8 @@ __device__ __forceinline__ void quant_rows(const NormTurnParams& np, int kind, i
             const TI* mine = static_cast<const TI*>(p.src[kind]) + t * p.src_token[kind] + h * src_head;
             return Exact<TI>{mine, weight, rotating ? p.turns : nullptr, p.pos, 0.0, p.tokens, t, place, p.rotary, p.adjacent};
         };
-        if (exact) store_codes<TI, true>(v, e, mine, u0, p.dim, np.team, again, np.eps, codes, scales);
-        else store_codes<TI, false>(v, e, mine, u0, p.dim, np.team, again, np.eps, codes, scales);
+        if (exact) store_codes<TI, true>(v, e, false, mine, u0, p.dim, np.team, again, np.eps, codes, scales);
+        else store_codes<TI, false>(v, e, far, mine, u0, p.dim, np.team, again, np.eps, codes, scales);
     }
 }
 

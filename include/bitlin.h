@@ -417,8 +417,11 @@ bitlin_status bitlin_rope_apply(bitlin_rope_t r, const bitlin_rows* x, int token
  *
  * out is good to 2e-6 (an f32 out) or 3.4e-6 (a 16-bit one, before its own
  * rounding) of its pair's norm (of the element itself past rotary_dim); each
- * output is rounded once to its type.  Requires head_dim <= 256.  out
- * may be x itself.  Otherwise as bitlin_rope_apply.
+ * output is rounded once to its type.  Squares are summed in f32: a head whose
+ * sum of squares passes 3.4e38 comes out as zeros, and where mean(x^2) + eps is
+ * below 1e-30, squares that underflow are lost.  (The append to 4 bits computes
+ * such heads of k in 64 bits.)  Requires head_dim <= 256.  out may be x itself.
+ * Otherwise as bitlin_rope_apply.
  */
 bitlin_status bitlin_rope_apply_normed(bitlin_rope_t r, const bitlin_rows* x, int tokens, int heads, int head_dim,
                                        const int32_t* pos, const float* weight, double eps, const bitlin_rows* out,

@@ -220,6 +220,8 @@ def test_normed_rotation_of_rows_that_are_zero_huge_or_not_finite(hrb):
     assert bool(torch.isnan(y[3]).all()) and bool(torch.isnan(y[4, 0, 63]))
     z = rope.apply(x[:1], pos[:1], norm=w, eps=0.0)
     assert bool(torch.isnan(z).all())
+    # a sum of squares past what f32 holds
+    assert bool((rope.apply(x[5:] * 1e25, pos[5:], norm=w) == 0).all())
 
 
 def gradient64(dy, x, w, pos, inv, axis, adjacent):
@@ -434,6 +436,31 @@ def test_normed_rows_at_borders_go_by_their_64_bit_values(hrb):
     at = (cache.table[0].cpu()[place // 16].long(), place % 16)
     assert torch.equal(cache.parts[2].cpu()[at], scales)
     assert torch.equal(unpacked(cache.parts[0].cpu()[at]), codes)
+
+
+@gpu
+@pytest.mark.parametrize("adjacent", [None, False, True])
+@pytest.mark.parametrize("src", [torch.float32, torch.bfloat16])
+def test_normed_rows_whose_squares_leave_the_range_of_f32(hrb, src, adjacent):
+    """Codes of rows whose squares overflow or underflow in 32 bits are those of the exact rows."""
+    dim, rotary = 64, 32
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    for eps, sizes in ((EPS, (1e18, 1e19, 1e25, 1e37, 1.0)), (0.0, (1e-18, 1e-22, 1e-30, 1e-37, 0.0)), (1e-40, (1e-18, 1e-20, 1e-22, 0.0, 1.0))):
+        x = torch.cat([torch.randn((4, 2, dim), generator=gen, device="cuda") * s for s in sizes]).to(src)
+        n, w = x.shape[0], weight(gen, dim)
+        rope = None if adjacent is None else hrb.Rope(freqs(rotary // 2), adjacent=adjacent)
+        pos = torch.randint(0, 9000, (1, n), generator=gen, device="cuda", dtype=torch.int32)
+        want = norm64(x, w, eps)
+        if rope is not None:
+            want = rotate64(want, pos, freqs(rotary // 2), [0] * (rotary // 2), adjacent)
+        cache = Cache(hrb, None, [n], 16, 2, dim, torch.bfloat16)
+        batch, _ = batch_of(hrb, [n], cache)
+        cache.kv.append(x, x, batch, rope=rope, pos=None if rope is None else pos, k_norm=w, eps=eps)
+        codes, scales = encode64(want)
+        place = torch.arange(n)
+        at = (cache.table[0].cpu()[place // 16].long(), place % 16)
+        assert torch.equal(cache.parts[2].cpu()[at], scales)
+        assert torch.equal(unpacked(cache.parts[0].cpu()[at]), codes)
 
 
 @gpu
