@@ -292,8 +292,9 @@ class QuantKV:
         """bitlin_kvq_attend: as PagedKV.attend, over the 4-bit cache.
 
         through  a 16-bit cache of the same pages, page size, heads and dtype whose pools are
-                 scratch (one serves all layers): calls whose sequences bring many tokens read
-                 their pages back into it and attend there, which is faster for prompts.
+                 scratch (one serves all layers): calls for a 16-bit output whose sequences
+                 bring many tokens read their pages back into it and attend there, which is
+                 faster for prompts (a float32 output, more exact without it, does not use it).
         """
         if through is not None and not through._h:
             raise ValueError("through's handle is closed")

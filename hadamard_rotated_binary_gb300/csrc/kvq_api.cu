@@ -12,10 +12,14 @@ using namespace bitlin_impl;
 namespace {
 
 // Rows (new tokens times query heads of a key head) that a sequence brings on average, from
-// which on it pays to read its pages back to 16 bits first.  Measured, in us, 8 sequences of
-// 2,000-6,000 keys, directly and through 16-bit pages: 128 dims, 64 rows 60 and 74, 128 rows
-// 105 and 77; 256 dims, 72 rows 67 and 80, 144 rows 111 and 91; 64 dims, 64 rows 42 and 50,
-// 128 rows 69 and 51.
+// which on it pays to read its pages back to 16 bits first, for a 16-bit output.  Measured, in
+// us, 8 sequences of 2,000-6,000 keys, directly and through 16-bit pages: 128 dims, 64 rows 60
+// and 74, 128 rows 105 and 77; 256 dims, 72 rows 67 and 80, 144 rows 111 and 91; 64 dims, 64
+// rows 42 and 50, 128 rows 69 and 51.  An f32 output is not taken through them: it would be up
+// to 3e-6 off, 2.4 (f16) and 12 (bf16) times as far as f32 arithmetic, and is closer than that
+// directly.  The price: 344 us for 141 (24-72 tokens a sequence on 210-1,050 keys, 24 heads of
+// 256), 9.3 ms for 1.6 (2,048 tokens over 32,768 keys); few key heads over long contexts gain
+// (82 us to 30).
 constexpr long long kThroughRows = 80;
 
 // The largest power of two that divides three strides.
@@ -201,7 +205,8 @@ bitlin_status bitlin_kvq_attend(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, 
     if (through && through->sticky != BITLIN_OK) return through->sticky;
     if (tokens == 0) return BITLIN_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (through && (long long)tokens * (heads / kvq->pool.kv_heads) > kThroughRows * (long long)batch->seqs) {
+    const long long rows = (long long)tokens * (heads / kvq->pool.kv_heads);
+    if (through && out->dtype != BITLIN_F32 && rows > kThroughRows * (long long)batch->seqs) {
         QuantUnpackParams u = {};
         u.pool = kvq->pool;
         u.batch = batch_of(batch);

@@ -679,8 +679,10 @@ bitlin_status bitlin_kvq_read(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, in
  *            pages, page_size, kv_heads and head_dim, whose pools are scratch
  *            (one for all layers of a model will do).  Calls whose sequences
  *            bring many rows (more than 80 new tokens times query heads of a
- *            key head on average) then read the sequences' pages back into it
- *            and attend there.  Without it such calls are right, but slower.
+ *            key head on average) for a 16-bit out then read the sequences'
+ *            pages back into it and attend there.  Without it such calls are
+ *            right, but slower; an f32 out, which would be less exact through
+ *            16-bit pages, does not use it.
  *   out      For a 16-bit out the probabilities are rounded to f16 before they
  *            meet the values (through 16-bit pages: to the handle's type); for
  *            an f32 out they are split in two f16 digits, 22 bits.

@@ -564,6 +564,7 @@ def test_attention(hrb, case):
 THROUGH = [c for c in ATTENDED if c[2] % 8 == 0] + [
     ([300, 80], [25, 25], 32, 2, 4, 128, torch.float16, torch.float16, True, "heads"),
     ([300, 80, 4], [60, 0, 9], 48, 2, 6, 256, torch.bfloat16, torch.float32, True, "slots"),
+    ([300, 80, 4], [60, 0, 9], 48, 2, 6, 256, torch.bfloat16, torch.bfloat16, True, "slots"),
     ([130, 0, 64], [130, 5, 0], 8, 3, 4, 64, torch.bfloat16, torch.bfloat16, False, "heads"),
 ]
 
@@ -576,9 +577,26 @@ def test_attention_through_16_bit_pages(hrb, case):
     scratch = [torch.full((need, page, kvh, dim), math.nan, dtype=dtype, device="cuda") for _ in range(2)]
     through = hrb.PagedKV(*scratch)
     cache, _, offsets, q, y, lse = attended(hrb, case, through=through)
-    many = offsets[-1] * group > 80 * len(lens)
+    many = out != torch.float32 and offsets[-1] * group > 80 * len(lens)
     check_attended(y, lse, reference(cache, offsets, lens, q, causal), dtype if many else torch.float16)
     assert cache.kv.get_error() == hrb.BITLIN_OK and through.get_error() == hrb.BITLIN_OK
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lens,new,group,dim", [([900, 3000], [60, 60], 4, 128), ([700], [300], 6, 256)])
+def test_f32_outputs_of_many_rows_are_as_exact_as_f32_arithmetic(hrb, dtype, lens, new, group, dim):
+    """With 16-bit pages at hand and without, the same bits, and 2^-20 off at most."""
+    case = (lens, new, 64, 2, group, dim, dtype, torch.float32, True, "heads")
+    need = sum(-(-n // 64) for n in lens) + 2
+    through = hrb.PagedKV(*(torch.zeros((need, 64, 2, dim), dtype=dtype, device="cuda") for _ in range(2)))
+    cache, batch, offsets, q, y, _ = attended(hrb, case, through=through)
+    assert torch.equal(y, cache.kv.attend(q, batch, dtype=torch.float32))
+    out = reference(cache, offsets, lens, q, True)[0]
+    ours = float((y.double().cpu() - out).norm() / out.norm())
+    # a weight is two f16 digits (2^-23 of it), its exponential and the sum's some 2^-21 at scores of 10, the
+    # additions, rounded, 2^-24 times the root of some 100 tiles: 2^-20 together
+    assert ours <= 2.0**-20, ours
 
 
 @gpu
@@ -588,6 +606,7 @@ def test_attention_over_pages_outside_and_lengths_past_the_table(hrb, many):
     gen = torch.Generator(device="cuda").manual_seed(3)
     cache = Cache(hrb, gen, lens, page, kvh, dim, torch.float16).random(gen)
     through = hrb.PagedKV(*(torch.zeros((8, page, kvh, dim), dtype=torch.float16, device="cuda") for _ in range(2))) if many else None
+    out = torch.float16 if many else torch.float32
     new = [30, 30] if many else [1, 1]  # 60 rows, or 2, of 8 query heads: the first through 16-bit pages
     q = torch.randn((sum(new), 8, dim), generator=gen, device="cuda").half()
     batch, offsets = batch_of(hrb, new, cache)
@@ -595,7 +614,7 @@ def test_attention_over_pages_outside_and_lengths_past_the_table(hrb, many):
     old = int(cache.table[1, 1])
     for bad in (8, -1, 2**31 - 1):
         cache.table[1, 1] = bad
-        y = cache.kv.attend(q, batch, dtype=torch.float32, through=through)
+        y = cache.kv.attend(q, batch, dtype=out, through=through)
         assert cache.kv.get_error() == hrb.BITLIN_EINDEX
         kk, vv = (torch.cat([x, torch.zeros_like(x[:1])]) for x in (k, v))
         table = cache.table.cpu().clone()
@@ -604,7 +623,7 @@ def test_attention_over_pages_outside_and_lengths_past_the_table(hrb, many):
     cache.table[1, 1] = old
     # (causal rows past the end of the table's row see all of it)
     batch, _ = batch_of(hrb, new, cache, [40, 1000])
-    y = cache.kv.attend(q, batch, dtype=torch.float32, causal=False, through=through)
+    y = cache.kv.attend(q, batch, dtype=out, causal=False, through=through)
     assert cache.kv.get_error() == hrb.BITLIN_EINDEX
     ref = attend64(q, k, v, offsets, [40, 48], cache.table, dim**-0.5, False)
     if int(cache.table[1, 2]) >= 0:
@@ -726,9 +745,9 @@ def test_prompts_then_captured_single_tokens(hrb):
         k, v = (x[starts[s]:starts[s] + at + 1].transpose(0, 1) for x in (kk, vv))
         return torch.softmax(q @ k.transpose(1, 2) / dim**0.5, -1).matmul(v).reshape(heads, dim)
 
-    def call(x, batch, pos):
+    def call(x, batch, pos, dtype=None):
         q = cache.kv.append(x["k"], x["v"], batch, rope=rope, pos=pos, q=x["q"], q_norm=qw, k_norm=kw)
-        return cache.kv.attend(q, batch, dtype=torch.float32, through=scratch)
+        return cache.kv.attend(q, batch, dtype=dtype, through=scratch)
 
     pick = torch.cat([torch.arange(n) + st for n, st in zip(lens, starts)]).cuda()
     batch, offsets = batch_of(hrb, lens, cache, lens)
@@ -749,7 +768,7 @@ def test_prompts_then_captured_single_tokens(hrb):
     torch.cuda.current_stream().wait_stream(stream)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        out = call(x, one, pos)
+        out = call(x, one, pos, torch.float32)
         one.kv_lens += 1
         pos += 1
     for i in range(steps):
