@@ -4,15 +4,19 @@ The layer's three kinds of work run through the library one after the other on o
 
   1. query/gate, key and value projections: folded 1-bit matrices (``BitLinear``);
   2. ``PagedKV.append``: keys rotated and written to the sequences' pages with the values, queries
-     rotated in the same call;
+     rotated in the same call (with ``--norms`` both are normed first, head by head);
   3. ``PagedKV.attend``: the new tokens over their sequences, in f32 as the output projection
      takes it, times the sigmoid of the gate, through the output projection.
 
 The single-token step is captured once in a CUDA graph and replayed: positions and lengths are
 device tensors, so nothing about a step is decided on the host.  Weights are random.
 
-    python examples/attention_layer.py
+With ``--bits 4`` the cache is a ``QuantKV``; prompts are attended through 16-bit pages, which one
+scratch cache would hold for all layers of a model.
+
+    python examples/attention_layer.py [--bits 4] [--norms]
 """
+import argparse
 import os
 import sys
 
@@ -33,9 +37,10 @@ def random_linear(n, k, gen):
 
 
 class AttentionLayer:
-    """pages: size of the cache's pool, in pages of PAGE tokens."""
+    """pages: size of the cache's pool, in pages of PAGE tokens.  bits: of the cache, 16 or 4.
+    norms: whether queries and keys are normed before their rotation."""
 
-    def __init__(self, pages, gen, dtype=torch.bfloat16):
+    def __init__(self, pages, gen, dtype=torch.bfloat16, bits=16, norms=False):
         self.q_gate = random_linear(2 * HEADS * DIM, MODEL, gen)  # queries of all heads, then their gates
         self.k = random_linear(KV_HEADS * DIM, MODEL, gen)
         self.v = random_linear(KV_HEADS * DIM, MODEL, gen)
@@ -43,8 +48,13 @@ class AttentionLayer:
         # three position axes (time, height, width) dealt out in turn; text has the same place on all
         pairs = ROTARY // 2
         self.rope = hrb.Rope([1e7 ** (-i / pairs) for i in range(pairs)], axis=[i % 3 for i in range(pairs)])
-        self.cache = hrb.PagedKV(*(torch.zeros((pages, PAGE, KV_HEADS, DIM), dtype=dtype, device="cuda")
-                                   for _ in range(2)))
+        pages16 = hrb.PagedKV(*(torch.zeros((pages, PAGE, KV_HEADS, DIM), dtype=dtype, device="cuda")
+                                for _ in range(2)))
+        self.cache = hrb.QuantKV(*hrb.QuantKV.pools(pages, PAGE, KV_HEADS, DIM), dtype=dtype) if bits == 4 else pages16
+        self.through = {"through": pages16, "f32_through": True} if bits == 4 else {}
+        self.norms = {}
+        if norms:
+            self.norms = {n: torch.rand(DIM, generator=gen, device="cuda") + 0.5 for n in ("q_norm", "k_norm")}
 
     def project(self, x):
         """x [T][MODEL] f32 -> queries, gates, keys, values."""
@@ -54,8 +64,8 @@ class AttentionLayer:
     def __call__(self, x, batch, pos):
         """x [T][MODEL] f32, pos int32 [3][T] -> [T][MODEL] f32; the cache takes the new tokens."""
         q, gate, k, v = self.project(x)
-        q = self.cache.append(k, v, batch, rope=self.rope, pos=pos, q=q)
-        a = self.cache.attend(q, batch, dtype=torch.float32)
+        q = self.cache.append(k, v, batch, rope=self.rope, pos=pos, q=q, **self.norms)
+        a = self.cache.attend(q, batch, dtype=torch.float32, **self.through)
         return self.out((a * torch.sigmoid(gate)).view(-1, HEADS * DIM))
 
 
@@ -93,12 +103,12 @@ class Decoder:
         return self.y
 
 
-def serve(prompt_lens, steps, seed=0, dtype=torch.bfloat16):
+def serve(prompt_lens, steps, seed=0, dtype=torch.bfloat16, bits=16, norms=False):
     """Runs prompts and `steps` single tokens.  Returns (layer, table, inputs, outputs) per part."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
     seqs = len(prompt_lens)
     need = -(-(max(prompt_lens) + steps + 1) // PAGE)
-    layer = AttentionLayer(seqs * need, gen, dtype)
+    layer = AttentionLayer(seqs * need, gen, dtype, bits, norms)
     table = torch.randperm(seqs * need, generator=gen, device="cuda").to(torch.int32).view(seqs, need)
 
     prompt = torch.randn((sum(prompt_lens), MODEL), generator=gen, device="cuda") * 0.1
@@ -115,8 +125,12 @@ def serve(prompt_lens, steps, seed=0, dtype=torch.bfloat16):
 
 
 def main():
+    parser = argparse.ArgumentParser()
+    parser.add_argument("--bits", type=int, choices=(16, 4), default=16, help="of the cache")
+    parser.add_argument("--norms", action="store_true", help="norm queries and keys before their rotation")
+    args = parser.parse_args()
     lens, steps = [700, 33, 2048, 1], 64
-    layer, table, _, _ = serve(lens, steps)
+    layer, table, _, _ = serve(lens, steps, bits=args.bits, norms=args.norms)
     decoder = Decoder(layer, [n + steps - 20 for n in lens], table)
     begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
     x = torch.randn((len(lens), MODEL), device="cuda") * 0.1

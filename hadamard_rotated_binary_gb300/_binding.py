@@ -135,7 +135,7 @@ def lib() -> ctypes.CDLL:
     L.bitlin_kvq_share.argtypes = [P, P]
     L.bitlin_kvq_append.argtypes = [P, B, i32, P, P, R, R, R, i32, R, N, P]
     L.bitlin_kvq_read.argtypes = [P, B, i32, R, R, P]
-    L.bitlin_kvq_attend.argtypes = [P, B, i32, R, i32, ctypes.c_float, i32, R, P, P, P]
+    L.bitlin_kvq_attend.argtypes = [P, B, i32, R, i32, ctypes.c_float, i32, R, P, P, i32, P]
     for name in ("bitlin_kvq_get_error", "bitlin_kvq_cuda_error", "bitlin_kvq_destroy"):
         getattr(L, name).argtypes = [P]
     for name in ("bitlin_rope_apply_normed", "bitlin_rope_gradient", "bitlin_kv_append_normed", "bitlin_kvq_create", "bitlin_kvq_share",

@@ -12,12 +12,12 @@ using namespace bitlin_impl;
 namespace {
 
 // Rows (new tokens times query heads of a key head) that a sequence brings on average, from
-// which on it pays to read its pages back to 16 bits first, for a 16-bit output.  Measured, in
-// us, 8 sequences of 2,000-6,000 keys, directly and through 16-bit pages: 128 dims, 64 rows 60
-// and 74, 128 rows 105 and 77; 256 dims, 72 rows 67 and 80, 144 rows 111 and 91; 64 dims, 64
-// rows 42 and 50, 128 rows 69 and 51.  An f32 output is not taken through them: it would be up
-// to 3e-6 off, 2.4 (f16) and 12 (bf16) times as far as f32 arithmetic, and is closer than that
-// directly.  The price: 344 us for 141 (24-72 tokens a sequence on 210-1,050 keys, 24 heads of
+// which on it pays to read its pages back to 16 bits first.  Measured, in us, 8 sequences of
+// 2,000-6,000 keys, directly and through 16-bit pages: 128 dims, 64 rows 60 and 74, 128 rows
+// 105 and 77; 256 dims, 72 rows 67 and 80, 144 rows 111 and 91; 64 dims, 64 rows 42 and 50,
+// 128 rows 69 and 51.  An f32 output goes through them only where the caller says so: it is
+// up to 3e-6 off there, 2.4 (f16) and 12 (bf16) times as far as f32 arithmetic, and closer than
+// that directly.  The price of that: 344 us for 141 (24-72 tokens a sequence on 210-1,050 keys, 24 heads of
 // 256), 9.3 ms for 1.6 (2,048 tokens over 32,768 keys); few key heads over long contexts gain
 // (82 us to 30).
 constexpr long long kThroughRows = 80;
@@ -195,18 +195,20 @@ bitlin_status bitlin_kvq_read(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, in
 
 bitlin_status bitlin_kvq_attend(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q,
                                 int heads, float scale, int causal, const bitlin_rows* out, float* lse,
-                                bitlin_kv_t through, bitlin_stream_t stream)
+                                bitlin_kv_t through, int f32_through, bitlin_stream_t stream)
 {
     if (!kvq || !batch_ok(batch) || !rows_ok(q, tokens) || !rows_ok(out, tokens) || q->dtype != kvq->dtype) return BITLIN_EINVAL;
     if (out->dtype != kvq->dtype && out->dtype != BITLIN_F32) return BITLIN_EINVAL;
-    if (!rows_wide(q) || !rows_wide(out) || !isfinite(scale) || (causal != 0 && causal != 1)) return BITLIN_EINVAL;
+    if (!rows_wide(q) || !rows_wide(out) || !isfinite(scale) || (causal != 0 && causal != 1) ||
+        (f32_through != 0 && f32_through != 1))
+        return BITLIN_EINVAL;
     if (!sizes_ok(tokens, heads, kvq->pool.dim) || heads % kvq->pool.kv_heads || heads / kvq->pool.kv_heads > 128) return BITLIN_EINVAL;
     if (!on_device(kvq->device) || (through && !passes(*kvq, through))) return BITLIN_EINVAL;
     if (through && through->sticky != BITLIN_OK) return through->sticky;
     if (tokens == 0) return BITLIN_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const long long rows = (long long)tokens * (heads / kvq->pool.kv_heads);
-    if (through && out->dtype != BITLIN_F32 && rows > kThroughRows * (long long)batch->seqs) {
+    if (through && (f32_through || out->dtype != BITLIN_F32) && rows > kThroughRows * (long long)batch->seqs) {
         QuantUnpackParams u = {};
         u.pool = kvq->pool;
         u.batch = batch_of(batch);

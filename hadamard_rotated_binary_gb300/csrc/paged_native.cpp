@@ -328,22 +328,22 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return any_ap
 PyObject* kvq_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return any_append<bitlin_kvq_t>(a, n, "bitlin_kvq_append"); }
 
 bitlin_status attend(bitlin_kv_t h, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q, int heads, float scale, int causal,
-                     const bitlin_rows* out, float* lse, bitlin_kv_t, bitlin_stream_t s)
+                     const bitlin_rows* out, float* lse, bitlin_kv_t, int, bitlin_stream_t s)
 {
     return bitlin_kv_attend(h, batch, tokens, q, heads, scale, causal, out, lse, s);
 }
 
 bitlin_status attend(bitlin_kvq_t h, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q, int heads, float scale, int causal,
-                     const bitlin_rows* out, float* lse, bitlin_kv_t through, bitlin_stream_t s)
+                     const bitlin_rows* out, float* lse, bitlin_kv_t through, int f32_through, bitlin_stream_t s)
 {
-    return bitlin_kvq_attend(h, batch, tokens, q, heads, scale, causal, out, lse, through, s);
+    return bitlin_kvq_attend(h, batch, tokens, q, heads, scale, causal, out, lse, through, f32_through, s);
 }
 
-// (handle, device, head_dim, cache dtype, batch, q, scale, causal, out, dtype, lse, stream[, through])
+// (handle, device, head_dim, cache dtype, batch, q, scale, causal, out, dtype, lse, stream[, through, f32_through])
 template <typename Handle>
 PyObject* any_attend(PyObject* const* a, Py_ssize_t n, const char* name, bool quant)
 {
-    if (!arguments(n, quant ? 13 : 12)) return nullptr;
+    if (!arguments(n, quant ? 14 : 12)) return nullptr;
     HANDLE_TH_ERRORS
     try {
         auto h = static_cast<Handle>(handle_of(a[0]));
@@ -368,8 +368,12 @@ PyObject* any_attend(PyObject* const* a, Py_ssize_t n, const char* name, bool qu
             lse = static_cast<float*>(t.data_ptr());
         }
         bitlin_kv_t through = nullptr;
-        if (quant && a[12] != Py_None) through = static_cast<bitlin_kv_t>(handle_of(a[12]));
-        check(attend(h, batch, size_of(q.size(0)), &qr, size_of(q.size(1)), (float)scale, PyObject_IsTrue(a[7]), &dst, lse, through, stream),
+        int f32_through = 0;
+        if (quant) {
+            if (a[12] != Py_None) through = static_cast<bitlin_kv_t>(handle_of(a[12]));
+            f32_through = PyObject_IsTrue(a[13]);
+        }
+        check(attend(h, batch, size_of(q.size(0)), &qr, size_of(q.size(1)), (float)scale, PyObject_IsTrue(a[7]), &dst, lse, through, f32_through, stream),
               name, h);
         return wrap(out, a[8]);
     } catch (const Refused&) {

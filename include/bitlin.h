@@ -679,10 +679,12 @@ bitlin_status bitlin_kvq_read(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, in
  *            pages, page_size, kv_heads and head_dim, whose pools are scratch
  *            (one for all layers of a model will do).  Calls whose sequences
  *            bring many rows (more than 80 new tokens times query heads of a
- *            key head on average) for a 16-bit out then read the sequences'
- *            pages back into it and attend there.  Without it such calls are
- *            right, but slower; an f32 out, which would be less exact through
- *            16-bit pages, does not use it.
+ *            key head on average) then read the sequences' pages back into it
+ *            and attend there.  Without it such calls are right, but slower.
+ *   f32_through  whether an f32 out goes through 16-bit pages too (1), where
+ *            it is as exact as bitlin_kv_attend's, up to 3e-6 off, and 2 to 7
+ *            times faster; or does not use them (0): up to 8e-7 off, as f32
+ *            arithmetic is.
  *   out      For a 16-bit out the probabilities are rounded to f16 before they
  *            meet the values (through 16-bit pages: to the handle's type); for
  *            an f32 out they are split in two f16 digits, 22 bits.
@@ -693,7 +695,7 @@ bitlin_status bitlin_kvq_read(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, in
  */
 bitlin_status bitlin_kvq_attend(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q,
                                 int heads, float scale, int causal, const bitlin_rows* out, float* lse,
-                                bitlin_kv_t through, bitlin_stream_t stream);
+                                bitlin_kv_t through, int f32_through, bitlin_stream_t stream);
 
 /* As bitlin_kv_get_error: BITLIN_EINDEX (once, then cleared) or BITLIN_ECUDA.  Synchronizes. */
 bitlin_status bitlin_kvq_get_error(bitlin_kvq_t kvq);

@@ -576,8 +576,8 @@ def test_attention_through_16_bit_pages(hrb, case):
     need = sum(-(-n // page) for n in lens) + 2
     scratch = [torch.full((need, page, kvh, dim), math.nan, dtype=dtype, device="cuda") for _ in range(2)]
     through = hrb.PagedKV(*scratch)
-    cache, _, offsets, q, y, lse = attended(hrb, case, through=through)
-    many = out != torch.float32 and offsets[-1] * group > 80 * len(lens)
+    cache, _, offsets, q, y, lse = attended(hrb, case, through=through, f32_through=True)
+    many = offsets[-1] * group > 80 * len(lens)
     check_attended(y, lse, reference(cache, offsets, lens, q, causal), dtype if many else torch.float16)
     assert cache.kv.get_error() == hrb.BITLIN_OK and through.get_error() == hrb.BITLIN_OK
 
@@ -805,6 +805,45 @@ def test_other_streams_and_a_shared_workspace(hrb):
         cache.kv.attend(q, batch)
 
 
+@gpu
+def test_layer_example_with_norms_over_4_bits(hrb):
+    """Prompts and captured single-token steps of the example's layer, its projections taken as given."""
+    import os
+    import sys
+
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "examples"))
+    import attention_layer as example
+
+    lens, steps = [70, 1, 133], 3
+    layer, table, inputs, outputs = example.serve(lens, steps, bits=4, norms=True)
+    pairs = example.ROTARY // 2
+    freq, axis = torch.tensor([1e7 ** (-i / pairs) for i in range(pairs)]).tolist(), [i % 3 for i in range(pairs)]  # (as f32)
+    past = [0] * len(lens)
+    for part, x in enumerate(inputs):
+        new = lens if part == 0 else [1] * len(lens)
+        past = [a + b for a, b in zip(past, new)]
+        batch, pos = example.make_batch(new, past, table)
+        q, gate, k, v = layer.project(x)
+        # what the cache holds of the new rows is what their 64-bit values come to
+        turned = rotate64(norm64(k, layer.norms["k_norm"]), pos, freq, axis, False)
+        for got, want in zip(layer.cache.read(batch, sum(new), dtype=torch.float32), (turned, v)):
+            code, byte = encode64(want)
+            assert torch.equal(got.double().cpu(), ((code.double() - 8).unflatten(-1, (4, -1)) * all_scales()[byte.long()][..., None]).flatten(-2))
+        q = layer.rope.apply(q, pos, dtype=torch.bfloat16, norm=layer.norms["q_norm"])
+        a = layer.cache.attend(q, batch, dtype=torch.float32, **layer.through)
+        offsets = [sum(new[:i]) for i in range(len(new) + 1)]
+        starts = [sum(past[:i]) for i in range(len(past) + 1)]
+        kk, vv = layer.cache.read(hrb.KVBatch(i32(starts), i32(past), table), starts[-1], dtype=torch.float32)
+        # pages of one slot, in the order that the rows were read in
+        places = torch.full((len(past), max(past)), -1)
+        for s, n in enumerate(past):
+            places[s, :n] = torch.arange(starts[s], starts[s + 1])
+        ref = attend64(q, kk[:, None], vv[:, None], offsets, past, places, example.DIM**-0.5, True)
+        check_attended(a, None, ref, torch.bfloat16 if part == 0 else torch.float16)
+        again = layer.out((a * torch.sigmoid(gate)).view(-1, example.HEADS * example.DIM))
+        assert torch.equal(again, outputs[part])
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_the_c_abi_refuses_without_a_device(hrb):
@@ -826,7 +865,7 @@ def test_the_c_abi_refuses_without_a_device(hrb):
     assert lib.bitlin_kvq_append(None, None, 1, None, None, None, None, None, 1, None, ctypes.byref(norms), None) == hrb.BITLIN_EINVAL
     assert lib.bitlin_kv_append_normed(None, None, 1, None, None, None, None, None, 1, None, ctypes.byref(norms), None) == hrb.BITLIN_EINVAL
     assert lib.bitlin_kvq_read(None, None, 1, None, None, None) == hrb.BITLIN_EINVAL
-    assert lib.bitlin_kvq_attend(None, None, 1, None, 1, 1.0, 1, None, None, None, None) == hrb.BITLIN_EINVAL
+    assert lib.bitlin_kvq_attend(None, None, 1, None, 1, 1.0, 1, None, None, None, 0, None) == hrb.BITLIN_EINVAL
     assert lib.bitlin_rope_apply_normed(None, None, 1, 1, 64, None, p, 1e-6, None, None) == hrb.BITLIN_EINVAL
     assert lib.bitlin_rope_gradient(None, None, None, 1, 1, 64, None, p, 1e-6, None, p, p, 1 << 20, None) == hrb.BITLIN_EINVAL
     assert lib.bitlin_kvq_share(None, None) == hrb.BITLIN_EINVAL and lib.bitlin_kvq_get_error(None) == hrb.BITLIN_EINVAL
