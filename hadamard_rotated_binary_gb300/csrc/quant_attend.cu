@@ -675,7 +675,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
         auto merge_at = [&](int who, int q, int i) {
             return reinterpret_cast<float2*>(smem) + (who * 8 + q) * C::kMergeRow + i + i / MT;
         };
-        const int rows = work.rows;
+        // after the last barrier below thread 0 may be at the next item, whose state takes this one's
+        // place: what the joining needs of it is read here
+        const int rows = work.rows, first_token = work.w.row0, tile_row0 = work.row0;
         const bool whole = work.whole;
         for (int row = warp; row < rows; row += kWarps) {
             const float2 x = lane < kWarps ? warp_ml[lane][row] : make_float2(0.f, 0.f);
@@ -706,7 +708,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
                 const int row = 8 * t + q;
                 const float2 ml = row_ml[row];
                 const float scale = !whole ? 1.f : ml.y == 0.f ? 0.f : 1.f / ml.y;
-                const Place place = place_of(p, work.w.row0, head, work.row0 + row);
+                const Place place = place_of(p, first_token, head, tile_row0 + row);
 #pragma unroll
                 for (int e = 0; e < (D + 127) / 128; ++e) {
                     const int d = 4 * (lane + 32 * e);
@@ -729,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
                 }
             }
         }
-        if (!whole && threadIdx.x == 0) shared[from == (int)blockIdx.x] = {from, last_cta(work), work.w.row0, head, work.row0, rows};
+        if (!whole && threadIdx.x == 0) shared[from == (int)blockIdx.x] = {from, last_cta(work), first_token, head, tile_row0, rows};
     }
 
     // ---- items that CTAs share: the last one to come joins the parts.  Many parts are joined

@@ -1,0 +1,65 @@
+"""Norms, gradients and the 4-bit cache where they once went wrong, or could: a test for each fault.
+
+Definitions, bounds and inputs are those of test_quant_cache.py.
+"""
+import os
+import re
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_quant_cache import attended, check_attended, gpu, hrb, reference  # noqa: E402,F401
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "hadamard_rotated_binary_gb300", "csrc")
+
+
+def body(text, opening):
+    """The braces that follow `opening`."""
+    at = text.index("{", text.index(opening))
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at:i + 1]
+    raise AssertionError(opening)
+
+
+# ------------------------------------------------------------------ attention
+
+# The largest value that attended() stores: 7 times scale byte 114, 10 / 16.
+LARGEST = 7 * 10 / 16
+
+
+def lost(lens):
+    """What weights near f16's smallest step, 2^-24, lose together: they are kept relative to 2^7 or more
+    for a row's largest, and each is off by half a step at most, 2^-32 of that, times the largest value.
+    Elements whose loud keys all hold zeros there are so small that it shows."""
+    return max(lens) * 2.0**-32 * LARGEST
+
+
+def test_an_items_state_is_not_read_behind_its_last_barrier():
+    """Thread 0 puts the next item's state in place of this one's as soon as it is through itself: the
+    other threads' reads have to stand before the item's last barrier."""
+    with open(os.path.join(CSRC, "quant_attend.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    items = body(text[text.index("bitlin_quant_attend(const __grid_constant__"):], "for (;;)")
+    tail = items[items.rindex("__syncthreads();"):]
+    assert "write_four" in tail  # (the rows' way out stands there)
+    assert [x for x in tail.splitlines() if re.search(r"\bwork\b", x) and "threadIdx.x == 0" not in x] == []
+
+
+@gpu
+@pytest.mark.parametrize("dim,group,out", [(256, 6, torch.bfloat16), (128, 4, torch.float32), (64, 8, torch.float32)])
+def test_ragged_items_one_after_the_other_in_a_cta(hrb, dim, group, out):
+    """Thousands of items of one step, with one to three tokens each: rows go to their own places."""
+    seqs = 900
+    lens, new = [3 + 7 * i % 41 for i in range(seqs)], [1 + (i * i) % 3 for i in range(seqs)]
+    case = (lens, new, 16, 2, group, dim, torch.bfloat16, out, True, "heads")
+    cache, batch, offsets, q, y, lse = attended(hrb, case, seed=21)
+    check_attended(y, lse, reference(cache, offsets, lens, q, True), torch.float16, lost(lens))
+    for _ in range(10):
+        again, again_lse = torch.full_like(y, 7.0), torch.full_like(lse, 7.0)
+        cache.kv.attend(q, batch, out=again, lse=again_lse)
+        assert torch.equal(again, y) and torch.equal(again_lse, lse)
+    assert cache.kv.get_error() == hrb.BITLIN_OK
