@@ -365,14 +365,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kBlocks) bit
         const int32_t* table = p.batch.table + work.seq * p.batch.table_stride;
         auto page_of = [&](int i) {  // the table's entry for this lane's key of tile i
             const int key = first + i * C::kStep + lane;
-            return i < n && key < end ? __ldg(table + (p.page_shift >= 0 ? key >> p.page_shift : key / p.pool.page_size)) : -2;
+            return i < n && key < end ? __ldg(table + (p.page_shift >= 0 ? key >> p.page_shift : key / p.pool.page_size)) : -1;
         };
         uint32_t at = 0, scale_at = 0;  // of this lane's key of the tile in issue
         bool held = false;
         auto aim = [&](int i, int page) {
             const int key = first + i * C::kStep + lane;
             held = page >= 0 && page < p.pool.pages;
-            if (page != -2 && !held) *p.index_error = 1;
+            if (!held && i < n && key < end) *p.index_error = 1;
             const int slot = p.page_shift >= 0 ? key & (p.pool.page_size - 1) : key % p.pool.page_size;
             at = held ? page * p.page_units + slot * p.slot_units + head * p.head_units : 0;
             scale_at = held ? page * p.scale_page_units + slot * p.scale_slot_units + head * p.scale_head_units : 0;

@@ -9,7 +9,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_quant_cache import attended, check_attended, gpu, hrb, reference  # noqa: E402,F401
+from test_attention_side import attend64  # noqa: E402
+from test_quant_cache import Cache, attended, batch_of, check_attended, gpu, hrb, reference  # noqa: E402,F401
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "hadamard_rotated_binary_gb300", "csrc")
 
@@ -63,3 +64,23 @@ def test_ragged_items_one_after_the_other_in_a_cta(hrb, dim, group, out):
         cache.kv.attend(q, batch, out=again, lse=again_lse)
         assert torch.equal(again, y) and torch.equal(again_lse, lse)
     assert cache.kv.get_error() == hrb.BITLIN_OK
+
+
+@gpu
+@pytest.mark.parametrize("bad", [-1, -2, -3, 8, -2**31])
+@pytest.mark.parametrize("out", [torch.float16, torch.float32])
+def test_every_page_outside_is_reported(hrb, bad, out):
+    lens, page, kvh, dim = [40, 40], 16, 2, 64
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    cache = Cache(hrb, gen, lens, page, kvh, dim, torch.float16).random(gen)
+    q = torch.randn((2, 8, dim), generator=gen, device="cuda").half()
+    batch, offsets = batch_of(hrb, [1, 1], cache)
+    cache.kv.attend(q, batch, dtype=out)
+    assert cache.kv.get_error() == hrb.BITLIN_OK
+    cache.table[1, 1] = bad
+    y = cache.kv.attend(q, batch, dtype=out)
+    assert cache.kv.get_error() == hrb.BITLIN_EINDEX and cache.kv.get_error() == hrb.BITLIN_OK
+    k, v = (torch.cat([x, torch.zeros_like(x[:1])]) for x in cache.values())
+    table = cache.table.cpu().clone()
+    table[1, 1] = k.shape[0] - 1
+    check_attended(y, None, attend64(q, k, v, offsets, lens, table, dim**-0.5, True), torch.float16)
