@@ -294,6 +294,7 @@ class QuantKV:
         through      a 16-bit cache of the same pages, page size, heads and dtype whose pools are
                      scratch (one serves all layers): calls whose sequences bring many tokens
                      read their pages back into it and attend there, faster for prompts
+                     (what goes wrong there, get_error of this handle tells)
         f32_through  whether float32 outputs go through it too: as exact as PagedKV.attend's
                      (up to 3e-6 off) and 2 to 7 times faster, where without it they are as
                      exact as float32 arithmetic

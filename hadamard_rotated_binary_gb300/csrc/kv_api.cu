@@ -96,6 +96,62 @@ cudaError_t new_workspace(bitlin_kv& h)
 
 }  // namespace
 
+bitlin_status bitlin_kv_attend_reporting(bitlin_kv_t kv, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q, int heads,
+                                         float scale, int causal, const bitlin_rows* out, float* lse, int* index_error,
+                                         bitlin_stream_t stream)
+{
+    if (!kv || !batch_ok(batch) || !rows_ok(q, tokens) || !rows_ok(out, tokens) || q->dtype != kv->dtype) return BITLIN_EINVAL;
+    if (out->dtype != kv->dtype && out->dtype != BITLIN_F32) return BITLIN_EINVAL;
+    if (!rows_wide(q) || !rows_wide(out) || !isfinite(scale) || (causal != 0 && causal != 1)) return BITLIN_EINVAL;
+    if (!sizes_ok(tokens, heads, kv->dim) || heads % kv->kv_heads || heads / kv->kv_heads > 128) return BITLIN_EINVAL;
+    if (!on_device(kv->device)) return BITLIN_EINVAL;
+    if (kv->sticky != BITLIN_OK) return kv->sticky;
+    if (tokens == 0) return BITLIN_OK;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const KvWorkspaceParts parts = bitlin_attend_workspace(kv->dim, kv->num_sms);
+    unsigned char* workspace = kv->workspace->data;
+    AttendParams p = {};
+    p.v_pool = kv->v;
+    p.page_stride = kv->page_stride;
+    p.slot_stride = kv->slot_stride;
+    p.head_stride = kv->head_stride;
+    p.batch = batch_of(batch);
+    p.out = out->data;
+    p.out_token = out->token_stride;
+    p.out_head = out->head_stride;
+    p.lse = lse;
+    p.ws_o = reinterpret_cast<float*>(workspace + parts.o);
+    p.ws_ml = reinterpret_cast<float*>(workspace + parts.ml);
+    p.tickets = reinterpret_cast<int*>(workspace);
+    p.timed_out = reinterpret_cast<int*>(workspace + parts.timed_out);
+    p.index_error = index_error;
+    p.wait_budget_ns = kv->wait_budget_ns;
+    p.pages = kv->pages;
+    p.page_size = kv->page_size;
+    p.page_shift = kv->page_size & (kv->page_size - 1) ? -1 : __builtin_ctz((unsigned)kv->page_size);
+    p.tokens = tokens;
+    p.heads = heads;
+    p.kv_heads = kv->kv_heads;
+    p.group = heads / kv->kv_heads;
+    p.dim = kv->dim;
+    p.causal = causal;
+    bitlin_attend_rows(tokens, batch->seqs, p.group, out->dtype, &p.tile_tokens, &p.q_box, &p.few);
+    p.item_extra = bitlin_attend_item_extra(kv->dim);
+    bitlin_attend_boxes(kv->dim, kv->page_size, &p.box_k, &p.box_v);
+    p.stall_test = kv->stall_test;
+    p.scale = scale;
+    alignas(64) unsigned char tmap_q[128];
+    const cudaError_t e = encode_queries(*kv, *q, tokens, heads, p.q_box, tmap_q);
+    if (e != cudaSuccess) return from_cuda(kv, e);
+    return from_cuda(kv, bitlin_launch_attend(p, kv->dtype, out->dtype, tmap_q, kv->tmap_k, kv->tmap_v, kv->num_sms, st));
+}
+
+cudaError_t bitlin_kv_timed_out(const KvWorkspace& w, int num_sms, int* timed_out)
+{
+    // (it lies at the same place for heads of every size)
+    return cudaMemcpy(timed_out, w.data + bitlin_attend_workspace(64, num_sms).timed_out, sizeof(int), cudaMemcpyDeviceToHost);
+}
+
 extern "C" {
 
 bitlin_status bitlin_rope_create(bitlin_rope_t* out, int rotary_dim, int axes, const float* inv_freq,
@@ -325,50 +381,7 @@ bitlin_status bitlin_kv_attend(bitlin_kv_t kv, const bitlin_kv_batch* batch, int
                                int heads, float scale, int causal, const bitlin_rows* out, float* lse,
                                bitlin_stream_t stream)
 {
-    if (!kv || !batch_ok(batch) || !rows_ok(q, tokens) || !rows_ok(out, tokens) || q->dtype != kv->dtype) return BITLIN_EINVAL;
-    if (out->dtype != kv->dtype && out->dtype != BITLIN_F32) return BITLIN_EINVAL;
-    if (!rows_wide(q) || !rows_wide(out) || !isfinite(scale) || (causal != 0 && causal != 1)) return BITLIN_EINVAL;
-    if (!sizes_ok(tokens, heads, kv->dim) || heads % kv->kv_heads || heads / kv->kv_heads > 128) return BITLIN_EINVAL;
-    if (!on_device(kv->device)) return BITLIN_EINVAL;
-    if (kv->sticky != BITLIN_OK) return kv->sticky;
-    if (tokens == 0) return BITLIN_OK;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const KvWorkspaceParts parts = bitlin_attend_workspace(kv->dim, kv->num_sms);
-    unsigned char* workspace = kv->workspace->data;
-    AttendParams p = {};
-    p.v_pool = kv->v;
-    p.page_stride = kv->page_stride;
-    p.slot_stride = kv->slot_stride;
-    p.head_stride = kv->head_stride;
-    p.batch = batch_of(batch);
-    p.out = out->data;
-    p.out_token = out->token_stride;
-    p.out_head = out->head_stride;
-    p.lse = lse;
-    p.ws_o = reinterpret_cast<float*>(workspace + parts.o);
-    p.ws_ml = reinterpret_cast<float*>(workspace + parts.ml);
-    p.tickets = reinterpret_cast<int*>(workspace);
-    p.timed_out = reinterpret_cast<int*>(workspace + parts.timed_out);
-    p.index_error = kv->index_error;
-    p.wait_budget_ns = kv->wait_budget_ns;
-    p.pages = kv->pages;
-    p.page_size = kv->page_size;
-    p.page_shift = kv->page_size & (kv->page_size - 1) ? -1 : __builtin_ctz((unsigned)kv->page_size);
-    p.tokens = tokens;
-    p.heads = heads;
-    p.kv_heads = kv->kv_heads;
-    p.group = heads / kv->kv_heads;
-    p.dim = kv->dim;
-    p.causal = causal;
-    bitlin_attend_rows(tokens, batch->seqs, p.group, out->dtype, &p.tile_tokens, &p.q_box, &p.few);
-    p.item_extra = bitlin_attend_item_extra(kv->dim);
-    bitlin_attend_boxes(kv->dim, kv->page_size, &p.box_k, &p.box_v);
-    p.stall_test = kv->stall_test;
-    p.scale = scale;
-    alignas(64) unsigned char tmap_q[128];
-    const cudaError_t e = encode_queries(*kv, *q, tokens, heads, p.q_box, tmap_q);
-    if (e != cudaSuccess) return from_cuda(kv, e);
-    return from_cuda(kv, bitlin_launch_attend(p, kv->dtype, out->dtype, tmap_q, kv->tmap_k, kv->tmap_v, kv->num_sms, st));
+    return bitlin_kv_attend_reporting(kv, batch, tokens, q, heads, scale, causal, out, lse, kv ? kv->index_error : nullptr, stream);
 }
 
 bitlin_status bitlin_kv_set_wait_budget(bitlin_kv_t kv, long long ns)
@@ -390,8 +403,7 @@ bitlin_status bitlin_kv_get_error(bitlin_kv_t kv)
     if (!kv) return BITLIN_EINVAL;
     cudaError_t e = cudaDeviceSynchronize();
     int timed_out = 0, index_error = 0;
-    const KvWorkspaceParts parts = bitlin_attend_workspace(kv->dim, kv->num_sms);
-    if (e == cudaSuccess) e = cudaMemcpy(&timed_out, kv->workspace->data + parts.timed_out, sizeof(int), cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess) e = bitlin_kv_timed_out(*kv->workspace, kv->num_sms, &timed_out);
     if (e == cudaSuccess) e = cudaMemcpy(&index_error, kv->index_error, sizeof(int), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return from_cuda(kv, e);
     if (timed_out) kv->sticky = BITLIN_ETIMEOUT;

@@ -240,7 +240,17 @@ struct bitlin_kvq {
     int last_cuda_error = 0;
     int* index_error = nullptr;
     std::shared_ptr<bitlin_impl::KvWorkspace> workspace;
+    // of the 16-bit cache that the last call went through, and whether a wait of such a call ran out
+    std::weak_ptr<bitlin_impl::KvWorkspace> through;
+    bool through_timed_out = false;
 };
+
+// bitlin_kv_attend whose pages outside the pool are reported to `index_error`.
+bitlin_status bitlin_kv_attend_reporting(bitlin_kv_t kv, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q, int heads,
+                                         float scale, int causal, const bitlin_rows* out, float* lse, int* index_error,
+                                         bitlin_stream_t stream);
+// Whether a bounded wait of a 16-bit cache's calls ran out in this workspace (the calls are through).
+cudaError_t bitlin_kv_timed_out(const bitlin_impl::KvWorkspace& w, int num_sms, int* timed_out);
 
 // Launchers (return a cudaError_t).
 cudaError_t bitlin_launch_norm_turn(const bitlin_impl::NormTurnParams& p, int src_dtype, int dst_dtype, bool quant, cudaStream_t s);

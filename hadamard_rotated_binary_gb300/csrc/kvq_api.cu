@@ -209,6 +209,12 @@ bitlin_status bitlin_kvq_attend(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const long long rows = (long long)tokens * (heads / kvq->pool.kv_heads);
     if (through && (f32_through || out->dtype != BITLIN_F32) && rows > kThroughRows * (long long)batch->seqs) {
+        if (kvq->through.lock() != through->workspace) {
+            kvq->through = through->workspace;
+            kvq->through_timed_out = false;
+        } else if (kvq->through_timed_out) {
+            return BITLIN_ETIMEOUT;
+        }
         QuantUnpackParams u = {};
         u.pool = kvq->pool;
         u.batch = batch_of(batch);
@@ -220,7 +226,7 @@ bitlin_status bitlin_kvq_attend(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, 
         u.index_error = kvq->index_error;
         const cudaError_t e = bitlin_launch_quant_unpack(u, kvq->dtype, kvq->num_sms, s);
         if (e != cudaSuccess) return from_cuda(kvq, e);
-        const bitlin_status st = bitlin_kv_attend(through, batch, tokens, q, heads, scale, causal, out, lse, stream);
+        const bitlin_status st = bitlin_kv_attend_reporting(through, batch, tokens, q, heads, scale, causal, out, lse, kvq->index_error, stream);
         if (st == BITLIN_ECUDA || st == BITLIN_ENOMEM) kvq->last_cuda_error = through->last_cuda_error;
         return st;
     }
@@ -265,9 +271,13 @@ bitlin_status bitlin_kvq_get_error(bitlin_kvq_t kvq)
 {
     if (!kvq) return BITLIN_EINVAL;
     cudaError_t e = cudaDeviceSynchronize();
-    int index_error = 0;
+    int index_error = 0, timed_out = 0;
+    const std::shared_ptr<KvWorkspace> through = kvq->through.lock();
+    if (e == cudaSuccess && through) e = bitlin_kv_timed_out(*through, kvq->num_sms, &timed_out);
     if (e == cudaSuccess) e = cudaMemcpy(&index_error, kvq->index_error, sizeof(int), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return from_cuda(kvq, e);
+    if (timed_out) kvq->through_timed_out = true;
+    if (kvq->through_timed_out) return BITLIN_ETIMEOUT;
     if (!index_error) return BITLIN_OK;
     e = cudaMemset(kvq->index_error, 0, sizeof(int));
     // before a later call, on whatever stream, can set it again

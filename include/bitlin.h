@@ -691,13 +691,21 @@ bitlin_status bitlin_kvq_read(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, in
  *
  * Calls that share a `through` must follow one another in stream order, as
  * those that share a workspace must.  Errors: as bitlin_kv_attend; the sticky
- * error is that of `through`.
+ * error is that of `through`, or a timeout that bitlin_kvq_get_error has told.
+ * What goes wrong on the device is reported by bitlin_kvq_get_error(kvq).
  */
 bitlin_status bitlin_kvq_attend(bitlin_kvq_t kvq, const bitlin_kv_batch* batch, int tokens, const bitlin_rows* q,
                                 int heads, float scale, int causal, const bitlin_rows* out, float* lse,
                                 bitlin_kv_t through, int f32_through, bitlin_stream_t stream);
 
-/* As bitlin_kv_get_error: BITLIN_EINDEX (once, then cleared) or BITLIN_ECUDA.  Synchronizes. */
+/*
+ * As bitlin_kv_get_error: BITLIN_EINDEX (once, then cleared; pages outside that a
+ * call met in `through` are this handle's too, not that of `through`), BITLIN_ECUDA,
+ * or BITLIN_ETIMEOUT: a wait of a call through 16-bit pages ran out, and its output
+ * is not valid.  That is told of the last `through` that a call used (of others
+ * bitlin_kv_get_error tells) and stays until a call uses one with another
+ * workspace.  Synchronizes.
+ */
 bitlin_status bitlin_kvq_get_error(bitlin_kvq_t kvq);
 
 /* The cudaError_t value behind the last BITLIN_ECUDA of this handle (0 if none). */

@@ -2,6 +2,7 @@
 
 Definitions, bounds and inputs are those of test_quant_cache.py.
 """
+import math
 import os
 import re
 
@@ -84,3 +85,41 @@ def test_every_page_outside_is_reported(hrb, bad, out):
     table = cache.table.cpu().clone()
     table[1, 1] = k.shape[0] - 1
     check_attended(y, None, attend64(q, k, v, offsets, lens, table, dim**-0.5, True), torch.float16)
+
+
+def scratch_of(hrb, cache):
+    shape = cache.parts[0].shape[:3] + (2 * cache.parts[0].shape[3],)
+    return hrb.PagedKV(*(torch.full(shape, math.nan, dtype=cache.kv.dtype, device="cuda") for _ in range(2)))
+
+
+@gpu
+def test_a_bad_page_through_16_bit_pages_is_reported_once(hrb):
+    case = ([40, 40], [30, 30], 16, 2, 4, 64, torch.float16, torch.float16, True, "heads")
+    cache, batch, offsets, q, y, _ = attended(hrb, case)
+    through = scratch_of(hrb, cache)
+    cache.table[1, 1] = 8
+    cache.kv.attend(q, batch, through=through)
+    assert cache.kv.get_error() == hrb.BITLIN_EINDEX and cache.kv.get_error() == hrb.BITLIN_OK
+    assert through.get_error() == hrb.BITLIN_OK
+    through.attend(q, batch)
+    assert through.get_error() == hrb.BITLIN_EINDEX and cache.kv.get_error() == hrb.BITLIN_OK
+
+
+@gpu
+def test_a_wait_that_runs_out_in_16_bit_pages_is_the_4_bit_caches_error(hrb):
+    case = ([300, 20], [40, 1], 16, 2, 4, 128, torch.bfloat16, torch.bfloat16, True, "heads")
+    cache, batch, offsets, q, want, _ = attended(hrb, case)
+    through = scratch_of(hrb, cache)
+    want = cache.kv.attend(q, batch, through=through)
+    assert cache.kv.get_error() == hrb.BITLIN_OK
+    through.set_wait_budget(2_000_000)
+    through.test_stall(True)
+    cache.kv.attend(q, batch, through=through)
+    through.test_stall(False)
+    assert cache.kv.get_error() == hrb.BITLIN_ETIMEOUT
+    with pytest.raises(hrb.BitlinError):
+        cache.kv.attend(q, batch, through=through)
+    assert cache.kv.get_error() == hrb.BITLIN_ETIMEOUT
+    fresh = scratch_of(hrb, cache)
+    assert torch.equal(cache.kv.attend(q, batch, through=fresh), want) and cache.kv.get_error() == hrb.BITLIN_OK
+    assert through.get_error() == hrb.BITLIN_ETIMEOUT
