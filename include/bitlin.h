@@ -413,7 +413,7 @@ bitlin_status bitlin_rope_apply(bitlin_rope_t r, const bitlin_rows* x, int token
  * and the rotation.
  *
  *   weight  device pointer, float [head_dim].
- *   eps     finite, >= 0.  A head of zeros with eps = 0 comes out as NaN.
+ *   eps     0 .. 1e38.  A head of zeros with eps = 0 comes out as NaN.
  *
  * out is good to 2e-6 (an f32 out) or 3.4e-6 (a 16-bit one, before its own
  * rounding) of its pair's norm (of the element itself past rotary_dim); each

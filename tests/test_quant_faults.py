@@ -10,8 +10,10 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_attention_side import attend64  # noqa: E402
-from test_quant_cache import Cache, attended, batch_of, check_attended, gpu, hrb, reference  # noqa: E402,F401
+from test_attention_side import attend64, freqs  # noqa: E402
+from test_quant_cache import (  # noqa: E402,F401
+    Cache, attended, batch_of, check_attended, encode64, gpu, hrb, norm64, reference, unpacked,
+)
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "hadamard_rotated_binary_gb300", "csrc")
 
@@ -123,3 +125,26 @@ def test_a_wait_that_runs_out_in_16_bit_pages_is_the_4_bit_caches_error(hrb):
     fresh = scratch_of(hrb, cache)
     assert torch.equal(cache.kv.attend(q, batch, through=fresh), want) and cache.kv.get_error() == hrb.BITLIN_OK
     assert through.get_error() == hrb.BITLIN_ETIMEOUT
+
+
+# ------------------------------------------------------------------ norms and the append
+
+
+@gpu
+def test_an_eps_that_f32_does_not_hold_is_refused(hrb):
+    rope, w = hrb.Rope(freqs(16)), torch.ones(64, device="cuda")
+    x, pos = 1e18 * torch.randn((16, 1, 64), device="cuda"), torch.arange(16, dtype=torch.int32, device="cuda")
+    cache = Cache(hrb, None, [16], 16, 1, 64, torch.bfloat16)
+    batch, _ = batch_of(hrb, [16], cache)
+    plain = hrb.PagedKV(*(torch.zeros((1, 16, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+    for eps in (1.1e38, 1e39, 1e300):
+        for call in (lambda: rope.apply(x, pos, norm=w, eps=eps), lambda: rope.gradient(x, x, pos, w, eps=eps),
+                     lambda: cache.kv.append(x, x, batch, k_norm=w, eps=eps), lambda: plain.append(x, x, batch, k_norm=w, eps=eps)):
+            with pytest.raises(hrb.BitlinError):
+                call()
+    # up to there, codes are those of the exact rows
+    cache.kv.append(x, x, batch, k_norm=w, eps=1e38)
+    codes, scales = encode64(norm64(x, w, 1e38))
+    page = int(cache.table[0, 0])
+    assert bool((scales > 0).all()) and torch.equal(cache.parts[2].cpu()[page], scales)
+    assert torch.equal(unpacked(cache.parts[0].cpu()[page]), codes)
