@@ -346,7 +346,8 @@ __device__ __forceinline__ void store_codes(float (&x)[8], const float (&size)[8
         // Does a border lie within an element's error, or between two scales within the largest's?
         emax *= kRowError;
         const float above = 3.5f * (s + quant_scale(c.scale + 1)), below = c.scale ? 3.5f * (s + quant_scale(c.scale - 1)) : -1.f;
-        const bool which = active && (far || (amax + emax >= above && c.scale < kQuantTopScale) || amax - emax <= below);
+        // (an infinite largest with an infinite error, where root times weight overflows, tells nothing either)
+        const bool which = active && (far || (amax + emax >= above && c.scale < kQuantTopScale) || !(amax - emax > below));
         if (__any_sync(0xffffffffu, active && (which || (near >= half && s > 0.f)))) {
             uint32_t doubt = 0;
 #pragma unroll

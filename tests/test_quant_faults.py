@@ -10,7 +10,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_attention_side import attend64, freqs  # noqa: E402
+from test_attention_side import attend64, freqs, rotate64  # noqa: E402
 from test_quant_cache import (  # noqa: E402,F401
     Cache, attended, batch_of, check_attended, encode64, gpu, hrb, norm64, reference, unpacked,
 )
@@ -147,4 +147,28 @@ def test_an_eps_that_f32_does_not_hold_is_refused(hrb):
     codes, scales = encode64(norm64(x, w, 1e38))
     page = int(cache.table[0, 0])
     assert bool((scales > 0).all()) and torch.equal(cache.parts[2].cpu()[page], scales)
+    assert torch.equal(unpacked(cache.parts[0].cpu()[page]), codes)
+
+
+@gpu
+@pytest.mark.parametrize("adjacent", [None, False, True])
+def test_codes_under_weights_whose_products_pass_f32(hrb, adjacent):
+    """Root times weight overflows in 32 bits where the row's values do not."""
+    dim, rotary = 64, 32
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    x = 2e-15 * torch.randn((16, 1, dim), generator=gen, device="cuda").sign()
+    x[..., 48:] = torch.randint(1, 90, (16, 1, 16), generator=gen, device="cuda") * 2.0**-149
+    w = torch.ones(dim, device="cuda")
+    w[48:] = 1e30
+    n = norm64(x, w, 0.0)
+    pos = torch.randint(0, 9000, (1, 16), generator=gen, device="cuda", dtype=torch.int32)
+    want = n if adjacent is None else rotate64(n, pos, freqs(rotary // 2), [0] * (rotary // 2), adjacent)
+    assert float(want[..., 48:].abs().max()) < 400
+    rope = None if adjacent is None else hrb.Rope(freqs(rotary // 2), adjacent=adjacent)
+    cache = Cache(hrb, None, [16], 16, 1, dim, torch.bfloat16)
+    batch, _ = batch_of(hrb, [16], cache)
+    cache.kv.append(x, x, batch, rope=rope, pos=None if rope is None else pos, k_norm=w, eps=0.0)
+    codes, scales = encode64(want)
+    page = int(cache.table[0, 0])
+    assert torch.equal(cache.parts[2].cpu()[page], scales)
     assert torch.equal(unpacked(cache.parts[0].cpu()[page]), codes)
