@@ -51,13 +51,18 @@ class Rope:
         (x itself is allowed) or a new tensor of `dtype` (x's where None).
 
         norm  float32 [dim]: each head is first divided by its root mean square (eps added to the
-              mean) and multiplied by this weight, in the same pass (bitlin_rope_apply_normed).
+              mean, 0 .. 1e38) and multiplied by this weight, in the same pass
+              (bitlin_rope_apply_normed).
+
+        Autograd does not record the call: the gradient is apply with inverse=True, or, with a norm,
+        `gradient`.
         """
         return native.rope_apply(self._h, self.device.index, self.axes, x, pos, out, dtype, inverse, stream, norm, eps)
 
     def gradient(self, dy, x, pos, norm, eps: float = 1e-6, dx=None, stream=None):
         """bitlin_rope_gradient: the gradient of apply(x, pos, norm=norm, eps=eps) from that of its
-        output: (dx in x's type, the weight's in float32).  dx: x, dy, or a tensor to write to."""
+        output: (dx in x's type, the weight's in float32).  dx: x, dy, or a tensor to write to.  Neither result
+        requires a gradient: hand them to a torch.autograd.Function's backward."""
         return native.rope_gradient(self._h, self.device.index, self.axes, dy, x, pos, norm, eps, dx, stream)
 
     def close(self):

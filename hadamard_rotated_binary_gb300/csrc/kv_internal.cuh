@@ -272,5 +272,5 @@ int bitlin_attend_item_extra(int dim);
 void bitlin_attend_boxes(int dim, int page_size, int* box_k, int* box_v);
 // The attention workspace's parts.
 bitlin_impl::KvWorkspaceParts bitlin_attend_workspace(int dim, int num_sms);
-// Load the kernels of a cache's calls (a first launch would, which a stream capture may not allow).
+// Load a cache's attention kernels and set their shared memory, so that no call has to.
 cudaError_t bitlin_attend_load(int dim, int dtype);

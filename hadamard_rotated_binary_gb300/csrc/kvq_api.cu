@@ -18,7 +18,7 @@ namespace {
 // 128 rows 69 and 51.  An f32 output goes through them only where the caller says so: it is
 // up to 3e-6 off there, 2.4 (f16) and 12 (bf16) times as far as f32 arithmetic, and closer than
 // that directly.  The price of that: 344 us for 141 (24-72 tokens a sequence on 210-1,050 keys, 24 heads of
-// 256), 9.3 ms for 1.6 (2,048 tokens over 32,768 keys); few key heads over long contexts gain
+// 256), 9.2 ms for 1.6 (2,048 tokens over 32,768 keys); few key heads over long contexts gain
 // (82 us to 30).
 constexpr long long kThroughRows = 80;
 

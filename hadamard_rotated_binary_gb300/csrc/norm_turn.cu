@@ -13,14 +13,16 @@
 // angles are computed once for them and their loads are in flight together, from
 // before the token's place is looked up (loads after it: 36.6 us for 31.5 below).
 // Where sizes, strides or alignment do not allow chunks, a lane takes up to four
-// pairs of single elements.
+// pairs of single elements: 2.5 times as long (8,192 x 16 x 80 bf16, 16 or 80 of 80
+// rotated 14.2 us, 20 of 80 35.7).
 //
 // In 4 bits the codes are those of the exact real-valued row, whatever the order
 // of the kernel's sums: a row is computed in 32 bits with a bound on its error
 // (24 units of 2^-24 of |a| + |b|: sum of squares 9 / 2, rsqrt 4, products 2,
 // angle, sine and cosine 4, rotation 2), and an element (or a group's scale)
 // that lies within it of a border between two codes is computed again in 64 bits,
-// one row in some 300; so is a row whose squares leave the range of 32 bits.  Rows
+// one row in 500 to 900 of normal ones (counted with these bounds); so is a row whose squares
+// leave the range of 32 bits.  Rows
 // that neither a norm nor a rotation touches are exact.
 // There a lane ends with eight consecutive elements (pairs half the rotated part
 // apart go through shared memory), and a team takes several heads one after the
@@ -29,11 +31,12 @@
 //
 // Measured (GB300, inputs changing from call to call; four and eight heads to a team,
 // two, in brackets): queries of 8,191 tokens, 32 heads of 128, bf16, 27.7 us (4.9 TB/s;
-// 41, 38, before 16-bit chunks were taken apart by words); 4,097 x 24 x 256 f32 32.8 us
+// 41, 38, before 16-bit chunks were taken apart by words); 4,097 x 24 x 256 f32 33.0 us
 // (6.1 TB/s), its gradient 50 us (6.0 TB/s; two heads at a time 53, blocks of 128 whose
 // sums are 608 rows to join 51); prompts of 8,191 tokens to 4 bits with their queries
-// and read back 76 us, issue at 80 % of its rate, with 72 registers of a thread (64 the
-// same, 96 eight to eleven more).  One token's queries 2.1 us in a graph.
+// and read back 77 us, issue at 80 % of its rate, with 72 registers of a thread (64 the
+// same, 96 eight to eleven more; with single elements 72 to 84 bytes of a thread spill).
+// One token's queries 2.1 us in a graph.
 #include "kv_internal.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -281,10 +284,11 @@ __device__ __noinline__ Codes codes_again(Codes c, Exact<TI> e, uint32_t doubt, 
 // of each, kRowError of which it may be off (EXACT: nothing; `far`: anything).  All lanes of the
 // warp take part.
 //
-// x / s comes from a product and one correction, which for 16-bit values lies on the right
-// side of every border (and on the border itself where x / s does); an f32 value's rest
-// x - c s, which is exact, decides.  Adding 1.5 2^23 + 8 rounds to the nearest (ties to even)
-// and leaves code + 8 in the low bits.
+// x / s comes from a product and one correction by its rest (Newton's iteration, as for
+// 1 / s), which for 16-bit values lies on the right side of every border (and on the
+// border itself where x / s does); an f32 value's rest x - c s, which is exact, decides.
+// Adding 1.5 2^23 + 8 rounds to the nearest (ties to even) and leaves code + 8 in the low
+// bits.
 template <typename TI, bool EXACT, typename Again>
 __device__ __forceinline__ void store_codes(float (&x)[8], const float (&size)[8], bool far, bool active, int u, int dim, int team, Again again,
                                             double eps, uint8_t* codes, uint8_t* scales)

@@ -30,6 +30,10 @@ __device__ __forceinline__ uint32_t quant_scale_code(T amax)
     return low + (amax > middle || (amax == middle && (low & 1)));
 }
 
+// Small integers to floats by joining them with a larger float's significand bits and taking that
+// float away again is a published conversion (Kim, Henry, Fahim and Awadalla, "Who Says Elephants
+// Can't Run", 2022, for 4 and 8 bits); the group's scale in its constants is this format's.
+//
 // Two nibbles of the same place in a word's halves, as f16 pairs: both of
 // (word & 0x000f000f) through `low`, of (word & 0x00f000f0) through `high`.
 struct QuantScale2 {

@@ -44,8 +44,10 @@
 // an item's begin takes 2 us and its end 1.5, which the other CTA on the SM covers in
 // part, a call's begin 4 us and its last join 4.  Measured (GB300, inputs changing from
 // call to call): one token over 131,072 keys, 138 MB, 45 us (f32 out); 64 over 100-8,000
-// keys, 282 MB, 70 us (4.0 TB/s), with heads of 128 dims 74 and of 64 (149 MB) 52; one
-// over 777 keys 11 us; 16 x 5 drafted tokens over 1,000-6,000 keys, 128 dims, 43 us.
+// keys, 274 MB, 70 us (3.9 TB/s; f32 out 80), with 8 heads of 128 dims (282 MB) 75 and of 64
+// (149 MB) 52; one over 777 keys 11 us; 16 x 5 drafted tokens over 1,000-6,000 keys, 128 dims,
+// 43 us, 256 dims 53; single tokens over 262,000 keys in all 68 us as 64 sequences, 78 as 256,
+// 133 as 1,000 and 379 as 4,000 (each CTA goes through all of them to find its part).
 #include <math.h>
 
 #include "kv_internal.cuh"
@@ -63,7 +65,9 @@ constexpr float kLazy = 8.f;      // log2 of the growth that another reference w
 
 template <int D, int NT>
 struct Cfg {
-    // Warps of a CTA and CTAs on an SM, so that a thread has the registers it needs.
+    // Warps of a CTA and CTAs on an SM, so that a thread has nearly the registers it needs: what
+    // spills (bytes stored) is 156 at 256 dims and 16 rows, 52 at 256 dims, 8 rows and an f32 output,
+    // 28 at most elsewhere.
     static constexpr int kOutputs = D / 32 * NT * 8;       // a thread's part of the output, in registers
     static constexpr int kBlocks = kOutputs > 64 ? 1 : 2;
     static constexpr int kWarps = kOutputs == 48 || kOutputs == 64 ? 6 : 8;
