@@ -126,10 +126,17 @@ class KVBatch:
         self.address = ctypes.addressof(self._c)
 
 
+def _same_kind(cache, kind, name: str):
+    """A handle reaches the library as an address, which does not say what lies there."""
+    if cache is not None and not isinstance(cache, kind):
+        raise ValueError(f"{name} must be a {kind.__name__}")
+
+
 def _rope_of(rope: Rope | None, device):
     """(handle, axes) of an append's rope."""
     if rope is None:
         return None, 0
+    _same_kind(rope, Rope, "rope")
     if not rope._h:
         raise ValueError("the rope's handle is closed")  # (None would mean no rotation)
     if rope.device != device:
@@ -158,6 +165,7 @@ class PagedKV:
             raise ValueError("k and v must be bfloat16 or float16 CUDA tensors with contiguous heads")
         if k.device != v.device:
             raise ValueError("k and v must be on one device")
+        _same_kind(share, PagedKV, "share")
         self.k, self.v = k, v
         self.device, self.dtype = k.device, k.dtype
         pages, page_size, self.kv_heads, self.head_dim = k.shape
@@ -251,6 +259,7 @@ class QuantKV:
             raise ValueError("k and v must have one layout, and their scales one")
         if dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("dtype must be bfloat16 or float16")
+        _same_kind(share, QuantKV, "share")
         self.k, self.v, self.k_scale, self.v_scale = parts
         self.device, self.dtype = k.device, dtype
         pages, page_size, self.kv_heads, self.head_dim = *k.shape[:3], 2 * k.shape[3]
@@ -304,6 +313,7 @@ class QuantKV:
                      (up to 3e-6 off) and 2 to 7 times faster, where without it they are as
                      exact as float32 arithmetic
         """
+        _same_kind(through, PagedKV, "through")
         if through is not None and not through._h:
             raise ValueError("through's handle is closed")
         return native.kvq_attend(self._h, self.device.index, self.head_dim, self.dtype, self._address_of(batch), q, scale,

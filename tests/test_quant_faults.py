@@ -372,3 +372,18 @@ def test_first_calls_can_be_captured(hrb):
     done = subprocess.run([sys.executable, "-c", FIRST, *calls], cwd=root, capture_output=True, text=True, timeout=300,
                           env={**os.environ, "CUDA_MODULE_LOADING": "LAZY"})
     assert done.returncode == 0 and done.stdout.split() == [w for c in calls for w in (c, "ok")], done.stderr[-2000:]
+
+
+@gpu
+def test_handles_of_another_kind_are_refused(hrb):
+    parts = hrb.QuantKV.pools(4, 16, 2, 64)
+    pools = [torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    small, plain, rope = hrb.QuantKV(*parts), hrb.PagedKV(*pools), hrb.Rope(freqs(16))
+    batch = hrb.KVBatch(*(torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 3], [3], [[1]])))
+    q = torch.randn((3, 4, 64), device="cuda").bfloat16()
+    for call in (lambda: hrb.QuantKV(*parts, share=plain), lambda: hrb.PagedKV(*pools, share=small), lambda: hrb.QuantKV(*parts, share=rope),
+                 lambda: small.attend(q, batch, through=small), lambda: small.attend(q, batch, through=rope),
+                 lambda: small.append(q[:, :2], q[:, :2], batch, rope=small), lambda: plain.append(q[:, :2], q[:, :2], batch, rope=plain)):
+        with pytest.raises(ValueError):
+            call()
+    assert small.get_error() == hrb.BITLIN_OK and plain.get_error() == hrb.BITLIN_OK
