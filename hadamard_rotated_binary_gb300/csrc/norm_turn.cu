@@ -673,8 +673,8 @@ __global__ void __launch_bounds__(kThreads, QUANT ? 7 : 1) bitlin_norm_turn(cons
             if (weight) {
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    x[j] *= r[h] * wx[i][j];
-                    y[j] *= r[h] * wy[i][j];
+                    x[j] = x[j] * r[h] * wx[i][j];  // (root times weight may overflow where this does not)
+                    y[j] = y[j] * r[h] * wy[i][j];
                 }
             }
             if (unit[i].turns) rotate<VEC>(x, y, cs[i], sn[i], p.adjacent);

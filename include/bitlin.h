@@ -444,7 +444,9 @@ size_t bitlin_rope_gradient_scratch(int tokens, int heads, int head_dim);
  *            aligned; in use until the call's work is done.
  *
  * Sums are held in f32 and joined in a fixed order: the same call gives the
- * same bits.  Asynchronous.  Errors: as bitlin_rope_apply_normed, and
+ * same bits.  Rows whose squares leave f32's range, as bitlin_rope_apply_normed
+ * says, or whose sum of dy * weight * x does, have no valid gradient.
+ * Asynchronous.  Errors: as bitlin_rope_apply_normed, and
  * BITLIN_ESCRATCH (NULL or too small).
  */
 bitlin_status bitlin_rope_gradient(bitlin_rope_t r, const bitlin_rows* dy, const bitlin_rows* x, int tokens, int heads,

@@ -196,6 +196,23 @@ def test_prompts_stored_several_heads_to_a_team(hrb, case):
     base.test_stored_codes_are_those_of_the_exact_rows(hrb, case)
 
 
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_normed_rows_under_weights_whose_products_pass_f32(hrb, dtype):
+    """Root times weight overflows in 32 bits where the row's values do not."""
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    rope, pos, w = hrb.Rope(freqs(16)), torch.zeros((1, 16), dtype=torch.int32, device="cuda"), torch.ones(64, device="cuda")
+    x = 2e-15 * torch.randn((16, 3, 64), generator=gen, device="cuda").sign()
+    x[..., 48:] *= 2.0**-30
+    w[48:] = 1e30
+    x = x.to(dtype)
+    want = norm64(x, w, 0.0)
+    assert 1e20 < float(want[..., 48:].abs().min()) and float(want.abs().max()) < 1e30
+    got = rope.apply(x, pos, norm=w, eps=0.0)
+    # the sum's root 4.5 u and rsqrt's 4, two products 2: 11 u, and the output's rounding
+    assert bool(((got.double().cpu() - want).abs() <= (11 * 2.0**-24 + 1.01 * U[dtype]) * want.abs()).all())
+
+
 # ------------------------------------------------------------------ the gradient
 
 COUNTED = [
