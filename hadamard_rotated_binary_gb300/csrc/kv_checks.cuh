@@ -93,7 +93,7 @@ inline void set_out(TurnParams& p, const bitlin_rows* r)
 constexpr int kNormMaxDim = 256;  // of a head with a norm
 
 inline bool weight_ok(const float* w) { return w && reinterpret_cast<uintptr_t>(w) % alignof(float) == 0; }
-// At most 1e38: with a mean that f32 holds, their sum stays in its range.
+// At most 1e38: added to the mean of two squares or more whose sum f32 holds, it stays in f32's range.
 inline bool eps_ok(double eps) { return eps >= 0 && eps <= 1e38; }
 inline bool norms_ok(const bitlin_head_norms* n)
 {

@@ -47,7 +47,8 @@
 // keys, 274 MB, 70 us (3.9 TB/s; f32 out 80), with 8 heads of 128 dims (282 MB) 75 and of 64
 // (149 MB) 52; one over 777 keys 11 us; 16 x 5 drafted tokens over 1,000-6,000 keys, 128 dims,
 // 43 us, 256 dims 53; single tokens over 262,000 keys in all 68 us as 64 sequences, 78 as 256,
-// 133 as 1,000 and 379 as 4,000 (each CTA goes through all of them to find its part).
+// 133 as 1,000 and 379 as 4,000 (more ends of items, and each CTA goes through all sequences to
+// find its part; how much each takes was not measured).
 #include <math.h>
 
 #include "kv_internal.cuh"
